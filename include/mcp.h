@@ -46,6 +46,7 @@
  *                    step's tokens ([W] "记录 KV Cache 的长度")
  *      slot_mapping  [T] int64, physical_page * P + offset; < 0 = skip
  *      lse           [T, H_q] float32, natural-log sum of exp of the scores
+ *    (the recurrent layers and the logits calls state their own types)
  *    Query head h uses kv head h / (H_q / H_kv) (grouped-query attention;
  *    with H_q == H_kv this is [K]'s multi-head indexing).
  */
@@ -584,6 +585,239 @@ mcp_status mcp_mixed_attn_fwd_varlen(const mcp_plan* plan, const void* q, const 
                                      float* lse, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
+/* ------------------------------------------------------------------------- */
+/* A step's tables, built on the device                                       */
+/* ------------------------------------------------------------------------- */
+/*
+ * mcp_build_slot_mapping, mcp_build_logits_indices and the page allocation of
+ * a step, from request lengths that live on the device ([L] 4.1, 4.2; [W]
+ * "输入组装"): the caller keeps one page-table row and one length per request
+ * and a list of free pages on the device; a step is given by the rows of its
+ * requests and their new tokens.  All memory is the caller's.
+ */
+typedef struct mcp_request_pool {
+  int32_t max_requests;      /* R, rows of request_pages and request_lens (<= 2^24)   */
+  int32_t max_pages_per_seq; /* row length of request_pages and of block_tables       */
+  int32_t page_size;         /* P: 1, 8, 16, 32 or 64                                 */
+  int32_t num_pages;         /* room of free_pages (the pages of the KV pool)         */
+  int32_t* request_pages;    /* device [R, max_pages_per_seq]: logical -> physical    */
+  int32_t* request_lens;     /* device [R]: tokens that each request holds            */
+  int32_t* free_pages;       /* device [num_pages]: entries [0, *free_count) are free */
+  int32_t* free_count;       /* device [1]                                            */
+} mcp_request_pool;
+
+/*
+ * For segment s with request row r = request_ids[s] and q = q_lens[s] new
+ * tokens: held = ceil(request_lens[r] / P) pages are there, after =
+ * ceil((request_lens[r] + q) / P) are needed.  The step's K = sum(after - held)
+ * new pages are the top of the free list in segment order: new page k is
+ * free_pages[*free_count - K + k].
+ *   cu_seqlens_q [S+1], seqlens_k [S] = request_lens[r] + q
+ *   block_tables [S, max_pages_per_seq]: the after pages, then -1
+ *   slot_mapping int64 [max_tokens]: the slot of each new token, -1 behind the
+ *       last one (mcp_paged_kv_append skips those)
+ *   positions    int32 [max_tokens] or NULL: position of each new token, then 0
+ *   logits_indices int32 [S] or NULL: the last token of every segment that has
+ *       one, in segment order, then -1
+ * request_ids[s] < 0 is a padding segment: no tokens, a row of -1 (a captured
+ * step of fixed size).  The new pages are also entered into request_pages
+ * behind the held ones; lengths and free list stay as they are until
+ * mcp_commit_step, so building the same step again gives the same tables.
+ *
+ * Sound as a whole or not at all: a request row outside [0, R) or in two
+ * segments, a negative length, more tokens than the table row or max_tokens
+ * hold (MCP_DEVERR_REQUEST), or fewer free pages than K (MCP_DEVERR_NO_PAGES),
+ * sets the error word and gives an empty step: cu_seqlens_q, seqlens_k and
+ * positions 0, everything else -1, request_pages untouched.
+ *
+ * request_ids, q_lens: device int32 [S].  S <= 8192.  request_pages,
+ * block_tables 16-byte aligned, max_pages_per_seq * P < 2^31.  error_word:
+ * device int32 or NULL.  Page ids are not checked here; the calls that read
+ * pages check them.  Steps of one pool must be ordered (one stream).
+ */
+mcp_status mcp_build_step_tables(const mcp_request_pool* pool, const int32_t* request_ids,
+                                 const int32_t* q_lens, int32_t num_seqs, int32_t max_tokens,
+                                 int32_t* cu_seqlens_q, int32_t* seqlens_k, int32_t* block_tables,
+                                 int64_t* slot_mapping, int32_t* positions,
+                                 int32_t* logits_indices, int32_t* error_word, void* stream);
+
+/*
+ * The step built from the same request_ids and q_lens (mcp_build_step_tables,
+ * earlier on the stream) is over: request_lens[r] = new_lens[s], with
+ * 0 <= new_lens[s] <= request_lens[r] + q_lens[s] (NULL: every new token
+ * stays), *free_count is moved and the pages behind each new length go back to
+ * the free list, in segment order from free_pages[*free_count - K] on.  Fewer
+ * tokens than were run: rejected speculated tokens.  Length 0: the request is
+ * over; its row may be used again.  A step that the build refused, or a length
+ * out of range, sets the error word and changes nothing.  Pages are counted by
+ * length: a request whose length does not match its page row corrupts the list.
+ */
+mcp_status mcp_commit_step(const mcp_request_pool* pool, const int32_t* request_ids,
+                           const int32_t* q_lens, const int32_t* new_lens, int32_t num_seqs,
+                           int32_t* error_word, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Recurrent layers over the packed stream                                    */
+/* ------------------------------------------------------------------------- */
+/*
+ * Models that mix attention with recurrent layers run those on the same
+ * stream: segment s is tokens cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1 of the
+ * request in row request_ids[s] of the state.  A segment whose seqlens_k
+ * counts more tokens than its own (history) continues the row's state, any
+ * other starts from zero; the state after its last token is written back.  A
+ * segment without tokens, and request_ids[s] < 0 (padding), leave the state
+ * as it is; tokens behind the last segment are neither read nor written.
+ *
+ * The metadata are device arrays, checked on the device.  A segment past
+ * total_tokens or with seqlens_k < its tokens sets MCP_DEVERR_SEGMENT (the
+ * first is left out), a request row >= num_requests MCP_DEVERR_REQUEST (its
+ * segment is left out).  cu_seqlens_q that does not start at 0 or decreases
+ * (MCP_DEVERR_SEGMENT) leaves the call's outputs undefined, a request in two
+ * segments that have tokens (MCP_DEVERR_REQUEST) its state and outputs.
+ *
+ * Token rows may be part of wider rows: *_stride is the distance of
+ * consecutive tokens in elements, a multiple of 8; tensors are 16-byte
+ * aligned.  Sums and the scan's state are fp32; outputs are rounded once.
+ */
+typedef enum mcp_dtype { MCP_DTYPE_BF16 = 0, MCP_DTYPE_FP16 = 1, MCP_DTYPE_FP32 = 2 } mcp_dtype;
+
+typedef struct mcp_conv_desc {
+  int32_t num_seqs;
+  int32_t total_tokens; /* rows of x and out                                 */
+  int32_t num_requests; /* rows of the state                                 */
+  int32_t channels;     /* a multiple of 8                                   */
+  int32_t width;        /* K: 2, 3 or 4                                      */
+  int32_t dtype;        /* MCP_DTYPE_BF16 or _FP16: x, weight, bias, state, out */
+  int32_t activation;   /* 0 none, 1 silu                                    */
+  int32_t reserved;     /* must be 0                                         */
+  int64_t x_stride, out_stride;
+} mcp_conv_desc;
+
+/*
+ * Short causal convolution, one filter per channel:
+ *   out[t,c] = act(bias[c] + sum_k weight[c,k] v[t-K+1+k,c]),
+ * v being the segment's inputs and, before its first, the K-1 inputs kept in
+ * state[r] (or zeros).  state[r] receives the last K-1 of them.
+ * x [total_tokens, channels], weight [channels, K], bias [channels] or NULL,
+ * state [num_requests, K-1, channels] (oldest input first), out as x (may not
+ * overlap x).
+ */
+mcp_status mcp_mixed_conv(const mcp_conv_desc* desc, const void* x, const void* weight,
+                          const void* bias, void* state, const int32_t* request_ids,
+                          const int32_t* cu_seqlens_q, const int32_t* seqlens_k, void* out,
+                          int32_t* error_word, void* stream);
+
+typedef struct mcp_scan_desc {
+  int32_t num_seqs;
+  int32_t total_tokens; /* rows of x, dt, z, B, C and out                        */
+  int32_t num_requests; /* rows of the state                                     */
+  int32_t channels;     /* a multiple of 8                                       */
+  int32_t state_size;   /* N: 8, 16, 32 or 64                                    */
+  int32_t num_groups;   /* channels share B and C in groups; channels/num_groups */
+                        /* a multiple of 32 unless num_groups is 1               */
+  int32_t dtype;        /* MCP_DTYPE_BF16 or _FP16: x, dt, z, B, C, out          */
+  int32_t softplus;     /* 1: d = ln(1 + exp(dt + dt_bias)), 0: d = dt + dt_bias */
+  int64_t x_stride, dt_stride, z_stride, b_stride, c_stride, out_stride;
+} mcp_scan_desc;
+
+typedef struct mcp_scan_tensors {
+  const void* x;        /* [total_tokens, channels]                            */
+  const void* dt;       /* [total_tokens, channels]                            */
+  const float* A;       /* [channels, N]                                       */
+  const void* B;        /* [total_tokens, num_groups, N]                       */
+  const void* C;        /* [total_tokens, num_groups, N]                       */
+  const float* D;       /* [channels] or NULL                                  */
+  const void* z;        /* [total_tokens, channels] or NULL                    */
+  const float* dt_bias; /* [channels] or NULL                                  */
+  float* state;         /* [num_requests, channels, N]                         */
+  void* out;            /* [total_tokens, channels]; may not overlap an input  */
+} mcp_scan_tensors;
+
+/*
+ * Selective state space scan, per channel c of group g and state n:
+ *   h[c,n] = exp(d A[c,n]) h[c,n] + d x B[g,n],
+ *   y = sum_n C[g,n] h[c,n] + D[c] x,   out = y z / (1 + exp(-z))  (y without z).
+ */
+mcp_status mcp_mixed_scan(const mcp_scan_desc* desc, const mcp_scan_tensors* tensors,
+                          const int32_t* request_ids, const int32_t* cu_seqlens_q,
+                          const int32_t* seqlens_k, int32_t* error_word, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* The sampled rows' logits                                                   */
+/* ------------------------------------------------------------------------- */
+/*
+ * [W] "采样": only the rows at logits_indices have logits.  What lies between
+ * the output head and the sampler reads which tokens the row's request has
+ * had; that state is kept on the device, per request row r, with
+ * W = ceil(vocab_size / 32):
+ *   seen   int32 [num_requests, 2, W]: bit (v % 32) of word v / 32 of plane 0:
+ *          token v is in the prompt; of plane 1: it was sampled
+ *   counts int32 [num_requests, 32 W]: how often token v was sampled
+ *
+ * mcp_update_token_counts adds tokens[cu_tokens[i] .. cu_tokens[i+1]-1] to
+ * request row request_ids[i], i < num_rows (cu_tokens NULL: token i alone, and
+ * num_tokens = num_rows): to the prompt (MCP_COUNT_PROMPT: plane 0) or to the
+ * sampled tokens (plane 1 and counts).  MCP_COUNT_RESET clears the rows first.
+ * A negative request row or token is padding; tokens behind cu_tokens[num_rows]
+ * are not read.  A row >= num_requests (MCP_DEVERR_REQUEST) or a token >=
+ * vocab_size (MCP_DEVERR_TOKEN_RANGE) is left out.  A request may stand in
+ * several rows; the result does not depend on the order.  Clearing counts
+ * relies on plane 1 marking every non-zero count (zero both to begin with).
+ */
+#define MCP_COUNT_PROMPT 0x1
+#define MCP_COUNT_RESET 0x2
+mcp_status mcp_update_token_counts(const int32_t* request_ids, int32_t num_rows,
+                                   const int32_t* tokens, int32_t num_tokens,
+                                   const int32_t* cu_tokens, int32_t* seen, int32_t* counts,
+                                   int32_t num_requests, int32_t vocab_size, int32_t flags,
+                                   int32_t* error_word, void* stream);
+
+typedef struct mcp_logits_desc {
+  int32_t num_rows;
+  int32_t vocab_size;
+  int32_t num_requests; /* rows of seen and counts (0 without them)              */
+  int32_t dtype;        /* of logits                                             */
+  int32_t out_dtype;    /* dtype, or MCP_DTYPE_FP32                              */
+  int32_t num_biases;   /* entries of bias_tokens and bias_values                */
+  int32_t num_masks;    /* rows of mask                                          */
+  int32_t reserved;     /* must be 0                                             */
+  int64_t logits_stride, out_stride; /* elements between rows, >= vocab_size     */
+} mcp_logits_desc;
+
+typedef struct mcp_logits_tensors {
+  const void* logits;              /* [num_rows, vocab_size]                      */
+  void* out;                       /* the same; == logits: in place               */
+  const int32_t* request_ids;      /* [num_rows] rows of seen / counts, or NULL   */
+  const int32_t* seen;
+  const int32_t* counts;
+  const float* temperature;        /* [num_rows] or NULL; <= 0: none              */
+  const float* repetition_penalty; /* [num_rows] > 0, or NULL                     */
+  const float* frequency_penalty;  /* [num_rows] or NULL                          */
+  const float* presence_penalty;   /* [num_rows] or NULL                          */
+  const int32_t* bias_offsets;     /* [num_rows + 1] or NULL: row i's biases are  */
+  const int32_t* bias_tokens;      /*   entries bias_offsets[i] .. [i+1]-1, with  */
+  const float* bias_values;        /*   strictly increasing tokens                */
+  const int32_t* mask;             /* [num_masks, W] or NULL: bit 0 = not allowed */
+  const int32_t* mask_rows;        /* [num_rows] row of mask, < 0: no mask; NULL: */
+                                   /*   row i has mask i                          */
+} mcp_logits_tensors;
+
+/*
+ * For every row i with request row r and token v, in fp32, rounded once:
+ *   x = logits[i,v] + bias;   x = x > 0 ? x / repetition : x * repetition  if v
+ *   is in the prompt or was sampled;   x -= frequency * counts[r,v] + presence
+ *   if it was sampled;   x /= temperature if > 0;   x = -inf if the mask's bit
+ *   is 0 (whatever x was, NaN included).
+ * A row with request_ids[i] < 0 is padding and is not written.  A request row
+ * >= num_requests or a mask row >= num_masks sets MCP_DEVERR_REQUEST and the
+ * row is not written; a bias token outside the vocabulary is left out, and it
+ * and tokens out of order set MCP_DEVERR_TOKEN_RANGE (of a repeated token one
+ * bias counts).  All tensors are device memory; logits and out need the
+ * alignment of their type only (rows of an odd vocabulary), counts 16 bytes.
+ */
+mcp_status mcp_process_logits(const mcp_logits_desc* desc, const mcp_logits_tensors* tensors,
+                              int32_t* error_word, void* stream);
+
 /* Device-check bits written to an error word. */
 #define MCP_DEVERR_TIMEOUT 0x1      /* a bounded mbarrier wait gave up           */
 #define MCP_DEVERR_PAGE_RANGE 0x2   /* a block-table page id outside the pool    */
@@ -591,6 +825,10 @@ mcp_status mcp_mixed_attn_fwd_varlen(const mcp_plan* plan, const void* q, const 
 #define MCP_DEVERR_ROW_RANGE 0x8    /* a gathered row index outside the source   */
 #define MCP_DEVERR_ITEM_KIND 0x10   /* a work item this head_dim has no path for */
 #define MCP_DEVERR_SLOT_DUP 0x20    /* two append tokens share a slot (MCP_CHECKED) */
+#define MCP_DEVERR_NO_PAGES 0x40    /* a step needs more pages than are free     */
+#define MCP_DEVERR_REQUEST 0x80     /* a request row outside its state, or twice */
+#define MCP_DEVERR_TOKEN_RANGE 0x100 /* a token outside the vocabulary           */
+#define MCP_DEVERR_SEGMENT 0x200    /* a segment outside the token stream        */
 
 #ifdef __cplusplus
 }

@@ -9,6 +9,7 @@ PyTorch fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -16,15 +17,20 @@ import numpy as np
 from . import _capi
 from ._capi import (  # noqa: F401
     DEVERR_ITEM_KIND,
+    DEVERR_NO_PAGES,
     DEVERR_PAGE_RANGE,
+    DEVERR_REQUEST,
     DEVERR_ROW_RANGE,
+    DEVERR_SEGMENT,
     DEVERR_SLOT_DUP,
     DEVERR_SLOT_RANGE,
     DEVERR_TIMEOUT,
+    DEVERR_TOKEN_RANGE,
     AttnDesc,
     MCPError,
     Plan,
     PlanOptions,
+    RequestPool,
 )
 
 __all__ = [
@@ -32,7 +38,8 @@ __all__ = [
     "build_slot_mapping", "mixed_attn_plan", "mixed_attn_fwd", "check_device_errors",
     "workspace_error_word", "merge_states", "make_desc", "mixed_attn_fwd_noalloc",
     "mixed_attn_plan_rows", "build_logits_indices", "gather_rows", "kv_copy_pages",
-    "mixed_attn_varlen",
+    "mixed_attn_varlen", "RequestPool", "make_request_pool", "build_step_tables", "commit_step",
+    "mixed_conv", "mixed_scan", "update_token_counts", "process_logits",
 ]
 
 
@@ -348,3 +355,323 @@ def mixed_attn_fwd_noalloc(desc: AttnDesc, h_cu_seqlens_q, h_seqlens_k, q, k_cac
         _stream(stream))
     _capi.check(st, "mixed_attn_fwd_noalloc")
     return int(ew.value or 0)
+
+
+# ---------------------------------------------------------------------------
+# the operators around a step's attention
+# ---------------------------------------------------------------------------
+
+def _on(t):
+    """The device that tensor ``t`` is on, as the current one."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return torch.cuda.device(t.device) if t.get_device() != torch.cuda.current_device() \
+        else contextlib.nullcontext()
+
+
+def _arg(t, dtype, name, like, shape=None):
+    """Device address of a contiguous CUDA tensor on the device of ``like`` (None: no address)."""
+    import torch
+
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _row_arg(t, name, like, shape):
+    """(address, stride between tokens) of [tokens, ...] rows of ``like``'s type that may be
+    part of wider rows: everything behind the first dimension is dense."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    row = 1
+    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != row:
+            raise ValueError(f"{name}: a token's row must be dense, got strides {t.stride()}")
+        row *= n
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else -(-row // 8) * 8
+
+
+def _error(error_word, like):
+    """Address of an error word: None, an int32 CUDA tensor, or a device address."""
+    import torch
+
+    if error_word is None or isinstance(error_word, torch.Tensor):
+        return _arg(error_word, torch.int32, "error_word", like)
+    return int(error_word)
+
+
+def _result(out, stream, make):
+    """``out``, or a new tensor of ``make()`` that ``stream`` may use."""
+    import torch
+
+    if out is not None:
+        return out
+    out = make()
+    if stream is not None:
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        out.record_stream(s)
+    return out
+
+
+def make_request_pool(request_pages, request_lens, free_pages, free_count,
+                      page_size) -> RequestPool:
+    """The device-side pages of all requests (see ``mcp_request_pool`` in include/mcp.h) over
+    int32 CUDA tensors: request_pages [R, max_pages_per_seq], request_lens [R], free_pages
+    [num_pages], free_count [1].  The tensors stay the caller's state; the pool keeps them."""
+    import torch
+
+    _on(request_pages)
+    if request_pages.dim() != 2:
+        raise ValueError("request_pages must be [max_requests, max_pages_per_seq]")
+    R, width = request_pages.shape
+    i32 = torch.int32
+    pool = RequestPool(
+        R, width, int(page_size), int(free_pages.numel()),
+        _arg(request_pages, i32, "request_pages", request_pages),
+        _arg(request_lens, i32, "request_lens", request_pages, (R,)),
+        _arg(free_pages, i32, "free_pages", request_pages),
+        _arg(free_count, i32, "free_count", request_pages, (1,)))
+    pool.tensors = (request_pages, request_lens, free_pages, free_count)
+    return pool
+
+
+def build_step_tables(pool: RequestPool, request_ids, q_lens, cu_seqlens_q, seqlens_k,
+                      block_tables, slot_mapping, positions=None, logits_indices=None,
+                      error_word=None, stream=None) -> None:
+    """Tables, slots and pages of a step from the lengths in ``pool`` (see include/mcp.h):
+    request_ids, q_lens [S] in; cu_seqlens_q [S + 1], seqlens_k [S], block_tables
+    [S, max_pages_per_seq], slot_mapping [max_tokens] (int64), positions [max_tokens] and
+    logits_indices [S] out, all int32 CUDA tensors otherwise."""
+    import torch
+
+    lib = load()
+    like, i32 = request_ids, torch.int32
+    with _on(like):
+        S, cap = int(request_ids.shape[0]), int(slot_mapping.shape[0])
+        one = (S,)
+        st = lib.mcp_build_step_tables(
+            ctypes.byref(pool), _arg(request_ids, i32, "request_ids", like, one),
+            _arg(q_lens, i32, "q_lens", like, one), S, cap,
+            _arg(cu_seqlens_q, i32, "cu_seqlens_q", like, (S + 1,)),
+            _arg(seqlens_k, i32, "seqlens_k", like, one),
+            _arg(block_tables, i32, "block_tables", like, (S, pool.max_pages_per_seq)),
+            _arg(slot_mapping, torch.int64, "slot_mapping", like, (cap,)),
+            _arg(positions, i32, "positions", like, (cap,)),
+            _arg(logits_indices, i32, "logits_indices", like, one),
+            _error(error_word, like), _stream(stream))
+    _capi.check(st, "build_step_tables")
+
+
+def commit_step(pool: RequestPool, request_ids, q_lens, new_lens=None, error_word=None,
+                stream=None) -> None:
+    """The built step is over: request lengths become ``new_lens`` [S] (None: every new token
+    stays, 0: the request is over) and pages behind them return to the pool."""
+    import torch
+
+    lib = load()
+    like, i32 = request_ids, torch.int32
+    with _on(like):
+        S = int(request_ids.shape[0])
+        st = lib.mcp_commit_step(
+            ctypes.byref(pool), _arg(request_ids, i32, "request_ids", like, (S,)),
+            _arg(q_lens, i32, "q_lens", like, (S,)), _arg(new_lens, i32, "new_lens", like, (S,)),
+            S, _error(error_word, like), _stream(stream))
+    _capi.check(st, "commit_step")
+
+
+def _dtype_code(t, name):
+    import torch
+
+    code = {torch.bfloat16: _capi.DTYPE_BF16, torch.float16: _capi.DTYPE_FP16,
+            torch.float32: _capi.DTYPE_FP32}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
+    return code
+
+
+def mixed_conv(x, weight, bias, state, request_ids, cu_seqlens_q, seqlens_k, activation="silu",
+               out=None, error_word=None, stream=None):
+    """Short causal convolution of every segment of the packed stream, continued from and
+    kept in ``state`` (see include/mcp.h): x [T, channels] (rows may be part of wider ones),
+    weight [channels, K], bias [channels] or None, state [requests, K - 1, channels], all of
+    one type (bf16 or fp16); request_ids, seqlens_k [S], cu_seqlens_q [S + 1] int32.
+    ``activation``: "silu" or "none".  Returns ``out`` [T, channels]."""
+    import torch
+
+    lib = load()
+    if activation not in ("silu", "none"):
+        raise ValueError("activation must be 'silu' or 'none'")
+    with _on(x):
+        if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
+            raise ValueError("x must be [T, channels], weight [channels, K], "
+                             "state [requests, K - 1, channels]")
+        T, d = x.shape
+        K, S, i32 = int(weight.shape[1]), int(request_ids.shape[0]), torch.int32
+        out = _result(out, stream, lambda: torch.empty((T, d), dtype=x.dtype, device=x.device))
+        px, ldx = _row_arg(x, "x", x, (T, d))
+        po, ldo = _row_arg(out, "out", x, (T, d))
+        desc = _capi.ConvDesc(S, T, int(state.shape[0]), d, K, _dtype_code(x, "x"),
+                              activation == "silu", 0, ldx, ldo)
+        st = lib.mcp_mixed_conv(
+            ctypes.byref(desc), px, _arg(weight, x.dtype, "weight", x, (d, K)),
+            _arg(bias, x.dtype, "bias", x, (d,)),
+            _arg(state, x.dtype, "state", x, (state.shape[0], K - 1, d)),
+            _arg(request_ids, i32, "request_ids", x, (S,)),
+            _arg(cu_seqlens_q, i32, "cu_seqlens_q", x, (S + 1,)),
+            _arg(seqlens_k, i32, "seqlens_k", x, (S,)), po, _error(error_word, x), _stream(stream))
+    _capi.check(st, "mixed_conv")
+    return out
+
+
+def mixed_scan(x, dt, A, B, C, state, request_ids, cu_seqlens_q, seqlens_k, D=None, z=None,
+               dt_bias=None, softplus=True, out=None, error_word=None, stream=None):
+    """Selective state space scan of every segment of the packed stream, continued from and
+    kept in ``state`` (see include/mcp.h): x, dt and z (or None) [T, channels], B and C
+    [T, groups, N] of one type (bf16 or fp16; rows may be part of wider ones); A [channels, N],
+    D and dt_bias [channels] (or None) and state [requests, channels, N] fp32; request_ids,
+    seqlens_k [S], cu_seqlens_q [S + 1] int32.  Returns ``out`` [T, channels]."""
+    import torch
+
+    lib = load()
+    with _on(x):
+        if x.dim() != 2 or B.dim() != 3 or state.dim() != 3:
+            raise ValueError("x must be [T, channels], B and C [T, groups, N], "
+                             "state [requests, channels, N]")
+        T, d = x.shape
+        G, N, S = int(B.shape[1]), int(B.shape[2]), int(request_ids.shape[0])
+        f32, i32 = torch.float32, torch.int32
+        out = _result(out, stream, lambda: torch.empty((T, d), dtype=x.dtype, device=x.device))
+        px, ldx = _row_arg(x, "x", x, (T, d))
+        pd, ldd = _row_arg(dt, "dt", x, (T, d))
+        pz, ldz = (None, 0) if z is None else _row_arg(z, "z", x, (T, d))
+        pb, ldb = _row_arg(B, "B", x, (T, G, N))
+        pc, ldc = _row_arg(C, "C", x, (T, G, N))
+        po, ldo = _row_arg(out, "out", x, (T, d))
+        desc = _capi.ScanDesc(S, T, int(state.shape[0]), d, N, G, _dtype_code(x, "x"),
+                              bool(softplus), ldx, ldd, ldz, ldb, ldc, ldo)
+        tensors = _capi.ScanTensors(
+            px, pd, _arg(A, f32, "A", x, (d, N)), pb, pc, _arg(D, f32, "D", x, (d,)), pz,
+            _arg(dt_bias, f32, "dt_bias", x, (d,)),
+            _arg(state, f32, "state", x, (state.shape[0], d, N)), po)
+        st = lib.mcp_mixed_scan(
+            ctypes.byref(desc), ctypes.byref(tensors),
+            _arg(request_ids, i32, "request_ids", x, (S,)),
+            _arg(cu_seqlens_q, i32, "cu_seqlens_q", x, (S + 1,)),
+            _arg(seqlens_k, i32, "seqlens_k", x, (S,)), _error(error_word, x), _stream(stream))
+    _capi.check(st, "mixed_scan")
+    return out
+
+
+def _token_state(seen, counts, vocab_size, like):
+    """Addresses of ``seen`` [R, 2, W] and ``counts`` [R, 32 W], W = ceil(vocab_size / 32)."""
+    import torch
+
+    W = (vocab_size + 31) // 32
+    if seen.dim() != 3:
+        raise ValueError("seen must be [requests, 2, ceil(vocab_size / 32)]")
+    R = int(seen.shape[0])
+    return (R, _arg(seen, torch.int32, "seen", like, (R, 2, W)),
+            _arg(counts, torch.int32, "counts", like, (R, 32 * W)))
+
+
+def update_token_counts(request_ids, tokens, seen, counts, vocab_size, cu_tokens=None,
+                        prompt=False, reset=False, error_word=None, stream=None) -> None:
+    """Add tokens to what each request has had (see include/mcp.h): row i's are
+    tokens[cu_tokens[i]:cu_tokens[i + 1]] (``cu_tokens`` None: token i alone), added to
+    request row request_ids[i] of seen [R, 2, W] and counts [R, 32 W], W = ceil(vocab_size /
+    32); all int32 CUDA tensors.  ``prompt``: they are prompt tokens; ``reset``: the rows are
+    cleared first."""
+    import torch
+
+    lib = load()
+    like, i32 = request_ids, torch.int32
+    with _on(like):
+        n, rows = int(tokens.shape[0]), int(request_ids.shape[0])
+        R, ps, pc = _token_state(seen, counts, int(vocab_size), like)
+        st = lib.mcp_update_token_counts(
+            _arg(request_ids, i32, "request_ids", like, (rows,)), rows,
+            _arg(tokens, i32, "tokens", like, (n,)), n,
+            _arg(cu_tokens, i32, "cu_tokens", like, (rows + 1,)), ps, pc, R, int(vocab_size),
+            (_capi.COUNT_PROMPT if prompt else 0) | (_capi.COUNT_RESET if reset else 0),
+            _error(error_word, like), _stream(stream))
+    _capi.check(st, "update_token_counts")
+
+
+def process_logits(logits, out=None, request_ids=None, seen=None, counts=None, temperature=None,
+                   repetition_penalty=None, frequency_penalty=None, presence_penalty=None,
+                   bias=None, mask=None, mask_rows=None, error_word=None, stream=None):
+    """Biases, penalties for repeated tokens, temperature and grammar masks on logits
+    [rows, vocab] (bf16, fp16 or fp32; rows may be part of wider ones), see include/mcp.h.
+    ``out``: None for in place, else [rows, vocab] of the logits' type or fp32.  The penalties
+    and the temperature are fp32 [rows]; request_ids [rows], seen and counts as in
+    ``update_token_counts``; ``bias``: (offsets [rows + 1], tokens, values fp32), the tokens of
+    a row strictly increasing; mask [masks, ceil(vocab / 32)] with a 1 bit for every allowed
+    token, mask_rows [rows] or None for one mask a row.  Returns the processed logits."""
+    import torch
+
+    lib = load()
+    with _on(logits):
+        out = logits if out is None else out
+        if logits.dim() != 2 or out.shape != logits.shape:
+            raise ValueError("logits and out must be [rows, vocab]")
+        rows, V = logits.shape
+        f32, i32 = torch.float32, torch.int32
+        one = (rows,)
+        for t, name in ((logits, "logits"), (out, "out")):
+            if V > 1 and t.stride(1) != 1:
+                raise ValueError(f"{name}: a row must be dense, got strides {t.stride()}")
+        if out.get_device() != logits.get_device():
+            raise ValueError(f"out must be on {logits.device}, got {out.device}")
+        R = ps = pc = None
+        if request_ids is not None:
+            if seen is None or counts is None:
+                raise ValueError("request_ids needs seen and counts")
+            R, ps, pc = _token_state(seen, counts, V, logits)
+        off = tok = val = None
+        if bias is not None:
+            off, tok, val = bias
+        masks = 0
+        if mask is not None:
+            masks = int(mask.shape[0])
+        desc = _capi.LogitsDesc(rows, V, R or 0, _dtype_code(logits, "logits"),
+                                _dtype_code(out, "out"), 0 if tok is None else int(tok.shape[0]),
+                                masks, 0, logits.stride(0) if rows > 1 else V,
+                                out.stride(0) if rows > 1 else V)
+        tensors = _capi.LogitsTensors(
+            logits.data_ptr(), out.data_ptr(),
+            _arg(request_ids, i32, "request_ids", logits, one), ps, pc,
+            _arg(temperature, f32, "temperature", logits, one),
+            _arg(repetition_penalty, f32, "repetition_penalty", logits, one),
+            _arg(frequency_penalty, f32, "frequency_penalty", logits, one),
+            _arg(presence_penalty, f32, "presence_penalty", logits, one),
+            _arg(off, i32, "bias offsets", logits, (rows + 1,)),
+            _arg(tok, i32, "bias tokens", logits),
+            _arg(val, f32, "bias values", logits, None if tok is None else tok.shape),
+            _arg(mask, i32, "mask", logits, (masks, (V + 31) // 32)),
+            _arg(mask_rows, i32, "mask_rows", logits, one))
+        st = lib.mcp_process_logits(ctypes.byref(desc), ctypes.byref(tensors),
+                                    _error(error_word, logits), _stream(stream))
+    _capi.check(st, "process_logits")
+    return out

@@ -23,7 +23,14 @@ DEVERR_SLOT_RANGE = 0x4
 DEVERR_ROW_RANGE = 0x8
 DEVERR_ITEM_KIND = 0x10
 DEVERR_SLOT_DUP = 0x20
+DEVERR_NO_PAGES = 0x40
+DEVERR_REQUEST = 0x80
+DEVERR_TOKEN_RANGE = 0x100
+DEVERR_SEGMENT = 0x200
 BUILD_CHECKED = 0x1
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
+COUNT_PROMPT = 0x1
+COUNT_RESET = 0x2
 
 
 class AttnDesc(ctypes.Structure):
@@ -123,6 +130,80 @@ class HostStepLimits(ctypes.Structure):
     ]
 
 
+class RequestPool(ctypes.Structure):
+    _fields_ = [
+        ("max_requests", c_int32),
+        ("max_pages_per_seq", c_int32),
+        ("page_size", c_int32),
+        ("num_pages", c_int32),
+        ("request_pages", c_void_p),
+        ("request_lens", c_void_p),
+        ("free_pages", c_void_p),
+        ("free_count", c_void_p),
+    ]
+
+
+class ConvDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", c_int32),
+        ("total_tokens", c_int32),
+        ("num_requests", c_int32),
+        ("channels", c_int32),
+        ("width", c_int32),
+        ("dtype", c_int32),
+        ("activation", c_int32),
+        ("reserved", c_int32),
+        ("x_stride", c_int64),
+        ("out_stride", c_int64),
+    ]
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", c_int32),
+        ("total_tokens", c_int32),
+        ("num_requests", c_int32),
+        ("channels", c_int32),
+        ("state_size", c_int32),
+        ("num_groups", c_int32),
+        ("dtype", c_int32),
+        ("softplus", c_int32),
+        ("x_stride", c_int64),
+        ("dt_stride", c_int64),
+        ("z_stride", c_int64),
+        ("b_stride", c_int64),
+        ("c_stride", c_int64),
+        ("out_stride", c_int64),
+    ]
+
+
+class ScanTensors(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "state",
+                                        "out")]
+
+
+class LogitsDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_rows", c_int32),
+        ("vocab_size", c_int32),
+        ("num_requests", c_int32),
+        ("dtype", c_int32),
+        ("out_dtype", c_int32),
+        ("num_biases", c_int32),
+        ("num_masks", c_int32),
+        ("reserved", c_int32),
+        ("logits_stride", c_int64),
+        ("out_stride", c_int64),
+    ]
+
+
+class LogitsTensors(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in (
+        "logits", "out", "request_ids", "seen", "counts", "temperature", "repetition_penalty",
+        "frequency_penalty", "presence_penalty", "bias_offsets", "bias_tokens", "bias_values",
+        "mask", "mask_rows")]
+
+
 # name -> (restype, argtypes); every symbol include/mcp.h declares
 SIGNATURES = {
     "mcp_status_string": (c_char_p, [c_int32]),
@@ -181,6 +262,20 @@ SIGNATURES = {
                                     POINTER(c_int64)]),
     "mcp_host_step_wait": (c_int32, [c_void_p, c_int64]),
     "mcp_host_step_destroy": (c_int32, [c_void_p]),
+    "mcp_build_step_tables": (c_int32, [POINTER(RequestPool), c_void_p, c_void_p, c_int32, c_int32,
+                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_void_p, c_void_p, c_void_p]),
+    "mcp_commit_step": (c_int32, [POINTER(RequestPool), c_void_p, c_void_p, c_void_p, c_int32,
+                                  c_void_p, c_void_p]),
+    "mcp_mixed_conv": (c_int32, [POINTER(ConvDesc), c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "mcp_mixed_scan": (c_int32, [POINTER(ScanDesc), POINTER(ScanTensors), c_void_p, c_void_p,
+                                 c_void_p, c_void_p, c_void_p]),
+    "mcp_update_token_counts": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
+                                          c_void_p, c_int32, c_int32, c_int32, c_void_p,
+                                          c_void_p]),
+    "mcp_process_logits": (c_int32, [POINTER(LogitsDesc), POINTER(LogitsTensors), c_void_p,
+                                     c_void_p]),
 }
 
 _lib = None

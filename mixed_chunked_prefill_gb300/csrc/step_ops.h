@@ -1,0 +1,41 @@
+// Internal declarations of the operators around a step's attention: launchers
+// (return a cudaError_t value; 0 = success) called by step_ops.cpp.
+#pragma once
+
+#include <stdint.h>
+
+#include "mcp.h"
+
+namespace mcp {
+
+constexpr int32_t kMaxStepSeqs = 8192;  // segments whose prefix sums fit one CTA's shared memory
+
+// tables.cu
+int launch_build_step_tables(const mcp_request_pool& pool, const int32_t* request_ids,
+                             const int32_t* q_lens, int32_t num_seqs, int32_t max_tokens,
+                             int32_t* cu_seqlens_q, int32_t* seqlens_k, int32_t* block_tables,
+                             int64_t* slot_mapping, int32_t* positions, int32_t* logits_indices,
+                             int32_t* error_word, void* stream);
+int launch_commit_step(const mcp_request_pool& pool, const int32_t* request_ids,
+                       const int32_t* q_lens, const int32_t* new_lens, int32_t num_seqs,
+                       int32_t* error_word, void* stream);
+// recurrent.cu
+int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight, const void* bias,
+                      void* state, const int32_t* request_ids, const int32_t* cu_seqlens_q,
+                      const int32_t* seqlens_k, void* out, int32_t* error_word, void* stream);
+int launch_mixed_scan(const mcp_scan_desc& d, const mcp_scan_tensors& t,
+                      const int32_t* request_ids, const int32_t* cu_seqlens_q,
+                      const int32_t* seqlens_k, int32_t* error_word, void* stream);
+// logits.cu
+int launch_update_token_counts(const int32_t* request_ids, int32_t num_rows,
+                               const int32_t* tokens, int32_t num_tokens,
+                               const int32_t* cu_tokens, int32_t* seen, int32_t* counts,
+                               int32_t num_requests, int32_t vocab_size, int32_t flags,
+                               int32_t* error_word, void* stream);
+int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,
+                          int32_t* error_word, void* stream);
+
+// SMs of the current device (read once per device).
+int step_num_sms();
+
+}  // namespace mcp

@@ -18,18 +18,35 @@ import numpy as np
 from . import (
     PlanOptions,
     build_slot_mapping,
+    build_step_tables,
     check_device_errors,
+    commit_step,
     make_desc,
+    make_request_pool,
     mixed_attn_fwd,
     mixed_attn_plan,
     mixed_attn_plan_rows,
     paged_kv_append,
+    process_logits,
+    update_token_counts,
     workspace_error_word,
 )
 
 
 def _i32(a):
     return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
+
+
+def _on_stream(stream):
+    """Allocations and copies inside belong to ``stream`` (None: the current one)."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
+                             else torch.cuda.ExternalStream(int(stream)))
 
 
 class MixedStep:
@@ -58,6 +75,30 @@ class MixedStep:
         self.sk_d = torch.from_numpy(self.sk_h).to(device)
         self.bt_d = torch.from_numpy(self.bt_h).to(device)
         self.slots_d = torch.from_numpy(self.slots_h).to(device)
+        self._plan(rows)
+
+    @classmethod
+    def from_tables(cls, tables, num_q_heads, num_kv_heads, head_dim, sm_scale, options=None,
+                    stream=None, rows=None):
+        """A step whose tables and slots were built on the device (``RequestTables.step``):
+        nothing but the work lists is copied to the device."""
+        self = cls.__new__(cls)
+        pool = tables.pool
+        self.cu_h, self.sk_h = tables.cu_h, tables.sk_h
+        self.desc = make_desc(len(self.sk_h), int(self.cu_h[-1]), num_q_heads, num_kv_heads,
+                              head_dim, pool.page_size, pool.max_pages_per_seq, pool.num_pages,
+                              sm_scale)
+        self.options, self.stream, self.device = options, stream, tables.block_tables.device
+        self.tables = tables
+        self.cu_d, self.sk_d = tables.cu_seqlens_q, tables.seqlens_k
+        self.bt_d, self.slots_d = tables.block_tables, tables.slot_mapping
+        self._plan(rows)
+        return self
+
+    def _plan(self, rows):
+        import torch
+
+        options, device, stream = self.options, self.device, self.stream
         if rows is None:
             def planner(ws=None, st=None):
                 return mixed_attn_plan(self.desc, self.cu_h, self.sk_h, options, ws, st)
@@ -88,6 +129,141 @@ class MixedStep:
     def check(self):
         """Synchronise and raise if a device-side check or bounded wait failed."""
         check_device_errors(self.error_word, self.stream)
+
+
+class StepTables:
+    """One step of ``RequestTables``: its metadata on the device (and the lengths on the
+    host), valid until the commit."""
+
+    def __init__(self, tables, request_ids, q_lens, max_tokens, stream):
+        import torch
+
+        self.pool = tables.pool
+        dev = tables.device
+        ids, q = _i32(request_ids), _i32(q_lens)
+        if ids.ndim != 1 or ids.shape != q.shape:
+            raise ValueError("request_ids and q_lens must be [num_seqs]")
+        live = ids >= 0
+        if (ids >= self.pool.max_requests).any() or len(set(ids[live])) != int(live.sum()):
+            raise ValueError("request_ids must be distinct rows of the pool (or < 0)")
+        if (q < 0).any():
+            raise ValueError("q_lens must be >= 0")
+        q = np.where(live, q, 0).astype(np.int32)
+        had = np.where(live, tables.lens_h[np.where(live, ids, 0)], 0)
+        P = self.pool.page_size
+        self.ids_h, self.q_h, self.sk_h = ids, q, (had + q).astype(np.int32)
+        self.cu_h = np.concatenate([[0], np.cumsum(q)]).astype(np.int32)
+        if (self.sk_h > self.pool.max_pages_per_seq * P).any():
+            raise ValueError("a request needs more than max_pages_per_seq pages")
+        self.new_pages = int((-(-self.sk_h // P) - -(-had // P)).sum())
+        if self.new_pages > tables.free_h:
+            raise ValueError(f"{self.new_pages} new pages, {tables.free_h} are free")
+        S, T = len(ids), int(self.cu_h[-1])
+        cap = T if max_tokens is None else int(max_tokens)
+        if T > cap:
+            raise ValueError(f"{T} tokens > max_tokens {cap}")
+        with _on_stream(stream):
+            both = torch.from_numpy(np.concatenate([ids, q])).to(dev)
+            self.request_ids, self.q_lens = both[:S], both[S:]
+            i32 = dict(dtype=torch.int32, device=dev)
+            self.cu_seqlens_q = torch.empty(S + 1, **i32)
+            self.seqlens_k = torch.empty(S, **i32)
+            self.block_tables = torch.empty((S, self.pool.max_pages_per_seq), **i32)
+            self.slot_mapping = torch.empty(cap, dtype=torch.int64, device=dev)
+            self.positions = torch.empty(cap, **i32)
+            self.logits_indices = torch.empty(S, **i32)
+            build_step_tables(self.pool, self.request_ids, self.q_lens, self.cu_seqlens_q,
+                              self.seqlens_k, self.block_tables, self.slot_mapping, self.positions,
+                              self.logits_indices, tables.error_word, stream)
+
+
+class RequestTables:
+    """Page tables, lengths and free pages of all requests on the device
+    (``mcp_build_step_tables`` / ``mcp_commit_step``), with the lengths mirrored on the host
+    for the planner.  ``step`` builds one step's tables from request rows and their new
+    tokens, ``commit`` moves the requests on, ``release`` ends requests.  One stream."""
+
+    def __init__(self, num_pages, page_size, max_requests, max_pages_per_seq, device="cuda"):
+        import torch
+
+        i32 = dict(dtype=torch.int32, device=device)
+        self.request_pages = torch.full((max_requests, max_pages_per_seq), -1, **i32)
+        self.request_lens = torch.zeros(max_requests, **i32)
+        self.free_pages = torch.arange(num_pages, **i32)
+        self.free_count = torch.full((1,), num_pages, **i32)
+        self.error_word = torch.zeros(1, **i32)
+        self.device = self.request_pages.device
+        self.pool = make_request_pool(self.request_pages, self.request_lens, self.free_pages,
+                                      self.free_count, page_size)
+        self.lens_h = np.zeros(max_requests, dtype=np.int64)
+        self.free_h = int(num_pages)
+
+    def step(self, request_ids, q_lens, max_tokens=None, stream=None) -> StepTables:
+        """Tables of a step in which request row request_ids[s] runs q_lens[s] new tokens
+        (request_ids[s] < 0: a padding segment).  ``max_tokens``: length of slot_mapping and
+        positions (padded behind the step's tokens), default the step's tokens."""
+        return StepTables(self, request_ids, q_lens, max_tokens, stream)
+
+    def commit(self, step: StepTables, new_lens=None, stream=None) -> None:
+        """The step ran: its requests hold their new tokens, or new_lens[s] tokens (fewer
+        after rejected speculated tokens, 0: the request is over)."""
+        import torch
+
+        live = step.ids_h >= 0
+        after = step.sk_h if new_lens is None else _i32(new_lens)
+        if after.shape != step.sk_h.shape or ((after < 0) | (after > step.sk_h))[live].any():
+            raise ValueError("new_lens must be [num_seqs], at most the step's lengths")
+        with _on_stream(stream):
+            to = None if new_lens is None else torch.from_numpy(after).to(self.device)
+            commit_step(self.pool, step.request_ids, step.q_lens, to, self.error_word, stream)
+        P = self.pool.page_size
+        kept = -(-after // P) - -(-step.sk_h // P)
+        self.lens_h[step.ids_h[live]] = after[live]
+        self.free_h -= step.new_pages + int(kept[live].sum())
+
+    def release(self, request_ids, stream=None) -> None:
+        """End requests: their pages are free and their rows may be used again."""
+        ids = _i32(request_ids)
+        none = np.zeros(len(ids), dtype=np.int32)
+        self.commit(self.step(ids, none, stream=stream), none, stream)
+
+    def check(self, stream=None) -> None:
+        """Synchronise and raise if a step was refused on the device."""
+        check_device_errors(self.error_word.data_ptr(), stream)
+
+
+class LogitsState:
+    """Which tokens each request has had, on the device, for the penalties of
+    ``process_logits``: rows are the request rows of the step."""
+
+    def __init__(self, max_requests, vocab_size, device="cuda"):
+        import torch
+
+        words = -(-vocab_size // 32)
+        self.vocab_size = int(vocab_size)
+        self.seen = torch.zeros((max_requests, 2, words), dtype=torch.int32, device=device)
+        self.counts = torch.zeros((max_requests, 32 * words), dtype=torch.int32, device=device)
+        self.error_word = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def admit(self, request_ids, tokens, cu_tokens, stream=None) -> None:
+        """New requests take rows: the rows are cleared and their prompts' tokens marked."""
+        update_token_counts(request_ids, tokens, self.seen, self.counts, self.vocab_size,
+                            cu_tokens, prompt=True, reset=True, error_word=self.error_word,
+                            stream=stream)
+
+    def add(self, request_ids, tokens, cu_tokens=None, stream=None) -> None:
+        """Sampled tokens: one a row, or tokens[cu_tokens[i]:cu_tokens[i + 1]]."""
+        update_token_counts(request_ids, tokens, self.seen, self.counts, self.vocab_size,
+                            cu_tokens, error_word=self.error_word, stream=stream)
+
+    def process(self, logits, request_ids, out=None, stream=None, **kw):
+        """``process_logits`` with this state (temperature, penalties, bias, mask by name)."""
+        return process_logits(logits, out, request_ids, self.seen, self.counts,
+                              error_word=self.error_word, stream=stream, **kw)
+
+    def check(self, stream=None) -> None:
+        """Synchronise and raise if a row or token was out of range."""
+        check_device_errors(self.error_word.data_ptr(), stream)
 
 
 def write_history(block_tables, hist_lens, k_hist, v_hist, k_cache, v_cache, page_size,
