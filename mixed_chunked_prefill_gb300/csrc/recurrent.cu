@@ -13,6 +13,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "mcp.h"
 #include "step_ops.h"
 
@@ -72,7 +74,10 @@ struct Segments {
   const int32_t* sk;
   int32_t S, T, R;
   int32_t* err;
+  int32_t sms;  // of the device
 };
+
+constexpr int kShortTokens = 4;  // the scan's short segments: decodes, a few speculated tokens
 
 // Segment s's tokens [q0, q1), request row and whether it continues a state;
 // id < 0: padding, or a segment the check reports (it is then left out).
@@ -287,18 +292,10 @@ int conv_width(const ConvArgs& a, int K, int grid, cudaStream_t st) {
 // and the recurrence multiplies by it once a token.
 //
 // Least traffic: x, dt, z read and out written once (8 bytes per token and
-// channel in 16 bits) and the states once.  One ex2 per token, channel and
-// state: at the measured 32 a clock and SM, 16 states bound the kernel at
-// 0.5 clocks per (token, channel), a little above the HBM time; the products
-// run as packed pairs (two fp32 lanes an instruction) to stay below that.
-//
-// A lane holds 4 states of one channel in registers; N / 4 neighbouring lanes
-// share a channel, 32 channels a CTA.  Tiles of 32 tokens go through shared
-// memory: the thread that loads 8 channels of a token turns dt and x into
-// (d, d x) there and keeps x and z in registers for its output, while the
-// next tile's loads are in flight.  y's sums over the lanes of a channel are
-// taken N / 4 tokens at a time (each exchange halves the tokens a lane
-// carries), one shuffle a token instead of log2(N / 4).
+// channel in 16 bits) and the states once.  Segments of a few tokens (decodes)
+// are bound by their states' traffic, long ones by one ex2 per token, channel
+// and state (32 a clock and SM: 16 states take longer than the HBM traffic)
+// and by the issue slots of the recurrence.  They run in two kernels.
 struct ScanArgs {
   Segments g;
   const void* x;
@@ -312,12 +309,14 @@ struct ScanArgs {
   float* state;
   void* out;
   int64_t ldx, lddt, ldz, ldb, ldc, ldo;
-  int32_t channels, per_group, softplus, blocks, split;  // split: CTAs the segments are dealt to
+  int32_t channels, per_group, softplus;
+  int32_t blocks;     // CTAs across the channels
+  int32_t split;      // CTAs (or warps) the segments are dealt to
+  int32_t short_max;  // segments of at most this many tokens are the short kernel's
 };
 
-constexpr int kScanChannels = 32;
-constexpr int kScanTile = 32;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
 
 using f32x2 = unsigned long long;  // two fp32 lanes in one register pair
 __device__ __forceinline__ f32x2 pack2(float a, float b) {
@@ -343,16 +342,172 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// log(1 + exp(v)), to fp32's precision for small results too (log1p): the
-// steps it gives may be 0.001 and less
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+__device__ __forceinline__ f32x2 ex2x2(f32x2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(ex2(a), ex2(b));
+}
+
+// max(v, 0) + log1p(exp(-|v|)), two values at a time, to a few ulp also where
+// it is small (steps of 0.001 and less).  exp(-t) = 2^(hi + lo): hi the rounded
+// product t log2 e, lo what the rounding lost.  log1p(e) = e P(e) on [0, 1], P
+// of degree 8 from a Remez exchange on the relative error (3e-8); Horner's
+// roundings leave 3 x 2^-24 in all.
+__device__ __forceinline__ void softplus2(float& v0, float& v1) {
+  const f32x2 t = pack2(-fabsf(v0), -fabsf(v1));
+  const f32x2 L = pack2(kLog2e, kLog2e);
+  const f32x2 hi = mul2(t, L);
+  const f32x2 neg = mul2(hi, pack2(-1.f, -1.f));
+  // log2 e - float(log2 e) = 1.925963e-8
+  const f32x2 lo = fma2(t, pack2(1.925963033e-8f, 1.925963033e-8f), fma2(t, L, neg));
+  f32x2 e = ex2x2(hi);
+  e = fma2(e, mul2(lo, pack2(kLn2, kLn2)), e);
+  f32x2 q = pack2(5.2326940931379795e-3f, 5.2326940931379795e-3f);
+  q = fma2(q, e, pack2(-2.950523979961872e-2f, -2.950523979961872e-2f));
+  q = fma2(q, e, pack2(7.822595536708832e-2f, 7.822595536708832e-2f));
+  q = fma2(q, e, pack2(-1.3663245737552643e-1f, -1.3663245737552643e-1f));
+  q = fma2(q, e, pack2(1.9106006622314453e-1f, 1.9106006622314453e-1f));
+  q = fma2(q, e, pack2(-2.484298199415207e-1f, -2.484298199415207e-1f));
+  q = fma2(q, e, pack2(3.331909775733948e-1f, 3.331909775733948e-1f));
+  q = fma2(q, e, pack2(-4.999949336051941e-1f, -4.999949336051941e-1f));
+  q = fma2(q, e, pack2(9.999999403953552e-1f, 9.999999403953552e-1f));
+  float p0, p1;
+  unpack2(mul2(q, e), p0, p1);
+  v0 = fmaxf(v0, 0.f) + p0;
+  v1 = fmaxf(v1, 0.f) + p1;
+}
+
+// ------------------------------------------------- scan of short segments
+// A warp takes 8 (N = 16) channels and runs over its share of the segments: 4
+// states a lane, so a request's state is one coalesced 16-byte access a lane.
+// A decode is one register-only step between the state's load and its store;
+// the loads of kAhead segments are in flight together, because the bound is
+// the states' HBM traffic (8 N bytes per channel and segment against 8).
+template <typename T>
+__device__ __forceinline__ float scalar(const void* p, int64_t i) {
+  if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
+    return __half2float(static_cast<const __half*>(p)[i]);
+  else
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+template <typename T>
+__device__ __forceinline__ void unpack4(const uint2& v, float* f) {
+  float g[8];
+  unpack8<T>(make_uint4(v.x, v.y, 0u, 0u), g);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = g[i];
+}
+
+template <typename T>
+__device__ __forceinline__ uint2 pack4(const float* f) {
+  const float g[8] = {f[0], f[1], f[2], f[3], 0.f, 0.f, 0.f, 0.f};
+  const uint4 v = pack8<T>(g);
+  return make_uint2(v.x, v.y);
+}
+
+constexpr int kShortThreads = 128;
+constexpr int kAhead = 4;
 
 template <typename T, int N>
-__global__ void __launch_bounds__(8 * N) mixed_scan_kernel(const ScanArgs p) {
+__global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const ScanArgs p) {
   if (blockIdx.x == 0) {
     check_segments(p.g);
     return;
   }
+  constexpr int LPC = N / 4;         // lanes of a channel
+  constexpr int CPW = 32 / LPC;      // channels of a warp
+  const int lane = threadIdx.x & 31, sub = lane % LPC;
+  const int32_t wid = (blockIdx.x - 1) * (kShortThreads / 32) + (threadIdx.x >> 5);
+  const int32_t c = wid % p.blocks * CPW + lane / LPC;  // blocks: warps across the channels
+  const int32_t first = wid / p.blocks;
+  if (first >= p.split) return;
+  const bool live = c < p.channels;
+  const int32_t cc = live ? c : p.channels - 1;  // idle lanes shadow the last channel
+  const int32_t gn = cc / p.per_group * N + 4 * sub;
+  const float4 av = *reinterpret_cast<const float4*>(p.A + static_cast<int64_t>(cc) * N + 4 * sub);
+  const float a[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
+  const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f, Dc = p.D ? p.D[cc] : 0.f;
+
+  for (int32_t s0 = first; s0 < p.g.S; s0 += p.split * kAhead) {
+    // lane i reads the metadata of segment s0 + i split
+    Segment m = {0, 0, -1, 0};
+    if (lane < kAhead && s0 + lane * p.split < p.g.S) m = read_segment(p.g, s0 + lane * p.split);
+    Segment sg[kAhead];
+    float4 h[kAhead];
+    float x[kAhead], d[kAhead], z[kAhead];
+    uint2 b[kAhead], q[kAhead];
+    float* st[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      sg[i].q0 = __shfl_sync(0xffffffffu, m.q0, i);
+      sg[i].q1 = __shfl_sync(0xffffffffu, m.q1, i);
+      sg[i].id = __shfl_sync(0xffffffffu, m.id, i);
+      sg[i].old = __shfl_sync(0xffffffffu, m.old, i);
+      const int32_t len = sg[i].q1 - sg[i].q0;
+      if (len <= 0 || len > p.short_max) sg[i].id = -1;
+      h[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (sg[i].id < 0) continue;
+      st[i] = p.state + (static_cast<int64_t>(sg[i].id) * p.channels + cc) * N + 4 * sub;
+      if (sg[i].old) h[i] = *reinterpret_cast<const float4*>(st[i]);
+      const int64_t t = sg[i].q0;
+      x[i] = scalar<T>(p.x, t * p.ldx + cc);
+      d[i] = scalar<T>(p.dt, t * p.lddt + cc);
+      z[i] = p.z ? scalar<T>(p.z, t * p.ldz + cc) : 0.f;
+      b[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.B) + t * p.ldb + gn);
+      q[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.C) + t * p.ldc + gn);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (sg[i].id < 0) continue;
+      float hh[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
+      for (int32_t t = sg[i].q0;;) {
+        float dd = d[i] + bias, two = 0.f, bb[4], qq[4];
+        if (p.softplus) softplus2(dd, two);
+        const float dx = dd * x[i];
+        unpack4<T>(b[i], bb);
+        unpack4<T>(q[i], qq);
+        float y = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          hh[n] = fmaf(ex2(dd * a[n]), hh[n], dx * bb[n]);
+          y = fmaf(qq[n], hh[n], y);
+        }
+#pragma unroll
+        for (int o = 1; o < LPC; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        y = fmaf(Dc, x[i], y);
+        if (p.z) y *= silu(z[i]);
+        if (live && sub == 0) static_cast<T*>(p.out)[t * p.ldo + c] = static_cast<T>(y);
+        if (++t >= sg[i].q1) break;
+        x[i] = scalar<T>(p.x, t * p.ldx + cc);
+        d[i] = scalar<T>(p.dt, t * p.lddt + cc);
+        z[i] = p.z ? scalar<T>(p.z, t * p.ldz + cc) : 0.f;
+        b[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.B) + t * p.ldb + gn);
+        q[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.C) + t * p.ldc + gn);
+      }
+      if (live) *reinterpret_cast<float4*>(st[i]) = make_float4(hh[0], hh[1], hh[2], hh[3]);
+    }
+  }
+}
+
+// -------------------------------------------------- scan of long segments
+// A lane holds 4 states of one channel in registers; N / 4 neighbouring lanes
+// share a channel, 32 channels a CTA.  Tiles of 32 tokens go through shared
+// memory: the thread that loads 8 channels of a token turns dt and x into
+// (d, d x) there and keeps x and z in registers for its output, while the
+// next tile's loads are in flight.  y's sums over the lanes of a channel are
+// taken N / 4 tokens at a time (each exchange halves the tokens a lane
+// carries), one shuffle a token instead of log2(N / 4).
+constexpr int kScanChannels = 32;
+constexpr int kScanTile = 32;
+
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(8 * N) scan_long_kernel(const ScanArgs p) {
   constexpr int LPC = N / 4;                  // lanes of a channel
   constexpr int kThreads = kScanChannels * LPC;
   constexpr int kItems = kScanTile * 4;       // (token, 8 channels) of a tile
@@ -363,7 +518,7 @@ __global__ void __launch_bounds__(8 * N) mixed_scan_kernel(const ScanArgs p) {
   __shared__ __align__(16) float ys[kScanTile][kYs];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t cb = (blockIdx.x - 1) % p.blocks * kScanChannels;
+  const int32_t cb = blockIdx.x % p.blocks * kScanChannels;
   const int sub = lane % LPC, cl = (warp * 32 + lane) / LPC;  // states 4 sub.., channel of the block
   const int32_t c = cb + cl;
   const bool live = c < p.channels;
@@ -384,10 +539,10 @@ __global__ void __launch_bounds__(8 * N) mixed_scan_kernel(const ScanArgs p) {
   const int64_t bc_ld = bc_which ? p.ldc : p.ldb;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
-  for (int32_t s = (blockIdx.x - 1) / p.blocks; s < p.g.S; s += p.split) {
+  for (int32_t s = blockIdx.x / p.blocks; s < p.g.S; s += p.split) {
     const Segment seg = read_segment(p.g, s);
     const int32_t len = seg.q1 - seg.q0;
-    if (seg.id < 0 || len == 0) continue;
+    if (seg.id < 0 || len <= p.short_max) continue;
     float* st = p.state + (static_cast<int64_t>(seg.id) * p.channels + c) * N + 4 * sub;
     f32x2 h01 = 0, h23 = 0;
     if (live && seg.old) {
@@ -429,7 +584,12 @@ __global__ void __launch_bounds__(8 * N) mixed_scan_kernel(const ScanArgs p) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if (p.dt_bias && on) d[e] += p.dt_bias[cb + it_ch + e];
-            if (p.softplus) d[e] = softplus(d[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; e += 2)
+            if (p.softplus) softplus2(d[e], d[e + 1]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
             if (!on) d[e] = 0.f;  // h stays: exp(0) h + 0
             x[e] *= d[e];
           }
@@ -492,7 +652,7 @@ __global__ void __launch_bounds__(8 * N) mixed_scan_kernel(const ScanArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (p.D) y[e] = fmaf(p.D[cb + it_ch + e], x[e], y[e]);
-          if (p.z) y[e] *= silu(z[e]);
+          if (p.z) y[e] *= z[e] * rcp(1.f + ex2(-kLog2e * z[e]));
         }
         *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (t0 + row) * p.ldo + cb + it_ch) = pack8<T>(y);
       }
@@ -506,13 +666,40 @@ __global__ void __launch_bounds__(8 * N) mixed_scan_kernel(const ScanArgs p) {
   }
 }
 
-template <typename T>
-int scan_launch(const ScanArgs& a, int N, int grid, cudaStream_t st) {
-  if (N == 8) mixed_scan_kernel<T, 8><<<grid, 64, 0, st>>>(a);
-  else if (N == 16) mixed_scan_kernel<T, 16><<<grid, 128, 0, st>>>(a);
-  else if (N == 32) mixed_scan_kernel<T, 32><<<grid, 256, 0, st>>>(a);
-  else mixed_scan_kernel<T, 64><<<grid, 512, 0, st>>>(a);
+template <typename T, int N>
+int scan_launch(ScanArgs a, cudaStream_t st) {
+  const int sms = a.g.sms;
+  const bool any_long = a.g.T > kShortTokens && a.g.T > a.g.S;
+  if (any_long) {
+    ScanArgs l = a;
+    l.short_max = kShortTokens;
+    l.blocks = (a.channels + kScanChannels - 1) / kScanChannels;
+    // a CTA for every long segment there can be, up to what fills the SMs
+    const int64_t longs = a.g.T / (kShortTokens + 1) < a.g.S ? a.g.T / (kShortTokens + 1) : a.g.S;
+    const int64_t want = (32LL * sms + l.blocks - 1) / l.blocks;
+    l.split = static_cast<int32_t>(want < longs ? want : longs);
+    const int64_t grid = static_cast<int64_t>(l.blocks) * l.split;
+    scan_long_kernel<T, N><<<static_cast<unsigned>(grid), 8 * N, 0, st>>>(l);
+    const cudaError_t f = cudaGetLastError();
+    if (f != cudaSuccess) return static_cast<int>(f);
+  }
+  // without the long kernel this one takes segments of any length
+  a.short_max = any_long ? kShortTokens : 0x7fffffff;
+  constexpr int per = 32 / (N / 4);
+  a.blocks = (a.channels + per - 1) / per;
+  const int64_t want = (48LL * sms + a.blocks - 1) / a.blocks;
+  a.split = static_cast<int32_t>(want < a.g.S ? want : a.g.S);
+  const int64_t warps = static_cast<int64_t>(a.blocks) * a.split;
+  const int64_t grid = (warps + kShortThreads / 32 - 1) / (kShortThreads / 32) + 1;
+  scan_short_kernel<T, N><<<static_cast<unsigned>(grid), kShortThreads, 0, st>>>(a);
   return static_cast<int>(cudaGetLastError());
+}
+template <typename T>
+int scan_states(const ScanArgs& a, int N, cudaStream_t st) {
+  if (N == 8) return scan_launch<T, 8>(a, st);
+  if (N == 16) return scan_launch<T, 16>(a, st);
+  if (N == 32) return scan_launch<T, 32>(a, st);
+  return scan_launch<T, 64>(a, st);
 }
 
 }  // namespace
@@ -521,7 +708,8 @@ int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight,
                       void* state, const int32_t* request_ids, const int32_t* cu_seqlens_q,
                       const int32_t* seqlens_k, void* out, int32_t* error_word, void* stream) {
   ConvArgs a;
-  a.g = {request_ids, cu_seqlens_q, seqlens_k, d.num_seqs, d.total_tokens, d.num_requests, error_word};
+  a.g = {request_ids, cu_seqlens_q, seqlens_k, d.num_seqs, d.total_tokens, d.num_requests, error_word,
+         step_num_sms()};
   a.x = x;
   a.w = weight;
   a.bias = bias;
@@ -549,7 +737,8 @@ int launch_mixed_scan(const mcp_scan_desc& d, const mcp_scan_tensors& t,
                       const int32_t* request_ids, const int32_t* cu_seqlens_q,
                       const int32_t* seqlens_k, int32_t* error_word, void* stream) {
   ScanArgs a;
-  a.g = {request_ids, cu_seqlens_q, seqlens_k, d.num_seqs, d.total_tokens, d.num_requests, error_word};
+  a.g = {request_ids, cu_seqlens_q, seqlens_k, d.num_seqs, d.total_tokens, d.num_requests, error_word,
+         step_num_sms()};
   a.x = t.x;
   a.dt = t.dt;
   a.A = t.A;
@@ -569,14 +758,9 @@ int launch_mixed_scan(const mcp_scan_desc& d, const mcp_scan_tensors& t,
   a.channels = d.channels;
   a.per_group = d.channels / d.num_groups;
   a.softplus = d.softplus;
-  a.blocks = (d.channels + kScanChannels - 1) / kScanChannels;
-  // enough CTAs for several per SM; more would only repeat the set-up
-  const int64_t want = (32LL * step_num_sms() + a.blocks - 1) / a.blocks;
-  a.split = static_cast<int32_t>(want < d.num_seqs ? want : d.num_seqs);
-  const int grid = a.blocks * a.split + 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d.dtype == MCP_DTYPE_BF16 ? scan_launch<__nv_bfloat16>(a, d.state_size, grid, st)
-                                   : scan_launch<__half>(a, d.state_size, grid, st);
+  return d.dtype == MCP_DTYPE_BF16 ? scan_states<__nv_bfloat16>(a, d.state_size, st)
+                                   : scan_states<__half>(a, d.state_size, st);
 }
 
 }  // namespace mcp
