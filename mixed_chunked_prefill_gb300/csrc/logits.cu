@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "mcp.h"
 #include "step_ops.h"
 
@@ -114,11 +116,13 @@ struct LogitArgs {
   const int32_t* mask_rows;
   int32_t* err;
   int64_t ld_in, ld_out;
-  int32_t rows, V, W, R, num_bias, num_masks, tiles, inplace;
+  int32_t rows, V, W, R, num_bias, num_masks, inplace;
+  int32_t tiles, parts;  // tiles of a CTA, CTAs of a row
 };
 
 constexpr int kLogitThreads = 256;
-constexpr int kLogitTile = 8 * kLogitThreads;  // tokens of one row a CTA takes
+constexpr int kLogitTile = 16 * kLogitThreads;  // tokens of one row that a CTA takes at a time
+constexpr int kLogitMaxTiles = 8;               // tiles of one CTA
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -137,178 +141,351 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return
 template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
-template <typename T>
-struct alignas(8 * sizeof(T) < 16 ? 8 * sizeof(T) : 16) Vec8 {
-  T v[8];
+template <typename T, int n>
+struct alignas(n * sizeof(T)) Vec {
+  T v[n];
 };
 
-struct RowParams {
-  float rho, freq, pres, temp;
-};
-
-__device__ __forceinline__ float process(float x, float bias, bool seen, int32_t count, bool allow,
-                                         const RowParams& r) {
-  x += bias;
-  if (seen) x = x > 0.f ? __fdiv_rn(x, r.rho) : x * r.rho;
-  if (count > 0) x = x - __fmul_rn(r.freq, static_cast<float>(count)) - r.pres;
-  if (r.temp > 0.f) x = __fdiv_rn(x, r.temp);
-  return allow ? x : -INFINITY;
+// The bias of token `tok`, which has one: entries [lo, hi) in rising order.
+__device__ __noinline__ float find_bias(const LogitArgs& p, int32_t lo, int32_t hi, int32_t tok) {
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (p.bias_tokens[mid] <= tok) lo = mid;
+    else hi = mid;
+  }
+  return p.bias_tokens[lo] == tok ? p.bias_values[lo] : 0.f;
 }
 
-// kVec 8: a thread takes 8 neighbouring tokens with 16-byte accesses (rows
-// that start on 16 bytes).  kVec 1: rows that start anywhere (an odd
-// vocabulary); a warp takes 32 neighbouring tokens at a time.
-template <typename TI, typename TO, int kVec>
-__global__ void __launch_bounds__(kLogitThreads) process_logits_kernel(const LogitArgs p) {
-  __shared__ float sbias[kLogitTile];
-  const int32_t row = blockIdx.x / p.tiles, tile = blockIdx.x - row * p.tiles;
-  const int32_t v0 = tile * kLogitTile;
+// 4, 8 or 16 bytes global -> shared without a register in between
+template <int n>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+__device__ __forceinline__ void prefetch(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// kWhole, kShifted: a thread takes 4 neighbouring tokens at a time, 8 bytes of
+// 16-bit logits in and 16 bytes of fp32 out.  A row that starts between those
+// addresses (an odd vocabulary: kShifted) is taken from up to 3 tokens before
+// its start, so that the accesses are aligned; its groups' bits then come from
+// two words.  kSingle, a warp on 32 neighbouring tokens: logits and out whose
+// rows are aligned differently.
+//
+// What bounds the pass is how many bytes are in flight.  A CTA reads all bits
+// of its part into shared memory at once, so that it knows which logits it
+// needs, and a ring of tiles in shared memory takes those (asynchronous
+// copies: no registers, and a thread reads only what it copied itself).
+//
+// Most tokens were neither seen nor biased: the pass gives them a conversion, a
+// product with 1 / temperature and a select, and leaves the others out.  Those
+// are listed and taken afterwards, one a thread.
+enum LogitRows { kWhole, kShifted, kSingle };
+
+constexpr int kLogitWords = kLogitMaxTiles * kLogitTile / 32;  // of a plane, in a part
+// tiles of logits in flight and CTAs an SM: 32 KB and 4 (16 bits), 48 KB and 3 (fp32)
+template <typename T>
+constexpr int kLogitSlots = sizeof(T) == 2 ? 4 : 3;
+template <typename T>
+constexpr int kLogitRing = kLogitSlots<T> * kLogitTile * static_cast<int>(sizeof(T));
+template <typename T>
+constexpr int kLogitSmem = 4 * 4 * (kLogitWords + 2) + kLogitRing<T>;
+
+template <typename TI, typename TO, int kRows>
+__global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) process_logits_kernel(const LogitArgs p) {
+  constexpr int kVec = kRows == kSingle ? 1 : 4;
+  constexpr int kGroups = kLogitTile / kLogitThreads / kVec;  // of a thread and tile
+  constexpr uint32_t kAll = (1u << kVec) - 1;
+  constexpr bool kAsync = kVec * sizeof(TI) >= 4;
+  constexpr int kSlots = kLogitSlots<TI>;
+  extern __shared__ __align__(16) unsigned char lsmem[];
+  TI* ring = reinterpret_cast<TI*>(lsmem);
+  uint32_t* plane = reinterpret_cast<uint32_t*>(lsmem + kLogitRing<TI>);  // prompt, sampled, allowed, biased
+  constexpr int kPlane = kLogitWords + 2;
+
+  const int32_t row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts;
   const int32_t id = p.ids ? p.ids[row] : 0;
-  int32_t mrow = !p.mask ? -1 : p.mask_rows ? p.mask_rows[row] : row;
+  const int32_t mrow = !p.mask ? -1 : p.mask_rows ? p.mask_rows[row] : row;
+  int32_t lo = 0, hi = 0;  // the row's biases
+  if (p.bias_offsets) lo = p.bias_offsets[row], hi = p.bias_offsets[row + 1];
   if (id < 0) return;  // padding: the row stays as it was
   if ((p.ids && id >= p.R) || mrow >= p.num_masks) {
-    if (tile == 0 && threadIdx.x == 0 && p.err) atomicOr(p.err, MCP_DEVERR_REQUEST);
+    if (part == 0 && threadIdx.x == 0 && p.err) atomicOr(p.err, MCP_DEVERR_REQUEST);
     return;
   }
-  RowParams r;
-  r.rho = p.repetition ? p.repetition[row] : 1.f;
-  r.freq = p.frequency ? p.frequency[row] : 0.f;
-  r.pres = p.presence ? p.presence[row] : 0.f;
-  r.temp = p.temperature ? p.temperature[row] : 0.f;
-  const bool every = !p.inplace || (r.temp > 0.f && r.temp != 1.f);
-
-  // biases of this tile
-  bool biased = false;
-  if (p.bias_offsets) {
-    int32_t lo = p.bias_offsets[row], hi = p.bias_offsets[row + 1];
-    int bad = 0;
-    if (lo < 0 || hi < lo || hi > p.num_bias) {
-      bad = MCP_DEVERR_TOKEN_RANGE;
-      lo = hi = 0;
-    }
-    bool mine = false;
-    for (int32_t e = lo + threadIdx.x; e < hi; e += kLogitThreads) {
-      const int32_t tok = p.bias_tokens[e];
-      if (tok < 0 || tok >= p.V || (e > lo && p.bias_tokens[e - 1] >= tok)) bad = MCP_DEVERR_TOKEN_RANGE;
-      mine |= tok >= v0 && tok < v0 + kLogitTile;
-    }
-    if (bad && tile == 0 && p.err) atomicOr(p.err, bad);
-    biased = __syncthreads_or(mine);
-    if (biased) {
-      for (int i = threadIdx.x; i < kLogitTile; i += kLogitThreads) sbias[i] = 0.f;
-      __syncthreads();
-      for (int32_t e = lo + threadIdx.x; e < hi; e += kLogitThreads) {
-        const int32_t tok = p.bias_tokens[e];
-        if (tok >= v0 && tok < v0 + kLogitTile && tok < p.V) sbias[tok - v0] = p.bias_values[e];
-      }
-      __syncthreads();
-    }
-  }
-  const TI* in = static_cast<const TI*>(p.logits) + row * p.ld_in;
-  TO* out = static_cast<TO*>(p.out) + row * p.ld_out;
-  const uint32_t* seen = reinterpret_cast<const uint32_t*>(p.seen) + static_cast<int64_t>(id) * 2 * p.W;
+  // tokens of this CTA: [begin, end), those below 0 do not exist
+  const int32_t shift =
+      kRows != kShifted ? 0 : static_cast<int32_t>((reinterpret_cast<uintptr_t>(p.out) / sizeof(TO) + row * p.ld_out) % 4);
+  const int32_t begin = part * p.tiles * kLogitTile - shift;
+  const int32_t end = min(p.V, begin + p.tiles * kLogitTile);
+  if (begin >= end) return;
+  const int32_t word0 = begin >> 5;  // of the planes' first entry (-1: one word of zeros)
+  const int32_t nwords = ((end - 1) >> 5) - word0 + 1;
+  const uint32_t* seen =
+      p.ids ? reinterpret_cast<const uint32_t*>(p.seen) + static_cast<int64_t>(id) * 2 * p.W : nullptr;
   const uint32_t* mask =
       mrow < 0 ? nullptr : reinterpret_cast<const uint32_t*>(p.mask) + static_cast<int64_t>(mrow) * p.W;
-  const int32_t* counts = p.counts + static_cast<int64_t>(id) * 32 * p.W;
+  int bad = 0;
+  if (lo < 0 || hi < lo || hi > p.num_bias) {
+    bad = MCP_DEVERR_TOKEN_RANGE;
+    lo = hi = 0;
+  }
+  // this thread's first bias, with the words' loads
+  int32_t tok = -1, before = -2;
+  if (lo + static_cast<int32_t>(threadIdx.x) < hi) {
+    tok = p.bias_tokens[lo + threadIdx.x];
+    if (threadIdx.x > 0) before = p.bias_tokens[lo + threadIdx.x - 1];
+  }
+#pragma unroll 4
+  for (int i = threadIdx.x; i < nwords; i += kLogitThreads) {
+    const int32_t w = word0 + i;
+    const bool in_row = w >= 0;
+    plane[i] = seen && in_row ? seen[w] : 0u;
+    plane[kPlane + i] = seen && in_row ? seen[p.W + w] : 0u;
+    plane[2 * kPlane + i] = mask ? in_row ? mask[w] : 0u : 0xffffffffu;
+    plane[3 * kPlane + i] = 0u;
+  }
+  const float rho = p.repetition ? p.repetition[row] : 1.f;
+  const float freq = p.frequency ? p.frequency[row] : 0.f;
+  const float pres = p.presence ? p.presence[row] : 0.f;
+  const float temp = p.temperature ? p.temperature[row] : 0.f;
+  const bool scale = temp > 0.f && temp != 1.f;
+  const bool every = !p.inplace || scale;
+  // quotients as products: one rounding more, a tenth of the instructions;
+  // divisors whose reciprocal overflows divide
+  const float inv = scale ? 1.f / temp : 1.f, rinv = 1.f / rho;
+  const bool divide = inv > 3.4e38f || rinv > 3.4e38f;
+  __syncthreads();
+  for (int32_t e = lo + threadIdx.x; e < hi; e += kLogitThreads) {
+    if (e != lo + static_cast<int32_t>(threadIdx.x)) {
+      tok = p.bias_tokens[e];
+      before = p.bias_tokens[e - 1];
+    }
+    if (tok < 0 || tok >= p.V || before >= tok) bad = MCP_DEVERR_TOKEN_RANGE;
+    if (tok >= max(begin, 0) && tok < end)
+      atomicOr(plane + 3 * kPlane + (tok >> 5) - word0, 1u << (tok & 31));
+  }
+  if (bad && part == 0 && p.err) atomicOr(p.err, bad);
+  __syncthreads();
 
-  if constexpr (kVec == 8) {
-    const int32_t t = 8 * threadIdx.x, v = v0 + t;
-    if (v >= p.V) return;
-    const int32_t w = v >> 5, sh = v & 31;
-    const int32_t n = min(8, p.V - v);
-    const uint32_t valid = (1u << n) - 1;
-    uint32_t pr = 0, ou = 0, al = 0xff;
-    if (p.ids) {
-      pr = seen[w] >> sh & 0xff;
-      ou = seen[p.W + w] >> sh & 0xff;
-    }
-    if (mrow >= 0) al = mask[w] >> sh & 0xff;
-    uint32_t touch = (every ? 0xffu : pr | ou | ~al) & valid;
-    float bias[8];
+  // from here plane 0 has the tokens that a bias or penalty changes: seen or
+  // biased, and allowed; the counts of the sampled ones are on their way to L2
+  for (int i = threadIdx.x; i < nwords; i += kLogitThreads) {
+    uint32_t had = plane[kPlane + i];
+    plane[i] = (plane[i] | had | plane[3 * kPlane + i]) & plane[2 * kPlane + i];
+    had &= plane[2 * kPlane + i];
+    const int32_t* c = p.counts + (static_cast<int64_t>(id) * p.W + word0 + i) * 32;
+    for (; had; had &= had - 1) prefetch(c + __ffs(had) - 1);
+  }
+  __syncthreads();
+
+  const TI* in = static_cast<const TI*>(p.logits) + row * p.ld_in;
+  TO* out = static_cast<TO*>(p.out) + row * p.ld_out;
+  const int32_t* counts = p.counts + static_cast<int64_t>(id) * 32 * p.W;
+  const int32_t first = (threadIdx.x >> 5) * 32 * kGroups * kVec + (threadIdx.x & 31) * kVec;
+  const int turn = (begin + first) & 31;  // the place of a thread's groups in their words
+  const uint32_t* bits0 = plane + ((begin + first) >> 5) - word0;
+
+  // bits of the thread's group g of the tile at `base` (a multiple of 32 behind begin)
+  auto bits_at = [&](int k, int32_t base, int g) {
+    const uint32_t* w = bits0 + k * kPlane + ((base - begin) >> 5) + g * kVec;
+    return kRows == kShifted ? __funnelshift_r(w[0], w[1], turn) : w[0] >> turn;
+  };
+  // tokens of the group that are in this part
+  auto valid_at = [&](int32_t v) {
+    const int32_t left = end - v;
+    uint32_t m = left >= kVec ? kAll : left <= 0 ? 0u : (1u << left) - 1;
+    if (kRows == kShifted && v < 0) m = m >> -v << -v;
+    return m;
+  };
+  auto whole_tile = [&](int32_t base) { return base >= 0 && base + kLogitTile <= end; };
+  // x / temperature, or the masked value
+  auto finish = [&](float x) { return divide ? scale ? __fdiv_rn(x, temp) : x : x * inv; };
+  auto put = [&](int32_t v, const float* x, uint32_t touch) {
+    Vec<TO, kVec> y;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      bias[i] = biased ? sbias[t + i] : 0.f;
-      if (bias[i] != 0.f) touch |= 1u << i;
-    }
-    touch &= valid;
-    if (!touch) return;
-    float x[8];
-    if (touch & al) {
-      if (n == 8) {
-        const Vec8<TI> q = *reinterpret_cast<const Vec8<TI>*>(in + v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_f(q.v[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < n ? to_f(in[v + i]) : 0.f;
-      }
+    for (int i = 0; i < kVec; ++i) y.v[i] = from_f<TO>(x[i]);
+    if (touch == kAll) {
+      *reinterpret_cast<Vec<TO, kVec>*>(out + v) = y;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    }
-    int32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (ou & al) {
-      const int4 a = *reinterpret_cast<const int4*>(counts + v);
-      const int4 b = *reinterpret_cast<const int4*>(counts + v + 4);
-      c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
-      c[4] = b.x, c[5] = b.y, c[6] = b.z, c[7] = b.w;
-    }
-    const uint32_t had = pr | ou;
-    Vec8<TO> y;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      y.v[i] = from_f<TO>(process(x[i], bias[i], had >> i & 1, ou >> i & 1 ? c[i] : 0, al >> i & 1, r));
-    if (n == 8 && (every || !p.inplace)) {
-      *reinterpret_cast<Vec8<TO>*>(out + v) = y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kVec; ++i)
         if (touch >> i & 1) out[v + i] = y.v[i];
     }
-  } else {
-    const int lane = threadIdx.x & 31;
-    const int32_t t = (threadIdx.x >> 5) * 256 + lane;
-    float x[8];
-    int32_t c[8];
-    uint32_t bits[8];  // 1 seen, 2 allowed, 4 touched
+  };
+  // Request the logits of a tile that are not masked, process a tile.  In
+  // place the tokens of plane 0 wait for their turn; elsewhere they are written
+  // twice, whole vectors being cheaper than single tokens.  kEnds: the tile
+  // may begin or end inside a group (a row's first and last).
+  auto request = [&](int32_t base, int slot) {
+    TI* to = ring + slot * kLogitTile + first;
+    const TI* at = in + base + first;
+    const bool whole = whole_tile(base);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int32_t v = v0 + t + 32 * i, w = v >> 5;
-      x[i] = 0.f;
-      c[i] = 0;
-      bits[i] = 0;
-      if (v >= p.V) continue;
-      uint32_t pr = 0, ou = 0, al = 1;
-      if (p.ids) {
-        pr = seen[w] >> lane & 1;
-        ou = seen[p.W + w] >> lane & 1;
-      }
-      if (mrow >= 0) al = mask[w] >> lane & 1;
-      const bool b = biased && sbias[t + 32 * i] != 0.f;
-      bits[i] = (pr | ou) | al << 1 | (every || pr || ou || !al || b ? 4 : 0);
-      if (al && bits[i] & 4) x[i] = to_f(in[v]);
-      if (al && ou) c[i] = counts[v];
+    for (int g = 0; g < kGroups; ++g) {
+      if (!whole && valid_at(base + first + g * 32 * kVec) != kAll) continue;
+      if (mask && !(bits_at(2, base, g) & kAll)) continue;
+      copy_async<kVec * sizeof(TI)>(to + g * 32 * kVec, at + g * 32 * kVec);
     }
+  };
+  auto process = [&](int32_t base, int slot, auto masked, auto ends) {
+    constexpr bool kMask = decltype(masked)::value, kEnds = decltype(ends)::value;
+    const TI* from = ring + slot * kLogitTile + first;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (!(bits[i] & 4)) continue;
-      out[v0 + t + 32 * i] = from_f<TO>(process(x[i], biased ? sbias[t + 32 * i] : 0.f, bits[i] & 1,
-                                                c[i], bits[i] & 2, r));
+    for (int g = 0; g < kGroups; ++g) {
+      const int32_t v = base + first + g * 32 * kVec;
+      const uint32_t valid = kEnds ? valid_at(v) : kAll;
+      if (kEnds && !valid) continue;
+      uint32_t ok = kMask ? bits_at(2, base, g) : kAll;
+      const uint32_t touch = p.inplace ? valid & ~bits_at(0, base, g) : valid;
+      float x[kVec];
+      if (kAsync && (!kEnds || valid == kAll)) {
+        const Vec<TI, kVec> q = *reinterpret_cast<const Vec<TI, kVec>*>(from + g * 32 * kVec);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) x[i] = to_f(q.v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) x[i] = touch & ok & 1u << i ? to_f(in[v + i]) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        x[i] = finish(x[i]);
+        // what was not requested is masked
+        if (kMask) x[i] = ok & 1u << i ? x[i] : -INFINITY;
+      }
+      put(v, x, touch);
+    }
+  };
+  using std::false_type;
+  using std::true_type;
+  if (every) {
+    if constexpr (kAsync) {
+#pragma unroll
+      for (int s = 0; s < kSlots - 1; ++s) {
+        if (begin + s * kLogitTile < end) request(begin + s * kLogitTile, s);
+        copy_commit();
+      }
+    }
+    int slot = 0;
+    for (int32_t base = begin; base < end; base += kLogitTile) {
+      if constexpr (kAsync) {
+        const int32_t ahead = base + (kSlots - 1) * kLogitTile;
+        if (ahead < end) request(ahead, slot == 0 ? kSlots - 1 : slot - 1);
+        copy_commit();
+        copy_wait<kSlots - 1>();
+      }
+      if (!whole_tile(base)) process(base, slot, true_type(), true_type());
+      else if (mask) process(base, slot, true_type(), false_type());
+      else process(base, slot, false_type(), false_type());
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
+    }
+  } else if (mask) {
+    // in place, as they are: only the masked tokens are written
+    float x[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) x[i] = -INFINITY;
+    for (int32_t base = begin; base < end; base += kLogitTile) {
+#pragma unroll 2
+      for (int g = 0; g < kGroups; ++g) {
+        const int32_t v = base + first + g * 32 * kVec;
+        const uint32_t touch = valid_at(v) & ~bits_at(2, base, g);
+        if (touch) put(v, x, touch);
+      }
     }
   }
+
+  // The tokens of plane 0, listed in shared memory (the ring is done with, and
+  // the barrier orders the pass's writes before these), so
+  // that every thread has as many as the next: a branch in the pass would cost
+  // every warp that has one of them.
+  uint16_t* list = reinterpret_cast<uint16_t*>(lsmem);
+  constexpr int kListWords = 2 * kLogitThreads;  // 16384 tokens: 32 KB of list
+  __shared__ int32_t warp_sum[kLogitThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int w0 = 0; w0 < nwords; w0 += kListWords) {
+    const int i = w0 + 2 * threadIdx.x;
+    const uint32_t a = i < nwords ? plane[i] : 0u, b = i + 1 < nwords ? plane[i + 1] : 0u;
+    const int mine = __popc(a) + __popc(b);
+    int at = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, at, d);
+      if (lane >= d) at += u;
+    }
+    __syncthreads();  // the ring, and the list before
+    if (lane == 31) warp_sum[warp] = at;
+    __syncthreads();
+    int total = 0;
+    at -= mine;
+#pragma unroll
+    for (int k = 0; k < kLogitThreads / 32; ++k) {
+      if (k < warp) at += warp_sum[k];
+      total += warp_sum[k];
+    }
+    for (uint32_t m = a; m; m &= m - 1) list[at++] = static_cast<uint16_t>(64 * threadIdx.x + __ffs(m) - 1);
+    for (uint32_t m = b; m; m &= m - 1) list[at++] = static_cast<uint16_t>(64 * threadIdx.x + 31 + __ffs(m));
+    __syncthreads();
+    constexpr int kAtOnce = 4;  // tokens of a thread whose loads are in flight together
+    for (int e0 = threadIdx.x; e0 < total; e0 += kAtOnce * kLogitThreads) {
+      int k[kAtOnce], sh[kAtOnce];
+      int32_t n[kAtOnce];
+      TI q[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int e = e0 + j * kLogitThreads;
+        k[j] = -1;
+        n[j] = 0;
+        if (e >= total) continue;
+        k[j] = w0 + (list[e] >> 5);
+        sh[j] = list[e] & 31;
+        const int32_t v = 32 * (word0 + k[j]) + sh[j];
+        q[j] = in[v];
+        if (plane[kPlane + k[j]] >> sh[j] & 1) n[j] = counts[v];
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (k[j] < 0) continue;
+        const int32_t v = 32 * (word0 + k[j]) + sh[j];
+        float x = to_f(q[j]);
+        bool had = true;
+        if (plane[3 * kPlane + k[j]] >> sh[j] & 1) {
+          x += find_bias(p, lo, hi, v);
+          had = seen && (seen[word0 + k[j]] | seen[p.W + word0 + k[j]]) >> sh[j] & 1;
+        }
+        if (had) x = x <= 0.f ? x * rho : divide ? __fdiv_rn(x, rho) : x * rinv;
+        if (n[j] > 0) x = x - __fmul_rn(freq, static_cast<float>(n[j])) - pres;
+        out[v] = from_f<TO>(finish(x));
+      }
+    }
+  }
+}
+
+template <typename TI, typename TO, int kRows>
+int logits_rows(const LogitArgs& a, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(process_logits_kernel<TI, TO, kRows>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kLogitSmem<TI>);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  const int64_t grid = static_cast<int64_t>(a.rows) * a.parts;
+  process_logits_kernel<TI, TO, kRows>
+      <<<static_cast<unsigned>(grid), kLogitThreads, kLogitSmem<TI>, st>>>(a);
+  return static_cast<int>(cudaGetLastError());
 }
 
 template <typename TI, typename TO>
 int logits_launch(const LogitArgs& a, cudaStream_t st) {
-  const int64_t grid = static_cast<int64_t>(a.rows) * a.tiles;
-  const bool vec =
-      ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0 &&
-      a.ld_in * sizeof(TI) % 16 == 0 && a.ld_out * sizeof(TO) % 16 == 0;
-  if (vec)
-    process_logits_kernel<TI, TO, 8><<<static_cast<unsigned>(grid), kLogitThreads, 0, st>>>(a);
-  else
-    process_logits_kernel<TI, TO, 1><<<static_cast<unsigned>(grid), kLogitThreads, 0, st>>>(a);
-  return static_cast<int>(cudaGetLastError());
+  // the same tokens stand on vector boundaries of both, in every row
+  const uintptr_t in = reinterpret_cast<uintptr_t>(a.logits), out = reinterpret_cast<uintptr_t>(a.out);
+  const bool vec = (in / sizeof(TI) - out / sizeof(TO)) % 4 == 0 && (a.ld_in - a.ld_out) % 4 == 0;
+  const bool even = (out / sizeof(TO)) % 4 == 0 && a.ld_out % 4 == 0;
+  return vec && even ? logits_rows<TI, TO, kWhole>(a, st)
+         : vec       ? logits_rows<TI, TO, kShifted>(a, st)
+                     : logits_rows<TI, TO, kSingle>(a, st);
 }
 
 }  // namespace
@@ -370,7 +547,16 @@ int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,
   a.R = d.num_requests;
   a.num_bias = d.num_biases;
   a.num_masks = d.num_masks;
-  a.tiles = (d.vocab_size + kLogitTile - 1) / kLogitTile;
+  // a CTA reads its row's parameters, bits and biases once for several tiles:
+  // as few CTAs as find a place on the SMs together (a second wave would wait
+  // for its own first loads again), up to the tiles that shared memory has bits for
+  const int64_t row_tiles = (d.vocab_size + 3LL + kLogitTile - 1) / kLogitTile;  // shifted by up to 3
+  const int64_t places = (d.dtype == MCP_DTYPE_FP32 ? 3LL : 4LL) * step_num_sms();
+  int64_t tiles = (row_tiles * d.num_rows + places - 1) / places;
+  tiles = tiles < 1 ? 1 : tiles > kLogitMaxTiles ? kLogitMaxTiles : tiles;
+  tiles = tiles > row_tiles ? row_tiles : tiles;
+  a.tiles = static_cast<int32_t>(tiles);
+  a.parts = static_cast<int32_t>((row_tiles + tiles - 1) / tiles);
   a.inplace = t.logits == t.out;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool same = d.dtype == d.out_dtype;
