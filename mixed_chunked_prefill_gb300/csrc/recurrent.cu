@@ -65,7 +65,59 @@ __device__ __forceinline__ uint4 pack8<__half>(const float* f) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+template <typename T>
+__device__ __forceinline__ void unpack4(const uint2& v, float* f) {
+  float g[8];
+  unpack8<T>(make_uint4(v.x, v.y, 0u, 0u), g);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = g[i];
+}
+
+template <typename T>
+__device__ __forceinline__ uint2 pack4(const float* f) {
+  const float g[8] = {f[0], f[1], f[2], f[3], 0.f, 0.f, 0.f, 0.f};
+  const uint4 v = pack8<T>(g);
+  return make_uint2(v.x, v.y);
+}
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+using f32x2 = unsigned long long;  // two fp32 lanes in one register pair
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ f32x2 ex2x2(f32x2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(ex2(a), ex2(b));
+}
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// v / (1 + exp(-v)); exp overflows to infinity and the quotient to 0
+__device__ __forceinline__ float silu(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }
 
 // ------------------------------------------------------------------ segments
 struct Segments {
@@ -77,7 +129,7 @@ struct Segments {
   int32_t sms;  // of the device
 };
 
-constexpr int kShortTokens = 4;  // the scan's short segments: decodes, a few speculated tokens
+constexpr int kShortTokens = 4;  // short segments: decodes, a few speculated tokens
 
 // Segment s's tokens [q0, q1), request row and whether it continues a state;
 // id < 0: padding, or a segment the check reports (it is then left out).
@@ -124,13 +176,14 @@ __device__ void check_segments(const Segments& g) {
 // y[t] = act(b + sum_k w[k] v[t - K + 1 + k]) per channel, v being the
 // segment's inputs and, before them, the K - 1 inputs its request kept.
 //
-// Each input is read once and each output written once; a thread carries the
-// K - 1 last inputs of 8 channels (one 16-byte vector a token) in registers
-// along a run of TT tokens, so only the first tokens of a run read inputs
-// again.  HBM-bound for chunks; for decodes the K - 1 kept inputs of each
-// request are read and written too and are most of the traffic.  The thread
-// that runs over a segment's first token also runs over its next K - 2 (even
-// past its run: those still need the kept inputs) and writes the new kept
+// Each input is read once and each output written once.  Segments of at most 4
+// tokens (decodes) get a CTA per segment and 512 channels: all their inputs and
+// kept inputs are requested at once, which is what their few microseconds
+// consist of.  The tokens of longer segments are dealt in runs of TT: a thread
+// carries the K - 1 last inputs of 4 channels in registers, so only the first
+// tokens of a run read inputs again (HBM-bound; 64 registers, so that 32 warps
+// an SM have 4 loads of 8 bytes in flight a thread).  The run that holds a segment's first token also takes its next K - 2
+// (even past its end: those still need the kept inputs) and writes the new kept
 // inputs, so nobody else reads or writes that state.
 struct ConvArgs {
   Segments g;
@@ -145,22 +198,123 @@ struct ConvArgs {
 
 constexpr int kConvThreads = 128;
 constexpr int kConvMaxRun = 16;
+constexpr int kConvCh = 4;  // channels of a thread
+
+// One thread's 4 channels: weights and the sum over the K taps.
+template <typename T, int K>
+struct ConvLane {
+  struct Four {
+    f32x2 v[2];  // channel pairs
+  };
+  f32x2 w[K][2], b[2];
+  int32_t act;
+
+  __device__ __forceinline__ void load(const ConvArgs& p, int32_t c) {
+    act = p.act;
+    float wf[4 * K];  // wf[i * K + k]: channel i, tap k (memory order)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      unpack4<T>(reinterpret_cast<const uint2*>(static_cast<const T*>(p.w) +
+                                                static_cast<int64_t>(c) * K)[k], wf + 4 * k);
+    float bf[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.bias)
+      unpack4<T>(*reinterpret_cast<const uint2*>(static_cast<const T*>(p.bias) + c), bf);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      b[e] = pack2(bf[2 * e], bf[2 * e + 1]);
+#pragma unroll
+      for (int k = 0; k < K; ++k) w[k][e] = pack2(wf[2 * e * K + k], wf[(2 * e + 1) * K + k]);
+    }
+  }
+  static __device__ __forceinline__ Four widen(const uint2& raw) {
+    float f[4];
+    unpack4<T>(raw, f);
+    return Four{{pack2(f[0], f[1]), pack2(f[2], f[3])}};
+  }
+  // the output of the token whose K inputs are v[0] .. v[K - 1]
+  __device__ __forceinline__ uint2 token(const Four* v) const {
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      f32x2 a = b[e];
+#pragma unroll
+      for (int k = 0; k < K; ++k) a = fma2(w[k][e], v[k].v[e], a);
+      unpack2(a, y[2 * e], y[2 * e + 1]);
+    }
+    if (act) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = silu(y[e]);
+    }
+    return pack4<T>(y);
+  }
+};
+
+// A whole segment of at most kShortTokens tokens.
+template <typename T, int K>
+__device__ __forceinline__ void conv_short(const ConvArgs& p, int32_t s, int32_t c) {
+  using L = ConvLane<T, K>;
+  L lane;
+  lane.load(p, c);
+  const Segment g = read_segment(p.g, s);
+  const int32_t len = g.q1 - g.q0;
+  if (g.id < 0 || len <= 0 || len > kShortTokens) return;
+  const uint2* X = reinterpret_cast<const uint2*>(static_cast<const T*>(p.x) + g.q0 * p.ldx + c);
+  uint2* O = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + g.q0 * p.ldo + c);
+  uint2* kept = reinterpret_cast<uint2*>(static_cast<T*>(p.state) +
+                                         static_cast<int64_t>(g.id) * (K - 1) * p.channels + c);
+  uint2 raw[K - 1 + kShortTokens];  // the kept inputs, then the segment's
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) raw[k] = g.old ? kept[k * (p.channels / 4)] : make_uint2(0u, 0u);
+#pragma unroll
+  for (int i = 0; i < kShortTokens; ++i)
+    raw[K - 1 + i] = i < len ? X[i * (p.ldx / 4)] : make_uint2(0u, 0u);
+  typename L::Four v[K - 1 + kShortTokens];
+#pragma unroll
+  for (int i = 0; i < K - 1 + kShortTokens; ++i) v[i] = L::widen(raw[i]);
+#pragma unroll
+  for (int i = 0; i < kShortTokens; ++i) {
+    if (i < len) O[i * (p.ldo / 4)] = lane.token(v + i);
+    if (i + 1 == len) {
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) kept[k * (p.channels / 4)] = raw[i + 1 + k];
+    }
+  }
+}
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kConvThreads) mixed_conv_kernel(const ConvArgs p) {
+__global__ void __launch_bounds__(kConvThreads, 8) mixed_conv_kernel(const ConvArgs p) {
   if (blockIdx.x == 0) {
     check_segments(p.g);
     return;
   }
-  constexpr int kBatch = 8;  // inputs requested together
+  const int32_t c = ((blockIdx.x - 1) % p.blocks * kConvThreads + threadIdx.x) * kConvCh;
+  int32_t tile = (blockIdx.x - 1) / p.blocks;
+  if (tile < p.g.S) {
+    if (c < p.channels) conv_short<T, K>(p, tile, c);
+    return;
+  }
+  tile -= p.g.S;
+  using L = ConvLane<T, K>;
+  constexpr int kBatch = 4;  // inputs requested together
   __shared__ Segment info[kConvMaxRun + K];
   __shared__ int32_t first;
-  const int32_t tile = (blockIdx.x - 1) / p.blocks;
-  const int32_t c = ((blockIdx.x - 1) % p.blocks * kConvThreads + threadIdx.x) * 8;
   const int32_t t0 = tile * p.tokens;
   const int32_t run = min(p.tokens, p.g.T - t0);
   const int32_t most = min(p.tokens + K - 2, p.g.T - t0);  // with a head that goes on
+  // the weights and the first inputs are on their way while the segments are looked up
+  const int32_t cc = min(c, p.channels - kConvCh);
+  const uint2* X = reinterpret_cast<const uint2*>(static_cast<const T*>(p.x) + cc);
+  uint2* O = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + cc);
+  const int64_t ldx = p.ldx / 4, ldo = p.ldo / 4, lds = p.channels / 4;
+  L lane;
+  lane.load(p, cc);
+  uint2 raw[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    if (i < run) raw[i] = X[(t0 + i) * ldx];
+
   // segments before the first token: those that end at or before it
+  const int32_t t = t0 + threadIdx.x;
   if (threadIdx.x == 0) first = 0;
   __syncthreads();
   int32_t n = 0;
@@ -169,116 +323,98 @@ __global__ void __launch_bounds__(kConvThreads) mixed_conv_kernel(const ConvArgs
   if ((threadIdx.x & 31) == 0 && n) atomicAdd(&first, n);
   __syncthreads();
   if (threadIdx.x < most) {
-    const int32_t t = t0 + threadIdx.x;
     int32_t lo = first, hi = p.g.S;  // first segment that ends behind t
-    if (lo < hi && p.g.cu[lo + 1] <= t) {
+    Segment mine = {0, 0, -1, 0};
+    if (lo < hi) mine = read_segment(p.g, lo);
+    if (lo < hi && mine.q1 <= t) {
       ++lo;
       while (lo < hi) {
         const int32_t mid = (lo + hi) >> 1;
         if (p.g.cu[mid + 1] <= t) lo = mid + 1;
         else hi = mid;
       }
+      if (lo < p.g.S) mine = read_segment(p.g, lo);
     }
-    Segment x = {0, 0, -1, 0};
-    if (lo < p.g.S) {
-      x = read_segment(p.g, lo);
-      if (t < x.q0 || t >= x.q1) x.id = -1;
-    }
-    info[threadIdx.x] = x;
+    // not a short segment's token; a segment's first K - 1 tokens belong to the
+    // run that its first token is in
+    const int32_t off = t - mine.q0;
+    if (off < 0 || t >= mine.q1 || mine.q1 - mine.q0 <= kShortTokens ||
+        !(off < K - 1 ? mine.q0 >= t0 && mine.q0 < t0 + run : t < t0 + run))
+      mine.id = -1;
+    info[threadIdx.x] = mine;
   }
   __syncthreads();
   if (c >= p.channels) return;
 
-  const uint4* X = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + c);
-  uint4* O = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + c);
-  const int64_t ldx = p.ldx / 8, ldo = p.ldo / 8, lds = p.channels / 8;
-  float w[8 * K], b[8];  // w[i * K + k]: channel i, tap k (memory order)
+  const Segment head = info[0];
+  if (run == p.tokens && run % kBatch == 0 && head.id >= 0 && t0 - head.q0 >= K - 1 &&
+      t0 + run <= head.q1) {
+    // the whole run lies inside one segment, behind its first tokens
+    const uint2* from = X + t0 * ldx;
+    uint2* to = O + t0 * ldo;
+    typename L::Four v[K - 1 + kBatch];
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-    unpack8<T>(reinterpret_cast<const uint4*>(static_cast<const T*>(p.w) +
-                                              static_cast<int64_t>(c) * K)[k], w + 8 * k);
-  if (p.bias) {
-    unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + c), b);
-  } else {
+    for (int k = 0; k < K - 1; ++k) v[k] = L::widen(from[(k - K + 1) * ldx]);
+    for (int i0 = 0; i0 < run; i0 += kBatch) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = 0.f;
+      for (int i = 0; i < kBatch; ++i) v[K - 1 + i] = L::widen(raw[i]);
+      if (i0 + kBatch < run) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) raw[i] = from[(kBatch + i) * ldx];
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) to[i * ldo] = lane.token(v + i);
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) v[k] = v[kBatch + k];
+      from += kBatch * ldx;
+      to += kBatch * ldo;
+    }
+    return;
   }
-  float win[K - 1][8];
-  bool have = false;  // win holds the K - 1 inputs before the next token
+  typename L::Four win[K];  // the K - 1 inputs before the next token, then its own
+  bool have = false;        // they are there
   for (int32_t i0 = 0; i0 < most; i0 += kBatch) {
-    uint4 raw[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (i0 + i < most) raw[i] = X[(t0 + i0 + i) * ldx];
+      if (i0 + i < most && (i0 > 0 || i >= run) && info[i0 + i].id >= 0) raw[i] = X[(t0 + i0 + i) * ldx];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int32_t at = i0 + i;
       if (at >= most) break;
       const Segment s = info[at];
-      const int32_t t = t0 + at, off = t - s.q0;
-      // a segment's first K - 1 tokens belong to the run its first token is in
-      const bool mine = s.id >= 0 && (off < K - 1 ? s.q0 >= t0 && s.q0 < t0 + run : at < run);
-      if (!mine) {
+      const int32_t tok = t0 + at, off = tok - s.q0;
+      if (s.id < 0) {
         have = false;
         continue;
       }
       if (off == 0) {
-        uint4* kept = reinterpret_cast<uint4*>(static_cast<T*>(p.state) +
+        uint2* kept = reinterpret_cast<uint2*>(static_cast<T*>(p.state) +
                                                static_cast<int64_t>(s.id) * (K - 1) * p.channels + c);
-        uint4 old[K - 1];
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) {
-          old[k] = s.old ? kept[k * lds] : make_uint4(0u, 0u, 0u, 0u);
-          unpack8<T>(old[k], win[k]);
-        }
-        // the kept inputs of the next step: the last K - 1 of (old, segment)
-        const int32_t len = s.q1 - s.q0;
+        for (int k = 0; k < K - 1; ++k) win[k] = L::widen(s.old ? kept[k * lds] : make_uint2(0u, 0u));
+        // the kept inputs of the next step (a segment has more than K - 1 tokens here)
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) {
-          const int32_t from = len - (K - 1) + k;  // in the segment; < 0: old[K - 1 + from]
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (from >= 0) {
-            v = X[(s.q0 + from) * ldx];
-          } else {
-#pragma unroll
-            for (int m = 1; m < K - 1; ++m)
-              if (K - 1 + from == m) v = old[m];
-          }
-          kept[k * lds] = v;
-        }
+        for (int k = 0; k < K - 1; ++k) kept[k * lds] = X[(s.q1 - (K - 1) + k) * ldx];
       } else if (!have) {
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) unpack8<T>(X[(t - (K - 1) + k) * ldx], win[k]);
+        for (int k = 0; k < K - 1; ++k) win[k] = L::widen(X[(tok - (K - 1) + k) * ldx]);
       }
       have = true;
-      float v[8], y[8];
-      unpack8<T>(raw[i], v);
+      win[K - 1] = L::widen(raw[i]);
+      O[tok * ldo] = lane.token(win);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float a = b[e];
-#pragma unroll
-        for (int k = 0; k < K - 1; ++k) a = fmaf(w[e * K + k], win[k][e], a);
-        a = fmaf(w[e * K + K - 1], v[e], a);
-        y[e] = p.act ? silu(a) : a;
-      }
-      O[t * ldo] = pack8<T>(y);
-#pragma unroll
-      for (int k = 0; k < K - 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) win[k][e] = win[k + 1][e];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) win[K - 2][e] = v[e];
+      for (int k = 0; k < K - 1; ++k) win[k] = win[k + 1];
     }
   }
 }
 
 template <typename T, int K>
-int conv_launch(const ConvArgs& a, int grid, cudaStream_t st) {
-  mixed_conv_kernel<T, K><<<grid, kConvThreads, 0, st>>>(a);
+int conv_launch(const ConvArgs& a, int64_t grid, cudaStream_t st) {
+  mixed_conv_kernel<T, K><<<static_cast<unsigned>(grid), kConvThreads, 0, st>>>(a);
   return static_cast<int>(cudaGetLastError());
 }
 template <typename T>
-int conv_width(const ConvArgs& a, int K, int grid, cudaStream_t st) {
+int conv_width(const ConvArgs& a, int K, int64_t grid, cudaStream_t st) {
   if (K == 2) return conv_launch<T, 2>(a, grid, st);
   if (K == 3) return conv_launch<T, 3>(a, grid, st);
   return conv_launch<T, 4>(a, grid, st);
@@ -314,39 +450,6 @@ struct ScanArgs {
   int32_t split;      // CTAs (or warps) the segments are dealt to
   int32_t short_max;  // segments of at most this many tokens are the short kernel's
 };
-
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-
-using f32x2 = unsigned long long;  // two fp32 lanes in one register pair
-__device__ __forceinline__ f32x2 pack2(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ f32x2 ex2x2(f32x2 v) {
-  float a, b;
-  unpack2(v, a, b);
-  return pack2(ex2(a), ex2(b));
-}
 
 // max(v, 0) + log1p(exp(-|v|)), two values at a time, to a few ulp also where
 // it is small (steps of 0.001 and less).  exp(-t) = 2^(hi + lo): hi the rounded
@@ -390,21 +493,6 @@ __device__ __forceinline__ float scalar(const void* p, int64_t i) {
   else
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
-template <typename T>
-__device__ __forceinline__ void unpack4(const uint2& v, float* f) {
-  float g[8];
-  unpack8<T>(make_uint4(v.x, v.y, 0u, 0u), g);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = g[i];
-}
-
-template <typename T>
-__device__ __forceinline__ uint2 pack4(const float* f) {
-  const float g[8] = {f[0], f[1], f[2], f[3], 0.f, 0.f, 0.f, 0.f};
-  const uint4 v = pack8<T>(g);
-  return make_uint2(v.x, v.y);
-}
-
 constexpr int kShortThreads = 128;
 constexpr int kAhead = 4;
 
@@ -499,12 +587,6 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const ScanArg
 // carries), one shuffle a token instead of log2(N / 4).
 constexpr int kScanChannels = 32;
 constexpr int kScanTile = 32;
-
-__device__ __forceinline__ float rcp(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 
 template <typename T, int N>
 __global__ void __launch_bounds__(8 * N) scan_long_kernel(const ScanArgs p) {
@@ -652,7 +734,7 @@ __global__ void __launch_bounds__(8 * N) scan_long_kernel(const ScanArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (p.D) y[e] = fmaf(p.D[cb + it_ch + e], x[e], y[e]);
-          if (p.z) y[e] *= z[e] * rcp(1.f + ex2(-kLog2e * z[e]));
+          if (p.z) y[e] *= silu(z[e]);
         }
         *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (t0 + row) * p.ldo + cb + it_ch) = pack8<T>(y);
       }
@@ -719,15 +801,17 @@ int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight,
   a.ldo = d.out_stride;
   a.channels = d.channels;
   a.act = d.activation;
-  a.blocks = (d.channels / 8 + kConvThreads - 1) / kConvThreads;
-  // long runs read fewer inputs twice (K - 1 in TT), short ones keep every SM
-  // busy when the stream is short
+  a.blocks = (d.channels / kConvCh + kConvThreads - 1) / kConvThreads;
+  // runs: long ones read fewer inputs twice (K - 1 in TT), shorter ones keep
+  // every SM busy when the stream is short
   int64_t tiles = 0;
-  for (a.tokens = kConvMaxRun;; a.tokens /= 4) {
+  for (a.tokens = kConvMaxRun;; a.tokens /= 2) {
     tiles = (static_cast<int64_t>(d.total_tokens) + a.tokens - 1) / a.tokens;
-    if (a.tokens == 1 || tiles * a.blocks >= 4 * step_num_sms()) break;
+    if (a.tokens == 8 || tiles * a.blocks >= 4 * step_num_sms()) break;
   }
-  const int grid = static_cast<int>(tiles * a.blocks) + 1;
+  if (d.total_tokens <= kShortTokens) tiles = 0;
+  const int64_t grid = (d.num_seqs + tiles) * a.blocks + 1;
+  if (grid > 0x7fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return d.dtype == MCP_DTYPE_BF16 ? conv_width<__nv_bfloat16>(a, d.width, grid, st)
                                    : conv_width<__half>(a, d.width, grid, st);
