@@ -9,7 +9,6 @@ PyTorch fallback.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import numpy as np
@@ -361,73 +360,109 @@ def mixed_attn_fwd_noalloc(desc: AttnDesc, h_cu_seqlens_q, h_seqlens_k, q, k_cac
 # the operators around a step's attention
 # ---------------------------------------------------------------------------
 
-def _on(t):
-    """The device that tensor ``t`` is on, as the current one."""
+# A step makes these calls for every layer or token, so the checks are written
+# for the good case: one comparison per property, the message worked out apart.
+
+def _gpu(t, name) -> int:
+    """Index of the device that tensor ``t`` is on."""
     import torch
 
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
-    if not t.is_cuda:
-        raise ValueError("tensors must be CUDA tensors")
-    return torch.cuda.device(t.device) if t.get_device() != torch.cuda.current_device() \
-        else contextlib.nullcontext()
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
 
-def _arg(t, dtype, name, like, shape=None):
-    """Device address of a contiguous CUDA tensor on the device of ``like`` (None: no address)."""
+def _refuse(t, dtype, name, dev, shape):
     import torch
 
-    if t is None:
-        return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _row_arg(t, name, like, shape):
-    """(address, stride between tokens) of [tokens, ...] rows of ``like``'s type that may be
-    part of wider rows: everything behind the first dimension is dense."""
-    import torch
+def _arg(t, dtype, name, dev, shape=None):
+    """Device address of a contiguous tensor on device ``dev`` (None: no address)."""
+    if t is None:
+        return None
+    try:
+        if (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, name, dev, shape)
 
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+def _row_arg(t, dtype, name, dev, shape):
+    """(address, stride between tokens) of [tokens, ...] rows that may be part of wider rows:
+    everything behind the first dimension is dense."""
+    try:
+        good = t.dtype is dtype and t.get_device() == dev and t.shape == shape
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse(t, dtype, name, dev, shape)
+    strides = t.stride()
     row = 1
-    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and s != row:
-            raise ValueError(f"{name}: a token's row must be dense, got strides {t.stride()}")
-        row *= n
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else -(-row // 8) * 8
+    for k in range(len(shape) - 1, 0, -1):
+        if shape[k] != 1 and strides[k] != row:
+            raise ValueError(f"{name}: a token's row must be dense, got strides {strides}")
+        row *= shape[k]
+    return t.data_ptr(), strides[0] if shape[0] > 1 else -(-row // 8) * 8
 
 
-def _error(error_word, like):
+def _error(error_word, dev):
     """Address of an error word: None, an int32 CUDA tensor, or a device address."""
+    if error_word is None:
+        return None
     import torch
 
-    if error_word is None or isinstance(error_word, torch.Tensor):
-        return _arg(error_word, torch.int32, "error_word", like)
+    if isinstance(error_word, torch.Tensor):
+        return _arg(error_word, torch.int32, "error_word", dev)
     return int(error_word)
+
+
+def _launch(where, dev, stream, fn, *args):
+    """Call ``fn(*args, stream)`` with ``dev`` as the current device."""
+    import torch
+
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(where, dev, stream, fn, *args)
+    if stream is None:
+        raw = _raw_stream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        raw = stream.cuda_stream
+    else:
+        raw = int(stream)
+    st = fn(*args, raw)
+    if st:
+        _capi.check(st, where)
+
+
+def _raw_stream(dev) -> int:
+    """The current stream of device ``dev`` (without a Stream object, where torch allows it)."""
+    import torch
+
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev) if get is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _result(out, stream, make):
     """``out``, or a new tensor of ``make()`` that ``stream`` may use."""
-    import torch
-
     if out is not None:
         return out
+    import torch
+
     out = make()
     if stream is not None:
         s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
@@ -442,17 +477,17 @@ def make_request_pool(request_pages, request_lens, free_pages, free_count,
     [num_pages], free_count [1].  The tensors stay the caller's state; the pool keeps them."""
     import torch
 
-    _on(request_pages)
+    dev = _gpu(request_pages, "request_pages")
     if request_pages.dim() != 2:
         raise ValueError("request_pages must be [max_requests, max_pages_per_seq]")
     R, width = request_pages.shape
     i32 = torch.int32
     pool = RequestPool(
         R, width, int(page_size), int(free_pages.numel()),
-        _arg(request_pages, i32, "request_pages", request_pages),
-        _arg(request_lens, i32, "request_lens", request_pages, (R,)),
-        _arg(free_pages, i32, "free_pages", request_pages),
-        _arg(free_count, i32, "free_count", request_pages, (1,)))
+        _arg(request_pages, i32, "request_pages", dev),
+        _arg(request_lens, i32, "request_lens", dev, (R,)),
+        _arg(free_pages, i32, "free_pages", dev),
+        _arg(free_count, i32, "free_count", dev, (1,)))
     pool.tensors = (request_pages, request_lens, free_pages, free_count)
     return pool
 
@@ -466,22 +501,17 @@ def build_step_tables(pool: RequestPool, request_ids, q_lens, cu_seqlens_q, seql
     logits_indices [S] out, all int32 CUDA tensors otherwise."""
     import torch
 
-    lib = load()
-    like, i32 = request_ids, torch.int32
-    with _on(like):
-        S, cap = int(request_ids.shape[0]), int(slot_mapping.shape[0])
-        one = (S,)
-        st = lib.mcp_build_step_tables(
-            ctypes.byref(pool), _arg(request_ids, i32, "request_ids", like, one),
-            _arg(q_lens, i32, "q_lens", like, one), S, cap,
-            _arg(cu_seqlens_q, i32, "cu_seqlens_q", like, (S + 1,)),
-            _arg(seqlens_k, i32, "seqlens_k", like, one),
-            _arg(block_tables, i32, "block_tables", like, (S, pool.max_pages_per_seq)),
-            _arg(slot_mapping, torch.int64, "slot_mapping", like, (cap,)),
-            _arg(positions, i32, "positions", like, (cap,)),
-            _arg(logits_indices, i32, "logits_indices", like, one),
-            _error(error_word, like), _stream(stream))
-    _capi.check(st, "build_step_tables")
+    dev, i32 = _gpu(request_ids, "request_ids"), torch.int32
+    S, cap = int(request_ids.shape[0]), int(slot_mapping.shape[0])
+    one = (S,)
+    _launch("build_step_tables", dev, stream, load().mcp_build_step_tables, ctypes.byref(pool),
+            _arg(request_ids, i32, "request_ids", dev, one), _arg(q_lens, i32, "q_lens", dev, one),
+            S, cap, _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),
+            _arg(seqlens_k, i32, "seqlens_k", dev, one),
+            _arg(block_tables, i32, "block_tables", dev, (S, pool.max_pages_per_seq)),
+            _arg(slot_mapping, torch.int64, "slot_mapping", dev, (cap,)),
+            _arg(positions, i32, "positions", dev, (cap,)),
+            _arg(logits_indices, i32, "logits_indices", dev, one), _error(error_word, dev))
 
 
 def commit_step(pool: RequestPool, request_ids, q_lens, new_lens=None, error_word=None,
@@ -490,25 +520,24 @@ def commit_step(pool: RequestPool, request_ids, q_lens, new_lens=None, error_wor
     stays, 0: the request is over) and pages behind them return to the pool."""
     import torch
 
-    lib = load()
-    like, i32 = request_ids, torch.int32
-    with _on(like):
-        S = int(request_ids.shape[0])
-        st = lib.mcp_commit_step(
-            ctypes.byref(pool), _arg(request_ids, i32, "request_ids", like, (S,)),
-            _arg(q_lens, i32, "q_lens", like, (S,)), _arg(new_lens, i32, "new_lens", like, (S,)),
-            S, _error(error_word, like), _stream(stream))
-    _capi.check(st, "commit_step")
+    dev, i32 = _gpu(request_ids, "request_ids"), torch.int32
+    one = (int(request_ids.shape[0]),)
+    _launch("commit_step", dev, stream, load().mcp_commit_step, ctypes.byref(pool),
+            _arg(request_ids, i32, "request_ids", dev, one), _arg(q_lens, i32, "q_lens", dev, one),
+            _arg(new_lens, i32, "new_lens", dev, one), one[0], _error(error_word, dev))
 
 
 def _dtype_code(t, name):
     import torch
 
-    code = {torch.bfloat16: _capi.DTYPE_BF16, torch.float16: _capi.DTYPE_FP16,
-            torch.float32: _capi.DTYPE_FP32}.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
-    return code
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        return _capi.DTYPE_BF16
+    if dtype is torch.float16:
+        return _capi.DTYPE_FP16
+    if dtype is torch.float32:
+        return _capi.DTYPE_FP32
+    raise TypeError(f"{name} must be bf16, fp16 or fp32, got {dtype}")
 
 
 def mixed_conv(x, weight, bias, state, request_ids, cu_seqlens_q, seqlens_k, activation="silu",
@@ -520,28 +549,25 @@ def mixed_conv(x, weight, bias, state, request_ids, cu_seqlens_q, seqlens_k, act
     ``activation``: "silu" or "none".  Returns ``out`` [T, channels]."""
     import torch
 
-    lib = load()
     if activation not in ("silu", "none"):
         raise ValueError("activation must be 'silu' or 'none'")
-    with _on(x):
-        if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
-            raise ValueError("x must be [T, channels], weight [channels, K], "
-                             "state [requests, K - 1, channels]")
-        T, d = x.shape
-        K, S, i32 = int(weight.shape[1]), int(request_ids.shape[0]), torch.int32
-        out = _result(out, stream, lambda: torch.empty((T, d), dtype=x.dtype, device=x.device))
-        px, ldx = _row_arg(x, "x", x, (T, d))
-        po, ldo = _row_arg(out, "out", x, (T, d))
-        desc = _capi.ConvDesc(S, T, int(state.shape[0]), d, K, _dtype_code(x, "x"),
-                              activation == "silu", 0, ldx, ldo)
-        st = lib.mcp_mixed_conv(
-            ctypes.byref(desc), px, _arg(weight, x.dtype, "weight", x, (d, K)),
-            _arg(bias, x.dtype, "bias", x, (d,)),
-            _arg(state, x.dtype, "state", x, (state.shape[0], K - 1, d)),
-            _arg(request_ids, i32, "request_ids", x, (S,)),
-            _arg(cu_seqlens_q, i32, "cu_seqlens_q", x, (S + 1,)),
-            _arg(seqlens_k, i32, "seqlens_k", x, (S,)), po, _error(error_word, x), _stream(stream))
-    _capi.check(st, "mixed_conv")
+    dev, dtype, i32 = _gpu(x, "x"), x.dtype, torch.int32
+    if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
+        raise ValueError("x must be [T, channels], weight [channels, K], "
+                         "state [requests, K - 1, channels]")
+    rows = x.shape
+    T, d = rows
+    K, S, R = weight.shape[1], request_ids.shape[0], state.shape[0]
+    out = _result(out, stream, lambda: torch.empty(rows, dtype=dtype, device=x.device))
+    px, ldx = _row_arg(x, dtype, "x", dev, rows)
+    po, ldo = _row_arg(out, dtype, "out", dev, rows)
+    desc = _capi.ConvDesc(S, T, R, d, K, _dtype_code(x, "x"), activation == "silu", 0, ldx, ldo)
+    _launch("mixed_conv", dev, stream, load().mcp_mixed_conv, ctypes.byref(desc), px,
+            _arg(weight, dtype, "weight", dev, (d, K)), _arg(bias, dtype, "bias", dev, (d,)),
+            _arg(state, dtype, "state", dev, (R, K - 1, d)),
+            _arg(request_ids, i32, "request_ids", dev, (S,)),
+            _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),
+            _arg(seqlens_k, i32, "seqlens_k", dev, (S,)), po, _error(error_word, dev))
     return out
 
 
@@ -554,46 +580,43 @@ def mixed_scan(x, dt, A, B, C, state, request_ids, cu_seqlens_q, seqlens_k, D=No
     seqlens_k [S], cu_seqlens_q [S + 1] int32.  Returns ``out`` [T, channels]."""
     import torch
 
-    lib = load()
-    with _on(x):
-        if x.dim() != 2 or B.dim() != 3 or state.dim() != 3:
-            raise ValueError("x must be [T, channels], B and C [T, groups, N], "
-                             "state [requests, channels, N]")
-        T, d = x.shape
-        G, N, S = int(B.shape[1]), int(B.shape[2]), int(request_ids.shape[0])
-        f32, i32 = torch.float32, torch.int32
-        out = _result(out, stream, lambda: torch.empty((T, d), dtype=x.dtype, device=x.device))
-        px, ldx = _row_arg(x, "x", x, (T, d))
-        pd, ldd = _row_arg(dt, "dt", x, (T, d))
-        pz, ldz = (None, 0) if z is None else _row_arg(z, "z", x, (T, d))
-        pb, ldb = _row_arg(B, "B", x, (T, G, N))
-        pc, ldc = _row_arg(C, "C", x, (T, G, N))
-        po, ldo = _row_arg(out, "out", x, (T, d))
-        desc = _capi.ScanDesc(S, T, int(state.shape[0]), d, N, G, _dtype_code(x, "x"),
-                              bool(softplus), ldx, ldd, ldz, ldb, ldc, ldo)
-        tensors = _capi.ScanTensors(
-            px, pd, _arg(A, f32, "A", x, (d, N)), pb, pc, _arg(D, f32, "D", x, (d,)), pz,
-            _arg(dt_bias, f32, "dt_bias", x, (d,)),
-            _arg(state, f32, "state", x, (state.shape[0], d, N)), po)
-        st = lib.mcp_mixed_scan(
-            ctypes.byref(desc), ctypes.byref(tensors),
-            _arg(request_ids, i32, "request_ids", x, (S,)),
-            _arg(cu_seqlens_q, i32, "cu_seqlens_q", x, (S + 1,)),
-            _arg(seqlens_k, i32, "seqlens_k", x, (S,)), _error(error_word, x), _stream(stream))
-    _capi.check(st, "mixed_scan")
+    dev, dtype = _gpu(x, "x"), x.dtype
+    f32, i32 = torch.float32, torch.int32
+    if x.dim() != 2 or B.dim() != 3 or state.dim() != 3:
+        raise ValueError("x must be [T, channels], B and C [T, groups, N], "
+                         "state [requests, channels, N]")
+    rows, bc = x.shape, B.shape
+    T, d = rows
+    G, N, S, R = bc[1], bc[2], request_ids.shape[0], state.shape[0]
+    out = _result(out, stream, lambda: torch.empty(rows, dtype=dtype, device=x.device))
+    px, ldx = _row_arg(x, dtype, "x", dev, rows)
+    pd, ldd = _row_arg(dt, dtype, "dt", dev, rows)
+    pz, ldz = (None, 0) if z is None else _row_arg(z, dtype, "z", dev, rows)
+    pb, ldb = _row_arg(B, dtype, "B", dev, (T, G, N))
+    pc, ldc = _row_arg(C, dtype, "C", dev, (T, G, N))
+    po, ldo = _row_arg(out, dtype, "out", dev, rows)
+    desc = _capi.ScanDesc(S, T, R, d, N, G, _dtype_code(x, "x"), bool(softplus), ldx, ldd, ldz,
+                          ldb, ldc, ldo)
+    tensors = _capi.ScanTensors(
+        px, pd, _arg(A, f32, "A", dev, (d, N)), pb, pc, _arg(D, f32, "D", dev, (d,)), pz,
+        _arg(dt_bias, f32, "dt_bias", dev, (d,)), _arg(state, f32, "state", dev, (R, d, N)), po)
+    _launch("mixed_scan", dev, stream, load().mcp_mixed_scan, ctypes.byref(desc),
+            ctypes.byref(tensors), _arg(request_ids, i32, "request_ids", dev, (S,)),
+            _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),
+            _arg(seqlens_k, i32, "seqlens_k", dev, (S,)), _error(error_word, dev))
     return out
 
 
-def _token_state(seen, counts, vocab_size, like):
+def _token_state(seen, counts, vocab_size, dev):
     """Addresses of ``seen`` [R, 2, W] and ``counts`` [R, 32 W], W = ceil(vocab_size / 32)."""
     import torch
 
     W = (vocab_size + 31) // 32
     if seen.dim() != 3:
         raise ValueError("seen must be [requests, 2, ceil(vocab_size / 32)]")
-    R = int(seen.shape[0])
-    return (R, _arg(seen, torch.int32, "seen", like, (R, 2, W)),
-            _arg(counts, torch.int32, "counts", like, (R, 32 * W)))
+    R = seen.shape[0]
+    return (R, _arg(seen, torch.int32, "seen", dev, (R, 2, W)),
+            _arg(counts, torch.int32, "counts", dev, (R, 32 * W)))
 
 
 def update_token_counts(request_ids, tokens, seen, counts, vocab_size, cu_tokens=None,
@@ -605,18 +628,15 @@ def update_token_counts(request_ids, tokens, seen, counts, vocab_size, cu_tokens
     cleared first."""
     import torch
 
-    lib = load()
-    like, i32 = request_ids, torch.int32
-    with _on(like):
-        n, rows = int(tokens.shape[0]), int(request_ids.shape[0])
-        R, ps, pc = _token_state(seen, counts, int(vocab_size), like)
-        st = lib.mcp_update_token_counts(
-            _arg(request_ids, i32, "request_ids", like, (rows,)), rows,
-            _arg(tokens, i32, "tokens", like, (n,)), n,
-            _arg(cu_tokens, i32, "cu_tokens", like, (rows + 1,)), ps, pc, R, int(vocab_size),
+    dev, i32 = _gpu(request_ids, "request_ids"), torch.int32
+    n, rows, V = tokens.shape[0], request_ids.shape[0], int(vocab_size)
+    R, ps, pc = _token_state(seen, counts, V, dev)
+    _launch("update_token_counts", dev, stream, load().mcp_update_token_counts,
+            _arg(request_ids, i32, "request_ids", dev, (rows,)), rows,
+            _arg(tokens, i32, "tokens", dev, (n,)), n,
+            _arg(cu_tokens, i32, "cu_tokens", dev, (rows + 1,)), ps, pc, R, V,
             (_capi.COUNT_PROMPT if prompt else 0) | (_capi.COUNT_RESET if reset else 0),
-            _error(error_word, like), _stream(stream))
-    _capi.check(st, "update_token_counts")
+            _error(error_word, dev))
 
 
 def process_logits(logits, out=None, request_ids=None, seen=None, counts=None, temperature=None,
@@ -631,47 +651,40 @@ def process_logits(logits, out=None, request_ids=None, seen=None, counts=None, t
     token, mask_rows [rows] or None for one mask a row.  Returns the processed logits."""
     import torch
 
-    lib = load()
-    with _on(logits):
-        out = logits if out is None else out
-        if logits.dim() != 2 or out.shape != logits.shape:
-            raise ValueError("logits and out must be [rows, vocab]")
-        rows, V = logits.shape
-        f32, i32 = torch.float32, torch.int32
-        one = (rows,)
-        for t, name in ((logits, "logits"), (out, "out")):
-            if V > 1 and t.stride(1) != 1:
-                raise ValueError(f"{name}: a row must be dense, got strides {t.stride()}")
-        if out.get_device() != logits.get_device():
-            raise ValueError(f"out must be on {logits.device}, got {out.device}")
-        R = ps = pc = None
-        if request_ids is not None:
-            if seen is None or counts is None:
-                raise ValueError("request_ids needs seen and counts")
-            R, ps, pc = _token_state(seen, counts, V, logits)
-        off = tok = val = None
-        if bias is not None:
-            off, tok, val = bias
-        masks = 0
-        if mask is not None:
-            masks = int(mask.shape[0])
-        desc = _capi.LogitsDesc(rows, V, R or 0, _dtype_code(logits, "logits"),
-                                _dtype_code(out, "out"), 0 if tok is None else int(tok.shape[0]),
-                                masks, 0, logits.stride(0) if rows > 1 else V,
-                                out.stride(0) if rows > 1 else V)
-        tensors = _capi.LogitsTensors(
-            logits.data_ptr(), out.data_ptr(),
-            _arg(request_ids, i32, "request_ids", logits, one), ps, pc,
-            _arg(temperature, f32, "temperature", logits, one),
-            _arg(repetition_penalty, f32, "repetition_penalty", logits, one),
-            _arg(frequency_penalty, f32, "frequency_penalty", logits, one),
-            _arg(presence_penalty, f32, "presence_penalty", logits, one),
-            _arg(off, i32, "bias offsets", logits, (rows + 1,)),
-            _arg(tok, i32, "bias tokens", logits),
-            _arg(val, f32, "bias values", logits, None if tok is None else tok.shape),
-            _arg(mask, i32, "mask", logits, (masks, (V + 31) // 32)),
-            _arg(mask_rows, i32, "mask_rows", logits, one))
-        st = lib.mcp_process_logits(ctypes.byref(desc), ctypes.byref(tensors),
-                                    _error(error_word, logits), _stream(stream))
-    _capi.check(st, "process_logits")
+    dev = _gpu(logits, "logits")
+    out = logits if out is None else out
+    if logits.dim() != 2 or out.shape != logits.shape:
+        raise ValueError("logits and out must be [rows, vocab]")
+    rows, V = logits.shape
+    f32, i32 = torch.float32, torch.int32
+    one = (rows,)
+    ld = []
+    for t, name in ((logits, "logits"), (out, "out")):
+        strides = t.stride()
+        if V > 1 and strides[1] != 1:
+            raise ValueError(f"{name}: a row must be dense, got strides {strides}")
+        ld.append(strides[0] if rows > 1 else V)
+    if out.get_device() != dev:
+        raise ValueError(f"out must be on {logits.device}, got {out.device}")
+    R, ps, pc = 0, None, None
+    if request_ids is not None:
+        if seen is None or counts is None:
+            raise ValueError("request_ids needs seen and counts")
+        R, ps, pc = _token_state(seen, counts, V, dev)
+    off, tok, val = (None, None, None) if bias is None else bias
+    masks = 0 if mask is None else mask.shape[0]
+    desc = _capi.LogitsDesc(rows, V, R, _dtype_code(logits, "logits"), _dtype_code(out, "out"),
+                            0 if tok is None else tok.shape[0], masks, 0, ld[0], ld[1])
+    tensors = _capi.LogitsTensors(
+        logits.data_ptr(), out.data_ptr(), _arg(request_ids, i32, "request_ids", dev, one), ps, pc,
+        _arg(temperature, f32, "temperature", dev, one),
+        _arg(repetition_penalty, f32, "repetition_penalty", dev, one),
+        _arg(frequency_penalty, f32, "frequency_penalty", dev, one),
+        _arg(presence_penalty, f32, "presence_penalty", dev, one),
+        _arg(off, i32, "bias offsets", dev, (rows + 1,)), _arg(tok, i32, "bias tokens", dev),
+        _arg(val, f32, "bias values", dev, None if tok is None else tok.shape),
+        _arg(mask, i32, "mask", dev, (masks, (V + 31) // 32)),
+        _arg(mask_rows, i32, "mask_rows", dev, one))
+    _launch("process_logits", dev, stream, load().mcp_process_logits, ctypes.byref(desc),
+            ctypes.byref(tensors), _error(error_word, dev))
     return out

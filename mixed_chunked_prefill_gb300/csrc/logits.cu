@@ -533,9 +533,7 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
 
 template <typename TI, typename TO, int kRows>
 int logits_rows(const LogitArgs& a, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(process_logits_kernel<TI, TO, kRows>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kLogitSmem<TI>);
-  if (e != cudaSuccess) return static_cast<int>(e);
+  if (const int e = allow_smem<process_logits_kernel<TI, TO, kRows>>(kLogitSmem<TI>)) return e;
   const int64_t grid = static_cast<int64_t>(a.rows) * a.parts;
   process_logits_kernel<TI, TO, kRows>
       <<<static_cast<unsigned>(grid), kLogitThreads, kLogitSmem<TI>, st>>>(a);

@@ -2,7 +2,10 @@
 // (return a cudaError_t value; 0 = success) called by step_ops.cpp.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "mcp.h"
 
@@ -35,7 +38,22 @@ int launch_update_token_counts(const int32_t* request_ids, int32_t num_rows,
 int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,
                           int32_t* error_word, void* stream);
 
-// SMs of the current device (read once per device).
+// SMs of the current device (read once per device and thread).
 int step_num_sms();
+
+// Allow `kernel` up to `bytes` of dynamic shared memory on the current device,
+// the same `bytes` in every call (done once per device: the attribute stays).
+// 0 or a cudaError_t value.
+template <auto kernel>
+int allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};  // a bit per device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return 0;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return static_cast<int>(e);
+}
 
 }  // namespace mcp

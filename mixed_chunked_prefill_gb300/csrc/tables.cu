@@ -383,11 +383,7 @@ int launch_build_step_tables(const mcp_request_pool& pool, const int32_t* reques
   a.pos = positions;
   a.rows = logits_indices;
   const size_t smem = step_smem(num_seqs, a.R);
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return static_cast<int>(e);
-  }
+  if (const int e = allow_smem<build_tables_kernel>(static_cast<int>(step_smem(kMaxStepSeqs, kWindow)))) return e;
   const int64_t pieces =
       static_cast<int64_t>(num_seqs) * ((a.width + kPiece - 1) / kPiece) +
       (static_cast<int64_t>(max_tokens) + kPiece - 1) / kPiece;
@@ -401,11 +397,7 @@ int launch_commit_step(const mcp_request_pool& pool, const int32_t* request_ids,
   StepArgs a = step_args(pool, request_ids, q_lens, num_seqs, error_word);
   a.new_lens = new_lens;
   const size_t smem = step_smem(num_seqs, a.R);
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return static_cast<int>(e);
-  }
+  if (const int e = allow_smem<commit_kernel>(static_cast<int>(step_smem(kMaxStepSeqs, kWindow)))) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t pieces = static_cast<int64_t>(num_seqs) * ((a.width + kPiece - 1) / kPiece);
   // a commit that keeps every token returns no page: one CTA moves the lengths on
