@@ -15,9 +15,9 @@
 // (written), 12 per token slot: a few MB at most, so latency bounds every
 // ordinary step.  One launch: every CTA computes the prefix sums of all
 // segments for itself (two dependent loads and one block scan; S <= 8192
-// segments are 4 x 32 KB of shared memory) and then writes its share of the
-// table rows and token slots.  A second launch that waited for the sums would
-// cost more than repeating them.
+// segments are 4 x 32 KB of shared memory), and its warps then write their share
+// of the table rows and token slots.  A second launch that waited for the sums
+// would cost more than repeating them.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -28,7 +28,8 @@ namespace mcp {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kPiece = 2048;       // table entries of one row, or token slots, per work piece
+constexpr int kUnit = 512;         // table entries of one row that a warp takes at a time
+constexpr int kTokenUnit = 128;    // token slots that a warp takes at a time
 constexpr int kWindow = 1 << 15;   // request rows per pass of the repeated-row check
 
 struct StepArgs {
@@ -57,9 +58,8 @@ struct Step {
   int32_t* page;   // [S + 1]
   int32_t* id;     // [S]
   int32_t* have;   // [S]
-  int32_t* seen;   // [kWindow / 32]
+  uint32_t* seen;  // [kWindow / 32]
   int32_t base;    // free[base] is the step's first new page
-  int32_t count;   // free_count before the step
   int32_t bad;     // error bits, 0: the step is sound
 };
 
@@ -67,52 +67,42 @@ __device__ __forceinline__ int32_t pages_of(int32_t tokens, int lg) {
   return static_cast<int32_t>((static_cast<int64_t>(tokens) + (1 << lg) - 1) >> lg);
 }
 
-// Exclusive block sums of a and b over the threads; totals in ta, tb.
-__device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t& ta, int64_t& tb) {
-  __shared__ int64_t wa[kThreads / 32], wb[kThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t a0 = a, b0 = b;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, b, d);
-    if (lane >= d) a += x, b += y;
-  }
-  __syncthreads();  // wa / wb may still be read from the scan before
-  if (lane == 31) wa[warp] = a, wb[warp] = b;
-  __syncthreads();
-  int64_t pa = 0, pb = 0;
-  ta = tb = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) pa = ta, pb = tb;
-    ta += wa[w];
-    tb += wb[w];
-  }
-  a = pa + a - a0;
-  b = pb + b - b0;
-}
-
 // Read the step's segments into shared memory, check them and scan.  Every
-// CTA does the same and comes to the same answer.  kCommit: `page` receives
-// the offsets of the returned pages.
+// CTA does the same and comes to the same answer.  A thread owns consecutive
+// segments from its first load to their prefix sums, so one barrier before (the
+// cleared marks), one inside the scan and one after are all.  kCommit: `page`
+// receives the offsets of the returned pages.  `rows` (build, one CTA): the
+// logits indices, which are one more prefix sum.
 template <bool kCommit>
-__device__ __forceinline__ void load_step(const StepArgs& p, Step& st, char* smem) {
+__device__ __forceinline__ void load_step(const StepArgs& p, Step& st, char* smem, int32_t* rows) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int64_t w_tok[kWarps], w_page[kWarps], w_need[kWarps];
+  __shared__ int32_t w_some[kWarps], w_bad[kWarps];
   const int32_t S = p.S;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   st.cu = reinterpret_cast<int32_t*>(smem);
   st.page = st.cu + S + 1;
   st.id = st.page + S + 1;
   st.have = st.id + S;
-  st.seen = st.have + S;
-  st.count = *p.free_count;
-  int bad = st.count < 0 || st.count > p.num_pages ? MCP_DEVERR_NO_PAGES : 0;
+  st.seen = reinterpret_cast<uint32_t*>(st.have + S);
+  const int per = (S + kThreads - 1) / kThreads;
+  const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
+  const int32_t count = *p.free_count;
+  const int32_t words = (min(kWindow, p.R) + 31) / 32;
+  for (int i = threadIdx.x; i < words; i += kThreads) st.seen[i] = 0;
+  __syncthreads();
   const int64_t most = static_cast<int64_t>(p.width) << p.P_log2;
-  int64_t need = 0;  // new pages of this thread's segments
-  for (int s = threadIdx.x; s < S; s += kThreads) {
+  int bad = count < 0 || count > p.num_pages ? MCP_DEVERR_NO_PAGES : 0;
+  int64_t tok = 0, page = 0, need = 0;
+  int32_t some = 0;
+  for (int s = s0; s < s1; ++s) {
     const int32_t id = p.ids[s];
     int32_t q = p.q_lens[s], have = 0, back = 0, grow = 0;
     if (id < 0) {
       q = 0;  // padding: an empty segment
     } else if (id >= p.R) {
       bad |= MCP_DEVERR_REQUEST;
+      q = 0;
     } else {
       have = p.request_lens[id];
       if (have < 0 || q < 0 || static_cast<int64_t>(have) + q > most) {
@@ -121,77 +111,97 @@ __device__ __forceinline__ void load_step(const StepArgs& p, Step& st, char* sme
       }
       const int32_t after = pages_of(have + q, p.P_log2);
       grow = after - pages_of(have, p.P_log2);
-      need += grow;
       if (kCommit) {
         const int32_t to = p.new_lens ? p.new_lens[s] : have + q;
-        if (to < 0 || to > have + q)
-          bad |= MCP_DEVERR_REQUEST;
-        else
-          back = after - pages_of(to, p.P_log2);
+        if (to < 0 || to > have + q) bad |= MCP_DEVERR_REQUEST;
+        else back = after - pages_of(to, p.P_log2);
+      }
+      // a request may stand once in a step
+      if (id < kWindow) {
+        const uint32_t bit = 1u << (id & 31);
+        if (atomicOr(st.seen + (id >> 5), bit) & bit) bad |= MCP_DEVERR_REQUEST;
       }
     }
     st.cu[s] = q;
     st.page[s] = kCommit ? back : grow;
     st.id[s] = id;
     st.have[s] = have;
+    tok += q;
+    page += kCommit ? back : grow;
+    need += grow;
+    some += q > 0;
   }
-  // a request may stand once in a step: mark the rows, a window at a time
-  for (int32_t w0 = 0; w0 < p.R; w0 += kWindow) {
-    const int32_t words = (min(kWindow, p.R - w0) + 31) / 32;
+  for (int32_t r0 = kWindow; r0 < p.R; r0 += kWindow) {  // the other rows, a window at a time
     __syncthreads();
-    for (int i = threadIdx.x; i < words; i += kThreads) st.seen[i] = 0;
+    for (int i = threadIdx.x; i < kWindow / 32; i += kThreads) st.seen[i] = 0;
     __syncthreads();
-    for (int s = threadIdx.x; s < S; s += kThreads) {
-      const int32_t r = st.id[s] - w0;
-      if (st.id[s] < 0 || r < 0 || r >= kWindow || st.id[s] >= p.R) continue;
-      const int32_t bit = static_cast<int32_t>(1u << (r & 31));
+    for (int s = s0; s < s1; ++s) {
+      const int32_t r = st.id[s] - r0;
+      if (r < 0 || r >= kWindow || st.id[s] >= p.R) continue;
+      const uint32_t bit = 1u << (r & 31);
       if (atomicOr(st.seen + (r >> 5), bit) & bit) bad |= MCP_DEVERR_REQUEST;
     }
   }
+  const int64_t tok0 = tok, page0 = page;
+  const int32_t some0 = some;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, tok, d), y = __shfl_up_sync(0xffffffffu, page, d);
+    const int32_t z = __shfl_up_sync(0xffffffffu, some, d);
+    if (lane >= d) tok += x, page += y, some += z;
+    need += __shfl_xor_sync(0xffffffffu, need, d);
+  }
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (lane == 31) {
+    w_tok[warp] = tok;
+    w_page[warp] = page;
+    w_some[warp] = some;
+    w_need[warp] = need;
+    w_bad[warp] = bad;
+  }
   __syncthreads();
-  // prefix sums: each thread owns consecutive segments
-  const int per = (S + kThreads - 1) / kThreads;
-  const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
-  int64_t a = 0, b = 0, ta, tb;
-  for (int s = s0; s < s1; ++s) a += st.cu[s], b += st.page[s];
-  block_scan2(a, b, ta, tb);
-  int64_t total_need = tb;
-  if (kCommit) {
-    int64_t none = 0, nt;
-    block_scan2(need, none, total_need, nt);
+  tok -= tok0;
+  page -= page0;
+  some -= some0;
+  int64_t all_tok = 0, all_page = 0, all_need = 0;
+  int32_t all_some = 0;
+  bad = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) tok += w_tok[w], page += w_page[w], some += w_some[w];
+    all_tok += w_tok[w];
+    all_page += w_page[w];
+    all_some += w_some[w];
+    all_need += w_need[w];
+    bad |= w_bad[w];
   }
-  if (total_need > st.count) bad |= MCP_DEVERR_NO_PAGES;
-  if (!kCommit && ta > p.max_tokens) bad |= MCP_DEVERR_REQUEST;
-  if (kCommit && st.count - total_need + tb > p.num_pages) bad |= MCP_DEVERR_NO_PAGES;
-  if (ta > 0x7fffffff) bad |= MCP_DEVERR_REQUEST;
-  // the error bits of all threads (two bits in use)
-  const int no_pages = __syncthreads_or(bad & MCP_DEVERR_NO_PAGES);
-  const int request = __syncthreads_or(bad & MCP_DEVERR_REQUEST);
-  st.bad = (no_pages ? MCP_DEVERR_NO_PAGES : 0) | (request ? MCP_DEVERR_REQUEST : 0);
-  st.base = st.count - static_cast<int32_t>(st.bad ? 0 : total_need);
-  if (st.bad) {
-    // an empty step: nothing is taken, every segment without tokens or pages
-    a = b = ta = tb = 0;
-    for (int s = s0; s < s1; ++s) st.cu[s] = st.page[s] = st.have[s] = 0, st.id[s] = -1;
-  }
+  if (all_need > count) bad |= MCP_DEVERR_NO_PAGES;
+  if (kCommit && count - all_need + all_page > p.num_pages) bad |= MCP_DEVERR_NO_PAGES;
+  if (all_tok > (kCommit ? 0x7fffffff : p.max_tokens)) bad |= MCP_DEVERR_REQUEST;
+  st.bad = bad;
+  st.base = bad ? count : count - static_cast<int32_t>(all_need);
   for (int s = s0; s < s1; ++s) {
-    const int32_t q = st.cu[s], n = st.page[s];
-    st.cu[s] = static_cast<int32_t>(a);
-    st.page[s] = static_cast<int32_t>(b);
-    a += q;
-    b += n;
+    // of an unsound step every segment is empty: nothing is taken
+    const int32_t q = bad ? 0 : st.cu[s], n = bad ? 0 : st.page[s];
+    if (bad) st.id[s] = -1, st.have[s] = 0, tok = page = 0;
+    st.cu[s] = static_cast<int32_t>(tok);
+    st.page[s] = static_cast<int32_t>(page);
+    tok += q;
+    page += n;
+    if (rows && q > 0) rows[some++] = static_cast<int32_t>(tok) - 1;
   }
   if (threadIdx.x == 0) {
-    st.cu[S] = static_cast<int32_t>(ta);
-    st.page[S] = static_cast<int32_t>(tb);
+    st.cu[S] = bad ? 0 : static_cast<int32_t>(all_tok);
+    st.page[S] = bad ? 0 : static_cast<int32_t>(all_page);
   }
+  if (rows)
+    for (int s = (bad ? 0 : all_some) + threadIdx.x; s < S; s += kThreads) rows[s] = -1;
   __syncthreads();
 }
 
-// Entry j of segment s's table row: a held page, a new page (also entered
-// into the request's own row), or -1.
-__device__ __forceinline__ int32_t table_entry(const StepArgs& p, const int32_t* row, int32_t j,
-                                               int32_t held, int32_t after, const int32_t* fresh) {
+// Entry j of segment s's table row: a held page, a new page, or -1.
+__device__ __forceinline__ int32_t table_entry(const int32_t* row, int32_t j, int32_t held,
+                                               int32_t after, const int32_t* fresh) {
   if (j < held) return row[j];
   return j < after ? fresh[j - held] : -1;
 }
@@ -199,35 +209,27 @@ __device__ __forceinline__ int32_t table_entry(const StepArgs& p, const int32_t*
 __global__ void __launch_bounds__(kThreads) build_tables_kernel(const StepArgs p) {
   extern __shared__ char smem[];
   Step st;
-  load_step<false>(p, st, smem);
+  load_step<false>(p, st, smem, blockIdx.x == 0 ? p.rows : nullptr);
   const int32_t S = p.S, lg = p.P_log2, width = p.width;
+  const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0 && st.bad && p.err) atomicOr(p.err, st.bad);
     for (int s = threadIdx.x; s <= S; s += kThreads) {
       p.cu[s] = st.cu[s];
       if (s < S) p.sk[s] = st.have[s] + st.cu[s + 1] - st.cu[s];
     }
-    if (p.rows) {
-      // the last token of every segment that has one, in segment order
-      const int per = (S + kThreads - 1) / kThreads;
-      const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
-      int64_t n = 0, none = 0, total, t2;
-      for (int s = s0; s < s1; ++s) n += st.cu[s + 1] > st.cu[s];
-      block_scan2(n, none, total, t2);
-      for (int s = s0; s < s1; ++s)
-        if (st.cu[s + 1] > st.cu[s]) p.rows[n++] = st.cu[s + 1] - 1;
-      for (int s = static_cast<int>(total) + threadIdx.x; s < S; s += kThreads) p.rows[s] = -1;
-    }
   }
-  const int32_t per_row = (width + kPiece - 1) / kPiece;
-  const int64_t table_pieces = static_cast<int64_t>(S) * per_row;
-  const int64_t pieces = table_pieces + (p.max_tokens + kPiece - 1) / kPiece;
+  // the warps of all CTAs deal out the tables' units and then the tokens'
+  const int32_t per_row = (width + kUnit - 1) / kUnit;
+  const int64_t tables = static_cast<int64_t>(S) * per_row;
+  const int64_t units = tables + (p.max_tokens + kTokenUnit - 1) / kTokenUnit;
   const bool vec = (width & 3) == 0;  // rows 16-byte aligned
-  for (int64_t w = blockIdx.x; w < pieces; w += gridDim.x) {
-    if (w < table_pieces) {
-      const int32_t s = static_cast<int32_t>(w / per_row);
-      const int32_t j0 = static_cast<int32_t>(w - static_cast<int64_t>(s) * per_row) * kPiece;
-      const int32_t j1 = min(width, j0 + kPiece);
+  for (int64_t u = blockIdx.x + static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x; u < units;
+       u += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
+    if (u < tables) {
+      const int32_t s = static_cast<int32_t>(u / per_row);
+      const int32_t j0 = static_cast<int32_t>(u - static_cast<int64_t>(s) * per_row) * kUnit;
+      const int32_t j1 = min(width, j0 + kUnit);
       const int32_t id = st.id[s];
       const int32_t held = pages_of(st.have[s], lg);
       const int32_t after = pages_of(st.have[s] + st.cu[s + 1] - st.cu[s], lg);
@@ -235,39 +237,62 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const StepArgs p
       const int32_t* fresh = p.free_pages + st.base + st.page[s];
       int32_t* dst = p.bt + static_cast<int64_t>(s) * width;
       if (vec) {
-        for (int32_t j = j0 + 4 * threadIdx.x; j < j1; j += 4 * kThreads) {
-          int4 v;
-          if (j + 4 <= held) {
-            v = *reinterpret_cast<const int4*>(row + j);
-          } else if (j >= after) {
-            v = make_int4(-1, -1, -1, -1);
-          } else {
-            v.x = table_entry(p, row, j, held, after, fresh);
-            v.y = table_entry(p, row, j + 1, held, after, fresh);
-            v.z = table_entry(p, row, j + 2, held, after, fresh);
-            v.w = table_entry(p, row, j + 3, held, after, fresh);
+        constexpr int kLoads = kUnit / 128;  // in flight together
+        int4 v[kLoads];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int32_t j = j0 + 4 * lane + 128 * k;
+          v[k] = make_int4(-1, -1, -1, -1);
+          if (j + 4 <= held) v[k] = *reinterpret_cast<const int4*>(row + j);
+        }
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int32_t j = j0 + 4 * lane + 128 * k;
+          if (j + 4 > held && j < after) {  // the last held pages and the new ones
+            v[k].x = table_entry(row, j, held, after, fresh);
+            v[k].y = table_entry(row, j + 1, held, after, fresh);
+            v[k].z = table_entry(row, j + 2, held, after, fresh);
+            v[k].w = table_entry(row, j + 3, held, after, fresh);
           }
-          *reinterpret_cast<int4*>(dst + j) = v;
+          if (j < j1) *reinterpret_cast<int4*>(dst + j) = v[k];
         }
       } else {
-        for (int32_t j = j0 + threadIdx.x; j < j1; j += kThreads)
-          dst[j] = table_entry(p, row, j, held, after, fresh);
+        constexpr int kLoads = kUnit / 32;
+        int32_t v[kLoads];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int32_t j = j0 + lane + 32 * k;
+          v[k] = -1;
+          if (j < held) v[k] = row[j];
+        }
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int32_t j = j0 + lane + 32 * k;
+          if (j >= held && j < after) v[k] = fresh[j - held];
+          if (j < j1) dst[j] = v[k];
+        }
       }
       // new pages go behind the held ones (nothing else reads or writes there)
-      for (int32_t j = max(j0, held) + threadIdx.x; j < min(j1, after); j += kThreads)
-        row[j] = fresh[j - held];
+      for (int32_t j = max(j0, held) + lane; j < min(j1, after); j += 32) row[j] = fresh[j - held];
     } else {
-      const int32_t t0 = static_cast<int32_t>(w - table_pieces) * kPiece;
-      const int32_t t1 = min(p.max_tokens, t0 + kPiece), T = st.cu[S];
-      for (int32_t t = t0 + threadIdx.x; t < t1; t += kThreads) {
+      const int32_t t0 = static_cast<int32_t>(u - tables) * kTokenUnit;
+      const int32_t T = st.cu[S];
+      int lo = 0;
+#pragma unroll
+      for (int k = 0; k < kTokenUnit / 32; ++k) {
+        const int32_t t = t0 + lane + 32 * k;
+        if (t >= p.max_tokens) break;
         int64_t slot = -1;
         int32_t at = 0;
         if (t < T) {
-          int lo = 0, hi = S;  // the last segment that begins at or before t and is not empty
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (st.cu[mid] <= t) lo = mid;
-            else hi = mid;
+          // the last segment that begins at or before t (it is not empty)
+          if (k == 0 || st.cu[lo + 1] <= t) {
+            int hi = S;
+            while (hi - lo > 1) {
+              const int mid = (lo + hi) >> 1;
+              if (st.cu[mid] <= t) lo = mid;
+              else hi = mid;
+            }
           }
           at = st.have[lo] + t - st.cu[lo];
           const int32_t held = pages_of(st.have[lo], lg), j = at >> lg;
@@ -284,34 +309,38 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const StepArgs p
 }
 
 // Pages behind each request's new length go back to the free list; the
-// lengths and the count move on.  `finish`: the launch's one CTA (or the
-// second launch's) writes lengths and count once every page was read; the
-// copies touch only free_pages, so both launches read the same state.
+// lengths and the count move on.  `copy` touches only free_pages, which
+// nothing here reads, and `finish` (one CTA) everything else: a launch of many
+// CTAs copies, and the one that finishes may begin beside it (programmatic
+// launch), as long as it writes only once all of them have read.
 __global__ void __launch_bounds__(kThreads)
     commit_kernel(const StepArgs p, const bool copy, const bool finish) {
   extern __shared__ char smem[];
+  asm volatile("griddepcontrol.launch_dependents;");
   Step st;
-  load_step<true>(p, st, smem);
+  load_step<true>(p, st, smem, nullptr);
   const int32_t S = p.S, lg = p.P_log2, width = p.width;
-  if (finish && threadIdx.x == 0 && st.bad && p.err) atomicOr(p.err, st.bad);
-  if (st.bad) return;
-  if (copy) {
-    const int32_t per_row = (width + kPiece - 1) / kPiece;
-    const int64_t pieces = static_cast<int64_t>(S) * per_row;
-    for (int64_t w = blockIdx.x; w < pieces; w += gridDim.x) {
-      const int32_t s = static_cast<int32_t>(w / per_row);
+  if (copy && !st.bad) {
+    const int lane = threadIdx.x & 31;
+    const int32_t per_row = (width + kUnit - 1) / kUnit;
+    const int64_t units = static_cast<int64_t>(S) * per_row;
+    for (int64_t u = blockIdx.x + static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x; u < units;
+         u += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
+      const int32_t s = static_cast<int32_t>(u / per_row);
       if (st.id[s] < 0) continue;
       const int32_t after = pages_of(st.have[s] + st.cu[s + 1] - st.cu[s], lg);
       const int32_t keep = after - (st.page[s + 1] - st.page[s]);
-      const int32_t j0 = static_cast<int32_t>(w - static_cast<int64_t>(s) * per_row) * kPiece;
+      const int32_t j0 = static_cast<int32_t>(u - static_cast<int64_t>(s) * per_row) * kUnit;
       const int32_t* row = p.request_pages + static_cast<int64_t>(st.id[s]) * width;
       int32_t* to = p.free_pages + st.base + st.page[s] - keep;
-      for (int32_t j = max(j0, keep) + threadIdx.x; j < min(j0 + kPiece, after); j += kThreads)
-        to[j] = row[j];
+#pragma unroll 4
+      for (int32_t j = max(j0, keep) + lane; j < min(j0 + kUnit, after); j += 32) to[j] = row[j];
     }
   }
   if (finish) {
-    __syncthreads();
+    if (threadIdx.x == 0 && st.bad && p.err) atomicOr(p.err, st.bad);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch that copies is over
+    if (st.bad) return;
     for (int s = threadIdx.x; s < S; s += kThreads) {
       if (st.id[s] < 0) continue;
       p.request_lens[st.id[s]] = p.new_lens ? p.new_lens[s] : st.have[s] + st.cu[s + 1] - st.cu[s];
@@ -349,11 +378,11 @@ StepArgs step_args(const mcp_request_pool& pool, const int32_t* ids, const int32
   return a;
 }
 
-// CTAs for `entries` words of work: one per piece, at most two per SM (each
-// repeats the prefix sums).
-int grid_of(int64_t pieces) {
+// CTAs for `units` warps' work: at most two per SM (each repeats the prefix sums).
+int grid_of(int64_t units) {
+  const int64_t ctas = (units + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t cap = 2 * static_cast<int64_t>(step_num_sms());
-  return static_cast<int>(pieces < 1 ? 1 : pieces > cap ? cap : pieces);
+  return static_cast<int>(ctas < 1 ? 1 : ctas > cap ? cap : ctas);
 }
 
 }  // namespace
@@ -384,10 +413,9 @@ int launch_build_step_tables(const mcp_request_pool& pool, const int32_t* reques
   a.rows = logits_indices;
   const size_t smem = step_smem(num_seqs, a.R);
   if (const int e = allow_smem<build_tables_kernel>(static_cast<int>(step_smem(kMaxStepSeqs, kWindow)))) return e;
-  const int64_t pieces =
-      static_cast<int64_t>(num_seqs) * ((a.width + kPiece - 1) / kPiece) +
-      (static_cast<int64_t>(max_tokens) + kPiece - 1) / kPiece;
-  build_tables_kernel<<<grid_of(pieces), kThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+  const int64_t units = static_cast<int64_t>(num_seqs) * ((a.width + kUnit - 1) / kUnit) +
+                        (static_cast<int64_t>(max_tokens) + kTokenUnit - 1) / kTokenUnit;
+  build_tables_kernel<<<grid_of(units), kThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -399,16 +427,27 @@ int launch_commit_step(const mcp_request_pool& pool, const int32_t* request_ids,
   const size_t smem = step_smem(num_seqs, a.R);
   if (const int e = allow_smem<commit_kernel>(static_cast<int>(step_smem(kMaxStepSeqs, kWindow)))) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t pieces = static_cast<int64_t>(num_seqs) * ((a.width + kPiece - 1) / kPiece);
-  // a commit that keeps every token returns no page: one CTA moves the lengths on
-  const int grid = new_lens ? grid_of(pieces) : 1;
-  if (grid <= 16) {
+  // a commit that keeps every token returns no page: one CTA moves the lengths
+  // on; it also copies what its own 16 warps copy in two rounds
+  const int64_t units = static_cast<int64_t>(num_seqs) * ((a.width + kUnit - 1) / kUnit);
+  if (!new_lens || units <= 2 * kThreads / 32) {
     commit_kernel<<<1, kThreads, smem, st>>>(a, new_lens != nullptr, true);
-  } else {
-    commit_kernel<<<grid, kThreads, smem, st>>>(a, true, false);
-    commit_kernel<<<1, kThreads, smem, st>>>(a, false, true);
+    return static_cast<int>(cudaGetLastError());
   }
-  return static_cast<int>(cudaGetLastError());
+  commit_kernel<<<grid_of(units), kThreads, smem, st>>>(a, true, false);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return static_cast<int>(e);
+  cudaLaunchAttribute beside = {};
+  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  beside.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &beside;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, commit_kernel, a, false, true));
 }
 
 }  // namespace mcp
