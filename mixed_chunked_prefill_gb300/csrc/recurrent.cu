@@ -481,20 +481,44 @@ __device__ __forceinline__ void softplus2(float& v0, float& v1) {
 }
 
 // ------------------------------------------------- scan of short segments
-// A warp takes 8 (N = 16) channels and runs over its share of the segments: 4
-// states a lane, so a request's state is one coalesced 16-byte access a lane.
-// A decode is one register-only step between the state's load and its store;
-// the loads of kAhead segments are in flight together, because the bound is
-// the states' HBM traffic (8 N bytes per channel and segment against 8).
+// A warp takes 16 (N = 16) channels and runs over its share of the segments: 4
+// states of 2 channels a lane, so a request's state is two coalesced 16-byte
+// accesses a lane.  A decode is one register-only step between the state's load
+// and its store.  The bound is the states' HBM traffic (8 N bytes per channel
+// and segment against 8), so what counts is bytes in flight and few
+// instructions: the metadata of 32 segments come in one load each, the states
+// and inputs of the next segments in asynchronous copies to the warp's ring in
+// shared memory, and a second channel halves what a segment costs beside its
+// arithmetic (with one, 225 instructions a warp and segment kept the issue slots
+// 80% busy).
 template <typename T>
-__device__ __forceinline__ float scalar(const void* p, int64_t i) {
-  if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
-    return __half2float(static_cast<const __half*>(p)[i]);
-  else
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+__device__ __forceinline__ float scalar(const T* p) {
+  if constexpr (std::is_same<T, __half>::value) return __half2float(*p);
+  else return __bfloat162float(*p);
 }
+// 4, 8 or 16 bytes global -> shared without a register in between
+template <int n>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(n) : "memory");
+}
+
 constexpr int kShortThreads = 128;
-constexpr int kAhead = 4;
+constexpr int kAhead = 4;  // slots of the ring
+
+template <int N>
+struct ShortCfg {
+  static constexpr int LPC = N / 4;                          // lanes of a channel
+  static constexpr int kHalf = 32 / LPC;                     // a lane's channels are c and c + kHalf
+  static constexpr int CPW = 2 * kHalf;                      // channels of a warp
+  static constexpr int kXBytes = CPW * 2;                    // of x, dt, z each
+  static constexpr int kXPiece = kXBytes < 16 ? kXBytes : 16;
+  static constexpr int kXPieces = kXBytes / kXPiece;
+  static constexpr int kBPieces = N * 2 / 16;                // of B and C each
+  static constexpr int kX = 1024;                            // offsets in a slot: state first
+  static constexpr int kB = kX + (3 * kXBytes + 15) / 16 * 16;
+  static constexpr int kSlot = kB + 2 * N * 2;
+};
 
 template <typename T, int N>
 __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const ScanArgs p) {
@@ -502,78 +526,160 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const ScanArg
     check_segments(p.g);
     return;
   }
-  constexpr int LPC = N / 4;         // lanes of a channel
-  constexpr int CPW = 32 / LPC;      // channels of a warp
-  const int lane = threadIdx.x & 31, sub = lane % LPC;
+  using C = ShortCfg<N>;
+  constexpr int LPC = C::LPC, CPW = C::CPW;
+  __shared__ __align__(16) unsigned char rings[kShortThreads / 32][kAhead][C::kSlot];
+  const int lane = threadIdx.x & 31, sub = lane % LPC, cl = lane / LPC;
+  unsigned char(*ring)[C::kSlot] = rings[threadIdx.x >> 5];
   const int32_t wid = (blockIdx.x - 1) * (kShortThreads / 32) + (threadIdx.x >> 5);
-  const int32_t c = wid % p.blocks * CPW + lane / LPC;  // blocks: warps across the channels
+  const int32_t c0 = wid % p.blocks * CPW;  // blocks: warps across the channels
   const int32_t first = wid / p.blocks;
   if (first >= p.split) return;
-  const bool live = c < p.channels;
-  const int32_t cc = live ? c : p.channels - 1;  // idle lanes shadow the last channel
-  const int32_t gn = cc / p.per_group * N + 4 * sub;
-  const float4 av = *reinterpret_cast<const float4*>(p.A + static_cast<int64_t>(cc) * N + 4 * sub);
-  const float a[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
-  const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f, Dc = p.D ? p.D[cc] : 0.f;
+  const int32_t gn = c0 / p.per_group * N;
+  bool live[2];
+  int32_t cc[2];
+  float a[2][4], bias[2], skip[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int32_t c = c0 + cl + e * C::kHalf;
+    live[e] = c < p.channels;
+    cc[e] = live[e] ? c : p.channels - 1;  // idle lanes shadow the last channel
+    const float4 v = *reinterpret_cast<const float4*>(p.A + static_cast<int64_t>(cc[e]) * N + 4 * sub);
+    a[e][0] = v.x * kLog2e, a[e][1] = v.y * kLog2e, a[e][2] = v.z * kLog2e, a[e][3] = v.w * kLog2e;
+    bias[e] = p.dt_bias ? p.dt_bias[cc[e]] : 0.f;
+    skip[e] = p.D ? p.D[cc[e]] : 0.f;
+  }
 
-  for (int32_t s0 = first; s0 < p.g.S; s0 += p.split * kAhead) {
-    // lane i reads the metadata of segment s0 + i split
-    Segment m = {0, 0, -1, 0};
-    if (lane < kAhead && s0 + lane * p.split < p.g.S) m = read_segment(p.g, s0 + lane * p.split);
-    Segment sg[kAhead];
-    float4 h[kAhead];
-    float x[kAhead], d[kAhead], z[kAhead];
-    uint2 b[kAhead], q[kAhead];
-    float* st[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      sg[i].q0 = __shfl_sync(0xffffffffu, m.q0, i);
-      sg[i].q1 = __shfl_sync(0xffffffffu, m.q1, i);
-      sg[i].id = __shfl_sync(0xffffffffu, m.id, i);
-      sg[i].old = __shfl_sync(0xffffffffu, m.old, i);
-      const int32_t len = sg[i].q1 - sg[i].q0;
-      if (len <= 0 || len > p.short_max) sg[i].id = -1;
-      h[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (sg[i].id < 0) continue;
-      st[i] = p.state + (static_cast<int64_t>(sg[i].id) * p.channels + cc) * N + 4 * sub;
-      if (sg[i].old) h[i] = *reinterpret_cast<const float4*>(st[i]);
-      const int64_t t = sg[i].q0;
-      x[i] = scalar<T>(p.x, t * p.ldx + cc);
-      d[i] = scalar<T>(p.dt, t * p.lddt + cc);
-      z[i] = p.z ? scalar<T>(p.z, t * p.ldz + cc) : 0.f;
-      b[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.B) + t * p.ldb + gn);
-      q[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.C) + t * p.ldc + gn);
+  // this lane's part of a segment's inputs beside the state: a piece of x, dt, z
+  // (what 0 .. 2) or of B, C (3, 4), or nothing (-1)
+  int what = -1, to = 0;
+  const T* src = nullptr;
+  int64_t ld = 0;
+  if (lane < 3 * C::kXPieces) {
+    const int k = lane / C::kXPieces, piece = lane % C::kXPieces;
+    const int32_t ch = c0 + piece * (C::kXPiece / 2);
+    const void* base = k == 0 ? p.x : k == 1 ? p.dt : p.z;
+    if (base && ch < p.channels) {
+      what = k;
+      src = static_cast<const T*>(base) + ch;
+      ld = k == 0 ? p.ldx : k == 1 ? p.lddt : p.ldz;
+      to = C::kX + k * C::kXBytes + piece * C::kXPiece;
     }
+  } else if (lane < 3 * C::kXPieces + 2 * C::kBPieces) {
+    const int k = (lane - 3 * C::kXPieces) / C::kBPieces, piece = (lane - 3 * C::kXPieces) % C::kBPieces;
+    what = 3 + k;
+    src = static_cast<const T*>(k ? p.C : p.B) + gn + 8 * piece;
+    ld = k ? p.ldc : p.ldb;
+    to = C::kB + k * 2 * N + 16 * piece;
+  }
+  const int64_t row = static_cast<int64_t>(p.channels) * N;
+  float* const state = p.state + static_cast<int64_t>(c0 + cl) * N + 4 * sub;
+  auto request = [&](int32_t q0, int32_t id, int32_t old, int slot) {
+    if (id >= 0) {
+      if (old) {
+        const float* from = state + id * row;
+        if (live[0]) copy_async<16>(ring[slot] + 16 * lane, from);
+        if (live[1]) copy_async<16>(ring[slot] + 512 + 16 * lane, from + C::kHalf * N);
+      }
+      if (what >= 3) copy_async<16>(ring[slot] + to, src + q0 * ld);
+      else if (what >= 0) copy_async<C::kXPiece>(ring[slot] + to, src + q0 * ld);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  // segments first + k split, k = k0 .. k0 + 31 in the lanes' registers
+  for (int32_t s0 = first; s0 < p.g.S; s0 += 32 * p.split) {
+    Segment m = {0, 0, -1, 0};
+    if (s0 + static_cast<int64_t>(lane) * p.split < p.g.S) m = read_segment(p.g, s0 + lane * p.split);
+    if (m.q1 <= m.q0 || m.q1 - m.q0 > p.short_max) m.id = -1;
+    // the segments to do, moved to the front
+    uint32_t todo = __ballot_sync(0xffffffffu, m.id >= 0);
+    const int n = __popc(todo);
+    const int from = __fns(todo, 0, lane + 1) & 31;
+    m.q0 = __shfl_sync(0xffffffffu, m.q0, from);
+    m.q1 = __shfl_sync(0xffffffffu, m.q1, from);
+    m.id = __shfl_sync(0xffffffffu, m.id, from);
+    m.old = __shfl_sync(0xffffffffu, m.old, from);
+    if (lane >= n) m.id = -1;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (sg[i].id < 0) continue;
-      float hh[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
-      for (int32_t t = sg[i].q0;;) {
-        float dd = d[i] + bias, two = 0.f, bb[4], qq[4];
-        if (p.softplus) softplus2(dd, two);
-        const float dx = dd * x[i];
-        unpack4<T>(b[i], bb);
-        unpack4<T>(q[i], qq);
-        float y = 0.f;
+    for (int i = 0; i < kAhead - 1; ++i)
+      request(__shfl_sync(0xffffffffu, m.q0, i), __shfl_sync(0xffffffffu, m.id, i),
+              __shfl_sync(0xffffffffu, m.old, i), i);
+    for (int i = 0; i < n; ++i) {
+      const int ahead = i + kAhead - 1;
+      int32_t id = __shfl_sync(0xffffffffu, m.id, ahead & 31);
+      if (ahead >= 32) id = -1;
+      request(__shfl_sync(0xffffffffu, m.q0, ahead & 31), id, __shfl_sync(0xffffffffu, m.old, ahead & 31),
+              ahead % kAhead);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      __syncwarp();
+      const unsigned char* slot = ring[i % kAhead];
+      const int32_t q0 = __shfl_sync(0xffffffffu, m.q0, i), q1 = __shfl_sync(0xffffffffu, m.q1, i);
+      const int32_t old = __shfl_sync(0xffffffffu, m.old, i);
+      id = __shfl_sync(0xffffffffu, m.id, i);
+      float h[2][4], x[2], d[2], z[2];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          hh[n] = fmaf(ex2(dd * a[n]), hh[n], dx * bb[n]);
-          y = fmaf(qq[n], hh[n], y);
+      for (int e = 0; e < 2; ++e) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (old) v = *reinterpret_cast<const float4*>(slot + 512 * e + 16 * lane);
+        h[e][0] = v.x, h[e][1] = v.y, h[e][2] = v.z, h[e][3] = v.w;
+        const T* xs = reinterpret_cast<const T*>(slot + C::kX) + cl + e * C::kHalf;
+        x[e] = scalar<T>(xs);
+        d[e] = scalar<T>(xs + CPW);
+        z[e] = p.z ? scalar<T>(xs + 2 * CPW) : 0.f;
+      }
+      uint2 b = *reinterpret_cast<const uint2*>(slot + C::kB + 8 * sub);
+      uint2 q = *reinterpret_cast<const uint2*>(slot + C::kB + 2 * N + 8 * sub);
+      for (int32_t t = q0;;) {
+        float bb[4], qq[4], y[2];
+        unpack4<T>(b, bb);
+        unpack4<T>(q, qq);
+        float d0 = d[0] + bias[0], d1 = d[1] + bias[1];
+        if (p.softplus) softplus2(d0, d1);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float dd = e ? d1 : d0, dx = dd * x[e];
+          y[e] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            h[e][k] = fmaf(ex2(dd * a[e][k]), h[e][k], dx * bb[k]);
+            y[e] = fmaf(qq[k], h[e][k], y[e]);
+          }
+        }
+        // the first exchange leaves a lane with one of the two channels
+        float s;
+        {
+          const bool up = lane & 1;
+          const float give = up ? y[0] : y[1], keep = up ? y[1] : y[0];
+          s = keep + __shfl_xor_sync(0xffffffffu, give, 1);
         }
 #pragma unroll
-        for (int o = 1; o < LPC; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        y = fmaf(Dc, x[i], y);
-        if (p.z) y *= silu(z[i]);
-        if (live && sub == 0) static_cast<T*>(p.out)[t * p.ldo + c] = static_cast<T>(y);
-        if (++t >= sg[i].q1) break;
-        x[i] = scalar<T>(p.x, t * p.ldx + cc);
-        d[i] = scalar<T>(p.dt, t * p.lddt + cc);
-        z[i] = p.z ? scalar<T>(p.z, t * p.ldz + cc) : 0.f;
-        b[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.B) + t * p.ldb + gn);
-        q[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.C) + t * p.ldc + gn);
+        for (int o = 2; o < LPC; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (sub < 2) {
+          const int e = sub;
+          s = fmaf(e ? skip[1] : skip[0], e ? x[1] : x[0], s);
+          if (p.z) s *= silu(e ? z[1] : z[0]);
+          if (e ? live[1] : live[0])
+            static_cast<T*>(p.out)[t * p.ldo + (e ? cc[1] : cc[0])] = static_cast<T>(s);
+        }
+        if (++t >= q1) break;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[e] = scalar<T>(static_cast<const T*>(p.x) + t * p.ldx + cc[e]);
+          d[e] = scalar<T>(static_cast<const T*>(p.dt) + t * p.lddt + cc[e]);
+          z[e] = p.z ? scalar<T>(static_cast<const T*>(p.z) + t * p.ldz + cc[e]) : 0.f;
+        }
+        b = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.B) + t * p.ldb + gn + 4 * sub);
+        q = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.C) + t * p.ldc + gn + 4 * sub);
       }
-      if (live) *reinterpret_cast<float4*>(st[i]) = make_float4(hh[0], hh[1], hh[2], hh[3]);
+      float* to_state = state + id * row;
+      if (live[0]) *reinterpret_cast<float4*>(to_state) = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
+      if (live[1])
+        *reinterpret_cast<float4*>(to_state + C::kHalf * N) = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
+      __syncwarp();  // the slot is read before it is requested again
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // the empty tail
+    __syncwarp();
   }
 }
 
@@ -767,9 +873,9 @@ int scan_launch(ScanArgs a, cudaStream_t st) {
   }
   // without the long kernel this one takes segments of any length
   a.short_max = any_long ? kShortTokens : 0x7fffffff;
-  constexpr int per = 32 / (N / 4);
+  constexpr int per = ShortCfg<N>::CPW;
   a.blocks = (a.channels + per - 1) / per;
-  const int64_t want = (48LL * sms + a.blocks - 1) / a.blocks;
+  const int64_t want = (64LL * sms + a.blocks - 1) / a.blocks;
   a.split = static_cast<int32_t>(want < a.g.S ? want : a.g.S);
   const int64_t warps = static_cast<int64_t>(a.blocks) * a.split;
   const int64_t grid = (warps + kShortThreads / 32 - 1) / (kShortThreads / 32) + 1;
