@@ -740,7 +740,20 @@ typedef struct mcp_scan_tensors {
  */
 mcp_status mcp_mixed_scan(const mcp_scan_desc* desc, const mcp_scan_tensors* tensors,
                           const int32_t* request_ids, const int32_t* cu_seqlens_q,
-                          const int32_t* seqlens_k, int32_t* error_word, void* stream);
+                          const int32_t* seqlens_k, void* workspace, size_t workspace_bytes,
+                          int32_t* error_word, void* stream);
+
+/*
+ * Bytes of device workspace with which mcp_mixed_scan of this description runs
+ * long segments in several pieces at once on the current device (0: it would
+ * not).  The call needs none: without (workspace NULL) a segment is run in one
+ * piece, which takes longer where few long segments leave most of the GPU idle.
+ * 256-byte aligned; its contents need no preparation and mean nothing after the
+ * call.  Calls that share one must be ordered.  The way a segment is cut does
+ * not depend on other segments' values, but changes results within fp32
+ * rounding.
+ */
+mcp_status mcp_mixed_scan_workspace(const mcp_scan_desc* desc, size_t* workspace_bytes);
 
 /* ------------------------------------------------------------------------- */
 /* The sampled rows' logits                                                   */

@@ -449,6 +449,18 @@ def _launch(where, dev, stream, fn, *args):
         _capi.check(st, where)
 
 
+def _launch_free(where, dev, fn, *args):
+    """Call ``fn(*args)``, which takes no stream, with ``dev`` as the current device."""
+    import torch
+
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch_free(where, dev, fn, *args)
+    st = fn(*args)
+    if st:
+        _capi.check(st, where)
+
+
 def _raw_stream(dev) -> int:
     """The current stream of device ``dev`` (without a Stream object, where torch allows it)."""
     import torch
@@ -572,12 +584,15 @@ def mixed_conv(x, weight, bias, state, request_ids, cu_seqlens_q, seqlens_k, act
 
 
 def mixed_scan(x, dt, A, B, C, state, request_ids, cu_seqlens_q, seqlens_k, D=None, z=None,
-               dt_bias=None, softplus=True, out=None, error_word=None, stream=None):
+               dt_bias=None, softplus=True, out=None, workspace=None, error_word=None,
+               stream=None):
     """Selective state space scan of every segment of the packed stream, continued from and
     kept in ``state`` (see include/mcp.h): x, dt and z (or None) [T, channels], B and C
     [T, groups, N] of one type (bf16 or fp16; rows may be part of wider ones); A [channels, N],
     D and dt_bias [channels] (or None) and state [requests, channels, N] fp32; request_ids,
-    seqlens_k [S], cu_seqlens_q [S + 1] int32.  Returns ``out`` [T, channels]."""
+    seqlens_k [S], cu_seqlens_q [S + 1] int32.  ``workspace``: uint8 tensor for long segments
+    run in pieces (``mcp_mixed_scan_workspace`` bytes), None to take one from torch for this
+    call.  Returns ``out`` [T, channels]."""
     import torch
 
     dev, dtype = _gpu(x, "x"), x.dtype
@@ -600,10 +615,19 @@ def mixed_scan(x, dt, A, B, C, state, request_ids, cu_seqlens_q, seqlens_k, D=No
     tensors = _capi.ScanTensors(
         px, pd, _arg(A, f32, "A", dev, (d, N)), pb, pc, _arg(D, f32, "D", dev, (d,)), pz,
         _arg(dt_bias, f32, "dt_bias", dev, (d,)), _arg(state, f32, "state", dev, (R, d, N)), po)
+    if workspace is None and T > S:
+        nbytes = ctypes.c_size_t()
+        _launch_free("mixed_scan_workspace", dev, load().mcp_mixed_scan_workspace,
+                     ctypes.byref(desc), ctypes.byref(nbytes))
+        if nbytes.value:
+            workspace = _result(None, stream, lambda: torch.empty(
+                nbytes.value, dtype=torch.uint8, device=x.device))
     _launch("mixed_scan", dev, stream, load().mcp_mixed_scan, ctypes.byref(desc),
             ctypes.byref(tensors), _arg(request_ids, i32, "request_ids", dev, (S,)),
             _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),
-            _arg(seqlens_k, i32, "seqlens_k", dev, (S,)), _error(error_word, dev))
+            _arg(seqlens_k, i32, "seqlens_k", dev, (S,)),
+            _arg(workspace, torch.uint8, "workspace", dev),
+            0 if workspace is None else workspace.numel(), _error(error_word, dev))
     return out
 
 

@@ -270,7 +270,8 @@ SIGNATURES = {
     "mcp_mixed_conv": (c_int32, [POINTER(ConvDesc), c_void_p, c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "mcp_mixed_scan": (c_int32, [POINTER(ScanDesc), POINTER(ScanTensors), c_void_p, c_void_p,
-                                 c_void_p, c_void_p, c_void_p]),
+                                 c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "mcp_mixed_scan_workspace": (c_int32, [POINTER(ScanDesc), POINTER(c_size_t)]),
     "mcp_update_token_counts": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
                                           c_void_p, c_int32, c_int32, c_int32, c_void_p,
                                           c_void_p]),

@@ -446,9 +446,13 @@ struct ScanArgs {
   void* out;
   int64_t ldx, lddt, ldz, ldb, ldc, ldo;
   int32_t channels, per_group, softplus;
-  int32_t blocks;     // CTAs across the channels
-  int32_t split;      // CTAs (or warps) the segments are dealt to
+  int32_t blocks;     // warps across the channels
+  int32_t split;      // warps the short segments are dealt to
   int32_t short_max;  // segments of at most this many tokens are the short kernel's
+  int32_t piece;      // longer segments are cut into pieces of at most so many tokens (0: not)
+  int32_t slots;      // room for pieces that another follows
+  int32_t* counter;   // in the workspace, as the sums and end states behind it
+  float* carries;
 };
 
 // max(v, 0) + log1p(exp(-|v|)), two values at a time, to a few ulp also where
@@ -684,190 +688,415 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const ScanArg
 }
 
 // -------------------------------------------------- scan of long segments
-// A lane holds 4 states of one channel in registers; N / 4 neighbouring lanes
-// share a channel, 32 channels a CTA.  Tiles of 32 tokens go through shared
-// memory: the thread that loads 8 channels of a token turns dt and x into
-// (d, d x) there and keeps x and z in registers for its output, while the
-// next tile's loads are in flight.  y's sums over the lanes of a channel are
-// taken N / 4 tokens at a time (each exchange halves the tokens a lane
-// carries), one shuffle a token instead of log2(N / 4).
-constexpr int kScanChannels = 32;
-constexpr int kScanTile = 32;
+// A lane holds up to 16 states of 2 neighbouring channels (N = 16: a warp has 64
+// channels, and nothing crosses its lanes), so a token's d, d x, y and output
+// stay in its registers, and shared memory gives it only B and C.  That is what
+// the layout is for: shared memory returns 128 bytes a clock, also for a
+// broadcast, and with fewer states times channels a lane the B and C loads
+// alone (32 to 40 clocks an SM for 32 channels of a token) outweigh the
+// arithmetic.  That is 107 instructions for 32 channels of a token and 16
+// states, 19 of them ex2 or reciprocals, some 40 packed pairs that take two
+// issue slots each: 178 clocks a sub-partition, whether 8, 12 or 16 warps an SM
+// run, with scalar products in place of the pairs or not (1.24 M such groups,
+// 12 x 340 tokens of 9728 channels: 183 us).  A lane of one channel needs 153
+// instructions and 221 clocks.  The next token's softplus stands beside the
+// recurrence, 32 independent chains of it.
+//
+// Tiles of 16 tokens of x, dt, z, B and C come in asynchronous copies to the
+// warp's own ring in shared memory, two tiles deep; there is no barrier but the
+// warp's.
+//
+// Tasks are (piece of a segment, 64 channels).  A segment of more than `piece`
+// tokens is cut, so that a lone chunk fills the GPU and the longest prompt of a
+// batch does not outlast the others.  The first launch takes the whole segments
+// and each cut one's piece 0, whose start is known, and runs the pieces between
+// the first and the last from a zero state, without C and y: that leaves the
+// state e they end with and the sum s of their d.  The second launch runs pieces
+// 1 and up; their start is piece 0's end and the carry over the pieces in
+// between, h <- exp(s_j A) h + e_j.  Only pieces in between run one and a half
+// times, and a request's state is read in the first launch and written in the
+// second.
+constexpr int long_warps(int N) { return N < 64 ? 12 : 8; }  // of a CTA, one CTA an SM
+constexpr int kTile = 16;
+constexpr int64_t kCutTenths = 9;  // a piece's tokens in tenths of a warp slot's share
+
+template <int N>
+struct LongCfg {
+  static constexpr int NS = N < 16 ? N : 16;  // states of a lane
+  static constexpr int LPC = N / NS;          // lanes of a channel
+  static constexpr int CPW = 64 / LPC;        // channels of a warp
+  static constexpr int kRow = CPW * 2;        // bytes of a token's x, dt or z
+  static constexpr int kBRow = N * 2;         // of its B or C
+  static constexpr int kRaw = kTile * (3 * kRow + 2 * kBRow);  // a stage of the ring
+  static constexpr int kWarpBytes = 2 * kRaw + 2 * kTile * N * 4;
+  static constexpr int kWarps = long_warps(N);
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
+};
 
 template <typename T, int N>
-__global__ void __launch_bounds__(8 * N) scan_long_kernel(const ScanArgs p) {
-  constexpr int LPC = N / 4;                  // lanes of a channel
-  constexpr int kThreads = kScanChannels * LPC;
-  constexpr int kItems = kScanTile * 4;       // (token, 8 channels) of a tile
-  constexpr int kPer = (kItems + kThreads - 1) / kThreads;
-  constexpr int kYs = kScanChannels + (LPC <= 4 ? 32 / LPC : 4);  // a warp's stores spread over the banks
-  __shared__ __align__(16) float2 dd[kScanTile][kScanChannels];
-  __shared__ __align__(16) float bc[2][kScanTile][N];
-  __shared__ __align__(16) float ys[kScanTile][kYs];
+struct LongScan {
+  using C = LongCfg<N>;
+  const ScanArgs& p;
+  unsigned char* ring;
+  float* bc;          // [2][kTile][N] fp32
+  int lane, cl, sub;  // cl: first of the lane's two channels in the warp's
+  int32_t cb, end, group;  // the warp's channels (up to the group's end)
+  float bias[2], skip[2];
+  f32x2 a[2][C::NS / 2], h[2][C::NS / 2];
+  float sum[2];
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t cb = blockIdx.x % p.blocks * kScanChannels;
-  const int sub = lane % LPC, cl = (warp * 32 + lane) / LPC;  // states 4 sub.., channel of the block
-  const int32_t c = cb + cl;
-  const bool live = c < p.channels;
-  const int32_t group = cb / p.per_group;
-
-  f32x2 a01 = 0, a23 = 0;
-  if (live) {
-    const float4 a = *reinterpret_cast<const float4*>(p.A + static_cast<int64_t>(c) * N + 4 * sub);
-    a01 = pack2(a.x * kLog2e, a.y * kLog2e);
-    a23 = pack2(a.z * kLog2e, a.w * kLog2e);
+  __device__ __forceinline__ void block(int32_t b) {
+    const int32_t per = (p.per_group + C::CPW - 1) / C::CPW;  // blocks of a group
+    group = b / per;
+    end = (group + 1) * p.per_group;
+    cb = group * p.per_group + (b - group * per) * C::CPW;
   }
-  // this thread's part of a tile: up to kPer (token, 8 channels) items and one
-  // vector of B or C
-  const int it_row = tid / 4, it_ch = (tid & 3) * 8;  // item i: row it_row + i * kThreads / 4
-  const bool it_live = tid < kItems && cb + it_ch < p.channels;
-  const int bc_which = tid / (4 * N), bc_row = tid % (4 * N) / (N / 8), bc_n = tid % (N / 8) * 8;
-  const T* bc_src = static_cast<const T*>(bc_which ? p.C : p.B) + group * N + bc_n;
-  const int64_t bc_ld = bc_which ? p.ldc : p.ldb;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-
-  for (int32_t s = blockIdx.x / p.blocks; s < p.g.S; s += p.split) {
-    const Segment seg = read_segment(p.g, s);
-    const int32_t len = seg.q1 - seg.q0;
-    if (seg.id < 0 || len <= p.short_max) continue;
-    float* st = p.state + (static_cast<int64_t>(seg.id) * p.channels + c) * N + 4 * sub;
-    f32x2 h01 = 0, h23 = 0;
-    if (live && seg.old) {
-      const float4 v = *reinterpret_cast<const float4*>(st);
-      h01 = pack2(v.x, v.y);
-      h23 = pack2(v.z, v.w);
+  __device__ __forceinline__ void weights() {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t c = min(cb + cl + e, p.channels - 1);
+#pragma unroll
+      for (int n = 0; n < C::NS / 4; ++n) {
+        const float4 v = *reinterpret_cast<const float4*>(p.A + c * N + sub * C::NS + 4 * n);
+        a[e][2 * n] = pack2(v.x * kLog2e, v.y * kLog2e);
+        a[e][2 * n + 1] = pack2(v.z * kLog2e, v.w * kLog2e);
+      }
+      bias[e] = p.dt_bias ? p.dt_bias[c] : 0.f;
+      skip[e] = p.D ? p.D[c] : 0.f;
     }
-    uint4 rx[kPer], rd[kPer], rz[kPer], rb;
-    auto load = [&](int32_t t0) {
-      const int32_t left = seg.q1 - t0;
+  }
+  // Rows of `bytes` bytes of tokens t0 .. t0 + nt - 1 into a ring stage.
+  template <int kBytes>
+  __device__ __forceinline__ void copy_rows(unsigned char* to, const T* from, int64_t ld, int nt,
+                                            int32_t limit) {
+    constexpr int kPieces = kBytes / 16, kAll = kTile * kPieces;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int row = it_row + i * (kThreads / 4);
-        const bool on = it_live && row < left;
-        const int64_t t = t0 + row;
-        const int64_t ch = cb + it_ch;
-        rx[i] = on ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + t * p.ldx + ch) : zero;
-        rd[i] = on ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.dt) + t * p.lddt + ch) : zero;
-        rz[i] = on && p.z ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.z) + t * p.ldz + ch)
-                          : zero;
-      }
-      rb = bc_row < left ? *reinterpret_cast<const uint4*>(bc_src + (t0 + bc_row) * bc_ld) : zero;
-    };
-    load(seg.q0);
-    for (int32_t t0 = seg.q0; t0 < seg.q1; t0 += kScanTile) {
-      const int32_t nt = min(kScanTile, seg.q1 - t0);
-      uint4 cx[kPer], cz[kPer];
+    for (int i = 0; i < (kAll + 31) / 32; ++i) {
+      const int k = lane + 32 * i, row = k / kPieces, piece = k % kPieces;
+      if ((kAll % 32 == 0 || k < kAll) && row < nt && piece * 8 < limit)
+        copy_async<16>(to + 16 * k, from + row * ld + piece * 8);
+    }
+  }
+  template <bool kAll>
+  __device__ __forceinline__ void request(int32_t t0, int32_t t1, int stage) {
+    const int nt = min(kTile, t1 - t0);
+    unsigned char* to = ring + stage * C::kRaw;
+    if (nt > 0) {
+      const int64_t t = t0;
+      const int32_t limit = end - cb;  // channels come in eights
+      copy_rows<C::kRow>(to, static_cast<const T*>(p.x) + t * p.ldx + cb, p.ldx, nt, limit);
+      copy_rows<C::kRow>(to + kTile * C::kRow, static_cast<const T*>(p.dt) + t * p.lddt + cb, p.lddt, nt, limit);
+      if (kAll && p.z)
+        copy_rows<C::kRow>(to + 2 * kTile * C::kRow, static_cast<const T*>(p.z) + t * p.ldz + cb, p.ldz, nt,
+                           limit);
+      unsigned char* tb = to + 3 * kTile * C::kRow;
+      copy_rows<C::kBRow>(tb, static_cast<const T*>(p.B) + t * p.ldb + group * N, p.ldb, nt, N);
+      if (kAll)
+        copy_rows<C::kBRow>(tb + kTile * C::kBRow, static_cast<const T*>(p.C) + t * p.ldc + group * N, p.ldc,
+                            nt, N);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ static void pair(const unsigned char* at, float& u, float& v) {
+    float f[4];
+    unpack4<T>(make_uint2(*reinterpret_cast<const uint32_t*>(at), 0u), f);
+    u = f[0];
+    v = f[1];
+  }
+  // (d, d x) of the lane's channels at a token of the stage
+  struct Token {
+    float d[2], x[2];
+  };
+  __device__ __forceinline__ Token token(const unsigned char* raw, int r) const {
+    Token k;
+    pair(raw + r * C::kRow + 2 * cl, k.x[0], k.x[1]);
+    pair(raw + kTile * C::kRow + r * C::kRow + 2 * cl, k.d[0], k.d[1]);
+    k.d[0] += bias[0];
+    k.d[1] += bias[1];
+    if (p.softplus) softplus2(k.d[0], k.d[1]);
+    return k;
+  }
+  // Tokens [t0, t1), whose first tile is requested, from the state in h.  kAll
+  // false: only the state and the sums of d.
+  template <bool kAll>
+  __device__ __forceinline__ void run(int32_t t0, int32_t t1) {
+    int stage = 0;
+    for (; t0 < t1; t0 += kTile, stage ^= 1) {
+      __syncwarp();  // the stage before this one is done with
+      request<kAll>(t0 + kTile, t1, stage ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      const int nt = min(kTile, t1 - t0);
+      const unsigned char* raw = ring + stage * C::kRaw;
+      // B and C as fp32 (what stands behind the last token is not used)
+      constexpr int kVecs = 2 * kTile * N / 8;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int row = it_row + i * (kThreads / 4);
-        cx[i] = rx[i];
-        cz[i] = rz[i];
-        if (tid < kItems && row < ((nt + LPC - 1) & ~(LPC - 1))) {
-          float x[8], d[8];
-          unpack8<T>(rx[i], x);
-          unpack8<T>(rd[i], d);
-          float4* to = reinterpret_cast<float4*>(&dd[row][it_ch]);
-          const bool on = it_live && row < nt;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (p.dt_bias && on) d[e] += p.dt_bias[cb + it_ch + e];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; e += 2)
-            if (p.softplus) softplus2(d[e], d[e + 1]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (!on) d[e] = 0.f;  // h stays: exp(0) h + 0
-            x[e] *= d[e];
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[e] = make_float4(d[2 * e], x[2 * e], d[2 * e + 1], x[2 * e + 1]);
-        }
-      }
-      {
+      for (int i = 0; i < (kVecs + 31) / 32; ++i) {
+        const int k = lane + 32 * i;
+        if (k >= (kAll ? kVecs : kVecs / 2)) continue;
         float f[8];
-        unpack8<T>(rb, f);
-        float4* to = reinterpret_cast<float4*>(&bc[bc_which][bc_row][bc_n]);
+        unpack8<T>(*reinterpret_cast<const uint4*>(raw + 3 * kTile * C::kRow + 16 * k), f);
+        float4* to = reinterpret_cast<float4*>(bc + 8 * k);
         to[0] = make_float4(f[0], f[1], f[2], f[3]);
         to[1] = make_float4(f[4], f[5], f[6], f[7]);
       }
-      __syncthreads();
-      if (t0 + kScanTile < seg.q1) load(t0 + kScanTile);
-      for (int r0 = 0; r0 < nt; r0 += LPC) {
-        float y[LPC];
+      __syncwarp();
+      T* out = static_cast<T*>(p.out) + t0 * p.ldo + cb + cl;
+      const ulonglong2* __restrict__ Bt = reinterpret_cast<const ulonglong2*>(bc + sub * C::NS);
+      const ulonglong2* __restrict__ Ct = Bt + kTile * N / 4;
+      Token cur = token(raw, 0);
+#pragma unroll 2
+      for (int r = 0; r < nt; ++r) {
+        const Token nxt = token(raw, min(r + 1, nt - 1));
+        float z0 = 0.f, z1 = 0.f;
+        if (kAll && p.z) pair(raw + 2 * kTile * C::kRow + r * C::kRow + 2 * cl, z0, z1);
+        f32x2 d[2], dx[2], y[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < LPC; ++i) {
-          const float2 d = dd[r0 + i][cl];
-          const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&bc[0][r0 + i][4 * sub]);
-          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&bc[1][r0 + i][4 * sub]);
-          const f32x2 dx = pack2(d.x, d.x), dy = pack2(d.y, d.y);
-          float e0, e1, e2, e3;
-          unpack2(mul2(dx, a01), e0, e1);
-          unpack2(mul2(dx, a23), e2, e3);
-          h01 = fma2(pack2(ex2(e0), ex2(e1)), h01, mul2(dy, b.x));
-          h23 = fma2(pack2(ex2(e2), ex2(e3)), h23, mul2(dy, b.y));
-          float y0, y1;
-          unpack2(fma2(h01, q.x, mul2(h23, q.y)), y0, y1);
-          y[i] = y0 + y1;
+        for (int e = 0; e < 2; ++e) {
+          const float v = cur.d[e] * cur.x[e];
+          d[e] = pack2(cur.d[e], cur.d[e]);
+          dx[e] = pack2(v, v);
+          if (!kAll) sum[e] += cur.d[e];
         }
-        // lane bit k halves the tokens: the lane is left with the sum of one
-        int row = r0;
 #pragma unroll
-        for (int w = LPC / 2, bit = 1; w >= 1; w >>= 1, bit <<= 1) {
-          const bool up = lane & bit;
+        for (int n = 0; n < C::NS / 4; ++n) {
+          const ulonglong2 b = Bt[r * (N / 4) + n];
 #pragma unroll
-          for (int i = 0; i < w; ++i) {
-            const float give = up ? y[i] : y[i + w], keep = up ? y[i + w] : y[i];
-            y[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+          for (int e = 0; e < 2; ++e) {
+            h[e][2 * n] = fma2(ex2x2(mul2(d[e], a[e][2 * n])), h[e][2 * n], mul2(dx[e], b.x));
+            h[e][2 * n + 1] = fma2(ex2x2(mul2(d[e], a[e][2 * n + 1])), h[e][2 * n + 1], mul2(dx[e], b.y));
           }
-          if (up) row += w;
-        }
-        ys[row][cl] = y[0];
-      }
-      __syncthreads();
+          if (kAll) {
+            const ulonglong2 q = Ct[r * (N / 4) + n];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int row = it_row + i * (kThreads / 4);
-        if (!it_live || row >= nt) continue;
-        float x[8], z[8], y[8];
-        unpack8<T>(cx[i], x);
-        unpack8<T>(cz[i], z);
-        const float4 lo = *reinterpret_cast<const float4*>(&ys[row][it_ch]);
-        const float4 hi = *reinterpret_cast<const float4*>(&ys[row][it_ch + 4]);
-        y[0] = lo.x, y[1] = lo.y, y[2] = lo.z, y[3] = lo.w;
-        y[4] = hi.x, y[5] = hi.y, y[6] = hi.z, y[7] = hi.w;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (p.D) y[e] = fmaf(p.D[cb + it_ch + e], x[e], y[e]);
-          if (p.z) y[e] *= silu(z[e]);
+            for (int e = 0; e < 2; ++e) {
+              y[e] = n ? fma2(h[e][2 * n], q.x, y[e]) : mul2(h[e][0], q.x);
+              y[e] = fma2(h[e][2 * n + 1], q.y, y[e]);
+            }
+          }
         }
-        *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (t0 + row) * p.ldo + cb + it_ch) = pack8<T>(y);
+        if (kAll) {
+          float s[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float u, v;
+            unpack2(y[e], u, v);
+            s[e] = u + v;
+          }
+          if constexpr (C::LPC > 1) {
+#pragma unroll
+            for (int o = 1; o < C::LPC; o <<= 1)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) s[e] += __shfl_xor_sync(0xffffffffu, s[e], o);
+          }
+          s[0] = fmaf(skip[0], cur.x[0], s[0]);
+          s[1] = fmaf(skip[1], cur.x[1], s[1]);
+          if (p.z) {
+            s[0] *= silu(z0);
+            s[1] *= silu(z1);
+          }
+          if (sub == 0 && cb + cl < end) {
+            const float f[4] = {s[0], s[1], 0.f, 0.f};
+            *reinterpret_cast<uint32_t*>(out + r * p.ldo) = pack4<T>(f).x;
+          }
+        }
+        cur = nxt;
       }
     }
-    if (live) {
-      float4 v;
-      unpack2(h01, v.x, v.y);
-      unpack2(h23, v.z, v.w);
-      *reinterpret_cast<float4*>(st) = v;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();  // the ring is done with
+  }
+  // h <-> memory [channels, N] at `base`
+  __device__ __forceinline__ void read(const float* base) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const ulonglong2* at = reinterpret_cast<const ulonglong2*>(
+          base + static_cast<int64_t>(min(cb + cl + e, p.channels - 1)) * N + sub * C::NS);
+#pragma unroll
+      for (int n = 0; n < C::NS / 4; ++n) {
+        const ulonglong2 v = at[n];
+        h[e][2 * n] = v.x;
+        h[e][2 * n + 1] = v.y;
+      }
     }
   }
+  __device__ __forceinline__ void write(float* base) const {
+    if (cb + cl >= end) return;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      ulonglong2* at =
+          reinterpret_cast<ulonglong2*>(base + static_cast<int64_t>(cb + cl + e) * N + sub * C::NS);
+#pragma unroll
+      for (int n = 0; n < C::NS / 4; ++n) at[n] = make_ulonglong2(h[e][2 * n], h[e][2 * n + 1]);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int n = 0; n < C::NS / 2; ++n) h[e][n] = 0;
+  }
+  // the state after a piece that ended with `e` from zero and whose d sum up to `s`
+  __device__ __forceinline__ void carry(const float* ends, const float* sums) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t c = min(cb + cl + e, p.channels - 1);
+      const ulonglong2* at = reinterpret_cast<const ulonglong2*>(ends + c * N + sub * C::NS);
+      const float s = sums[c];
+      const f32x2 s2 = pack2(s, s);
+#pragma unroll
+      for (int n = 0; n < C::NS / 4; ++n) {
+        const ulonglong2 v = at[n];
+        h[e][2 * n] = fma2(ex2x2(mul2(s2, a[e][2 * n])), h[e][2 * n], v.x);
+        h[e][2 * n + 1] = fma2(ex2x2(mul2(s2, a[e][2 * n + 1])), h[e][2 * n + 1], v.y);
+      }
+    }
+  }
+};
+
+// kFirst: whole segments, pieces 0, and what the pieces in between leave; else
+// pieces 1 and up.  p.carries: sums [slots, channels] and end states [slots,
+// channels, N] of the pieces that another follows; p.counter: what the second
+// launch takes its tasks from (the first deals them in turn).
+template <typename T, int N, bool kFirst>
+__global__ void __launch_bounds__(32 * long_warps(N), 1) scan_long_kernel(const ScanArgs p) {
+  using C = LongCfg<N>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned char* mine = smem + warp * C::kWarpBytes;
+  LongScan<T, N> w{p, mine, reinterpret_cast<float*>(mine + 2 * C::kRaw)};
+  w.lane = lane;
+  w.sub = lane % C::LPC;
+  w.cl = lane / C::LPC * 2;
+  float* const sums = p.carries;
+  float* const ends = p.carries + static_cast<int64_t>(p.slots) * p.channels;
+  const int64_t state = static_cast<int64_t>(p.channels) * N;
+  if (kFirst && p.counter && blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;
+
+  // dealt over the CTAs first: neighbouring tasks (pieces of one length) on
+  // different SMs
+  int32_t task = blockIdx.x + warp * gridDim.x;
+  // 32 segments from s0 on, in the lanes: pieces of each; tasks and slots before
+  int32_t s0 = 0, base = 0, slot0 = 0;
+  Segment m;
+  int32_t k = 0, tasks = 0, incl = 0, slots_incl = 0;
+  auto chunk = [&]() {
+    m = {0, 0, -1, 0};
+    if (s0 + lane < p.g.S) m = read_segment(p.g, s0 + lane);
+    const int32_t len = m.q1 - m.q0;
+    k = m.id < 0 || len <= p.short_max ? 0 : p.piece > 0 ? (len + p.piece - 1) / p.piece : 1;
+    slots_incl = k > 1 ? k - 1 : 0;
+    tasks = incl = kFirst && k == 1 ? 1 : slots_incl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, slots_incl, o);
+      if (lane >= o) incl += u, slots_incl += v;
+    }
+  };
+  chunk();
+  while (true) {
+    const int32_t at = task / p.blocks;
+    while (at >= base + __shfl_sync(0xffffffffu, incl, 31)) {
+      base += __shfl_sync(0xffffffffu, incl, 31);
+      slot0 += __shfl_sync(0xffffffffu, slots_incl, 31);
+      s0 += 32;
+      if (s0 >= p.g.S) return;
+      chunk();
+    }
+    const int from = __ffs(__ballot_sync(0xffffffffu, base + incl > at)) - 1;
+    Segment s;
+    s.q0 = __shfl_sync(0xffffffffu, m.q0, from);
+    s.q1 = __shfl_sync(0xffffffffu, m.q1, from);
+    s.id = __shfl_sync(0xffffffffu, m.id, from);
+    s.old = __shfl_sync(0xffffffffu, m.old, from);
+    const int32_t pieces = __shfl_sync(0xffffffffu, k, from);
+    const int32_t i = at - (base + __shfl_sync(0xffffffffu, incl - tasks, from)) + (kFirst ? 0 : 1);
+    const int32_t slot = slot0 + __shfl_sync(0xffffffffu, slots_incl, from) - (pieces - 1);  // of piece 0
+    const int32_t len = s.q1 - s.q0;
+    const int32_t size = ((len + pieces - 1) / pieces + kTile - 1) / kTile * kTile;
+    const int32_t t0 = min(s.q1, s.q0 + i * size), t1 = min(s.q1, t0 + size);
+    const int32_t now = task;
+    if (kFirst) {
+      task += gridDim.x * C::kWarps;
+    } else {
+      int32_t next = 0;
+      if (lane == 0) next = atomicAdd(p.counter, 1);
+      task = gridDim.x * C::kWarps + __shfl_sync(0xffffffffu, next, 0);
+    }
+    // overlapping segments (reported) could ask for more slots than there are
+    if (pieces > 1 && slot + pieces - 1 > p.slots) continue;
+    w.block(now % p.blocks);
+    float* st = p.state + s.id * state;
+    const bool carry = kFirst && i > 0;
+    // the first tile is on its way while the weights and the start are read
+    if (carry) w.template request<false>(t0, t1, 0);
+    else w.template request<true>(t0, t1, 0);
+    w.weights();
+    if (carry) {
+      w.clear();
+      w.sum[0] = w.sum[1] = 0.f;
+      w.template run<false>(t0, t1);
+      if (w.sub == 0 && w.cb + w.cl < w.end)
+        *reinterpret_cast<float2*>(sums + static_cast<int64_t>(slot + i) * p.channels + w.cb + w.cl) =
+            make_float2(w.sum[0], w.sum[1]);
+    } else {
+      if (!kFirst) {
+        w.read(ends + slot * state);
+#pragma unroll 2
+        for (int32_t j = 1; j < i; ++j)
+          w.carry(ends + (slot + j) * state, sums + static_cast<int64_t>(slot + j) * p.channels);
+      } else if (s.old) {
+        w.read(st);
+      } else {
+        w.clear();
+      }
+      w.template run<true>(t0, t1);
+    }
+    w.write(i == pieces - 1 ? st : ends + (slot + i) * state);
+  }
+}
+
+// How a scan is cut: tokens of a piece, slots for the pieces that another follows.
+struct ScanCut {
+  int32_t piece, slots;
+  size_t bytes;  // of workspace: the counter, the sums, the end states
+};
+ScanCut scan_cut(const mcp_scan_desc& d, int sms) {
+  // a warp slot's share of the work, in tokens; pieces a little longer (the two
+  // launches need not be perfectly full), not below 4 tiles
+  const int ns = d.state_size < 16 ? d.state_size : 16, cpw = 64 / (d.state_size / ns);
+  const int64_t per_group = d.channels / d.num_groups;
+  const int64_t blocks = d.num_groups * ((per_group + cpw - 1) / cpw), slots = static_cast<int64_t>(sms) * long_warps(d.state_size);
+  const int64_t share = (d.total_tokens * blocks * kCutTenths + 10 * slots - 1) / (10 * slots);
+  int64_t piece = (share + kTile - 1) / kTile * kTile;
+  if (piece < 4 * kTile) piece = 4 * kTile;
+  ScanCut c = {0, 0, 0};
+  if (d.total_tokens <= piece || d.total_tokens <= d.num_seqs) return c;
+  c.piece = static_cast<int32_t>(piece);
+  c.slots = static_cast<int32_t>(d.total_tokens / piece);
+  c.bytes = 256 + static_cast<size_t>(c.slots) * d.channels * (d.state_size + 1) * sizeof(float);
+  return c;
 }
 
 template <typename T, int N>
 int scan_launch(ScanArgs a, cudaStream_t st) {
+  using C = LongCfg<N>;
   const int sms = a.g.sms;
   const bool any_long = a.g.T > kShortTokens && a.g.T > a.g.S;
   if (any_long) {
     ScanArgs l = a;
     l.short_max = kShortTokens;
-    l.blocks = (a.channels + kScanChannels - 1) / kScanChannels;
-    // a CTA for every long segment there can be, up to what fills the SMs
+    l.blocks = a.channels / a.per_group * ((a.per_group + C::CPW - 1) / C::CPW);
+    // one CTA an SM stays; fewer where there cannot be as many tasks
     const int64_t longs = a.g.T / (kShortTokens + 1) < a.g.S ? a.g.T / (kShortTokens + 1) : a.g.S;
-    const int64_t want = (32LL * sms + l.blocks - 1) / l.blocks;
-    l.split = static_cast<int32_t>(want < longs ? want : longs);
-    const int64_t grid = static_cast<int64_t>(l.blocks) * l.split;
-    scan_long_kernel<T, N><<<static_cast<unsigned>(grid), 8 * N, 0, st>>>(l);
+    const int64_t tasks = (longs + a.slots) * l.blocks;
+    const int64_t ctas = (tasks + C::kWarps - 1) / C::kWarps;
+    const unsigned grid = static_cast<unsigned>(ctas < sms ? ctas : sms);
+    if (const int e = allow_smem<scan_long_kernel<T, N, true>>(C::kSmem)) return e;
+    if (const int e = allow_smem<scan_long_kernel<T, N, false>>(C::kSmem)) return e;
+    scan_long_kernel<T, N, true><<<grid, 32 * C::kWarps, C::kSmem, st>>>(l);
+    if (l.piece > 0) scan_long_kernel<T, N, false><<<grid, 32 * C::kWarps, C::kSmem, st>>>(l);
     const cudaError_t f = cudaGetLastError();
     if (f != cudaSuccess) return static_cast<int>(f);
   }
@@ -875,6 +1104,7 @@ int scan_launch(ScanArgs a, cudaStream_t st) {
   a.short_max = any_long ? kShortTokens : 0x7fffffff;
   constexpr int per = ShortCfg<N>::CPW;
   a.blocks = (a.channels + per - 1) / per;
+  // more warps than stay at once: a warp's last segments end unevenly
   const int64_t want = (64LL * sms + a.blocks - 1) / a.blocks;
   a.split = static_cast<int32_t>(want < a.g.S ? want : a.g.S);
   const int64_t warps = static_cast<int64_t>(a.blocks) * a.split;
@@ -923,10 +1153,13 @@ int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight,
                                    : conv_width<__half>(a, d.width, grid, st);
 }
 
+size_t mixed_scan_workspace(const mcp_scan_desc& d, int sms) { return scan_cut(d, sms).bytes; }
+
 int launch_mixed_scan(const mcp_scan_desc& d, const mcp_scan_tensors& t,
                       const int32_t* request_ids, const int32_t* cu_seqlens_q,
-                      const int32_t* seqlens_k, int32_t* error_word, void* stream) {
-  ScanArgs a;
+                      const int32_t* seqlens_k, void* workspace, int32_t* error_word,
+                      void* stream) {
+  ScanArgs a = {};
   a.g = {request_ids, cu_seqlens_q, seqlens_k, d.num_seqs, d.total_tokens, d.num_requests, error_word,
          step_num_sms()};
   a.x = t.x;
@@ -948,6 +1181,13 @@ int launch_mixed_scan(const mcp_scan_desc& d, const mcp_scan_tensors& t,
   a.channels = d.channels;
   a.per_group = d.channels / d.num_groups;
   a.softplus = d.softplus;
+  const ScanCut cut = scan_cut(d, step_num_sms());
+  if (workspace && cut.piece > 0) {
+    a.piece = cut.piece;
+    a.slots = cut.slots;
+    a.counter = static_cast<int32_t*>(workspace);
+    a.carries = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return d.dtype == MCP_DTYPE_BF16 ? scan_states<__nv_bfloat16>(a, d.state_size, st)
                                    : scan_states<__half>(a, d.state_size, st);

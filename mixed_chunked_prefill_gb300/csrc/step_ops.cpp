@@ -28,6 +28,12 @@ mcp_status done(int e, const char* what) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+#define MCP_TRY(expr)                    \
+  do {                                   \
+    const mcp_status st_ = (expr);       \
+    if (st_ != MCP_OK) return st_;       \
+  } while (0)
+
 mcp_status check_pool(const mcp_request_pool* p, int32_t num_seqs, const int32_t* ids,
                       const int32_t* q_lens) {
   if (!p) return fail(MCP_ERR_INVALID_ARG, "pool is NULL");
@@ -53,9 +59,8 @@ mcp_status check_pool(const mcp_request_pool* p, int32_t num_seqs, const int32_t
   return MCP_OK;
 }
 
-mcp_status check_stream_meta(int32_t num_seqs, int32_t tokens, int32_t requests, int32_t channels,
-                             int32_t dtype, const int32_t* ids, const int32_t* cu,
-                             const int32_t* sk) {
+mcp_status check_stream_sizes(int32_t num_seqs, int32_t tokens, int32_t requests, int32_t channels,
+                              int32_t dtype) {
   if (num_seqs < 0 || tokens < 0)
     return fail(MCP_ERR_INVALID_ARG, "num_seqs %d / total_tokens %d < 0", num_seqs, tokens);
   if (requests <= 0 || channels <= 0)
@@ -65,7 +70,6 @@ mcp_status check_stream_meta(int32_t num_seqs, int32_t tokens, int32_t requests,
     return fail(MCP_ERR_INVALID_ARG, "channels %d is not a multiple of 8", channels);
   if (dtype != MCP_DTYPE_BF16 && dtype != MCP_DTYPE_FP16)
     return fail(MCP_ERR_UNSUPPORTED, "dtype %d (built: bf16, fp16)", dtype);
-  if (num_seqs > 0 && (!ids || !cu || !sk)) return fail(MCP_ERR_INVALID_ARG, "NULL metadata pointer");
   return MCP_OK;
 }
 
@@ -79,11 +83,21 @@ mcp_status check_rows(const void* t, int64_t stride, int64_t row, const char* na
   return MCP_OK;
 }
 
-#define MCP_TRY(expr)                    \
-  do {                                   \
-    const mcp_status st_ = (expr);       \
-    if (st_ != MCP_OK) return st_;       \
-  } while (0)
+mcp_status check_scan_desc(const mcp_scan_desc* d) {
+  if (!d) return fail(MCP_ERR_INVALID_ARG, "desc is NULL");
+  MCP_TRY(check_stream_sizes(d->num_seqs, d->total_tokens, d->num_requests, d->channels, d->dtype));
+  if (d->state_size != 8 && d->state_size != 16 && d->state_size != 32 && d->state_size != 64)
+    return fail(MCP_ERR_UNSUPPORTED, "state_size %d (built: 8, 16, 32, 64)", d->state_size);
+  if (d->num_groups <= 0 || d->channels % d->num_groups != 0)
+    return fail(MCP_ERR_INVALID_ARG, "num_groups %d does not divide channels %d", d->num_groups,
+                d->channels);
+  if (d->num_groups > 1 && d->channels / d->num_groups % 32 != 0)
+    return fail(MCP_ERR_UNSUPPORTED, "%d channels a group (built: multiples of 32)",
+                d->channels / d->num_groups);
+  if (d->softplus != 0 && d->softplus != 1)
+    return fail(MCP_ERR_INVALID_ARG, "softplus %d (0 or 1)", d->softplus);
+  return MCP_OK;
+}
 
 }  // namespace
 
@@ -122,8 +136,9 @@ mcp_status mcp_mixed_conv(const mcp_conv_desc* d, const void* x, const void* wei
                           const int32_t* cu_seqlens_q, const int32_t* seqlens_k, void* out,
                           int32_t* error_word, void* stream) {
   if (!d) return fail(MCP_ERR_INVALID_ARG, "desc is NULL");
-  MCP_TRY(check_stream_meta(d->num_seqs, d->total_tokens, d->num_requests, d->channels, d->dtype,
-                            request_ids, cu_seqlens_q, seqlens_k));
+  MCP_TRY(check_stream_sizes(d->num_seqs, d->total_tokens, d->num_requests, d->channels, d->dtype));
+  if (d->num_seqs > 0 && (!request_ids || !cu_seqlens_q || !seqlens_k))
+    return fail(MCP_ERR_INVALID_ARG, "NULL metadata pointer");
   if (d->width < 2 || d->width > 4)
     return fail(MCP_ERR_UNSUPPORTED, "width %d (built: 2, 3, 4)", d->width);
   if (d->activation != 0 && d->activation != 1)
@@ -140,22 +155,21 @@ mcp_status mcp_mixed_conv(const mcp_conv_desc* d, const void* x, const void* wei
               "mixed_conv launch");
 }
 
+mcp_status mcp_mixed_scan_workspace(const mcp_scan_desc* d, size_t* workspace_bytes) {
+  if (!workspace_bytes) return fail(MCP_ERR_INVALID_ARG, "workspace_bytes is NULL");
+  MCP_TRY(check_scan_desc(d));
+  *workspace_bytes = mcp::mixed_scan_workspace(*d, mcp::step_num_sms());
+  return done(0, "");
+}
+
 mcp_status mcp_mixed_scan(const mcp_scan_desc* d, const mcp_scan_tensors* t,
                           const int32_t* request_ids, const int32_t* cu_seqlens_q,
-                          const int32_t* seqlens_k, int32_t* error_word, void* stream) {
-  if (!d || !t) return fail(MCP_ERR_INVALID_ARG, "desc or tensors is NULL");
-  MCP_TRY(check_stream_meta(d->num_seqs, d->total_tokens, d->num_requests, d->channels, d->dtype,
-                            request_ids, cu_seqlens_q, seqlens_k));
-  if (d->state_size != 8 && d->state_size != 16 && d->state_size != 32 && d->state_size != 64)
-    return fail(MCP_ERR_UNSUPPORTED, "state_size %d (built: 8, 16, 32, 64)", d->state_size);
-  if (d->num_groups <= 0 || d->channels % d->num_groups != 0)
-    return fail(MCP_ERR_INVALID_ARG, "num_groups %d does not divide channels %d", d->num_groups,
-                d->channels);
-  if (d->num_groups > 1 && d->channels / d->num_groups % 32 != 0)
-    return fail(MCP_ERR_UNSUPPORTED, "%d channels a group (built: multiples of 32)",
-                d->channels / d->num_groups);
-  if (d->softplus != 0 && d->softplus != 1)
-    return fail(MCP_ERR_INVALID_ARG, "softplus %d (0 or 1)", d->softplus);
+                          const int32_t* seqlens_k, void* workspace, size_t workspace_bytes,
+                          int32_t* error_word, void* stream) {
+  MCP_TRY(check_scan_desc(d));
+  if (!t) return fail(MCP_ERR_INVALID_ARG, "tensors is NULL");
+  if (d->num_seqs > 0 && (!request_ids || !cu_seqlens_q || !seqlens_k))
+    return fail(MCP_ERR_INVALID_ARG, "NULL metadata pointer");
   if (d->num_seqs == 0 || d->total_tokens == 0) return done(0, "");
   const int64_t gn = static_cast<int64_t>(d->num_groups) * d->state_size;
   MCP_TRY(check_rows(t->x, d->x_stride, d->channels, "x"));
@@ -167,7 +181,14 @@ mcp_status mcp_mixed_scan(const mcp_scan_desc* d, const mcp_scan_tensors* t,
   if (!t->A || !t->state) return fail(MCP_ERR_INVALID_ARG, "NULL tensor pointer");
   if (!aligned(t->A, 16) || !aligned(t->state, 16) || !aligned(t->D, 16) || !aligned(t->dt_bias, 16))
     return fail(MCP_ERR_INVALID_ARG, "A, D, dt_bias and state must be 16-byte aligned");
-  return done(mcp::launch_mixed_scan(*d, *t, request_ids, cu_seqlens_q, seqlens_k, error_word, stream),
+  if (workspace) {
+    if (!aligned(workspace, 256)) return fail(MCP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    const size_t need = mcp::mixed_scan_workspace(*d, mcp::step_num_sms());
+    if (workspace_bytes < need)
+      return fail(MCP_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", workspace_bytes, need);
+  }
+  return done(mcp::launch_mixed_scan(*d, *t, request_ids, cu_seqlens_q, seqlens_k, workspace,
+                                     error_word, stream),
               "mixed_scan launch");
 }
 

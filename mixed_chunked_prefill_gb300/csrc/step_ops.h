@@ -28,7 +28,9 @@ int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight,
                       const int32_t* seqlens_k, void* out, int32_t* error_word, void* stream);
 int launch_mixed_scan(const mcp_scan_desc& d, const mcp_scan_tensors& t,
                       const int32_t* request_ids, const int32_t* cu_seqlens_q,
-                      const int32_t* seqlens_k, int32_t* error_word, void* stream);
+                      const int32_t* seqlens_k, void* workspace, int32_t* error_word,
+                      void* stream);
+size_t mixed_scan_workspace(const mcp_scan_desc& d, int sms);  // bytes; 0: none is of use
 // logits.cu
 int launch_update_token_counts(const int32_t* request_ids, int32_t num_rows,
                                const int32_t* tokens, int32_t num_tokens,

@@ -91,7 +91,7 @@ def test_mixed_conv_refusals(lib, over, status):
     assert conv(lib, **over) == status
 
 
-def scan(lib, meta=(P16, P16, P16), tensors=(), **over):
+def scan(lib, meta=(P16, P16, P16), tensors=(), workspace=(None, 0), **over):
     f = dict(num_seqs=3, total_tokens=10, num_requests=4, channels=64, state_size=16, num_groups=1,
              dtype=0, softplus=1, x_stride=64, dt_stride=64, z_stride=64, b_stride=16, c_stride=16,
              out_stride=64)
@@ -100,7 +100,7 @@ def scan(lib, meta=(P16, P16, P16), tensors=(), **over):
     a = {n: P16 for n, _ in _capi.ScanTensors._fields_}
     a.update(tensors)
     t = _capi.ScanTensors(*(a[n] for n, _ in _capi.ScanTensors._fields_))
-    return lib.mcp_mixed_scan(ctypes.byref(d), ctypes.byref(t), *meta, None, None)
+    return lib.mcp_mixed_scan(ctypes.byref(d), ctypes.byref(t), *meta, *workspace, None, None)
 
 
 @pytest.mark.parametrize("over,status", [
@@ -113,6 +113,9 @@ def scan(lib, meta=(P16, P16, P16), tensors=(), **over):
     *[(dict(tensors={n: None}), INVALID) for n in ("x", "dt", "A", "B", "C", "state", "out")],
     *[(dict(tensors={n: P16 + 8}), INVALID) for n in
       ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "state", "out")],
+    (dict(workspace=(P16 + 128, 1 << 40)), INVALID),
+    (dict(total_tokens=100000, channels=8192, x_stride=8192, dt_stride=8192, z_stride=8192,
+          out_stride=8192, workspace=(P16, 256)), _capi.MCP_ERR_WORKSPACE_TOO_SMALL),
     (dict(num_seqs=0), OK), (dict(total_tokens=0), OK),
 ])
 def test_mixed_scan_refusals(lib, over, status):
