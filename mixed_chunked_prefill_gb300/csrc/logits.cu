@@ -340,13 +340,17 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
   __syncthreads();
 
   // from here plane 0 has the tokens that a bias or penalty changes: seen or
-  // biased, and allowed; the counts of the sampled ones are on their way to L2
+  // biased, and allowed, without those of the neighbouring parts in a shifted
+  // row's first and last word; the counts of the sampled ones are on their way to L2
   for (int i = threadIdx.x; i < nwords; i += kLogitThreads) {
-    uint32_t had = plane[kPlane + i];
-    plane[i] = (plane[i] | had | plane[3 * kPlane + i]) & plane[2 * kPlane + i];
-    had &= plane[2 * kPlane + i];
+    const int32_t v = 32 * (word0 + i);
+    uint32_t own = plane[2 * kPlane + i];
+    if (v < begin) own = own >> (begin - v) << (begin - v);
+    if (end - v < 32) own &= (1u << (end - v)) - 1;
+    const uint32_t had = plane[kPlane + i] & own;
+    plane[i] = (plane[i] | plane[kPlane + i] | plane[3 * kPlane + i]) & own;
     const int32_t* c = p.counts + (static_cast<int64_t>(id) * p.W + word0 + i) * 32;
-    for (; had; had &= had - 1) prefetch(c + __ffs(had) - 1);
+    for (uint32_t m = had; m; m &= m - 1) prefetch(c + __ffs(m) - 1);
   }
   __syncthreads();
 

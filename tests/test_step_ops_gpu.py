@@ -470,6 +470,44 @@ def test_logits(mcp, B, V, dtype, out, on):
         assert np.array_equal(g[i][~fine], want[i][~fine], equal_nan=True)
 
 
+@pytest.mark.parametrize("V,dtype,out,off,temp", [
+    (60001, "bf16", None, 0, True), (60001, "fp16", None, 0, False), (60002, "fp32", None, 0, True),
+    (60000, "bf16", "fp32", 0, True), (60001, "bf16", "fp32", 1, True), (60003, "fp32", "fp32", 3, False),
+    (65536, "bf16", "bf16", 0, True),
+])
+def test_logits_of_rows_in_several_parts(mcp, V, dtype, out, off, temp):
+    """Rows that several CTAs take, each of them more than one tile, with most tokens seen:
+    every token is processed once, also where one part ends and the next begins."""
+    rng = np.random.default_rng(V + off)
+    B, R = 90, 4
+    x, _ = values(rng, (B, V), dtype, 4.0)
+    wide = torch.zeros((B, V + off), dtype=DT[dtype], device="cuda")
+    wide[:, off:] = torch.from_numpy(x).to(DT[dtype])
+    seen = rng.random((R, 2, V)) < 0.7
+    counts = np.where(seen[:, 1], rng.integers(1, 9, (R, V)), 0)
+    sd, cd = device_state(seen, counts)
+    ids = rng.integers(0, R, B)
+    f = {k: torch.from_numpy(rng.uniform(*r, B)).float() for k, r in
+         dict(repetition_penalty=(0.5, 2), frequency_penalty=(-1, 1), presence_penalty=(-1, 1),
+              temperature=(0.3, 2)).items()}
+    allow = rng.random((2, V)) < 0.6
+    mrows = rng.integers(-1, 2, B)
+    dst = None if out is None else torch.empty((B, V), dtype=DT[out], device="cuda")
+    got = mcp.process_logits(
+        wide[:, off:], dst, i32(ids), sd, cd, f["temperature"].cuda() if temp else None,
+        f["repetition_penalty"].cuda(), f["frequency_penalty"].cuda(), f["presence_penalty"].cuda(),
+        mask=torch.from_numpy(ref.pack_bits(allow)).cuda(), mask_rows=i32(mrows))
+    n = {k: t.double().numpy() for k, t in f.items()}
+    want, bound = ref.logits(x, ids, seen, counts, n["temperature"] if temp else None,
+                             n["repetition_penalty"], n["frequency_penalty"], n["presence_penalty"], {},
+                             [allow[m] if m >= 0 else None for m in mrows], out or dtype)
+    g = f64(got)
+    fine = np.isfinite(want)
+    assert (np.abs(g[fine] - want[fine]) <= bound[fine]).all()
+    assert np.array_equal(g[~fine], want[~fine])
+    assert not wide[:, :off].any()
+
+
 def test_logits_of_a_padded_head(mcp):
     """Rows of a head whose vocabulary is padded, in place: the padding stays as it was."""
     rng = np.random.default_rng(4)
