@@ -300,6 +300,49 @@ def test_scan_of_large_and_vanishing_steps(mcp):
     assert (np.abs(f64(v["state"][1]) - end) <= ebound).all()
 
 
+def test_scan_in_one_piece_and_in_several(mcp):
+    """The C entry without a workspace runs a segment in one piece, with one in several
+    (of which those in between are run twice); both stay in the bounds, and a workspace
+    that is too small is refused."""
+    import ctypes
+
+    from mixed_chunked_prefill_gb300 import _capi
+
+    rng = np.random.default_rng(12)
+    T, d, N = 500, 96, 16
+    lens, hist = [70, 1, 300, 129], [0, 4, 9, 9]
+    ids, cu, sk, R, T = stream(rng, lens, hist, 1, 2)
+    v = scan_inputs(rng, T, d, N, 1, "bf16", R, True, 1.0)
+    h = {k: t[0] for k, t in v.items()}
+    want, bound, end, ebound = ref.scan(h["x"], h["dt"], h["A"], h["B"], h["C"], h["D"], h["z"], h["bias"],
+                                        True, h["state"], ids, cu, sk, "bf16")
+    dev = {k: t[1] for k, t in v.items()}
+    lib = mcp.load()
+    meta = [i32(a) for a in (ids, cu, sk)]
+    S = len(ids)
+    desc = _capi.ScanDesc(S, T, R, d, N, 1, 0, 1, d, d, d, N, N, d)
+    need = ctypes.c_size_t()
+    assert lib.mcp_mixed_scan_workspace(ctypes.byref(desc), ctypes.byref(need)) == 0 and need.value > 256
+    stream_ = torch.cuda.current_stream().cuda_stream
+    results = []
+    for n in (0, need.value - 1, need.value):
+        ws = torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")
+        out = torch.full((T, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        st = dev["state"].clone()
+        tensors = _capi.ScanTensors(*(t.data_ptr() for t in (
+            dev["x"], dev["dt"], dev["A"], dev["B"], dev["C"], dev["D"], dev["z"], dev["bias"], st, out)))
+        r = lib.mcp_mixed_scan(ctypes.byref(desc), ctypes.byref(tensors), *(t.data_ptr() for t in meta),
+                               ws.data_ptr() if n else None, n, None, stream_)
+        if n == need.value - 1:
+            assert r == _capi.MCP_ERR_WORKSPACE_TOO_SMALL and torch.equal(st, dev["state"])
+            continue
+        assert r == 0
+        assert (np.abs(f64(out)[:cu[-1]] - want[:cu[-1]]) <= bound[:cu[-1]]).all()
+        assert (np.abs(f64(st) - end) <= ebound).all()
+        results.append(st)
+    assert not torch.equal(*results)  # the second was cut
+
+
 def test_parts_of_wider_rows(mcp):
     """x and z from one projection, B and C from another, the output inside a wider buffer."""
     rng = np.random.default_rng(8)
