@@ -631,7 +631,8 @@ typedef struct mcp_request_pool {
  * positions 0, everything else -1, request_pages untouched.
  *
  * request_ids, q_lens: device int32 [S].  S <= 8192.  request_pages,
- * block_tables 16-byte aligned, max_pages_per_seq * P < 2^31.  error_word:
+ * block_tables 16-byte aligned, max_requests <= 2^24, max_pages_per_seq <=
+ * 2^28 and max_pages_per_seq * P < 2^31, max_tokens <= 2^30.  error_word:
  * device int32 or NULL.  Page ids are not checked here; the calls that read
  * pages check them.  Steps of one pool must be ordered (one stream).
  */
@@ -678,6 +679,7 @@ mcp_status mcp_commit_step(const mcp_request_pool* pool, const int32_t* request_
  * Token rows may be part of wider rows: *_stride is the distance of
  * consecutive tokens in elements, a multiple of 8; tensors are 16-byte
  * aligned.  Sums and the scan's state are fp32; outputs are rounded once.
+ * num_seqs <= 2^20, total_tokens <= 2^30, num_requests <= 2^24.
  */
 typedef enum mcp_dtype { MCP_DTYPE_BF16 = 0, MCP_DTYPE_FP16 = 1, MCP_DTYPE_FP32 = 2 } mcp_dtype;
 
@@ -776,6 +778,7 @@ mcp_status mcp_mixed_scan_workspace(const mcp_scan_desc* desc, size_t* workspace
  * vocab_size (MCP_DEVERR_TOKEN_RANGE) is left out.  A request may stand in
  * several rows; the result does not depend on the order.  Clearing counts
  * relies on plane 1 marking every non-zero count (zero both to begin with).
+ * num_tokens <= 2^30, vocab_size <= 2^28 (of the logits also).
  */
 #define MCP_COUNT_PROMPT 0x1
 #define MCP_COUNT_RESET 0x2
@@ -821,6 +824,7 @@ typedef struct mcp_logits_tensors {
  *   is in the prompt or was sampled;   x -= frequency * counts[r,v] + presence
  *   if it was sampled;   x /= temperature if > 0;   x = -inf if the mask's bit
  *   is 0 (whatever x was, NaN included).
+ * out is logits, or does not overlap it.
  * A row with request_ids[i] < 0 is padding and is not written.  A request row
  * >= num_requests or a mask row >= num_masks sets MCP_DEVERR_REQUEST and the
  * row is not written; a bias token outside the vocabulary is left out, and it

@@ -1187,7 +1187,29 @@ int scan_states(const ScanArgs& a, int N, cudaStream_t st) {
   return scan_launch<T, 64>(a, st);
 }
 
+// How a convolution is dealt out: tokens of a run, CTAs across the channels.
+struct ConvCut {
+  int32_t tokens, blocks;
+  int64_t grid;
+};
+ConvCut conv_cut(const mcp_conv_desc& d) {
+  ConvCut c;
+  c.blocks = (d.channels / kConvCh + kConvThreads - 1) / kConvThreads;
+  // runs: long ones read fewer inputs twice (K - 1 in TT), shorter ones keep
+  // every SM busy when the stream is short
+  int64_t tiles = 0;
+  for (c.tokens = kConvMaxRun;; c.tokens /= 2) {
+    tiles = (static_cast<int64_t>(d.total_tokens) + c.tokens - 1) / c.tokens;
+    if (c.tokens == 8 || tiles * c.blocks >= 4 * step_num_sms()) break;
+  }
+  if (d.total_tokens <= kShortTokens) tiles = 0;
+  c.grid = (d.num_seqs + tiles) * c.blocks + 1;
+  return c;
+}
+
 }  // namespace
+
+bool mixed_conv_fits(const mcp_conv_desc& d) { return conv_cut(d).grid <= 0x7fffffff; }
 
 int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight, const void* bias,
                       void* state, const int32_t* request_ids, const int32_t* cu_seqlens_q,
@@ -1204,20 +1226,12 @@ int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight,
   a.ldo = d.out_stride;
   a.channels = d.channels;
   a.act = d.activation;
-  a.blocks = (d.channels / kConvCh + kConvThreads - 1) / kConvThreads;
-  // runs: long ones read fewer inputs twice (K - 1 in TT), shorter ones keep
-  // every SM busy when the stream is short
-  int64_t tiles = 0;
-  for (a.tokens = kConvMaxRun;; a.tokens /= 2) {
-    tiles = (static_cast<int64_t>(d.total_tokens) + a.tokens - 1) / a.tokens;
-    if (a.tokens == 8 || tiles * a.blocks >= 4 * step_num_sms()) break;
-  }
-  if (d.total_tokens <= kShortTokens) tiles = 0;
-  const int64_t grid = (d.num_seqs + tiles) * a.blocks + 1;
-  if (grid > 0x7fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);
+  const ConvCut cut = conv_cut(d);
+  a.tokens = cut.tokens;
+  a.blocks = cut.blocks;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d.dtype == MCP_DTYPE_BF16 ? conv_width<__nv_bfloat16>(a, d.width, grid, st)
-                                   : conv_width<__half>(a, d.width, grid, st);
+  return d.dtype == MCP_DTYPE_BF16 ? conv_width<__nv_bfloat16>(a, d.width, cut.grid, st)
+                                   : conv_width<__half>(a, d.width, cut.grid, st);
 }
 
 size_t mixed_scan_workspace(const mcp_scan_desc& d, int sms) { return scan_cut(d, sms).bytes; }

@@ -26,6 +26,13 @@ mcp_status done(int e, const char* what) {
   return static_cast<mcp_status>(mcp::set_error_code(MCP_OK, ""));
 }
 
+// Sizes up to which the kernels' 32-bit indices cannot overflow (a launch rounds
+// them up to its tiles).
+constexpr int32_t kMaxTokens = 1 << 30;   // of a step, a stream, a list
+constexpr int32_t kMaxRow = 1 << 28;      // entries of a table row, tokens of a vocabulary
+constexpr int32_t kMaxRows = 1 << 24;     // request rows
+constexpr int32_t kMaxSegments = 1 << 20;
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 #define MCP_TRY(expr)                    \
@@ -43,8 +50,9 @@ mcp_status check_pool(const mcp_request_pool* p, int32_t num_seqs, const int32_t
   if (p->max_requests <= 0 || p->max_pages_per_seq <= 0 || p->num_pages <= 0)
     return fail(MCP_ERR_INVALID_ARG, "pool sizes must be positive (requests %d, row %d, pages %d)",
                 p->max_requests, p->max_pages_per_seq, p->num_pages);
-  if (p->max_requests > 1 << 24)
-    return fail(MCP_ERR_UNSUPPORTED, "max_requests %d > 2^24", p->max_requests);
+  if (p->max_requests > kMaxRows || p->max_pages_per_seq > kMaxRow)
+    return fail(MCP_ERR_UNSUPPORTED, "max_requests %d > 2^24 or max_pages_per_seq %d > 2^28", p->max_requests,
+                p->max_pages_per_seq);
   if (p->page_size != 1 && p->page_size != 8 && p->page_size != 16 && p->page_size != 32 &&
       p->page_size != 64)
     return fail(MCP_ERR_UNSUPPORTED, "page_size %d (built: 1, 8, 16, 32, 64)", p->page_size);
@@ -66,6 +74,9 @@ mcp_status check_stream_sizes(int32_t num_seqs, int32_t tokens, int32_t requests
   if (requests <= 0 || channels <= 0)
     return fail(MCP_ERR_INVALID_ARG, "num_requests %d / channels %d must be positive", requests,
                 channels);
+  if (num_seqs > kMaxSegments || tokens > kMaxTokens || requests > kMaxRows)
+    return fail(MCP_ERR_UNSUPPORTED, "num_seqs %d > 2^20, total_tokens %d > 2^30 or num_requests %d > 2^24",
+                num_seqs, tokens, requests);
   if (channels % 8 != 0)
     return fail(MCP_ERR_INVALID_ARG, "channels %d is not a multiple of 8", channels);
   if (dtype != MCP_DTYPE_BF16 && dtype != MCP_DTYPE_FP16)
@@ -110,6 +121,7 @@ mcp_status mcp_build_step_tables(const mcp_request_pool* pool, const int32_t* re
                                  int32_t* logits_indices, int32_t* error_word, void* stream) {
   MCP_TRY(check_pool(pool, num_seqs, request_ids, q_lens));
   if (max_tokens < 0) return fail(MCP_ERR_INVALID_ARG, "max_tokens %d < 0", max_tokens);
+  if (max_tokens > kMaxTokens) return fail(MCP_ERR_UNSUPPORTED, "max_tokens %d > 2^30", max_tokens);
   if (!cu_seqlens_q || (num_seqs > 0 && (!seqlens_k || !block_tables)) ||
       (max_tokens > 0 && !slot_mapping))
     return fail(MCP_ERR_INVALID_ARG, "NULL output pointer");
@@ -150,6 +162,10 @@ mcp_status mcp_mixed_conv(const mcp_conv_desc* d, const void* x, const void* wei
   if (!weight || !state) return fail(MCP_ERR_INVALID_ARG, "NULL tensor pointer");
   if (!aligned(weight, 16) || !aligned(bias, 16) || !aligned(state, 16))
     return fail(MCP_ERR_INVALID_ARG, "weight, bias and state must be 16-byte aligned");
+  if (out == x) return fail(MCP_ERR_INVALID_ARG, "out may not overlap x (a token reads those before it)");
+  if (!mcp::mixed_conv_fits(*d))
+    return fail(MCP_ERR_UNSUPPORTED, "num_seqs %d, total_tokens %d and channels %d exceed a launch", d->num_seqs,
+                d->total_tokens, d->channels);
   return done(mcp::launch_mixed_conv(*d, x, weight, bias, state, request_ids, cu_seqlens_q, seqlens_k,
                                      out, error_word, stream),
               "mixed_conv launch");
@@ -187,6 +203,8 @@ mcp_status mcp_mixed_scan(const mcp_scan_desc* d, const mcp_scan_tensors* t,
     if (workspace_bytes < need)
       return fail(MCP_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", workspace_bytes, need);
   }
+  for (const void* in : {t->x, t->dt, t->B, t->C, t->z})
+    if (t->out == in) return fail(MCP_ERR_INVALID_ARG, "out may not overlap an input");
   return done(mcp::launch_mixed_scan(*d, *t, request_ids, cu_seqlens_q, seqlens_k, workspace,
                                      error_word, stream),
               "mixed_scan launch");
@@ -202,6 +220,8 @@ mcp_status mcp_update_token_counts(const int32_t* request_ids, int32_t num_rows,
   if (num_requests <= 0 || vocab_size <= 0)
     return fail(MCP_ERR_INVALID_ARG, "num_requests %d / vocab_size %d must be positive", num_requests,
                 vocab_size);
+  if (num_tokens > kMaxTokens || vocab_size > kMaxRow)
+    return fail(MCP_ERR_UNSUPPORTED, "num_tokens %d > 2^30 or vocab_size %d > 2^28", num_tokens, vocab_size);
   if (flags & ~(MCP_COUNT_PROMPT | MCP_COUNT_RESET))
     return fail(MCP_ERR_INVALID_ARG, "flags 0x%x", flags);
   if (!cu_tokens && num_tokens != num_rows)
@@ -220,6 +240,7 @@ mcp_status mcp_process_logits(const mcp_logits_desc* d, const mcp_logits_tensors
   if (!d || !t) return fail(MCP_ERR_INVALID_ARG, "desc or tensors is NULL");
   if (d->num_rows < 0 || d->vocab_size <= 0)
     return fail(MCP_ERR_INVALID_ARG, "num_rows %d / vocab_size %d", d->num_rows, d->vocab_size);
+  if (d->vocab_size > kMaxRow) return fail(MCP_ERR_UNSUPPORTED, "vocab_size %d > 2^28", d->vocab_size);
   if (d->dtype != MCP_DTYPE_BF16 && d->dtype != MCP_DTYPE_FP16 && d->dtype != MCP_DTYPE_FP32)
     return fail(MCP_ERR_UNSUPPORTED, "dtype %d", d->dtype);
   if (d->out_dtype != d->dtype && d->out_dtype != MCP_DTYPE_FP32)

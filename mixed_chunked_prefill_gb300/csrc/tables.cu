@@ -388,7 +388,7 @@ int grid_of(int64_t units) {
 }  // namespace
 
 int step_num_sms() {
-  static thread_local int dev_of = -1, sms = 148;
+  static thread_local int dev_of = -1, sms = 152;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != dev_of) {

@@ -41,6 +41,7 @@ def build_tables(lib, p, ids=P16, q=P16, S=4, cap=64, cu=P16, sk=P16, bt=P16, sl
     (dict(max_requests=0), INVALID), (dict(max_pages_per_seq=0), INVALID),
     (dict(num_pages=0), INVALID), (dict(max_requests=(1 << 24) + 1), UNSUPPORTED),
     (dict(page_size=4), UNSUPPORTED), (dict(page_size=0), UNSUPPORTED),
+    (dict(max_pages_per_seq=(1 << 28) + 1, page_size=1), UNSUPPORTED),
     (dict(max_pages_per_seq=1 << 27), UNSUPPORTED), (dict(request_pages=None), INVALID),
     (dict(request_lens=None), INVALID), (dict(free_pages=None), INVALID),
     (dict(free_count=None), INVALID), (dict(request_pages=P16 + 8), INVALID),
@@ -55,7 +56,7 @@ def test_pool_refusals(lib, over, status):
     (dict(S=-1), INVALID), (dict(S=8193), UNSUPPORTED), (dict(cap=-1), INVALID),
     (dict(ids=None), INVALID), (dict(q=None), INVALID), (dict(cu=None), INVALID),
     (dict(sk=None), INVALID), (dict(bt=None), INVALID), (dict(slots=None), INVALID),
-    (dict(bt=P16 + 4), INVALID), (dict(slots=P16 + 4), INVALID),
+    (dict(bt=P16 + 4), INVALID), (dict(slots=P16 + 4), INVALID), (dict(cap=(1 << 30) + 1), UNSUPPORTED),
 ])
 def test_build_step_tables_refusals(lib, over, status):
     assert build_tables(lib, pool(), **over) == status
@@ -86,6 +87,11 @@ def conv(lib, meta=(P16, P16, P16), x=P16, w=P16, b=None, state=P16, out=P16, **
     (dict(x=None), INVALID), (dict(x=P16 + 8), INVALID), (dict(w=None), INVALID),
     (dict(b=P16 + 2), INVALID), (dict(state=None), INVALID), (dict(state=P16 + 8), INVALID),
     (dict(out=None), INVALID), (dict(num_seqs=0), OK), (dict(total_tokens=0, x=None), OK),
+    (dict(), INVALID),  # out == x
+    (dict(num_seqs=(1 << 20) + 1), UNSUPPORTED), (dict(total_tokens=(1 << 30) + 1), UNSUPPORTED),
+    (dict(num_requests=(1 << 24) + 1), UNSUPPORTED),
+    (dict(num_seqs=1 << 20, channels=1 << 20, x_stride=1 << 20, out_stride=1 << 20, out=2 * P16),
+     UNSUPPORTED),  # 2^31 CTAs
 ])
 def test_mixed_conv_refusals(lib, over, status):
     assert conv(lib, **over) == status
@@ -117,6 +123,10 @@ def scan(lib, meta=(P16, P16, P16), tensors=(), workspace=(None, 0), **over):
     (dict(total_tokens=100000, channels=8192, x_stride=8192, dt_stride=8192, z_stride=8192,
           out_stride=8192, workspace=(P16, 256)), _capi.MCP_ERR_WORKSPACE_TOO_SMALL),
     (dict(num_seqs=0), OK), (dict(total_tokens=0), OK),
+    *[(dict(tensors={n: 2 * P16 for n in ("x", "dt", "B", "C", "z") if n != same}), INVALID)
+      for same in ("x", "dt", "B", "C", "z")],  # out is that one
+    (dict(num_seqs=(1 << 20) + 1), UNSUPPORTED), (dict(total_tokens=(1 << 30) + 1), UNSUPPORTED),
+    (dict(num_requests=(1 << 24) + 1), UNSUPPORTED),
 ])
 def test_mixed_scan_refusals(lib, over, status):
     assert scan(lib, **over) == status
@@ -131,6 +141,7 @@ def counts(lib, ids=P16, rows=4, tokens=P16, n=4, cu=None, seen=P16, cnt=P16, R=
     (dict(flags=4), INVALID), (dict(n=5), INVALID), (dict(ids=None), INVALID),
     (dict(tokens=None), INVALID), (dict(seen=None), INVALID), (dict(cnt=None), INVALID),
     (dict(rows=0, n=0), OK), (dict(rows=0, n=7, cu=P16), OK),
+    (dict(n=(1 << 30) + 1, cu=P16), UNSUPPORTED), (dict(V=(1 << 28) + 1), UNSUPPORTED),
 ])
 def test_update_token_counts_refusals(lib, over, status):
     assert counts(lib, **over) == status
