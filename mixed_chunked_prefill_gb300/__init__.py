@@ -469,17 +469,21 @@ def _raw_stream(dev) -> int:
     return get(dev) if get is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _result(out, stream, make):
-    """``out``, or a new tensor of ``make()`` that ``stream`` may use."""
-    if out is not None:
-        return out
+def _empty(shape, dtype, device, stream, result=False):
+    """A new tensor for a call on ``stream`` (None: the current one): its memory belongs to
+    that stream, so that nothing else that is queued can still write it.  ``result``: the
+    caller keeps it and may use it on the current stream."""
     import torch
 
-    out = make()
-    if stream is not None:
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-        out.record_stream(s)
-    return out
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    there = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device)
+    with torch.cuda.stream(there):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result and there.cuda_stream != here.cuda_stream:
+        t.record_stream(here)
+    return t
 
 
 def make_request_pool(request_pages, request_lens, free_pages, free_count,
@@ -570,7 +574,8 @@ def mixed_conv(x, weight, bias, state, request_ids, cu_seqlens_q, seqlens_k, act
     rows = x.shape
     T, d = rows
     K, S, R = weight.shape[1], request_ids.shape[0], state.shape[0]
-    out = _result(out, stream, lambda: torch.empty(rows, dtype=dtype, device=x.device))
+    if out is None:
+        out = _empty(rows, dtype, x.device, stream, result=True)
     px, ldx = _row_arg(x, dtype, "x", dev, rows)
     po, ldo = _row_arg(out, dtype, "out", dev, rows)
     desc = _capi.ConvDesc(S, T, R, d, K, _dtype_code(x, "x"), activation == "silu", 0, ldx, ldo)
@@ -603,7 +608,8 @@ def mixed_scan(x, dt, A, B, C, state, request_ids, cu_seqlens_q, seqlens_k, D=No
     rows, bc = x.shape, B.shape
     T, d = rows
     G, N, S, R = bc[1], bc[2], request_ids.shape[0], state.shape[0]
-    out = _result(out, stream, lambda: torch.empty(rows, dtype=dtype, device=x.device))
+    if out is None:
+        out = _empty(rows, dtype, x.device, stream, result=True)
     px, ldx = _row_arg(x, dtype, "x", dev, rows)
     pd, ldd = _row_arg(dt, dtype, "dt", dev, rows)
     pz, ldz = (None, 0) if z is None else _row_arg(z, dtype, "z", dev, rows)
@@ -620,8 +626,7 @@ def mixed_scan(x, dt, A, B, C, state, request_ids, cu_seqlens_q, seqlens_k, D=No
         _launch_free("mixed_scan_workspace", dev, load().mcp_mixed_scan_workspace,
                      ctypes.byref(desc), ctypes.byref(nbytes))
         if nbytes.value:
-            workspace = _result(None, stream, lambda: torch.empty(
-                nbytes.value, dtype=torch.uint8, device=x.device))
+            workspace = _empty(nbytes.value, torch.uint8, x.device, stream)
     _launch("mixed_scan", dev, stream, load().mcp_mixed_scan, ctypes.byref(desc),
             ctypes.byref(tensors), _arg(request_ids, i32, "request_ids", dev, (S,)),
             _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),

@@ -133,12 +133,12 @@ class MixedStep:
 
 class StepTables:
     """One step of ``RequestTables``: its metadata on the device (and the lengths on the
-    host), valid until the commit."""
+    host), valid until the next commit of the same tables, which may be this step's only."""
 
     def __init__(self, tables, request_ids, q_lens, max_tokens, stream):
         import torch
 
-        self.pool = tables.pool
+        self.pool, self.after = tables.pool, tables.commits
         dev = tables.device
         ids, q = _i32(request_ids), _i32(q_lens)
         if ids.ndim != 1 or ids.shape != q.shape:
@@ -197,6 +197,7 @@ class RequestTables:
                                       self.free_count, page_size)
         self.lens_h = np.zeros(max_requests, dtype=np.int64)
         self.free_h = int(num_pages)
+        self.commits = 0
 
     def step(self, request_ids, q_lens, max_tokens=None, stream=None) -> StepTables:
         """Tables of a step in which request row request_ids[s] runs q_lens[s] new tokens
@@ -209,6 +210,8 @@ class RequestTables:
         after rejected speculated tokens, 0: the request is over)."""
         import torch
 
+        if step.pool is not self.pool or step.after != self.commits:
+            raise ValueError("the step was built before another commit, or from other tables")
         live = step.ids_h >= 0
         after = step.sk_h if new_lens is None else _i32(new_lens)
         if after.shape != step.sk_h.shape or ((after < 0) | (after > step.sk_h))[live].any():
@@ -216,6 +219,7 @@ class RequestTables:
         with _on_stream(stream):
             to = None if new_lens is None else torch.from_numpy(after).to(self.device)
             commit_step(self.pool, step.request_ids, step.q_lens, to, self.error_word, stream)
+        self.commits += 1
         P = self.pool.page_size
         kept = -(-after // P) - -(-step.sk_h // P)
         self.lens_h[step.ids_h[live]] = after[live]

@@ -4,9 +4,12 @@ definitions carry along (roundings of every intermediate, half a step of the typ
 
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 
+from mixed_chunked_prefill_gb300 import _capi
 from oracle import step_ops_ref as ref
 
 torch = pytest.importorskip("torch")
@@ -304,10 +307,6 @@ def test_scan_in_one_piece_and_in_several(mcp):
     """The C entry without a workspace runs a segment in one piece, with one in several
     (of which those in between are run twice); both stay in the bounds, and a workspace
     that is too small is refused."""
-    import ctypes
-
-    from mixed_chunked_prefill_gb300 import _capi
-
     rng = np.random.default_rng(12)
     T, d, N = 500, 96, 16
     lens, hist = [70, 1, 300, 129], [0, 4, 9, 9]
@@ -793,6 +792,63 @@ def test_calls_on_another_stream(mcp):
     for got, w in zip(d.build([1], [20], 20, s.cuda_stream), p.build([1], [20], 20)):
         s.synchronize()
     assert int(d.err) == 0
+
+
+def test_results_taken_for_another_stream(mcp):
+    """A result (and a workspace) that the call takes for itself is memory of the stream it
+    runs on, not memory that the current stream has freed but still writes."""
+    rng = np.random.default_rng(42)
+    d, N = 64, 16
+    ids, cu, sk, R, T = stream(rng, [300, 1, 190], [0, 3, 7], 1, 0)
+    v = scan_inputs(rng, T, d, N, 1, "bf16", R, True, 1.0)
+    w = values(rng, (d, 4), "bf16", 0.5)[1]
+    meta = [i32(a) for a in (ids, cu, sk)]
+    state = torch.zeros((R, 3, d), dtype=torch.bfloat16, device="cuda")
+    x, dt, B, C = (v[k][1] for k in ("x", "dt", "B", "C"))
+
+    def calls(st, **kw):
+        y = mcp.mixed_conv(x, w, None, state.clone() if st is None else st[0], *meta, **kw)
+        s = mcp.mixed_scan(x, dt, v["A"][1], B, C, v["state"][1].clone() if st is None else st[1], *meta, **kw)
+        return y, s
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    other, busy = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    n = ctypes.c_size_t()
+    desc = _capi.ScanDesc(len(ids), T, R, d, N, 1, 0, 1, d, d, d, N, N, d)
+    assert mcp.load().mcp_mixed_scan_workspace(ctypes.byref(desc), ctypes.byref(n)) == 0
+    for s in (other, other.cuda_stream):
+        kept = state.clone(), v["state"][1].clone()
+        blocks = [torch.empty_like(want[0]), torch.empty_like(want[1]),
+                  torch.empty(n.value, dtype=torch.uint8, device="cuda")]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            torch.mm(busy, busy)
+        for b in blocks:
+            b.view(torch.uint8).fill_(255)
+        del b, blocks
+        got = calls(kept, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_stale_steps_are_refused(mcp):
+    """A step may be committed once, and not behind another commit."""
+    from mixed_chunked_prefill_gb300.step import RequestTables
+
+    tables, others = RequestTables(20, 16, 4, 6), RequestTables(20, 16, 4, 6)
+    a, b = tables.step([0], [20]), tables.step([1], [40])
+    with pytest.raises(ValueError):
+        others.commit(a)
+    tables.commit(b)
+    for step in (a, b):
+        with pytest.raises(ValueError):
+            tables.commit(step)
+    tables.commit(tables.step([0, 1], [20, 1]))
+    tables.check()
+    assert int(tables.free_count) == tables.free_h == 20 - 2 - 3
+    tables.release([1, 0])
+    assert sorted(tables.free_pages.tolist()) == list(range(20))
 
 
 def test_python_refusals(mcp):
