@@ -36,6 +36,7 @@ struct CountArgs {
 // Clear the rows' state: both planes whole, counts only where a bit says that
 // one may be there (a row of counts is 32 times its plane).
 __global__ void __launch_bounds__(kCountThreads) clear_counts_kernel(const CountArgs p) {
+  asm volatile("griddepcontrol.launch_dependents;");
   const int64_t total = static_cast<int64_t>(p.rows) * p.W;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCountThreads + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * kCountThreads) {
@@ -54,102 +55,160 @@ __global__ void __launch_bounds__(kCountThreads) clear_counts_kernel(const Count
   }
 }
 
-// Adding and marking are atomic, so the result does not depend on the order and
-// a request may stand in several rows; a mark that is already there is only
-// read (text repeats few words very often).  A thread takes kPer neighbouring
-// tokens whose loads are in flight together; the row of a CTA's first token is
-// looked up once, and a token looks its own up only behind that row's end.
-// Repeats within a CTA's part of that row are dropped by a bitmap in shared
-// memory: a cleared row whose most frequent tokens were all marked at once took
-// 20 us longer for 64 prompts of 24000 tokens, one word taking thousands of
-// atomics.
-constexpr int kFilterTokens = 1 << 17;  // 16 KB; tokens from there on are not filtered
+// First row that ends behind token c (`rows`: none), looked up by all threads of
+// the CTA together: their loads are in flight at once, where a binary search
+// makes one after the other.
+template <int kThreads>
+__device__ __forceinline__ int32_t first_row(const CountArgs& p, int32_t c) {
+  int32_t n = 0;
+  for (int32_t s0 = 0; s0 < p.rows; s0 += kThreads) {
+    const int32_t s = s0 + threadIdx.x;
+    const int32_t here = __syncthreads_count(s < p.rows && p.cu[s + 1] <= c);
+    n += here;
+    if (here < kThreads) break;
+  }
+  return n;
+}
+// The row that token i is in, not before `lo` (-1: in none)
+__device__ __forceinline__ int32_t row_of(const CountArgs& p, int32_t i, int32_t lo) {
+  if (lo < p.rows && p.cu[lo + 1] <= i) {
+    ++lo;
+    if (lo < p.rows && p.cu[lo + 1] <= i) {
+      int32_t hi = p.rows;
+      while (lo < hi) {
+        const int32_t mid = (lo + hi) >> 1;
+        if (p.cu[mid + 1] <= i) lo = mid + 1;
+        else hi = mid;
+      }
+    }
+  }
+  return lo < p.rows && p.cu[lo] <= i ? lo : -1;
+}
 
-template <int kPer>
+// A token of row `row` (-1: of none), added where it belongs.  Adding and marking
+// are atomic, so the result does not depend on the order and a request may stand
+// in several rows; a mark that is already there is only read (text repeats few
+// words very often).  Returns error bits.
+__device__ __forceinline__ int add_token(const CountArgs& p, int32_t tok, int32_t row) {
+  const int32_t id = row < 0 ? -1 : p.ids[row];
+  if (id < 0 || tok < 0) return id >= p.R ? MCP_DEVERR_REQUEST : 0;
+  if (id >= p.R) return MCP_DEVERR_REQUEST;
+  if (tok >= p.V) return MCP_DEVERR_TOKEN_RANGE;
+  int32_t* word = p.seen + (static_cast<int64_t>(id) * 2 + (p.prompt ? 0 : 1)) * p.W + (tok >> 5);
+  const uint32_t had = *reinterpret_cast<volatile uint32_t*>(word), bit = 1u << (tok & 31);
+  if (!p.prompt) atomicAdd(p.counts + static_cast<int64_t>(id) * 32 * p.W + tok, 1);
+  if (!(had & bit)) atomicOr(reinterpret_cast<unsigned int*>(word), bit);
+  return 0;
+}
+
+// A thread a token: the chain of loads from the row's end to the mark is what
+// this takes (250 sampled tokens 3.0 us, 2.3 of them the launch).
 __global__ void __launch_bounds__(kCountThreads) add_tokens_kernel(const CountArgs p) {
-  __shared__ int32_t s_row, s_end;
-  __shared__ __align__(16) uint32_t filter[kPer > 1 ? kFilterTokens / 32 : 4];
-  const int32_t c0 = blockIdx.x * (kCountThreads * kPer);
-  auto find = [&](int32_t i) {  // first row that ends behind token i
-    int32_t lo = 0, hi = p.rows;
-    while (lo < hi) {
-      const int32_t mid = (lo + hi) >> 1;
-      if (p.cu[mid + 1] <= i) lo = mid + 1;
-      else hi = mid;
-    }
-    return lo;
-  };
-  const int32_t i0 = c0 + threadIdx.x * kPer;
-  int32_t tok[kPer];
-  // whole vectors where the tokens are aligned; behind num_tokens nothing is read
-  const bool vec = kPer % 4 == 0 && (reinterpret_cast<uintptr_t>(p.tokens) & 15) == 0 && i0 + kPer <= p.n;
-  if constexpr (kPer % 4 == 0) {
-    if (vec) {
-#pragma unroll
-      for (int k = 0; k < kPer; k += 4) {
-        const int4 q = *reinterpret_cast<const int4*>(p.tokens + i0 + k);
-        tok[k] = q.x, tok[k + 1] = q.y, tok[k + 2] = q.z, tok[k + 3] = q.w;
-      }
-    }
-  }
-  if (!vec) {
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) tok[k] = i0 + k < p.n ? p.tokens[i0 + k] : -1;
-  }
-  int32_t row0 = 0, end0 = 0;
-  if (p.cu && kPer > 1) {
-    const int words = (min(p.V, kFilterTokens) + 127) / 128;
-    for (int w = threadIdx.x; w < words; w += kCountThreads)
-      reinterpret_cast<uint4*>(filter)[w] = make_uint4(0u, 0u, 0u, 0u);
-    if (threadIdx.x == 0) {
-      s_row = find(c0);
-      s_end = s_row < p.rows ? p.cu[s_row + 1] : 0;
-    }
-    __syncthreads();
-    row0 = s_row;
-    end0 = s_end;
-    if (row0 < p.rows && p.cu[row0] > c0) end0 = 0;  // tokens before the first row
-  }
+  const int32_t c = blockIdx.x * kCountThreads, i = c + threadIdx.x;
+  const int32_t tok = i < p.n ? p.tokens[i] : -1;
+  int32_t row = i;
+  if (p.cu) row = row_of(p, i, first_row<kCountThreads>(p, c));
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows are cleared
+  if (i >= p.n) return;
+  const int bad = add_token(p, tok, row);
+  if (bad && p.err) atomicOr(p.err, bad);
+}
+
+// Long texts.  A CTA takes `chunk` tokens and marks those of one row in a bitmap
+// in shared memory, whose words then go to the row by one atomic each, 32
+// neighbouring ones a warp: a cleared row whose most frequent tokens were marked
+// one by one took hundreds of atomics on the same word.  The bitmap is filled
+// while the launch before clears the rows.  Parts of rows shorter than kDense
+// tokens are not worth a pass over it.
+//
+// Taken from 4096 tokens and an average of 2048 a row on.  Prompts marked like
+// this and token by token, rows cleared first, us: 64 of 500 tokens 8.6 / 6.1,
+// 64 of 4000 8.5 / 9.1, 64 of 8000 8.6 / 13.6, 64 of 32768 11.7 / 38.  Sampled
+// tokens have their counts' atomics beside the marks: from 8192 a row on (64 of
+// 4096 6.4 / 5.0, 64 of 32768 22 / 33).
+constexpr int kMarkThreads = 1024;
+constexpr int kDense = 1024;
+constexpr int kMarkTokens = 4096, kMarkRow = 2048, kCountRow = 8192;
+constexpr int kMapTokens = 1 << 18;  // 32 KB; tokens from there on are marked one by one
+
+__global__ void __launch_bounds__(kMarkThreads) mark_texts_kernel(const CountArgs p, const int32_t chunk) {
+  extern __shared__ __align__(16) uint32_t map[];
+  const int32_t mapped = min(p.V, kMapTokens), words = (mapped + 31) / 32;
+  for (int w = threadIdx.x; w < words; w += kMarkThreads) map[w] = 0;
+  const bool vec = (reinterpret_cast<uintptr_t>(p.tokens) & 15) == 0;
+  int32_t c = blockIdx.x * chunk;
+  const int32_t c1 = min(p.n, c + chunk);
   int bad = 0;
-  int32_t* word[kPer];
-  uint32_t had[kPer];
-  int32_t id = -1, last = -2;  // request row of the row `last`
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int32_t i = i0 + k;
-    word[k] = nullptr;
-    had[k] = 0xffffffffu;
-    if (i >= p.n) continue;
-    int32_t row = i;
-    if (p.cu) {
-      row = row0;
-      if (i >= end0) {
-        row = find(i);
-        if (row < p.rows && p.cu[row] > i) row = p.rows;
-      }
+  int32_t row = first_row<kMarkThreads>(p, c);
+  if (!p.prompt) asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();  // the cleared map
+  while (c < c1 && row < p.rows) {
+    const int32_t begin = p.cu[row], end = min(c1, p.cu[row + 1]);
+    if (end <= c) {  // rows without tokens
+      row = max(row + 1, first_row<kMarkThreads>(p, c));
+      continue;
     }
-    if (row != last) id = row < p.rows ? p.ids[row] : -1;
-    last = row;
-    if (id >= p.R) {
-      bad |= MCP_DEVERR_REQUEST;
-    } else if (id >= 0 && tok[k] >= p.V) {
-      bad |= MCP_DEVERR_TOKEN_RANGE;
-    } else if (id >= 0 && tok[k] >= 0) {
-      const uint32_t bit = 1u << (tok[k] & 31);
-      const bool repeat = kPer > 1 && p.cu && row == row0 && i < end0 && tok[k] < kFilterTokens &&
-                          (atomicOr(filter + (tok[k] >> 5), bit) & bit);
-      if (!repeat) {
-        word[k] = p.seen + (static_cast<int64_t>(id) * 2 + (p.prompt ? 0 : 1)) * p.W + (tok[k] >> 5);
-        had[k] = *reinterpret_cast<volatile uint32_t*>(word[k]);
-      }
-      if (!p.prompt) atomicAdd(p.counts + static_cast<int64_t>(id) * 32 * p.W + tok[k], 1);
+    if (begin > c) {  // tokens before the first row
+      c = min(c1, begin);
+      continue;
     }
+    if (end - c < kDense) {
+      const int32_t i = c + threadIdx.x;
+      const int32_t r = i < c1 ? row_of(p, i, row) : -1;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (r >= 0) bad |= add_token(p, p.tokens[i], r);
+      c = min(c1, c + kMarkThreads);
+      row = end < c ? first_row<kMarkThreads>(p, c) : row;
+      continue;
+    }
+    const int32_t id = p.ids[row];
+    if (id >= p.R) bad |= MCP_DEVERR_REQUEST;
+    if (id >= 0 && id < p.R) {
+      uint32_t* seen = reinterpret_cast<uint32_t*>(p.seen) + (static_cast<int64_t>(id) * 2 + (p.prompt ? 0 : 1)) * p.W;
+      int32_t* counts = p.counts + static_cast<int64_t>(id) * 32 * p.W;
+      auto mark = [&](int32_t tok) {
+        if (tok < 0) return;
+        if (tok >= p.V) {
+          bad |= MCP_DEVERR_TOKEN_RANGE;
+          return;
+        }
+        if (!p.prompt) atomicAdd(counts + tok, 1);
+        const uint32_t bit = 1u << (tok & 31);
+        if (tok < mapped) {
+          if (!(map[tok >> 5] & bit)) atomicOr(map + (tok >> 5), bit);
+        } else {
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          atomicOr(seen + (tok >> 5), bit);
+        }
+      };
+      if (vec) {  // whole vectors of four tokens, those that reach into a neighbour token by token
+        const int32_t a0 = (c + 3) & ~3, a1 = end & ~3;
+        if (threadIdx.x < a0 - c) mark(p.tokens[c + threadIdx.x]);
+        if (threadIdx.x < end - a1) mark(p.tokens[a1 + threadIdx.x]);
+#pragma unroll 2
+        for (int32_t i = a0 + 4 * static_cast<int32_t>(threadIdx.x); i < a1; i += 4 * kMarkThreads) {
+          const int4 q = *reinterpret_cast<const int4*>(p.tokens + i);
+          mark(q.x), mark(q.y), mark(q.z), mark(q.w);
+        }
+      } else {
+#pragma unroll 4
+        for (int32_t i = c + static_cast<int32_t>(threadIdx.x); i < end; i += kMarkThreads) mark(p.tokens[i]);
+      }
+      __syncthreads();
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int w = threadIdx.x; w < words; w += kMarkThreads) {
+        const uint32_t v = map[w];
+        if (v) {
+          atomicOr(seen + w, v);
+          map[w] = 0;
+        }
+      }
+      __syncthreads();
+    }
+    c = end;
+    ++row;
   }
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const uint32_t bit = 1u << (tok[k] & 31);
-    if (word[k] && !(had[k] & bit)) atomicOr(reinterpret_cast<unsigned int*>(word[k]), bit);
-  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what follows this launch follows the clearing too
   if (bad && p.err) atomicOr(p.err, bad);
 }
 
@@ -583,15 +642,27 @@ int launch_update_token_counts(const int32_t* request_ids, int32_t num_rows,
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return static_cast<int>(e);
   }
-  // eight tokens a thread once they fill the SMs
-  constexpr int kMany = 8;
-  if (num_tokens >= kMany * kCountThreads * step_num_sms()) {
-    constexpr int chunk = kMany * kCountThreads;
-    add_tokens_kernel<kMany><<<(num_tokens - 1) / chunk + 1, kCountThreads, 0, st>>>(a);
-  } else if (num_tokens > 0) {
-    add_tokens_kernel<1><<<(num_tokens - 1) / kCountThreads + 1, kCountThreads, 0, st>>>(a);
+  if (num_tokens == 0) return 0;
+  cudaLaunchAttribute beside = {};  // begins while the rows are cleared
+  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  beside.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cfg.attrs = &beside;
+  cfg.numAttrs = flags & MCP_COUNT_RESET ? 1 : 0;
+  if (cu_tokens && num_tokens >= kMarkTokens && num_tokens / num_rows >= (a.prompt ? kMarkRow : kCountRow)) {
+    const int32_t sms = step_num_sms();
+    int32_t chunk = ((num_tokens + sms - 1) / sms + kMarkThreads - 1) / kMarkThreads * kMarkThreads;
+    if (chunk < 2 * kMarkThreads) chunk = 2 * kMarkThreads;
+    const int32_t words = ((vocab_size < kMapTokens ? vocab_size : kMapTokens) + 31) / 32;
+    cfg.gridDim = dim3((num_tokens - 1) / chunk + 1);
+    cfg.blockDim = dim3(kMarkThreads);
+    cfg.dynamicSmemBytes = 4 * words;
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, mark_texts_kernel, a, chunk));
   }
-  return static_cast<int>(cudaGetLastError());
+  cfg.gridDim = dim3((num_tokens - 1) / kCountThreads + 1);
+  cfg.blockDim = dim3(kCountThreads);
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, add_tokens_kernel, a));
 }
 
 int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,

@@ -428,6 +428,36 @@ def test_update_counts(mcp, V, prompt, reset):
     assert torch.equal(sd, want[0]) and torch.equal(cd, want[1]) and int(err) == 0
 
 
+@pytest.mark.parametrize("lens,prompt,V,first", [
+    ([9000, 0, 0, 3, 5000, 1, 8000], True, 1000, 0), ([30000], True, 50000, 0),
+    ([5, 7, 0, 40000], True, 300001, 3), ([12000, 0, 9000], False, 70, 1),
+    ([3000, 6000, 1023, 1024, 1025], True, 262200, 0), ([20001, 1], False, 5001, 2),
+    ([0] * 20 + [45000], True, 128000, 0),
+])
+@pytest.mark.parametrize("reset", [False, True])
+def test_counts_of_long_texts(mcp, lens, prompt, V, first, reset):
+    """Texts long enough for bitmaps, between short and empty ones, on addresses of any
+    alignment, with padding tokens, rows of the same request and ranges left out."""
+    rng = np.random.default_rng(len(lens) + V + first)
+    R, rows, W = 6, len(lens), -(-V // 32)
+    ids = rng.integers(0, R, rows)
+    cu = np.concatenate([[0], np.cumsum(lens)]) + first
+    n = int(cu[-1]) + 100  # tokens behind the last row are not read
+    tokens = np.minimum(((V + 1.0) ** rng.random(n) - 1).astype(np.int64), V - 1)
+    tokens[rng.random(n) < 0.05] = -1
+    tokens[rng.integers(first, int(cu[-1]))] = V
+    seen, counts = token_state(rng, R, V, 40)
+    sd, cd = device_state(seen, counts)
+    err = i32([0])
+    td = i32(np.concatenate([[0] * (first % 4), tokens]))[first % 4:]
+    mcp.update_token_counts(i32(ids), td, sd, cd, V, i32(cu), prompt, reset, err)
+    legal = np.where(tokens >= V, -1, tokens)
+    seen, counts = ref.update_counts(seen, counts, ids, legal, cu, V, prompt, reset)
+    want = device_state(seen, counts)
+    assert torch.equal(sd, want[0]) and torch.equal(cd, want[1])
+    assert int(err) == _capi.DEVERR_TOKEN_RANGE and W == sd.shape[2]
+
+
 def test_counts_out_of_range_are_left_out(mcp):
     seen, counts = np.zeros((2, 2, 40), bool), np.zeros((2, 40), np.int64)
     for ids, tok, bit in (([0, 1], [40, 3], 0x100), ([2, 1], [1, 3], 0x80)):
