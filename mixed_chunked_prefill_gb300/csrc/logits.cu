@@ -271,13 +271,14 @@ struct alignas(n * sizeof(T)) Vec {
 };
 
 // The bias of token `tok`, which has one: entries [lo, hi) in rising order.
-__device__ __noinline__ float find_bias(const LogitArgs& p, int32_t lo, int32_t hi, int32_t tok) {
+template <typename Tokens, typename Values>
+__device__ __forceinline__ float find_bias(Tokens tokens, Values values, int32_t lo, int32_t hi, int32_t tok) {
   while (hi - lo > 1) {
     const int32_t mid = (lo + hi) >> 1;
-    if (p.bias_tokens[mid] <= tok) lo = mid;
+    if (tokens[mid] <= tok) lo = mid;
     else hi = mid;
   }
-  return p.bias_tokens[lo] == tok ? p.bias_values[lo] : 0.f;
+  return tokens[lo] == tok ? values[lo] : 0.f;
 }
 
 // 4, 8 or 16 bytes global -> shared without a register in between
@@ -309,9 +310,18 @@ __device__ __forceinline__ void prefetch(const void* p) {
 //
 // Most tokens were neither seen nor biased: the pass gives them a conversion, a
 // product with 1 / temperature and a select, and leaves the others out.  Those
-// are listed and taken afterwards, one a thread.
+// are listed and taken afterwards, one a thread (a row's first biases are kept
+// in shared memory for that: looked up in global memory, 16 biases a row took 15
+// us longer for 512 rows).
+//
+// 512 rows of 128000 tokens, bf16 to fp32, us: 72 without anything seen (5.6
+// TB/s), 93 with 2000 seen tokens a row; half of the rows masked, 72 and 86.
+// Beside the traffic it is the phases of a CTA, each of which begins with loads
+// that nothing hides but the other three CTAs of the SM: no stall reason is above
+// 15%, 39% of the issue slots are used.
 enum LogitRows { kWhole, kShifted, kSingle };
 
+constexpr int kLogitPlanes = 5;  // changed, sampled, allowed, biased, seen (prompt or sampled)
 constexpr int kLogitWords = kLogitMaxTiles * kLogitTile / 32;  // of a plane, in a part
 // tiles of logits in flight and CTAs an SM: 32 KB and 4 (16 bits), 48 KB and 3 (fp32)
 template <typename T>
@@ -319,7 +329,7 @@ constexpr int kLogitSlots = sizeof(T) == 2 ? 4 : 3;
 template <typename T>
 constexpr int kLogitRing = kLogitSlots<T> * kLogitTile * static_cast<int>(sizeof(T));
 template <typename T>
-constexpr int kLogitSmem = 4 * 4 * (kLogitWords + 2) + kLogitRing<T>;
+constexpr int kLogitSmem = kLogitPlanes * 4 * (kLogitWords + 2) + kLogitRing<T>;
 
 template <typename TI, typename TO, int kRows>
 __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) process_logits_kernel(const LogitArgs p) {
@@ -330,7 +340,10 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
   constexpr int kSlots = kLogitSlots<TI>;
   extern __shared__ __align__(16) unsigned char lsmem[];
   TI* ring = reinterpret_cast<TI*>(lsmem);
-  uint32_t* plane = reinterpret_cast<uint32_t*>(lsmem + kLogitRing<TI>);  // prompt, sampled, allowed, biased
+  uint32_t* plane = reinterpret_cast<uint32_t*>(lsmem + kLogitRing<TI>);
+  __shared__ int32_t s_tok[kLogitThreads];  // the row's first biases
+  __shared__ float s_val[kLogitThreads];
+  __shared__ int32_t s_total, s_listed;  // tokens of plane 0, of the list
   constexpr int kPlane = kLogitWords + 2;
 
   const int32_t row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts;
@@ -364,6 +377,8 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
   int32_t tok = -1, before = -2;
   if (lo + static_cast<int32_t>(threadIdx.x) < hi) {
     tok = p.bias_tokens[lo + threadIdx.x];
+    s_tok[threadIdx.x] = tok;
+    s_val[threadIdx.x] = p.bias_values[lo + threadIdx.x];
     if (threadIdx.x > 0) before = p.bias_tokens[lo + threadIdx.x - 1];
   }
 #pragma unroll 4
@@ -375,6 +390,7 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
     plane[2 * kPlane + i] = mask ? in_row ? mask[w] : 0u : 0xffffffffu;
     plane[3 * kPlane + i] = 0u;
   }
+  if (threadIdx.x == 0) s_total = s_listed = 0;
   const float rho = p.repetition ? p.repetition[row] : 1.f;
   const float freq = p.frequency ? p.frequency[row] : 0.f;
   const float pres = p.presence ? p.presence[row] : 0.f;
@@ -401,16 +417,22 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
   // from here plane 0 has the tokens that a bias or penalty changes: seen or
   // biased, and allowed, without those of the neighbouring parts in a shifted
   // row's first and last word; the counts of the sampled ones are on their way to L2
+  int total = 0;
   for (int i = threadIdx.x; i < nwords; i += kLogitThreads) {
     const int32_t v = 32 * (word0 + i);
     uint32_t own = plane[2 * kPlane + i];
     if (v < begin) own = own >> (begin - v) << (begin - v);
     if (end - v < 32) own &= (1u << (end - v)) - 1;
-    const uint32_t had = plane[kPlane + i] & own;
-    plane[i] = (plane[i] | plane[kPlane + i] | plane[3 * kPlane + i]) & own;
+    const uint32_t had = plane[kPlane + i] & own, any = plane[i] | plane[kPlane + i];
+    plane[4 * kPlane + i] = any;
+    const uint32_t changed = (any | plane[3 * kPlane + i]) & own;
+    plane[i] = changed;
+    total += __popc(changed);
     const int32_t* c = p.counts + (static_cast<int64_t>(id) * p.W + word0 + i) * 32;
     for (uint32_t m = had; m; m &= m - 1) prefetch(c + __ffs(m) - 1);
   }
+  total = __reduce_add_sync(0xffffffffu, total);
+  if ((threadIdx.x & 31) == 0 && total) atomicAdd(&s_total, total);
   __syncthreads();
 
   const TI* in = static_cast<const TI*>(p.logits) + row * p.ld_in;
@@ -533,34 +555,48 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
   // that every thread has as many as the next: a branch in the pass would cost
   // every warp that has one of them.
   uint16_t* list = reinterpret_cast<uint16_t*>(lsmem);
-  constexpr int kListWords = 2 * kLogitThreads;  // 16384 tokens: 32 KB of list
-  __shared__ int32_t warp_sum[kLogitThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int w0 = 0; w0 < nwords; w0 += kListWords) {
-    const int i = w0 + 2 * threadIdx.x;
-    const uint32_t a = i < nwords ? plane[i] : 0u, b = i + 1 < nwords ? plane[i + 1] : 0u;
-    const int mine = __popc(a) + __popc(b);
-    int at = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, at, d);
-      if (lane >= d) at += u;
-    }
+  constexpr int kList = kLogitRing<TI> / 2;  // entries
+  const int lane = threadIdx.x & 31;
+  const int window = s_total <= kList ? nwords : kList / 32;  // words whose tokens the list has room for
+  for (int w0 = 0; w0 < nwords && s_total > 0; w0 += window) {
     __syncthreads();  // the ring, and the list before
-    if (lane == 31) warp_sum[warp] = at;
-    __syncthreads();
-    int total = 0;
-    at -= mine;
-#pragma unroll
-    for (int k = 0; k < kLogitThreads / 32; ++k) {
-      if (k < warp) at += warp_sum[k];
-      total += warp_sum[k];
+    if (w0 > 0) {
+      if (threadIdx.x == 0) s_listed = 0;
+      __syncthreads();
     }
-    for (uint32_t m = a; m; m &= m - 1) list[at++] = static_cast<uint16_t>(64 * threadIdx.x + __ffs(m) - 1);
-    for (uint32_t m = b; m; m &= m - 1) list[at++] = static_cast<uint16_t>(64 * threadIdx.x + 31 + __ffs(m));
+    const int w1 = min(nwords, w0 + window);
+    for (int at_w = w0 + (threadIdx.x & ~31); at_w < w1; at_w += kLogitThreads) {
+      const int w = at_w + lane;
+      const uint32_t m = w < w1 ? plane[w] : 0u;
+      const int n = __popc(m);
+      if (!__any_sync(0xffffffffu, n)) continue;
+      int at = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= d) at += u;
+      }
+      int base = 0;
+      if (lane == 31) base = atomicAdd(&s_listed, at);
+      at += __shfl_sync(0xffffffffu, base, 31) - n;
+      // words of a few tokens each by its lane, full ones by the warp (frequent
+      // tokens are neighbours: each by its lane took 98 us instead of 93)
+      constexpr int kFew = 4;
+      if (n <= kFew) {
+        int a = at;
+        for (uint32_t x = m; x; x &= x - 1) list[a++] = static_cast<uint16_t>(32 * w + __ffs(x) - 1);
+      }
+      for (uint32_t full = __ballot_sync(0xffffffffu, n > kFew); full; full &= full - 1) {
+        const int src = __ffs(full) - 1;
+        const uint32_t x = __shfl_sync(0xffffffffu, m, src);
+        const int a = __shfl_sync(0xffffffffu, at, src);
+        if (x >> lane & 1) list[a + __popc(x & ((1u << lane) - 1))] = static_cast<uint16_t>(32 * (at_w + src) + lane);
+      }
+    }
     __syncthreads();
+    const int listed = s_listed;
     constexpr int kAtOnce = 4;  // tokens of a thread whose loads are in flight together
-    for (int e0 = threadIdx.x; e0 < total; e0 += kAtOnce * kLogitThreads) {
+    for (int e0 = threadIdx.x; e0 < listed; e0 += kAtOnce * kLogitThreads) {
       int k[kAtOnce], sh[kAtOnce];
       int32_t n[kAtOnce];
       TI q[kAtOnce];
@@ -569,8 +605,8 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
         const int e = e0 + j * kLogitThreads;
         k[j] = -1;
         n[j] = 0;
-        if (e >= total) continue;
-        k[j] = w0 + (list[e] >> 5);
+        if (e >= listed) continue;
+        k[j] = list[e] >> 5;
         sh[j] = list[e] & 31;
         const int32_t v = 32 * (word0 + k[j]) + sh[j];
         q[j] = in[v];
@@ -583,8 +619,9 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
         float x = to_f(q[j]);
         bool had = true;
         if (plane[3 * kPlane + k[j]] >> sh[j] & 1) {
-          x += find_bias(p, lo, hi, v);
-          had = seen && (seen[word0 + k[j]] | seen[p.W + word0 + k[j]]) >> sh[j] & 1;
+          x += hi - lo <= kLogitThreads ? find_bias(s_tok, s_val, 0, hi - lo, v)
+                                        : find_bias(p.bias_tokens, p.bias_values, lo, hi, v);
+          had = plane[4 * kPlane + k[j]] >> sh[j] & 1;
         }
         if (had) x = x <= 0.f ? x * rho : divide ? __fdiv_rn(x, rho) : x * rinv;
         if (n[j] > 0) x = x - __fmul_rn(freq, static_cast<float>(n[j])) - pres;
