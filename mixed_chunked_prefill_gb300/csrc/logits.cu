@@ -680,26 +680,16 @@ int launch_update_token_counts(const int32_t* request_ids, int32_t num_rows,
     if (e != cudaSuccess) return static_cast<int>(e);
   }
   if (num_tokens == 0) return 0;
-  cudaLaunchAttribute beside = {};  // begins while the rows are cleared
-  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  beside.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = st;
-  cfg.attrs = &beside;
-  cfg.numAttrs = flags & MCP_COUNT_RESET ? 1 : 0;
+  const bool beside = flags & MCP_COUNT_RESET;  // begins while the rows are cleared
   if (cu_tokens && num_tokens >= kMarkTokens && num_tokens / num_rows >= (a.prompt ? kMarkRow : kCountRow)) {
     const int32_t sms = step_num_sms();
     int32_t chunk = ((num_tokens + sms - 1) / sms + kMarkThreads - 1) / kMarkThreads * kMarkThreads;
     if (chunk < 2 * kMarkThreads) chunk = 2 * kMarkThreads;
     const int32_t words = ((vocab_size < kMapTokens ? vocab_size : kMapTokens) + 31) / 32;
-    cfg.gridDim = dim3((num_tokens - 1) / chunk + 1);
-    cfg.blockDim = dim3(kMarkThreads);
-    cfg.dynamicSmemBytes = 4 * words;
-    return static_cast<int>(cudaLaunchKernelEx(&cfg, mark_texts_kernel, a, chunk));
+    return launch_beside(mark_texts_kernel, beside, (num_tokens - 1) / chunk + 1, kMarkThreads, 4 * words, st, a,
+                         chunk);
   }
-  cfg.gridDim = dim3((num_tokens - 1) / kCountThreads + 1);
-  cfg.blockDim = dim3(kCountThreads);
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, add_tokens_kernel, a));
+  return launch_beside(add_tokens_kernel, beside, (num_tokens - 1) / kCountThreads + 1, kCountThreads, 0, st, a);
 }
 
 int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,

@@ -526,8 +526,11 @@ struct ShortCfg {
 
 template <typename T, int N>
 __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const ScanArgs p) {
+  // nothing here depends on the long segments' launches, which this one may run
+  // beside; it ends behind them
   if (blockIdx.x == 0) {
     check_segments(p.g);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   using C = ShortCfg<N>;
@@ -976,6 +979,7 @@ template <typename T, int N, bool kFirst>
 __global__ void __launch_bounds__(32 * long_warps(N), 1) scan_long_kernel(const ScanArgs p) {
   using C = LongCfg<N>;
   extern __shared__ __align__(16) unsigned char smem[];
+  asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned char* mine = smem + warp * C::kWarpBytes;
   LongScan<T, N> w{p, mine, reinterpret_cast<float*>(mine + 2 * C::kRaw)};
@@ -1009,6 +1013,7 @@ __global__ void __launch_bounds__(32 * long_warps(N), 1) scan_long_kernel(const 
     }
   };
   chunk();
+  if (!kFirst) asm volatile("griddepcontrol.wait;" ::: "memory");  // the carry is over
   while (true) {
     const int32_t at = task / p.blocks;
     while (at >= base + __shfl_sync(0xffffffffu, incl, 31)) {
@@ -1078,6 +1083,7 @@ __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const ScanArg
   const int lane = threadIdx.x & 31;
   const int64_t state = static_cast<int64_t>(p.channels) * N;
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * kCarryThreads + threadIdx.x) * 4;
+  asm volatile("griddepcontrol.launch_dependents;");
   const bool live = at < state;
   const int32_t c = live ? static_cast<int32_t>(at / N) : 0;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1085,6 +1091,7 @@ __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const ScanArg
   const float* sums = p.carries + c;
   float* ends = p.carries + static_cast<int64_t>(p.slots) * p.channels + (live ? at : 0);
   const int32_t piece = piece_of(p, static_cast<int64_t>(p.g.sms) * LongCfg<N>::kWarps);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the first launch is over
   int32_t slot0 = 0;
   for (int32_t s0 = 0; s0 < p.g.S; s0 += 32) {
     Segment m = {0, 0, -1, 0};
@@ -1157,15 +1164,16 @@ int scan_launch(ScanArgs a, cudaStream_t st) {
     const unsigned grid = static_cast<unsigned>(ctas < sms ? ctas : sms);
     if (const int e = allow_smem<scan_long_kernel<T, N, true>>(C::kSmem)) return e;
     if (const int e = allow_smem<scan_long_kernel<T, N, false>>(C::kSmem)) return e;
-    scan_long_kernel<T, N, true><<<grid, 32 * C::kWarps, C::kSmem, st>>>(l);
+    if (const int e = launch_beside(scan_long_kernel<T, N, true>, false, grid, 32 * C::kWarps, C::kSmem, st, l))
+      return e;
     if (l.piece > 0) {
       const int64_t quads = static_cast<int64_t>(a.channels) * N / 4;
-      scan_carry_kernel<N><<<static_cast<unsigned>((quads + kCarryThreads - 1) / kCarryThreads),
-                             kCarryThreads, 0, st>>>(l);
-      scan_long_kernel<T, N, false><<<grid, 32 * C::kWarps, C::kSmem, st>>>(l);
+      if (const int e = launch_beside(scan_carry_kernel<N>, true, (quads + kCarryThreads - 1) / kCarryThreads,
+                                      kCarryThreads, 0, st, l))
+        return e;
+      if (const int e = launch_beside(scan_long_kernel<T, N, false>, true, grid, 32 * C::kWarps, C::kSmem, st, l))
+        return e;
     }
-    const cudaError_t f = cudaGetLastError();
-    if (f != cudaSuccess) return static_cast<int>(f);
   }
   // without the long kernel this one takes segments of any length
   a.short_max = any_long ? kShortTokens : 0x7fffffff;
@@ -1176,8 +1184,7 @@ int scan_launch(ScanArgs a, cudaStream_t st) {
   a.split = static_cast<int32_t>(want < a.g.S ? want : a.g.S);
   const int64_t warps = static_cast<int64_t>(a.blocks) * a.split;
   const int64_t grid = (warps + kShortThreads / 32 - 1) / (kShortThreads / 32) + 1;
-  scan_short_kernel<T, N><<<static_cast<unsigned>(grid), kShortThreads, 0, st>>>(a);
-  return static_cast<int>(cudaGetLastError());
+  return launch_beside(scan_short_kernel<T, N>, any_long, grid, kShortThreads, 0, st, a);
 }
 template <typename T>
 int scan_states(const ScanArgs& a, int N, cudaStream_t st) {

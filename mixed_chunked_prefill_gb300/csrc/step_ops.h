@@ -44,6 +44,26 @@ int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,
 // SMs of the current device (read once per device and thread).
 int step_num_sms();
 
+// Launch a kernel that may begin beside the launch before it on the stream
+// (`beside`: programmatic stream serialization).  It must not touch what that
+// launch writes before its griddepcontrol.wait, and must come to that wait, so
+// that what follows on the stream follows both.  0 or a cudaError_t value.
+template <typename... P>
+int launch_beside(void (*kernel)(P...), bool beside, int64_t grid, int block, size_t smem, cudaStream_t st,
+                  const P&... args) {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &a;
+  cfg.numAttrs = beside ? 1 : 0;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
 // Allow `kernel` up to `bytes` of dynamic shared memory on the current device,
 // the same `bytes` in every call (done once per device: the attribute stays).
 // 0 or a cudaError_t value.

@@ -437,17 +437,7 @@ int launch_commit_step(const mcp_request_pool& pool, const int32_t* request_ids,
   commit_kernel<<<grid_of(units), kThreads, smem, st>>>(a, true, false);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return static_cast<int>(e);
-  cudaLaunchAttribute beside = {};
-  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  beside.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &beside;
-  cfg.numAttrs = 1;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, commit_kernel, a, false, true));
+  return launch_beside(commit_kernel, true, 1, kThreads, smem, st, a, false, true);
 }
 
 }  // namespace mcp
