@@ -1077,6 +1077,7 @@ __global__ void __launch_bounds__(32 * long_warps(N), 1) scan_long_kernel(const 
 // ended with from zero, in place.  A warp takes 128 states (four a lane) along
 // every cut segment; the loads do not depend on each other.
 constexpr int kCarryThreads = 128;
+constexpr int kCarryLoads = 16;  // pieces whose loads are in flight together
 
 template <int N>
 __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const ScanArgs p) {
@@ -1110,16 +1111,24 @@ __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const ScanArg
       const int32_t slot = slot0 + __shfl_sync(0xffffffffu, incl, from) - n;
       if (!live || slot + n > p.slots) continue;
       float4 h = *reinterpret_cast<const float4*>(ends + slot * state);
-#pragma unroll 4
-      for (int32_t j = 1; j < n; ++j) {
-        const float s = sums[static_cast<int64_t>(slot + j) * p.channels] * kLog2e;
-        float4* e = reinterpret_cast<float4*>(ends + (slot + j) * state);
-        const float4 v = *e;
-        h.x = fmaf(ex2(s * a.x), h.x, v.x);
-        h.y = fmaf(ex2(s * a.y), h.y, v.y);
-        h.z = fmaf(ex2(s * a.z), h.z, v.z);
-        h.w = fmaf(ex2(s * a.w), h.w, v.w);
-        *e = h;
+      for (int32_t j0 = 1; j0 < n; j0 += kCarryLoads) {
+        float s[kCarryLoads];
+        float4 v[kCarryLoads];
+#pragma unroll
+        for (int j = 0; j < kCarryLoads; ++j) {
+          if (j0 + j >= n) break;
+          s[j] = sums[static_cast<int64_t>(slot + j0 + j) * p.channels] * kLog2e;
+          v[j] = *reinterpret_cast<const float4*>(ends + (slot + j0 + j) * state);
+        }
+#pragma unroll
+        for (int j = 0; j < kCarryLoads; ++j) {
+          if (j0 + j >= n) break;
+          h.x = fmaf(ex2(s[j] * a.x), h.x, v[j].x);
+          h.y = fmaf(ex2(s[j] * a.y), h.y, v[j].y);
+          h.z = fmaf(ex2(s[j] * a.z), h.z, v[j].z);
+          h.w = fmaf(ex2(s[j] * a.w), h.w, v[j].w);
+          *reinterpret_cast<float4*>(ends + (slot + j0 + j) * state) = h;
+        }
       }
     }
     slot0 += __shfl_sync(0xffffffffu, incl, 31);
