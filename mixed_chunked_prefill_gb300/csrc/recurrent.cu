@@ -177,9 +177,10 @@ __device__ void check_segments(const Segments& g) {
 // segment's inputs and, before them, the K - 1 inputs its request kept.
 //
 // Each input is read once and each output written once.  Segments of at most 4
-// tokens (decodes) get a CTA per segment and 512 channels: all their inputs and
-// kept inputs are requested at once, which is what their few microseconds
-// consist of.  The tokens of longer segments are dealt in runs of TT: a thread
+// tokens (decodes) get a CTA per two of them and 512 channels: the kept inputs
+// and first tokens of both are requested at once, which is what their few
+// microseconds consist of (1000 decodes of 8192 channels: 27 us, 4.8 TB/s; one, three
+// or four segments a CTA 31, 32 and 33 us).  The tokens of longer segments are dealt in runs of TT: a thread
 // carries the K - 1 last inputs of 4 channels in registers, so only the first
 // tokens of a run read inputs again (HBM-bound; 64 registers, so that 32 warps
 // an SM have 4 loads of 8 bytes in flight a thread).  The run that holds a segment's first token also takes its next K - 2
@@ -249,35 +250,62 @@ struct ConvLane {
   }
 };
 
-// A whole segment of at most kShortTokens tokens.
+// kPack whole segments of at most kShortTokens tokens, from s on.
+constexpr int kPack = 2;
 template <typename T, int K>
 __device__ __forceinline__ void conv_short(const ConvArgs& p, int32_t s, int32_t c) {
   using L = ConvLane<T, K>;
   L lane;
   lane.load(p, c);
-  const Segment g = read_segment(p.g, s);
-  const int32_t len = g.q1 - g.q0;
-  if (g.id < 0 || len <= 0 || len > kShortTokens) return;
-  const uint2* X = reinterpret_cast<const uint2*>(static_cast<const T*>(p.x) + g.q0 * p.ldx + c);
-  uint2* O = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + g.q0 * p.ldo + c);
-  uint2* kept = reinterpret_cast<uint2*>(static_cast<T*>(p.state) +
-                                         static_cast<int64_t>(g.id) * (K - 1) * p.channels + c);
-  uint2 raw[K - 1 + kShortTokens];  // the kept inputs, then the segment's
+  Segment g[kPack];
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) raw[k] = g.old ? kept[k * (p.channels / 4)] : make_uint2(0u, 0u);
+  for (int e = 0; e < kPack; ++e) {
+    g[e] = {0, 0, -1, 0};
+    if (s + e < p.g.S) g[e] = read_segment(p.g, s + e);
+  }
+  const int64_t ldx = p.ldx / 4, ldo = p.ldo / 4, lds = p.channels / 4;
+  const uint2* X[kPack];
+  uint2* kept[kPack];
+  uint2 raw[kPack][K];  // the kept inputs and the first token's
 #pragma unroll
-  for (int i = 0; i < kShortTokens; ++i)
-    raw[K - 1 + i] = i < len ? X[i * (p.ldx / 4)] : make_uint2(0u, 0u);
-  typename L::Four v[K - 1 + kShortTokens];
+  for (int e = 0; e < kPack; ++e) {
+    const int32_t len = g[e].q1 - g[e].q0;
+    if (len <= 0 || len > kShortTokens) g[e].id = -1;
+    if (g[e].id < 0) continue;
+    X[e] = reinterpret_cast<const uint2*>(static_cast<const T*>(p.x) + g[e].q0 * p.ldx + c);
+    kept[e] = reinterpret_cast<uint2*>(static_cast<T*>(p.state) +
+                                       static_cast<int64_t>(g[e].id) * (K - 1) * p.channels + c);
 #pragma unroll
-  for (int i = 0; i < K - 1 + kShortTokens; ++i) v[i] = L::widen(raw[i]);
+    for (int k = 0; k < K - 1; ++k) raw[e][k] = g[e].old ? kept[e][k * lds] : make_uint2(0u, 0u);
+    raw[e][K - 1] = X[e][0];
+  }
 #pragma unroll
-  for (int i = 0; i < kShortTokens; ++i) {
-    if (i < len) O[i * (p.ldo / 4)] = lane.token(v + i);
-    if (i + 1 == len) {
+  for (int e = 0; e < kPack; ++e) {
+    if (g[e].id < 0) continue;
+    const int32_t len = g[e].q1 - g[e].q0;
+    uint2* O = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + g[e].q0 * p.ldo + c);
+    uint2 more[kShortTokens - 1];
 #pragma unroll
-      for (int k = 0; k < K - 1; ++k) kept[k * (p.channels / 4)] = raw[i + 1 + k];
+    for (int i = 1; i < kShortTokens; ++i)
+      if (i < len) more[i - 1] = X[e][i * ldx];
+    typename L::Four win[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) win[k] = L::widen(raw[e][k]);
+    O[0] = lane.token(win);
+#pragma unroll
+    for (int i = 1; i < kShortTokens; ++i) {
+      if (i >= len) break;
+#pragma unroll
+      for (int k = 0; k + 1 < K; ++k) {
+        win[k] = win[k + 1];
+        raw[e][k] = raw[e][k + 1];
+      }
+      raw[e][K - 1] = more[i - 1];
+      win[K - 1] = L::widen(more[i - 1]);
+      O[i * ldo] = lane.token(win);
     }
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) kept[e][k * lds] = raw[e][k + 1];
   }
 }
 
@@ -289,11 +317,12 @@ __global__ void __launch_bounds__(kConvThreads, 8) mixed_conv_kernel(const ConvA
   }
   const int32_t c = ((blockIdx.x - 1) % p.blocks * kConvThreads + threadIdx.x) * kConvCh;
   int32_t tile = (blockIdx.x - 1) / p.blocks;
-  if (tile < p.g.S) {
-    if (c < p.channels) conv_short<T, K>(p, tile, c);
+  const int32_t packs = (p.g.S + kPack - 1) / kPack;
+  if (tile < packs) {
+    if (c < p.channels) conv_short<T, K>(p, tile * kPack, c);
     return;
   }
-  tile -= p.g.S;
+  tile -= packs;
   using L = ConvLane<T, K>;
   constexpr int kBatch = 4;  // inputs requested together
   __shared__ Segment info[kConvMaxRun + K];
@@ -1219,7 +1248,7 @@ ConvCut conv_cut(const mcp_conv_desc& d) {
     if (c.tokens == 8 || tiles * c.blocks >= 4 * step_num_sms()) break;
   }
   if (d.total_tokens <= kShortTokens) tiles = 0;
-  c.grid = (d.num_seqs + tiles) * c.blocks + 1;
+  c.grid = ((d.num_seqs + kPack - 1) / kPack + tiles) * c.blocks + 1;
   return c;
 }
 
