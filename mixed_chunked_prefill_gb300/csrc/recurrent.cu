@@ -194,7 +194,7 @@ struct ConvArgs {
   void* state;       // [R, K - 1, channels]
   void* out;
   int64_t ldx, ldo;
-  int32_t channels, act, tokens, blocks;  // tokens: TT; blocks: CTAs across the channels
+  int32_t channels, act, tokens, runs, blocks;  // tokens: TT; blocks: CTAs across the channels
 };
 
 constexpr int kConvThreads = 128;
@@ -316,13 +316,13 @@ __global__ void __launch_bounds__(kConvThreads, 8) mixed_conv_kernel(const ConvA
     return;
   }
   const int32_t c = ((blockIdx.x - 1) % p.blocks * kConvThreads + threadIdx.x) * kConvCh;
-  int32_t tile = (blockIdx.x - 1) / p.blocks;
-  const int32_t packs = (p.g.S + kPack - 1) / kPack;
-  if (tile < packs) {
-    if (c < p.channels) conv_short<T, K>(p, tile * kPack, c);
+  const int32_t tile = (blockIdx.x - 1) / p.blocks;
+  // the runs first: they take longest (2048 tokens and 64 decodes of 8192
+  // channels 17.3 us, behind the decodes 18.0)
+  if (tile >= p.runs) {
+    if (c < p.channels) conv_short<T, K>(p, (tile - p.runs) * kPack, c);
     return;
   }
-  tile -= packs;
   using L = ConvLane<T, K>;
   constexpr int kBatch = 4;  // inputs requested together
   __shared__ Segment info[kConvMaxRun + K];
@@ -1232,9 +1232,9 @@ int scan_states(const ScanArgs& a, int N, cudaStream_t st) {
   return scan_launch<T, 64>(a, st);
 }
 
-// How a convolution is dealt out: tokens of a run, CTAs across the channels.
+// How a convolution is dealt out: tokens of a run, runs, CTAs across the channels.
 struct ConvCut {
-  int32_t tokens, blocks;
+  int32_t tokens, runs, blocks;
   int64_t grid;
 };
 ConvCut conv_cut(const mcp_conv_desc& d) {
@@ -1242,19 +1242,21 @@ ConvCut conv_cut(const mcp_conv_desc& d) {
   c.blocks = (d.channels / kConvCh + kConvThreads - 1) / kConvThreads;
   // runs: long ones read fewer inputs twice (K - 1 in TT), shorter ones keep
   // every SM busy when the stream is short
-  int64_t tiles = 0;
   for (c.tokens = kConvMaxRun;; c.tokens /= 2) {
-    tiles = (static_cast<int64_t>(d.total_tokens) + c.tokens - 1) / c.tokens;
-    if (c.tokens == 8 || tiles * c.blocks >= 4 * step_num_sms()) break;
+    c.runs = (d.total_tokens + c.tokens - 1) / c.tokens;
+    if (c.tokens == 8 || static_cast<int64_t>(c.runs) * c.blocks >= 4 * step_num_sms()) break;
   }
-  if (d.total_tokens <= kShortTokens) tiles = 0;
-  c.grid = ((d.num_seqs + kPack - 1) / kPack + tiles) * c.blocks + 1;
+  if (d.total_tokens <= kShortTokens) c.runs = 0;
+  c.grid = ((d.num_seqs + kPack - 1) / kPack + static_cast<int64_t>(c.runs)) * c.blocks + 1;
   return c;
 }
 
 }  // namespace
 
-bool mixed_conv_fits(const mcp_conv_desc& d) { return conv_cut(d).grid <= 0x7fffffff; }
+bool mixed_conv_fits(const mcp_conv_desc& d) {
+  const ConvCut c = conv_cut(d);  // a bound on the grid: a CTA a segment
+  return (d.num_seqs + static_cast<int64_t>(c.runs)) * c.blocks < 0x7fffffff;
+}
 
 int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight, const void* bias,
                       void* state, const int32_t* request_ids, const int32_t* cu_seqlens_q,
@@ -1273,6 +1275,7 @@ int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight,
   a.act = d.activation;
   const ConvCut cut = conv_cut(d);
   a.tokens = cut.tokens;
+  a.runs = cut.runs;
   a.blocks = cut.blocks;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return d.dtype == MCP_DTYPE_BF16 ? conv_width<__nv_bfloat16>(a, d.width, cut.grid, st)
