@@ -246,7 +246,8 @@ struct LogitArgs {
 
 constexpr int kLogitThreads = 256;
 constexpr int kLogitTile = 16 * kLogitThreads;  // tokens of one row that a CTA takes at a time
-constexpr int kLogitMaxTiles = 8;               // tiles of one CTA
+constexpr int kLogitMaxTiles = 4;               // tiles of one CTA
+constexpr int kLogitSlots = 2;                  // tiles of logits in flight
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -314,30 +315,31 @@ __device__ __forceinline__ void prefetch(const void* p) {
 // in shared memory for that: looked up in global memory, 16 biases a row took 15
 // us longer for 512 rows).
 //
-// 512 rows of 128000 tokens, bf16 to fp32, us: 72 without anything seen (5.6
-// TB/s), 93 with 2000 seen tokens a row; half of the rows masked, 72 and 86.
+// 512 rows of 128000 tokens, bf16 to fp32, us: 65 without anything seen (6.3
+// TB/s), 76 with 2000 seen tokens a row; half of the rows masked, 63 and 74.
 // Beside the traffic it is the phases of a CTA, each of which begins with loads
-// that nothing hides but the other three CTAs of the SM: no stall reason is above
-// 15%, 39% of the issue slots are used.
+// that nothing hides but the SM's other CTAs.
 enum LogitRows { kWhole, kShifted, kSingle };
 
 constexpr int kLogitPlanes = 5;  // changed, sampled, allowed, biased, seen (prompt or sampled)
 constexpr int kLogitWords = kLogitMaxTiles * kLogitTile / 32;  // of a plane, in a part
-// tiles of logits in flight and CTAs an SM: 32 KB and 4 (16 bits), 48 KB and 3 (fp32)
+// CTAs of an SM: tiles in flight beyond two, or longer parts, are worth less than
+// more CTAs (512 rows of 128000, us: 6 CTAs of 4 tiles 74, of 2 77, of 6 82; 5 CTAs
+// with three in flight 75; 4 CTAs of 8 tiles with four in flight 83).
 template <typename T>
-constexpr int kLogitSlots = sizeof(T) == 2 ? 4 : 3;
+constexpr int kLogitCtas = sizeof(T) == 2 ? 6 : 4;
 template <typename T>
-constexpr int kLogitRing = kLogitSlots<T> * kLogitTile * static_cast<int>(sizeof(T));
+constexpr int kLogitRing = kLogitSlots * kLogitTile * static_cast<int>(sizeof(T));
 template <typename T>
 constexpr int kLogitSmem = kLogitPlanes * 4 * (kLogitWords + 2) + kLogitRing<T>;
 
 template <typename TI, typename TO, int kRows>
-__global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) process_logits_kernel(const LogitArgs p) {
+__global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_kernel(const LogitArgs p) {
   constexpr int kVec = kRows == kSingle ? 1 : 4;
   constexpr int kGroups = kLogitTile / kLogitThreads / kVec;  // of a thread and tile
   constexpr uint32_t kAll = (1u << kVec) - 1;
   constexpr bool kAsync = kVec * sizeof(TI) >= 4;
-  constexpr int kSlots = kLogitSlots<TI>;
+  constexpr int kSlots = kLogitSlots;
   extern __shared__ __align__(16) unsigned char lsmem[];
   TI* ring = reinterpret_cast<TI*>(lsmem);
   uint32_t* plane = reinterpret_cast<uint32_t*>(lsmem + kLogitRing<TI>);
@@ -398,9 +400,11 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
   const bool scale = temp > 0.f && temp != 1.f;
   const bool every = !p.inplace || scale;
   // quotients as products: one rounding more, a tenth of the instructions;
-  // divisors whose reciprocal overflows divide
-  const float inv = scale ? 1.f / temp : 1.f, rinv = 1.f / rho;
-  const bool divide = inv > 3.4e38f || rinv > 3.4e38f;
+  // a temperature whose reciprocal overflows (subnormal) is taken 2^64 times, and
+  // its quotients again; such a repetition penalty divides
+  const float after = scale && temp < 1e-37f ? 0x1p64f : 1.f;
+  const float inv = scale ? 1.f / (temp * after) : 1.f, rinv = 1.f / rho;
+  const bool divide = rinv > 3.4e38f;
   __syncthreads();
   for (int32_t e = lo + threadIdx.x; e < hi; e += kLogitThreads) {
     if (e != lo + static_cast<int32_t>(threadIdx.x)) {
@@ -456,7 +460,7 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
   };
   auto whole_tile = [&](int32_t base) { return base >= 0 && base + kLogitTile <= end; };
   // x / temperature, or the masked value
-  auto finish = [&](float x) { return divide ? scale ? __fdiv_rn(x, temp) : x : x * inv; };
+  auto finish = [&](float x) { return x * inv * after; };
   auto put = [&](int32_t v, const float* x, uint32_t touch) {
     Vec<TO, kVec> y;
 #pragma unroll
@@ -633,10 +637,10 @@ __global__ void __launch_bounds__(kLogitThreads, sizeof(TI) == 2 ? 4 : 3) proces
 
 template <typename TI, typename TO, int kRows>
 int logits_rows(const LogitArgs& a, cudaStream_t st) {
-  if (const int e = allow_smem<process_logits_kernel<TI, TO, kRows>>(kLogitSmem<TI>)) return e;
+  constexpr auto kernel = process_logits_kernel<TI, TO, kRows>;
+  if (const int e = allow_smem<kernel>(kLogitSmem<TI>)) return e;
   const int64_t grid = static_cast<int64_t>(a.rows) * a.parts;
-  process_logits_kernel<TI, TO, kRows>
-      <<<static_cast<unsigned>(grid), kLogitThreads, kLogitSmem<TI>, st>>>(a);
+  kernel<<<static_cast<unsigned>(grid), kLogitThreads, kLogitSmem<TI>, st>>>(a);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -718,11 +722,11 @@ int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,
   a.R = d.num_requests;
   a.num_bias = d.num_biases;
   a.num_masks = d.num_masks;
-  // a CTA reads its row's parameters, bits and biases once for several tiles:
-  // as few CTAs as find a place on the SMs together (a second wave would wait
-  // for its own first loads again), up to the tiles that shared memory has bits for
+  // a CTA reads its row's parameters, bits and biases once for several tiles
+  // where there are enough for every SM: four CTAs each (64 rows in place, three
+  // and four tiles a CTA: 12.2 us both, two 13.2)
   const int64_t row_tiles = (d.vocab_size + 3LL + kLogitTile - 1) / kLogitTile;  // shifted by up to 3
-  const int64_t places = (d.dtype == MCP_DTYPE_FP32 ? 3LL : 4LL) * step_num_sms();
+  const int64_t places = 4LL * step_num_sms();
   int64_t tiles = (row_tiles * d.num_rows + places - 1) / places;
   tiles = tiles < 1 ? 1 : tiles > kLogitMaxTiles ? kLogitMaxTiles : tiles;
   tiles = tiles > row_tiles ? row_tiles : tiles;
