@@ -179,8 +179,10 @@ __device__ void check_segments(const Segments& g) {
 // Each input is read once and each output written once.  Segments of at most 4
 // tokens (decodes) get a CTA per two of them and 512 channels: the kept inputs
 // and first tokens of both are requested at once, which is what their few
-// microseconds consist of (1000 decodes of 8192 channels: 27 us, 4.8 TB/s; one, three
-// or four segments a CTA 31, 32 and 33 us).  The tokens of longer segments are dealt in runs of TT: a thread
+// microseconds consist of (1000 decodes of 8192 channels: 27 us, 4.8 TB/s; one,
+// three or four segments a CTA 31, 32 and 33 us; 256 decodes: 8.3 us).  The
+// tokens of longer segments are dealt in runs of TT (8192 tokens of 8192
+// channels: 51 us, 5.3 TB/s; runs of 32 49, but 2048 tokens then take longer): a thread
 // carries the K - 1 last inputs of 4 channels in registers, so only the first
 // tokens of a run read inputs again (HBM-bound; 64 registers, so that 32 warps
 // an SM have 4 loads of 8 bytes in flight a thread).  The run that holds a segment's first token also takes its next K - 2
@@ -523,7 +525,8 @@ __device__ __forceinline__ void softplus2(float& v0, float& v1) {
 // and inputs of the next segments in asynchronous copies to the warp's ring in
 // shared memory, and a second channel halves what a segment costs beside its
 // arithmetic (with one, 225 instructions a warp and segment kept the issue slots
-// 80% busy).
+// 80% busy).  256 decodes of 8192 channels and 16 states: 49 us, 5.8 TB/s; one
+// channel a lane 61 us.
 template <typename T>
 __device__ __forceinline__ float scalar(const T* p) {
   if constexpr (std::is_same<T, __half>::value) return __half2float(*p);

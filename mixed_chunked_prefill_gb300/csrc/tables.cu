@@ -13,7 +13,8 @@
 //
 // Work: 12 bytes per segment, 4 per held page (read) and per table entry
 // (written), 12 per token slot: a few MB at most, so latency bounds every
-// ordinary step.  One launch: every CTA computes the prefix sums of all
+// ordinary step (1024 segments with contexts up to 32768: 9.1 us, of which the
+// bytes are 1.9).  One launch: every CTA computes the prefix sums of all
 // segments for itself (two dependent loads and one block scan; S <= 8192
 // segments are 4 x 32 KB of shared memory), and its warps then write their share
 // of the table rows and token slots.  A second launch that waited for the sums
