@@ -433,9 +433,11 @@ def _error(error_word, dev):
 
 def _launch(where, dev, stream, fn, *args):
     """Call ``fn(*args, stream)`` with ``dev`` as the current device."""
-    import torch
+    if _current_device is None:
+        _bind()
+    if dev != _current_device():
+        import torch
 
-    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _launch(where, dev, stream, fn, *args)
     if stream is None:
@@ -451,9 +453,11 @@ def _launch(where, dev, stream, fn, *args):
 
 def _launch_free(where, dev, fn, *args):
     """Call ``fn(*args)``, which takes no stream, with ``dev`` as the current device."""
-    import torch
+    if _current_device is None:
+        _bind()
+    if dev != _current_device():
+        import torch
 
-    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _launch_free(where, dev, fn, *args)
     st = fn(*args)
@@ -461,12 +465,18 @@ def _launch_free(where, dev, fn, *args):
         _capi.check(st, where)
 
 
-def _raw_stream(dev) -> int:
-    """The current stream of device ``dev`` (without a Stream object, where torch allows it)."""
+_current_device = _raw_stream = None
+
+
+def _bind():
+    """What a call asks torch for: the current device, and the current stream of a device
+    (without a Stream object, where torch allows it)."""
+    global _current_device, _raw_stream
     import torch
 
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(dev) if get is not None else torch.cuda.current_stream(dev).cuda_stream
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _empty(shape, dtype, device, stream, result=False):
@@ -505,7 +515,15 @@ def make_request_pool(request_pages, request_lens, free_pages, free_count,
         _arg(free_pages, i32, "free_pages", dev),
         _arg(free_count, i32, "free_count", dev, (1,)))
     pool.tensors = (request_pages, request_lens, free_pages, free_count)
+    pool.device = dev
     return pool
+
+
+def _pool_device(pool, request_ids) -> int:
+    dev = _gpu(request_ids, "request_ids")
+    if getattr(pool, "device", dev) != dev:
+        raise ValueError(f"request_ids must be on cuda:{pool.device}, where the pool is")
+    return dev
 
 
 def build_step_tables(pool: RequestPool, request_ids, q_lens, cu_seqlens_q, seqlens_k,
@@ -517,7 +535,7 @@ def build_step_tables(pool: RequestPool, request_ids, q_lens, cu_seqlens_q, seql
     logits_indices [S] out, all int32 CUDA tensors otherwise."""
     import torch
 
-    dev, i32 = _gpu(request_ids, "request_ids"), torch.int32
+    dev, i32 = _pool_device(pool, request_ids), torch.int32
     S, cap = int(request_ids.shape[0]), int(slot_mapping.shape[0])
     one = (S,)
     _launch("build_step_tables", dev, stream, load().mcp_build_step_tables, ctypes.byref(pool),
@@ -536,7 +554,7 @@ def commit_step(pool: RequestPool, request_ids, q_lens, new_lens=None, error_wor
     stays, 0: the request is over) and pages behind them return to the pool."""
     import torch
 
-    dev, i32 = _gpu(request_ids, "request_ids"), torch.int32
+    dev, i32 = _pool_device(pool, request_ids), torch.int32
     one = (int(request_ids.shape[0]),)
     _launch("commit_step", dev, stream, load().mcp_commit_step, ctypes.byref(pool),
             _arg(request_ids, i32, "request_ids", dev, one), _arg(q_lens, i32, "q_lens", dev, one),

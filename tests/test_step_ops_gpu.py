@@ -896,6 +896,11 @@ def test_python_refusals(mcp):
         a.update(kw)
         with pytest.raises(e):
             mcp.mixed_conv(**a)
+    d = Device(mcp, 8, 16, 2, 4)
+    d.pool.device = 1  # as if it had been made there
+    for call in (lambda: d.build([1], [20], 20, None), lambda: mcp.commit_step(d.pool, ids, ids)):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
     f = torch.zeros((2, 64), device="cuda")
     with pytest.raises(ValueError):
         mcp.process_logits(f.T)
