@@ -293,9 +293,6 @@ template <int n>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
-__device__ __forceinline__ void prefetch(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
 
 // kWhole, kShifted: a thread takes 4 neighbouring tokens at a time, 8 bytes of
 // 16-bit logits in and 16 bytes of fp32 out.  A row that starts between those
@@ -420,20 +417,18 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_
 
   // from here plane 0 has the tokens that a bias or penalty changes: seen or
   // biased, and allowed, without those of the neighbouring parts in a shifted
-  // row's first and last word; the counts of the sampled ones are on their way to L2
+  // row's first and last word
   int total = 0;
   for (int i = threadIdx.x; i < nwords; i += kLogitThreads) {
     const int32_t v = 32 * (word0 + i);
     uint32_t own = plane[2 * kPlane + i];
     if (v < begin) own = own >> (begin - v) << (begin - v);
     if (end - v < 32) own &= (1u << (end - v)) - 1;
-    const uint32_t had = plane[kPlane + i] & own, any = plane[i] | plane[kPlane + i];
+    const uint32_t any = plane[i] | plane[kPlane + i];
     plane[4 * kPlane + i] = any;
     const uint32_t changed = (any | plane[3 * kPlane + i]) & own;
     plane[i] = changed;
     total += __popc(changed);
-    const int32_t* c = p.counts + (static_cast<int64_t>(id) * p.W + word0 + i) * 32;
-    for (uint32_t m = had; m; m &= m - 1) prefetch(c + __ffs(m) - 1);
   }
   total = __reduce_add_sync(0xffffffffu, total);
   if ((threadIdx.x & 31) == 0 && total) atomicAdd(&s_total, total);
@@ -569,8 +564,8 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_
       __syncthreads();
     }
     const int w1 = min(nwords, w0 + window);
-    for (int at_w = w0 + (threadIdx.x & ~31); at_w < w1; at_w += kLogitThreads) {
-      const int w = at_w + lane;
+    for (int w8 = w0 + (threadIdx.x >> 5); w8 < w1; w8 += kLogitThreads) {
+      const int w = w8 + kLogitThreads / 32 * lane;
       const uint32_t m = w < w1 ? plane[w] : 0u;
       const int n = __popc(m);
       if (!__any_sync(0xffffffffu, n)) continue;
@@ -584,7 +579,8 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_
       if (lane == 31) base = atomicAdd(&s_listed, at);
       at += __shfl_sync(0xffffffffu, base, 31) - n;
       // words of a few tokens each by its lane, full ones by the warp (frequent
-      // tokens are neighbours: each by its lane took 98 us instead of 93)
+      // tokens are neighbours: each by its lane took 98 us instead of 93); a
+      // warp's words are not neighbours, so that full ones meet in none
       constexpr int kFew = 4;
       if (n <= kFew) {
         int a = at;
@@ -594,7 +590,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_
         const int src = __ffs(full) - 1;
         const uint32_t x = __shfl_sync(0xffffffffu, m, src);
         const int a = __shfl_sync(0xffffffffu, at, src);
-        if (x >> lane & 1) list[a + __popc(x & ((1u << lane) - 1))] = static_cast<uint16_t>(32 * (at_w + src) + lane);
+        if (x >> lane & 1) list[a + __popc(x & ((1u << lane) - 1))] = static_cast<uint16_t>(32 * (w8 + kLogitThreads / 32 * src) + lane);
       }
     }
     __syncthreads();
