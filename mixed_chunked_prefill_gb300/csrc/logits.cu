@@ -313,7 +313,7 @@ __device__ __forceinline__ void copy_wait() {
 // us longer for 512 rows).
 //
 // 512 rows of 128000 tokens, bf16 to fp32, us: 65 without anything seen (6.3
-// TB/s), 76 with 2000 seen tokens a row; half of the rows masked, 63 and 74.
+// TB/s), 73 with 2000 seen tokens a row; half of the rows masked, 64 and 72.
 // Beside the traffic it is the phases of a CTA, each of which begins with loads
 // that nothing hides but the SM's other CTAs.
 enum LogitRows { kWhole, kShifted, kSingle };
@@ -578,10 +578,10 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_
       int base = 0;
       if (lane == 31) base = atomicAdd(&s_listed, at);
       at += __shfl_sync(0xffffffffu, base, 31) - n;
-      // words of a few tokens each by its lane, full ones by the warp (frequent
-      // tokens are neighbours: each by its lane took 98 us instead of 93); a
-      // warp's words are not neighbours, so that full ones meet in none
-      constexpr int kFew = 4;
+      // words of a few tokens each by its lane, full ones by the warp; a warp's
+      // words are not neighbours, as frequent tokens are: full words that met in
+      // one warp cost 64 rows 2 us
+      constexpr int kFew = 8;
       if (n <= kFew) {
         int a = at;
         for (uint32_t x = m; x; x &= x - 1) list[a++] = static_cast<uint16_t>(32 * w + __ffs(x) - 1);
@@ -719,10 +719,10 @@ int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,
   a.num_bias = d.num_biases;
   a.num_masks = d.num_masks;
   // a CTA reads its row's parameters, bits and biases once for several tiles
-  // where there are enough for every SM: four CTAs each (64 rows in place, three
-  // and four tiles a CTA: 12.2 us both, two 13.2)
+  // where there are enough for six CTAs on every SM (64 rows in place, 2000 seen
+  // tokens: 8.0 us; for three, four and eight 9.1)
   const int64_t row_tiles = (d.vocab_size + 3LL + kLogitTile - 1) / kLogitTile;  // shifted by up to 3
-  const int64_t places = 4LL * step_num_sms();
+  const int64_t places = 6LL * step_num_sms();
   int64_t tiles = (row_tiles * d.num_rows + places - 1) / places;
   tiles = tiles < 1 ? 1 : tiles > kLogitMaxTiles ? kLogitMaxTiles : tiles;
   tiles = tiles > row_tiles ? row_tiles : tiles;
