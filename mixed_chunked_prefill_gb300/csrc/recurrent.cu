@@ -1224,8 +1224,12 @@ int scan_launch(ScanArgs a, cudaStream_t st) {
   a.short_max = any_long ? kShortTokens : 0x7fffffff;
   constexpr int per = ShortCfg<N>::CPW;
   a.blocks = (a.channels + per - 1) / per;
-  // more warps than stay at once: a warp's last segments end unevenly
-  const int64_t want = (64LL * sms + a.blocks - 1) / a.blocks;
+  // more warps than stay at once (32 an SM), as a warp's last segments end
+  // unevenly; for little work one round of them, whose starts are not repeated
+  // (8192 channels, 28 and 64 warps an SM: 16 segments 6.6 and 8.0 us, 64 16.1 and
+  // 16.9, 128 28.4 and 27.7, 256 53 and 49)
+  const int64_t per_sm = static_cast<int64_t>(a.blocks) * a.g.S < 256LL * sms ? 28 : 64;
+  const int64_t want = (per_sm * sms + a.blocks - 1) / a.blocks;
   a.split = static_cast<int32_t>(want < a.g.S ? want : a.g.S);
   const int64_t warps = static_cast<int64_t>(a.blocks) * a.split;
   const int64_t grid = (warps + kShortThreads / 32 - 1) / (kShortThreads / 32) + 1;
