@@ -797,6 +797,56 @@ def test_captured_step_follows_its_inputs(mcp):
             assert (f64(lo)[i] == 3).all() if r < 0 else (np.abs(f64(lo)[i] - lw[i]) <= lb[i]).all()
 
 
+def test_captured_calls_of_several_launches(mcp):
+    """Calls that launch kernels beside each other, captured: a scan in pieces (two graphs
+    share its workspace) and texts counted on cleared rows, replayed in turn, give what the
+    same calls give one by one."""
+    rng = np.random.default_rng(33)
+    d, N, V, R = 96, 16, 3000, 4
+    sets = []
+    for k in range(2):
+        ids, cu, sk, rows, T = stream(rng, [700, 2, 333, 90, 1], [0, 3, 8, 0, 7], 1, 0)
+        v = scan_inputs(rng, T, d, N, 1, "bf16", rows, True, 1.0)
+        lens = rng.integers(1500, 4000, 6)
+        text = i32(rng.integers(0, V, lens.sum()))
+        sets.append(dict(v={n: t[1] for n, t in v.items()}, meta=[i32(a) for a in (ids, cu, sk)], T=T, text=text,
+                         rows=i32(rng.integers(0, R, 6)), cu=i32(np.concatenate([[0], np.cumsum(lens)])),
+                         state0=v["state"][1].clone(), out=torch.zeros((T, d), dtype=torch.bfloat16, device="cuda"),
+                         tok=device_state(np.zeros((R, 2, V), bool), np.zeros((R, V), np.int64))))
+    desc = _capi.ScanDesc(6, sets[0]["T"], 7, d, N, 1, 0, 1, d, d, d, N, N, d)
+    n = ctypes.c_size_t()
+    assert mcp.load().mcp_mixed_scan_workspace(ctypes.byref(desc), ctypes.byref(n)) == 0 and n.value > 256
+    shared = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+
+    def calls(s):
+        v = s["v"]
+        v["state"].copy_(s["state0"])
+        mcp.mixed_scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["state"], *s["meta"], D=v["D"], z=v["z"],
+                       dt_bias=v["bias"], out=s["out"], workspace=shared)
+        for prompt in (True, False):
+            mcp.update_token_counts(s["rows"], s["text"], *s["tok"], V, s["cu"], prompt, prompt)
+
+    want = []
+    for s in sets:
+        calls(s)
+        want.append([t.clone() for t in (s["out"], s["v"]["state"], *s["tok"])])
+    torch.cuda.synchronize()
+    graphs = []
+    for s in sets:
+        side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+            calls(s)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        shared.fill_(255)
+        for s, g in zip(sets, graphs):
+            s["out"].zero_()
+            g.replay()
+        for s, w in zip(sets, want):
+            assert all(torch.equal(a, b) for a, b in zip((s["out"], s["v"]["state"], *s["tok"]), w))
+
+
 def test_calls_on_another_stream(mcp):
     """The calls run on the stream they are given, behind what that stream already holds."""
     rng = np.random.default_rng(41)
