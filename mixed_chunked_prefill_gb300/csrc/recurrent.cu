@@ -180,7 +180,7 @@ __device__ void check_segments(const Segments& g) {
 // tokens (decodes) get a CTA per two of them and 512 channels: the kept inputs
 // and first tokens of both are requested at once, which is what their few
 // microseconds consist of (1000 decodes of 8192 channels: 27 us, 4.8 TB/s; one,
-// three or four segments a CTA 31, 32 and 33 us; 256 decodes: 8.3 us).  The
+// three or four segments a CTA 31, 32 and 33 us; 256 decodes: 8.8 us).  The
 // tokens of longer segments are dealt in runs of TT (8192 tokens of 8192
 // channels: 51 us, 5.3 TB/s; runs of 32 49, but 2048 tokens then take longer): a thread
 // carries the K - 1 last inputs of 4 channels in registers, so only the first
