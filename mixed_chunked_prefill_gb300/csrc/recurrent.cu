@@ -101,6 +101,12 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+// the smaller; NaN if one is
+__device__ __forceinline__ float least(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -487,19 +493,19 @@ struct ScanArgs {
 };
 
 // max(v, 0) + log1p(exp(-|v|)), two values at a time, to a few ulp also where
-// it is small (steps of 0.001 and less).  exp(-t) = 2^(hi + lo): hi the rounded
-// product t log2 e, lo what the rounding lost.  log1p(e) = e P(e) on [0, 1], P
+// it is small (steps of 0.001 and less).  exp(-u) = 2^(hi - lo): hi the rounded
+// product -u log2 e, lo what the rounding lost.  log1p(e) = e P(e) on [0, 1], P
 // of degree 8 from a Remez exchange on the relative error (3e-8); Horner's
 // roundings leave 3 x 2^-24 in all.
 __device__ __forceinline__ void softplus2(float& v0, float& v1) {
-  const f32x2 t = pack2(-fabsf(v0), -fabsf(v1));
-  const f32x2 L = pack2(kLog2e, kLog2e);
-  const f32x2 hi = mul2(t, L);
-  const f32x2 neg = mul2(hi, pack2(-1.f, -1.f));
+  // u = |v|, at most 128: exp(-128) is 0 in fp32, and of an infinite product
+  // nothing finite is lost
+  const f32x2 u = pack2(least(fabsf(v0), 128.f), least(fabsf(v1), 128.f));
+  const f32x2 hi = mul2(u, pack2(-kLog2e, -kLog2e));
   // log2 e - float(log2 e) = 1.925963e-8
-  const f32x2 lo = fma2(t, pack2(1.925963033e-8f, 1.925963033e-8f), fma2(t, L, neg));
+  const f32x2 lo = fma2(u, pack2(1.925963033e-8f, 1.925963033e-8f), fma2(u, pack2(kLog2e, kLog2e), hi));
   f32x2 e = ex2x2(hi);
-  e = fma2(e, mul2(lo, pack2(kLn2, kLn2)), e);
+  e = fma2(e, mul2(lo, pack2(-kLn2, -kLn2)), e);
   f32x2 q = pack2(5.2326940931379795e-3f, 5.2326940931379795e-3f);
   q = fma2(q, e, pack2(-2.950523979961872e-2f, -2.950523979961872e-2f));
   q = fma2(q, e, pack2(7.822595536708832e-2f, 7.822595536708832e-2f));
@@ -1150,7 +1156,8 @@ __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const ScanArg
 #pragma unroll
         for (int j = 0; j < kCarryLoads; ++j) {
           if (j0 + j >= n) break;
-          s[j] = sums[static_cast<int64_t>(slot + j0 + j) * p.channels] * kLog2e;
+          // finite, so that A = 0 keeps its state
+          s[j] = least(sums[static_cast<int64_t>(slot + j0 + j) * p.channels], 2e38f) * kLog2e;
           v[j] = *reinterpret_cast<const float4*>(ends + (slot + j0 + j) * state);
         }
 #pragma unroll

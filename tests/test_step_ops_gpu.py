@@ -303,6 +303,38 @@ def test_scan_of_large_and_vanishing_steps(mcp):
     assert (np.abs(f64(v["state"][1]) - end) <= ebound).all()
 
 
+@pytest.mark.parametrize("T", [1, 3, 70, 400])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_scan_of_infinite_steps(mcp, T, dtype):
+    """A step of minus infinity (or the type's lowest value) is softplus 0: the state stays
+    and the output is C h + D x, as for a step of -9984.  The highest value with x = 0 ends
+    in a state of 0, and NaN stays NaN in its own channel."""
+    rng = np.random.default_rng(T)
+    d, N = 64, 16
+    ids, cu, sk = [1], [0, T], [T + 9]
+    v = scan_inputs(rng, T, d, N, 1, dtype, 2, True, 1.0)
+    at = T // 2
+    v["A"][1][41] = 0.0
+    states, outs = [], []
+    for low in (-9984.0, float("-inf"), torch.finfo(DT[dtype]).min):
+        dt, st = v["dt"][1].clone(), v["state"][1].clone()
+        dt[at, :32] = low
+        dt[0, 32:40] = torch.finfo(DT[dtype]).max
+        dt[at, 40] = float("nan")
+        x = v["x"][1].clone()
+        x[:, 32:40] = 0
+        dt[:, 41], x[:, 41] = torch.finfo(DT[dtype]).max, 0
+        outs.append(mcp.mixed_scan(x, dt, v["A"][1], v["B"][1], v["C"][1], st, i32(ids), i32(cu), i32(sk),
+                                   D=v["D"][1], z=v["z"][1], dt_bias=v["bias"][1]))
+        states.append(st)
+    for o, s in zip(outs, states):
+        keep = torch.arange(d, device="cuda") != 40
+        assert torch.equal(o[:, keep], outs[0][:, keep]) and torch.equal(s[:, keep], states[0][:, keep])
+        assert torch.isfinite(s[:, keep]).all() and not s[1, 32:40].any()
+        assert torch.equal(s[1, 41], v["state"][1][1, 41])  # A = 0: kept, whatever the step
+        assert s[1, 40].isnan().all() and o[at:, 40].isnan().all() and torch.isfinite(o[:at]).all()
+
+
 def test_scan_in_one_piece_and_in_several(mcp):
     """The C entry without a workspace runs a segment in one piece, with one in several
     (of which those in between are run twice); both stay in the bounds, and a workspace
