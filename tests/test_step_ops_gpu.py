@@ -612,6 +612,30 @@ def test_logits_of_rows_in_several_parts(mcp, V, dtype, out, off, temp):
     assert not wide[:, :off].any()
 
 
+@pytest.mark.parametrize("inplace", [False, True])
+def test_logits_with_the_smallest_temperatures(mcp, inplace):
+    """Temperatures whose reciprocal is no fp32 number: quotients are right where they are
+    finite and infinite where they are not.  Each is two products with three roundings
+    (reciprocal, product, and the half step of a subnormal temperature's own scaling: none,
+    2^64 being a power of two), so within 3 x 2^-24."""
+    temps = np.array([1e-45, 1e-40, 2.8e-39, 3e-39, 9e-38, 1.1e-37, 1.0, 3e38], np.float32)
+    x = np.array([0.0, 1e-38, -2e-38, 3e-7, -1.0, 2.5, 1e30, -np.inf], np.float32)
+    V = 70
+    rows = np.tile(np.resize(x, V), (len(temps), 1))
+    src = torch.from_numpy(rows).cuda()
+    got = mcp.process_logits(src, None if inplace else torch.empty_like(src),
+                             temperature=torch.from_numpy(temps).cuda())
+    with np.errstate(over="ignore"):
+        want = rows.astype(np.float64) / temps.astype(np.float64)[:, None]
+        as32 = want.astype(np.float32)
+    g = got.cpu().numpy()
+    normal = np.isfinite(as32) & (np.abs(want) > 2e-38)
+    assert np.array_equal(g[~np.isfinite(as32)], as32[~np.isfinite(as32)])
+    assert (np.abs(g[normal] - want[normal]) <= 3 * 2.0 ** -24 * np.abs(want[normal])).all()
+    small = np.isfinite(as32) & ~normal  # subnormal quotients: steps of 2^-149
+    assert (np.abs(g[small] - want[small]) <= 2.0 ** -148 + 3 * 2.0 ** -24 * np.abs(want[small])).all()
+
+
 def test_logits_of_a_padded_head(mcp):
     """Rows of a head whose vocabulary is padded, in place: the padding stays as it was."""
     rng = np.random.default_rng(4)
