@@ -622,7 +622,7 @@ typedef struct mcp_request_pool {
  * request_ids[s] < 0 is a padding segment: no tokens, a row of -1 (a captured
  * step of fixed size).  The new pages are also entered into request_pages
  * behind the held ones; lengths and free list stay as they are until
- * mcp_commit_step, so building the same step again gives the same tables.
+ * the commit, so building the same step again gives the same tables.
  *
  * Sound as a whole or not at all: a request row outside [0, R) or in two
  * segments, a negative length, more tokens than the table row or max_tokens
@@ -652,7 +652,15 @@ mcp_status mcp_build_step_tables(const mcp_request_pool* pool, const int32_t* re
  * over; its row may be used again.  A step that the build refused, or a length
  * out of range, sets the error word and changes nothing.  Pages are counted by
  * length: a request whose length does not match its page row corrupts the list.
+ *
+ * max_tokens: the build's, without which a step refused for its number of
+ * tokens alone could not be told from a sound one.  mcp_commit_step has 2^30
+ * there, the most that a build takes: it is for steps whose tokens the caller
+ * knows to have been within the build's max_tokens.
  */
+mcp_status mcp_commit_built_step(const mcp_request_pool* pool, const int32_t* request_ids,
+                                 const int32_t* q_lens, const int32_t* new_lens, int32_t num_seqs,
+                                 int32_t max_tokens, int32_t* error_word, void* stream);
 mcp_status mcp_commit_step(const mcp_request_pool* pool, const int32_t* request_ids,
                            const int32_t* q_lens, const int32_t* new_lens, int32_t num_seqs,
                            int32_t* error_word, void* stream);

@@ -546,19 +546,23 @@ def build_step_tables(pool: RequestPool, request_ids, q_lens, cu_seqlens_q, seql
             _arg(slot_mapping, torch.int64, "slot_mapping", dev, (cap,)),
             _arg(positions, i32, "positions", dev, (cap,)),
             _arg(logits_indices, i32, "logits_indices", dev, one), _error(error_word, dev))
+    pool.max_tokens = cap
 
 
 def commit_step(pool: RequestPool, request_ids, q_lens, new_lens=None, error_word=None,
-                stream=None) -> None:
+                stream=None, max_tokens=None) -> None:
     """The built step is over: request lengths become ``new_lens`` [S] (None: every new token
-    stays, 0: the request is over) and pages behind them return to the pool."""
+    stays, 0: the request is over) and pages behind them return to the pool.  A step that the
+    build refused is refused; ``max_tokens`` is what the build had (its slot_mapping's length),
+    None for that of the last build with this handle."""
     import torch
 
     dev, i32 = _pool_device(pool, request_ids), torch.int32
     one = (int(request_ids.shape[0]),)
-    _launch("commit_step", dev, stream, load().mcp_commit_step, ctypes.byref(pool),
+    cap = getattr(pool, "max_tokens", _capi.MAX_TOKENS) if max_tokens is None else int(max_tokens)
+    _launch("commit_step", dev, stream, load().mcp_commit_built_step, ctypes.byref(pool),
             _arg(request_ids, i32, "request_ids", dev, one), _arg(q_lens, i32, "q_lens", dev, one),
-            _arg(new_lens, i32, "new_lens", dev, one), one[0], _error(error_word, dev))
+            _arg(new_lens, i32, "new_lens", dev, one), one[0], cap, _error(error_word, dev))
 
 
 def _dtype_code(t, name):

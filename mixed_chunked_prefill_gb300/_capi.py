@@ -31,6 +31,7 @@ BUILD_CHECKED = 0x1
 DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 COUNT_PROMPT = 0x1
 COUNT_RESET = 0x2
+MAX_TOKENS = 1 << 30  # of a build of step tables
 
 
 class AttnDesc(ctypes.Structure):
@@ -265,6 +266,8 @@ SIGNATURES = {
     "mcp_build_step_tables": (c_int32, [POINTER(RequestPool), c_void_p, c_void_p, c_int32, c_int32,
                                         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                         c_void_p, c_void_p, c_void_p]),
+    "mcp_commit_built_step": (c_int32, [POINTER(RequestPool), c_void_p, c_void_p, c_void_p, c_int32,
+                                        c_int32, c_void_p, c_void_p]),
     "mcp_commit_step": (c_int32, [POINTER(RequestPool), c_void_p, c_void_p, c_void_p, c_int32,
                                   c_void_p, c_void_p]),
     "mcp_mixed_conv": (c_int32, [POINTER(ConvDesc), c_void_p, c_void_p, c_void_p, c_void_p,

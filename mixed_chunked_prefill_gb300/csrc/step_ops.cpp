@@ -67,6 +67,12 @@ mcp_status check_pool(const mcp_request_pool* p, int32_t num_seqs, const int32_t
   return MCP_OK;
 }
 
+mcp_status check_max_tokens(int32_t max_tokens) {
+  if (max_tokens < 0) return fail(MCP_ERR_INVALID_ARG, "max_tokens %d < 0", max_tokens);
+  if (max_tokens > kMaxTokens) return fail(MCP_ERR_UNSUPPORTED, "max_tokens %d > 2^30", max_tokens);
+  return MCP_OK;
+}
+
 mcp_status check_stream_sizes(int32_t num_seqs, int32_t tokens, int32_t requests, int32_t channels,
                               int32_t dtype) {
   if (num_seqs < 0 || tokens < 0)
@@ -120,8 +126,7 @@ mcp_status mcp_build_step_tables(const mcp_request_pool* pool, const int32_t* re
                                  int64_t* slot_mapping, int32_t* positions,
                                  int32_t* logits_indices, int32_t* error_word, void* stream) {
   MCP_TRY(check_pool(pool, num_seqs, request_ids, q_lens));
-  if (max_tokens < 0) return fail(MCP_ERR_INVALID_ARG, "max_tokens %d < 0", max_tokens);
-  if (max_tokens > kMaxTokens) return fail(MCP_ERR_UNSUPPORTED, "max_tokens %d > 2^30", max_tokens);
+  MCP_TRY(check_max_tokens(max_tokens));
   if (!cu_seqlens_q || (num_seqs > 0 && (!seqlens_k || !block_tables)) ||
       (max_tokens > 0 && !slot_mapping))
     return fail(MCP_ERR_INVALID_ARG, "NULL output pointer");
@@ -136,10 +141,18 @@ mcp_status mcp_build_step_tables(const mcp_request_pool* pool, const int32_t* re
 mcp_status mcp_commit_step(const mcp_request_pool* pool, const int32_t* request_ids,
                            const int32_t* q_lens, const int32_t* new_lens, int32_t num_seqs,
                            int32_t* error_word, void* stream) {
+  return mcp_commit_built_step(pool, request_ids, q_lens, new_lens, num_seqs, kMaxTokens, error_word,
+                               stream);
+}
+
+mcp_status mcp_commit_built_step(const mcp_request_pool* pool, const int32_t* request_ids,
+                                 const int32_t* q_lens, const int32_t* new_lens, int32_t num_seqs,
+                                 int32_t max_tokens, int32_t* error_word, void* stream) {
   MCP_TRY(check_pool(pool, num_seqs, request_ids, q_lens));
+  MCP_TRY(check_max_tokens(max_tokens));
   if (num_seqs == 0) return done(0, "");
-  return done(mcp::launch_commit_step(*pool, request_ids, q_lens, new_lens, num_seqs, error_word,
-                                      stream),
+  return done(mcp::launch_commit_step(*pool, request_ids, q_lens, new_lens, num_seqs, max_tokens,
+                                      error_word, stream),
               "commit_step launch");
 }
 

@@ -21,7 +21,7 @@ int launch_build_step_tables(const mcp_request_pool& pool, const int32_t* reques
                              int32_t* error_word, void* stream);
 int launch_commit_step(const mcp_request_pool& pool, const int32_t* request_ids,
                        const int32_t* q_lens, const int32_t* new_lens, int32_t num_seqs,
-                       int32_t* error_word, void* stream);
+                       int32_t max_tokens, int32_t* error_word, void* stream);
 // recurrent.cu
 bool mixed_conv_fits(const mcp_conv_desc& d);  // its grid is one that can be launched
 int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight, const void* bias,

@@ -178,7 +178,7 @@ __device__ __forceinline__ void load_step(const StepArgs& p, Step& st, char* sme
   }
   if (all_need > count) bad |= MCP_DEVERR_NO_PAGES;
   if (kCommit && count - all_need + all_page > p.num_pages) bad |= MCP_DEVERR_NO_PAGES;
-  if (all_tok > (kCommit ? 0x7fffffff : p.max_tokens)) bad |= MCP_DEVERR_REQUEST;
+  if (all_tok > p.max_tokens) bad |= MCP_DEVERR_REQUEST;
   st.bad = bad;
   st.base = bad ? count : count - static_cast<int32_t>(all_need);
   for (int s = s0; s < s1; ++s) {
@@ -449,9 +449,10 @@ int launch_build_step_tables(const mcp_request_pool& pool, const int32_t* reques
 
 int launch_commit_step(const mcp_request_pool& pool, const int32_t* request_ids,
                        const int32_t* q_lens, const int32_t* new_lens, int32_t num_seqs,
-                       int32_t* error_word, void* stream) {
+                       int32_t max_tokens, int32_t* error_word, void* stream) {
   StepArgs a = step_args(pool, request_ids, q_lens, num_seqs, error_word);
   a.new_lens = new_lens;
+  a.max_tokens = max_tokens;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return num_seqs <= kFewSegments ? commit_launch<256>(a, st) : commit_launch<512>(a, st);
 }

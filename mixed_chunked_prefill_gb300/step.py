@@ -218,7 +218,8 @@ class RequestTables:
             raise ValueError("new_lens must be [num_seqs], at most the step's lengths")
         with _on_stream(stream):
             to = None if new_lens is None else torch.from_numpy(after).to(self.device)
-            commit_step(self.pool, step.request_ids, step.q_lens, to, self.error_word, stream)
+            commit_step(self.pool, step.request_ids, step.q_lens, to, self.error_word, stream,
+                        max_tokens=step.slot_mapping.shape[0])
         self.commits += 1
         P = self.pool.page_size
         kept = -(-after // P) - -(-step.sk_h // P)

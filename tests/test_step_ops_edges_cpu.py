@@ -1,0 +1,24 @@
+"""Operators around a step's attention, without a GPU: refusals at the ends of what the
+calls take."""
+
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+from mixed_chunked_prefill_gb300 import _capi
+from test_step_ops_cpu import INVALID, OK, P16, UNSUPPORTED, lib, pool
+
+assert lib is not None  # the fixture that builds and loads the library
+
+
+@pytest.mark.parametrize("cap,over,ids,S,status", [
+    (-1, {}, P16, 4, INVALID), ((1 << 30) + 1, {}, P16, 4, UNSUPPORTED), (64, dict(num_pages=0), P16, 4, INVALID),
+    (64, {}, None, 4, INVALID), (64, {}, P16, 8193, UNSUPPORTED), (0, {}, None, 0, OK), (-1, {}, None, 0, INVALID),
+])
+def test_commit_built_step_refusals(lib, cap, over, ids, S, status):
+    p = pool(**over)
+    assert lib.mcp_commit_built_step(ctypes.byref(p), ids, P16, None, S, cap, None, None) == status
+    assert lib.mcp_commit_built_step(None, P16, P16, None, 4, 64, None, None) == INVALID
+    assert _capi.MAX_TOKENS == 1 << 30

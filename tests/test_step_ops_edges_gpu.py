@@ -1,0 +1,102 @@
+"""Operators around a step's attention on the GPU: calls that their documentation allows
+at the edges of what they take -- refused steps that are committed all the same, steps
+built in another order than they are committed, malformed streams, factors near the ends
+of fp32, streams of many segments."""
+
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from mixed_chunked_prefill_gb300 import _capi
+from oracle import step_ops_ref as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_step_ops_gpu import (  # noqa: E402
+    DT, Device, device_state, err_word, f64, i32, mcp, run_scan, scan_inputs, stream, values)
+
+assert mcp is not None  # the fixture that builds and loads the library
+
+
+# --------------------------------------------------------------------------- tables
+@pytest.mark.parametrize("ids,q,cap", [([0, 1], [5, 4], 8), ([1], [20], 8), ([2], [1], 0),
+                                       ([0, -1, 1], [13, 9, 33], 45)])
+@pytest.mark.parametrize("how", ["keep", "end", "cut"])
+def test_step_past_max_tokens_is_not_committed(mcp, ids, q, cap, how):
+    """A step that the build refused for max_tokens alone: the commit refuses it too, also
+    where the step needs no new page."""
+    p, d = ref.Pool(10, 16, 3, 4), Device(mcp, 10, 16, 3, 4)
+    want = p.build([2, 0], [17, 3], 20)
+    d.build([2, 0], [17, 3], 20)
+    d.commit([2, 0], [17, 3])
+    p.commit([2, 0], [17, 3], [17, 3], want[6])
+    new = {"keep": None, "end": [0] * len(ids), "cut": [max(0, p.lens[r]) if r >= 0 else 0 for r in ids]}[how]
+    before = [t.clone() for t in (d.pages, d.lens, d.free, d.count)]
+    cu, *_ = d.build(ids, q, cap)
+    assert int(d.err) == _capi.DEVERR_REQUEST and not cu.any()
+    d.err.zero_()
+    d.commit(ids, q, new)
+    assert int(d.err) == _capi.DEVERR_REQUEST
+    assert all(torch.equal(a, b) for a, b in zip(before, (d.pages, d.lens, d.free, d.count)))
+    d.err.zero_()
+    want = p.build(ids, q, 60)  # with room it is sound
+    for got, w in zip(d.build(ids, q, 60), want[:6]):
+        assert np.array_equal(got, w)
+    new = want[1].tolist() if new is None else new
+    d.commit(ids, q, None if how == "keep" else new)
+    p.commit(ids, q, new, want[6])
+    d.equal(p)
+
+
+def test_commit_is_told_max_tokens(mcp):
+    """A handle that has built nothing takes every step unless it is told the build's
+    max_tokens; so does the C entry without the argument."""
+    d = Device(mcp, 10, 16, 3, 4)
+    one, many = i32([1]), i32([20])
+    for cap, lens in ((19, 0), (20, 20)):
+        mcp.commit_step(d.pool, one, many, None, d.err, max_tokens=cap)
+        assert int(d.lens[1]) == lens and int(d.err) == (0 if lens else _capi.DEVERR_REQUEST)
+        d.err.zero_()
+    mcp.commit_step(d.pool, one, many, None, d.err)
+    assert int(d.lens[1]) == 40 and int(d.err) == 0
+    lib = mcp.load()
+    s = torch.cuda.current_stream().cuda_stream
+    assert lib.mcp_commit_step(ctypes.byref(d.pool), one.data_ptr(), many.data_ptr(), None, 1,
+                               d.err.data_ptr(), s) == 0
+    assert int(d.lens[1]) == 60 and int(d.err) == 0
+
+
+def test_captured_step_past_max_tokens(mcp):
+    """Build and commit in one graph of fixed max_tokens: a replay with too many tokens
+    leaves the pool as it was, the next goes on from there."""
+    p, d = ref.Pool(10, 16, 3, 4), Device(mcp, 10, 16, 3, 4)
+    ids, q = i32([-1, -1]), i32([0, 0])
+    cu, sk, bt = i32([0] * 3), i32([0] * 2), torch.zeros((2, 4), dtype=torch.int32, device="cuda")
+    slots = torch.zeros(24, dtype=torch.int64, device="cuda")
+
+    def calls():
+        mcp.build_step_tables(d.pool, ids, q, cu, sk, bt, slots, error_word=d.err)
+        mcp.commit_step(d.pool, ids, q, None, d.err)
+
+    calls()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+        calls()
+    torch.cuda.synchronize()
+    for step in (([0, 2], [20, 4]), ([0, 1], [13, 12]), ([1, 0], [15, 9]), ([2, 1], [25, 0])):
+        ids.copy_(i32(step[0]))
+        q.copy_(i32(step[1]))
+        g.replay()
+        torch.cuda.synchronize()
+        if sum(step[1]) <= 24:
+            want = p.build(*step, 24)
+            p.commit(*step, want[1].tolist(), want[6])
+            assert np.array_equal(bt.cpu().numpy(), want[2])
+        else:
+            assert int(d.err) == _capi.DEVERR_REQUEST
+            d.err.zero_()
+        d.equal(p)
