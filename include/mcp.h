@@ -644,7 +644,9 @@ mcp_status mcp_build_step_tables(const mcp_request_pool* pool, const int32_t* re
 
 /*
  * The step built from the same request_ids and q_lens (mcp_build_step_tables,
- * earlier on the stream) is over: request_lens[r] = new_lens[s], with
+ * earlier on the stream) is over.  It is the step that was built last on the
+ * pool: another build enters its own new pages into the same page rows (build
+ * the step again if there was one).  request_lens[r] = new_lens[s], with
  * 0 <= new_lens[s] <= request_lens[r] + q_lens[s] (NULL: every new token
  * stays), *free_count is moved and the pages behind each new length go back to
  * the free list, in segment order from free_pages[*free_count - K] on.  Fewer

@@ -172,9 +172,13 @@ class StepTables:
             self.slot_mapping = torch.empty(cap, dtype=torch.int64, device=dev)
             self.positions = torch.empty(cap, **i32)
             self.logits_indices = torch.empty(S, **i32)
-            build_step_tables(self.pool, self.request_ids, self.q_lens, self.cu_seqlens_q,
-                              self.seqlens_k, self.block_tables, self.slot_mapping, self.positions,
-                              self.logits_indices, tables.error_word, stream)
+            self._build(tables, stream)
+
+    def _build(self, tables, stream):
+        build_step_tables(self.pool, self.request_ids, self.q_lens, self.cu_seqlens_q,
+                          self.seqlens_k, self.block_tables, self.slot_mapping, self.positions,
+                          self.logits_indices, tables.error_word, stream)
+        tables.last = self
 
 
 class RequestTables:
@@ -198,6 +202,7 @@ class RequestTables:
         self.lens_h = np.zeros(max_requests, dtype=np.int64)
         self.free_h = int(num_pages)
         self.commits = 0
+        self.last = None  # the step built last: the page rows hold its new pages
 
     def step(self, request_ids, q_lens, max_tokens=None, stream=None) -> StepTables:
         """Tables of a step in which request row request_ids[s] runs q_lens[s] new tokens
@@ -217,10 +222,13 @@ class RequestTables:
         if after.shape != step.sk_h.shape or ((after < 0) | (after > step.sk_h))[live].any():
             raise ValueError("new_lens must be [num_seqs], at most the step's lengths")
         with _on_stream(stream):
+            if step is not self.last:  # another step entered its pages since: the same again
+                step._build(self, stream)
             to = None if new_lens is None else torch.from_numpy(after).to(self.device)
             commit_step(self.pool, step.request_ids, step.q_lens, to, self.error_word, stream,
                         max_tokens=step.slot_mapping.shape[0])
         self.commits += 1
+        self.last = None
         P = self.pool.page_size
         kept = -(-after // P) - -(-step.sk_h // P)
         self.lens_h[step.ids_h[live]] = after[live]

@@ -100,3 +100,36 @@ def test_captured_step_past_max_tokens(mcp):
             assert int(d.err) == _capi.DEVERR_REQUEST
             d.err.zero_()
         d.equal(p)
+
+
+@pytest.mark.parametrize("later", [[([0], [20])], [([0], [20]), ([0], [40])], [([1, 0], [40, 20]), ([3], [1])],
+                                   [([0, 1], [0, 0])], [([0, 1], [20, 20])]])
+def test_step_committed_after_another_was_built(mcp, later):
+    """A step is valid until the next commit: other steps built since, over the same page
+    rows, change nothing for it; they are stale behind it."""
+    from mixed_chunked_prefill_gb300.step import RequestTables
+
+    tables, p = RequestTables(20, 16, 4, 6), ref.Pool(20, 16, 4, 6)
+    first = ([2, 1], [7, 3])
+    want = p.build(*first, 10)
+    tables.commit(tables.step(*first))
+    p.commit(*first, want[1].tolist(), want[6])
+    a = tables.step([0, 1], [20, 20])
+    want = p.build([0, 1], [20, 20], 40)
+    others = [tables.step(*s) for s in later]
+    tables.commit(a)
+    p.commit([0, 1], [20, 20], want[1].tolist(), want[6])
+    for got, w in zip((a.cu_seqlens_q, a.seqlens_k, a.block_tables, a.slot_mapping, a.positions,
+                       a.logits_indices), want):
+        assert np.array_equal(got.cpu().numpy(), w)
+    for s in others:
+        with pytest.raises(ValueError):
+            tables.commit(s)
+    tables.check()
+    n = len(p.free)
+    assert int(tables.free_count) == tables.free_h == n and tables.free_pages[:n].tolist() == p.free
+    assert tables.request_lens.tolist() == p.lens == tables.lens_h.tolist()
+    for r, pages in enumerate(p.pages):
+        assert tables.request_pages[r, :len(pages)].tolist() == pages
+    tables.release([0, 1, 2])
+    assert sorted(tables.free_pages.tolist()) == list(range(20))
