@@ -433,6 +433,9 @@ __global__ void __launch_bounds__(kConvThreads, 8) mixed_conv_kernel(const ConvA
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) kept[k * lds] = X[(s.q1 - (K - 1) + k) * ldx];
       } else if (!have) {
+        // behind a first token of another segment's: a prefix sum that decreases
+        // (reported); the inputs before this one may lie outside the stream
+        if (off < K - 1) continue;
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) win[k] = L::widen(X[(tok - (K - 1) + k) * ldx]);
       }

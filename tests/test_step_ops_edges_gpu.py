@@ -133,3 +133,60 @@ def test_step_committed_after_another_was_built(mcp, later):
         assert tables.request_pages[r, :len(pages)].tolist() == pages
     tables.release([0, 1, 2])
     assert sorted(tables.free_pages.tolist()) == list(range(20))
+
+
+# ------------------------------------------------------------------ malformed streams
+def bad_streams():
+    """Prefix sums that decrease, overlap or leave the stream, most with tokens enough for
+    runs: (ids, cu, sk, T)."""
+    rng = np.random.default_rng(77)
+    out = [([0, 1, 2], [0, 2, 1, 9], [9, 9, 9], 9), ([0, 1, 2], [0, 5, 3, 12], [9, 9, 9], 12),
+           ([0, 1, 2, 3], [0, 20, 17, 18, 40], [40] * 4, 40), ([1, 0], [0, 16, 15], [16, 16], 30),
+           ([2, 1, 0], [0, 100, 2, 100], [100] * 3, 100), ([0, 1, 2, 3], [0, 200, 0, 200, 1], [200] * 4, 200)]
+    for _ in range(60):
+        T, S = int(rng.integers(5, 60)), int(rng.integers(1, 7))
+        cu = rng.integers(-2, T + 3, S + 1)
+        cu[0] = 0
+        if (np.diff(cu) >= 0).all() and cu.min() >= 0 and cu.max() <= T:
+            cu[-1] = T + 1
+        out.append((rng.permutation(S).tolist(), cu.tolist(), [T] * S, T))
+    return out
+
+
+@pytest.mark.parametrize("K,dtype,d", [(4, "bf16", 72), (3, "fp16", 8), (2, "bf16", 520)])
+def test_conv_of_malformed_streams(mcp, K, dtype, d):
+    """Reported, and nothing outside the stream's rows and the named requests is touched: the
+    inputs are a slice of rows whose neighbours are NaN, which no finite output can have met."""
+    rng = np.random.default_rng(K)
+    for ids, cu, sk, T in bad_streams():
+        R = len(ids) + 2
+        x = torch.full((T + 8, d), float("nan"), dtype=DT[dtype], device="cuda")
+        x[4:T + 4] = values(rng, (T, d), dtype)[1]
+        w, b = values(rng, (d, K), dtype)[1], values(rng, (d,), dtype)[1]
+        state = values(rng, (R, K - 1, d), dtype)[1]
+        kept = state.clone()
+        out = torch.full((T + 8, d), 7.0, dtype=DT[dtype], device="cuda")
+        err = err_word()
+        mcp.mixed_conv(x[4:T + 4], w, b, state, i32(ids), i32(cu), i32(sk), "silu", out[4:T + 4], err)
+        assert int(err) & _capi.DEVERR_SEGMENT, (cu, T)
+        assert (out[:4] == 7).all() and (out[T + 4:] == 7).all() and torch.isfinite(out).all(), (cu, T)
+        assert torch.isfinite(state).all() and torch.equal(state[len(ids):], kept[len(ids):])
+
+
+@pytest.mark.parametrize("N,d", [(16, 72), (64, 40)])
+def test_scan_of_malformed_streams(mcp, N, d):
+    rng = np.random.default_rng(N)
+    for ids, cu, sk, T in bad_streams():
+        R = len(ids) + 2
+        v = {k: t[1] for k, t in scan_inputs(rng, T + 8, d, N, 1, "bf16", R, True, 1.0).items()}
+        for k in ("x", "dt", "z", "B", "C"):
+            v[k][:4], v[k][T + 4:] = float("nan"), float("nan")
+        kept = v["state"].clone()
+        out = torch.full((T + 8, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        err = err_word()
+        at = slice(4, T + 4)
+        mcp.mixed_scan(v["x"][at], v["dt"][at], v["A"], v["B"][at], v["C"][at], v["state"], i32(ids), i32(cu),
+                       i32(sk), D=v["D"], z=v["z"][at], dt_bias=v["bias"], out=out[at], error_word=err)
+        assert int(err) & _capi.DEVERR_SEGMENT, (cu, T)
+        assert (out[:4] == 7).all() and (out[T + 4:] == 7).all() and torch.isfinite(out).all(), (cu, T)
+        assert torch.isfinite(v["state"]).all() and torch.equal(v["state"][len(ids):], kept[len(ids):])
