@@ -107,6 +107,12 @@ __device__ __forceinline__ float least(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+// the larger; NaN if one is
+__device__ __forceinline__ float greatest(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -1115,6 +1121,14 @@ __global__ void __launch_bounds__(32 * long_warps(N), 1) scan_long_kernel(const 
   }
 }
 
+// h 2^t + v.  The factor of a whole piece can leave fp32 where the product does
+// not (h = 0, or a small h that grew), so it is taken as the cube of 2^(t/3): at t/3
+// = 126 every h but 0 has overflowed, below -126 nothing is left of any.
+__device__ __forceinline__ float carried(float t, float h, float v) {
+  const float f = ex2(least(t * (1.f / 3.f), 126.f));
+  return fmaf(h * f * f, f, v);
+}
+
 // The end states of cut segments' pieces 1 .. (all but the last) from those they
 // ended with from zero, in place.  A warp takes 128 states (four a lane) along
 // every cut segment; the loads do not depend on each other.
@@ -1159,17 +1173,17 @@ __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const ScanArg
 #pragma unroll
         for (int j = 0; j < kCarryLoads; ++j) {
           if (j0 + j >= n) break;
-          // finite, so that A = 0 keeps its state
-          s[j] = least(sums[static_cast<int64_t>(slot + j0 + j) * p.channels], 2e38f) * kLog2e;
+          // finite, so that A = 0 keeps its state (steps without softplus may be negative)
+          s[j] = greatest(least(sums[static_cast<int64_t>(slot + j0 + j) * p.channels], 2e38f), -2e38f) * kLog2e;
           v[j] = *reinterpret_cast<const float4*>(ends + (slot + j0 + j) * state);
         }
 #pragma unroll
         for (int j = 0; j < kCarryLoads; ++j) {
           if (j0 + j >= n) break;
-          h.x = fmaf(ex2(s[j] * a.x), h.x, v[j].x);
-          h.y = fmaf(ex2(s[j] * a.y), h.y, v[j].y);
-          h.z = fmaf(ex2(s[j] * a.z), h.z, v[j].z);
-          h.w = fmaf(ex2(s[j] * a.w), h.w, v[j].w);
+          h.x = carried(s[j] * a.x, h.x, v[j].x);
+          h.y = carried(s[j] * a.y, h.y, v[j].y);
+          h.z = carried(s[j] * a.z, h.z, v[j].z);
+          h.w = carried(s[j] * a.w, h.w, v[j].w);
           *reinterpret_cast<float4*>(ends + (slot + j0 + j) * state) = h;
         }
       }

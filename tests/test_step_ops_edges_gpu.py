@@ -190,3 +190,72 @@ def test_scan_of_malformed_streams(mcp, N, d):
         assert int(err) & _capi.DEVERR_SEGMENT, (cu, T)
         assert (out[:4] == 7).all() and (out[T + 4:] == 7).all() and torch.isfinite(out).all(), (cu, T)
         assert torch.isfinite(v["state"]).all() and torch.equal(v["state"][len(ids):], kept[len(ids):])
+
+
+# ---------------------------------------------------------------------- ends of fp32
+def scan_both(mcp, v, ids, cu, sk, R, T, d, N, softplus):
+    """(out, state) without and with a workspace: a segment in one piece and in several."""
+    lib = mcp.load()
+    dev = {k: t[1] for k, t in v.items()}
+    desc = _capi.ScanDesc(len(ids), T, R, d, N, 1, 0, softplus, d, d, d, N, N, d)
+    need = ctypes.c_size_t()
+    assert lib.mcp_mixed_scan_workspace(ctypes.byref(desc), ctypes.byref(need)) == 0 and need.value > 256
+    ws = torch.full((need.value,), 255, dtype=torch.uint8, device="cuda")
+    got = []
+    for n in (0, need.value):
+        out = torch.full((T, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        st = dev["state"].clone()
+        tensors = _capi.ScanTensors(*(t.data_ptr() for t in (
+            dev["x"], dev["dt"], dev["A"], dev["B"], dev["C"], dev["D"], dev["z"])), None, st.data_ptr(),
+            out.data_ptr())
+        meta = [i32(a) for a in (ids, cu, sk)]
+        assert lib.mcp_mixed_scan(ctypes.byref(desc), ctypes.byref(tensors), *(t.data_ptr() for t in meta),
+                                  ws.data_ptr() if n else None, n, None,
+                                  torch.cuda.current_stream().cuda_stream) == 0
+        got.append((f64(out), f64(st)))
+    return got
+
+
+@pytest.mark.parametrize("name", ["zero", "grows", "shrinks", "kept"])
+def test_carried_states_at_the_ends_of_fp32(mcp, name):
+    """Factors over a whole piece that leave fp32 where the state times them does not: a state
+    of 0 stays 0, a small one that grows and falls again comes back, a large one falls to
+    what is left of it, and A = 0 keeps it whatever the steps sum to."""
+    rng = np.random.default_rng(3)
+    T, d, N = 320, 64, 16
+    ids, cu, sk = [1], [0, T], [T + 9]
+    v = scan_inputs(rng, T, d, N, 1, "bf16", 2, False, 1.0)
+
+    def put(k, a):
+        t = torch.from_numpy(np.broadcast_to(a, v[k][0].shape).copy()).to(v[k][1].dtype)
+        v[k] = (t.double().numpy(), t.cuda())
+
+    A, dt = np.ones((d, N)), np.zeros((T, 1))
+    if name == "zero":  # nothing comes in before the last tokens
+        dt += 3.0
+        x = np.zeros((T, 1))
+        x[T - 3:] = 1.0
+        put("x", x)
+        put("state", 0.0)
+    elif name == "grows":  # e^96 up and down again within four pieces, from 1e-30
+        dt[64:96], dt[96:128] = 3.0, -3.0
+        put("x", 0.0)
+        put("state", 1e-30 * rng.uniform(1, 2, (2, d, N)))
+    elif name == "shrinks":  # e^-96 of 1e30
+        dt[64:96] = 3.0
+        A = -A
+        put("x", 0.0)
+        put("state", 1e30 * rng.uniform(1, 2, (2, d, N)))
+    else:
+        dt = np.full((T, d), float(torch.finfo(torch.bfloat16).min))
+        A = 0 * A
+        put("x", 0.0)
+    put("A", A)
+    put("dt", dt)
+    h = {k: t[0] for k, t in v.items()}
+    want, bound, end, ebound = ref.scan(h["x"], h["dt"], h["A"], h["B"], h["C"], h["D"], h["z"], 0 * h["bias"],
+                                        False, h["state"], ids, cu, sk, "bf16")
+    for out, st in scan_both(mcp, v, ids, cu, sk, 2, T, d, N, 0):
+        assert np.isfinite(st).all()
+        assert (np.abs(st - end) <= ebound).all()
+        assert (np.abs(out - want) <= bound).all()
