@@ -722,10 +722,15 @@ def process_logits(logits, out=None, request_ids=None, seen=None, counts=None, t
         if seen is None or counts is None:
             raise ValueError("request_ids needs seen and counts")
         R, ps, pc = _token_state(seen, counts, V, dev)
-    off, tok, val = (None, None, None) if bias is None else bias
+    off, tok, val, biases = None, None, None, 0
+    if bias is not None:
+        off, tok, val = bias
+        if off is None or tok is None or val is None or tok.dim() != 1:
+            raise ValueError("bias must be (offsets [rows + 1], tokens [n], values [n])")
+        biases = tok.shape[0]
     masks = 0 if mask is None else mask.shape[0]
     desc = _capi.LogitsDesc(rows, V, R, _dtype_code(logits, "logits"), _dtype_code(out, "out"),
-                            0 if tok is None else tok.shape[0], masks, 0, ld[0], ld[1])
+                            biases, masks, 0, ld[0], ld[1])
     tensors = _capi.LogitsTensors(
         logits.data_ptr(), out.data_ptr(), _arg(request_ids, i32, "request_ids", dev, one), ps, pc,
         _arg(temperature, f32, "temperature", dev, one),
@@ -733,7 +738,7 @@ def process_logits(logits, out=None, request_ids=None, seen=None, counts=None, t
         _arg(frequency_penalty, f32, "frequency_penalty", dev, one),
         _arg(presence_penalty, f32, "presence_penalty", dev, one),
         _arg(off, i32, "bias offsets", dev, (rows + 1,)), _arg(tok, i32, "bias tokens", dev),
-        _arg(val, f32, "bias values", dev, None if tok is None else tok.shape),
+        _arg(val, f32, "bias values", dev, (biases,)),
         _arg(mask, i32, "mask", dev, (masks, (V + 31) // 32)),
         _arg(mask_rows, i32, "mask_rows", dev, one))
     _launch("process_logits", dev, stream, load().mcp_process_logits, ctypes.byref(desc),

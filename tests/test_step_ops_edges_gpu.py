@@ -259,3 +259,20 @@ def test_carried_states_at_the_ends_of_fp32(mcp, name):
         assert np.isfinite(st).all()
         assert (np.abs(st - end) <= ebound).all()
         assert (np.abs(out - want) <= bound).all()
+
+
+# --------------------------------------------------------------------------- logits
+def test_biases_of_another_shape_are_refused(mcp):
+    """Biases are one list with offsets; a [rows, k] pair would lose most of them."""
+    x = torch.zeros((3, 64), device="cuda")
+    off, tok, val = i32([0, 2, 4, 6]), i32([1, 5, 2, 9, 3, 7]), torch.ones(6, device="cuda")
+    for bias in ((off, tok.view(3, 2), val.view(3, 2)), (off, tok, val.view(3, 2)), (off, tok.view(3, 2), val),
+                 (off, tok, val[:5]), (off, tok, None), (off, None, val), (None, tok, val),
+                 (off.view(2, 2), tok, val)):
+        with pytest.raises((ValueError, TypeError, mcp.MCPError)):
+            mcp.process_logits(x, bias=bias)
+    assert not x.any()
+    mcp.process_logits(x, bias=(off, tok, val))
+    assert int(x.sum()) == 6
+    mcp.process_logits(x, bias=(i32([0] * 4), tok[:0], val[:0]))
+    assert int(x.sum()) == 6
