@@ -128,8 +128,13 @@ __device__ __forceinline__ float rcp(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// v / (1 + exp(-v)); exp overflows to infinity and the quotient to 0
-__device__ __forceinline__ float silu(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }
+// v / (1 + exp(-v)), exp as the square of its root and the sum taken 2^-20 times, so
+// that neither overflows and the reciprocal is no subnormal (flushed to 0) before v
+// = -101, where the quotient is below what bf16 holds.
+__device__ __forceinline__ float silu(float v) {
+  const float root = ex2(-0.5f * kLog2e * v);
+  return v * (rcp(fmaf(0x1p-20f * root, root, 0x1p-20f)) * 0x1p-20f);
+}
 
 // ------------------------------------------------------------------ segments
 struct Segments {

@@ -276,3 +276,31 @@ def test_biases_of_another_shape_are_refused(mcp):
     assert int(x.sum()) == 6
     mcp.process_logits(x, bias=(i32([0] * 4), tok[:0], val[:0]))
     assert int(x.sum()) == 6
+
+
+SILU_AT = np.concatenate([np.linspace(-97.25, -80, 70), np.linspace(-12, 12, 97), [-3e38, -1e4, -128.0, 100.0, 3e38, 0.0]])
+
+
+@pytest.mark.parametrize("T", [1, 3, 80])
+def test_silu_far_below_zero(mcp, T):
+    """v / (1 + exp(-v)) down to where bf16 has no value for it, in the convolution (one tap of
+    1: its sum is exact) and as the scan's gate (B = 0, D x = 1).  Off by at most what the
+    definition allows its roundings, and an fp32 step where the quotient is subnormal."""
+    d = 256
+    v = torch.from_numpy(np.resize(SILU_AT, (T, d))).to(torch.bfloat16)
+    v64 = v.double().numpy()
+    with np.errstate(over="ignore"):
+        want = ref._silu(v64)
+        err = np.where(want == 0, 0, ref._silu_err(np.where(want == 0, 0, v64), 0))
+    # the quotient's own step, times v
+    bound = ref._rounded(want, err + np.minimum(np.abs(v64), 128) * 2.0 ** -149, "bf16")
+    w = torch.zeros((d, 2), dtype=torch.bfloat16, device="cuda")
+    w[:, 1] = 1
+    meta = i32([0]), i32([0, T]), i32([T])
+    got = f64(mcp.mixed_conv(v.cuda(), w, None, torch.zeros((1, 1, d), dtype=torch.bfloat16, device="cuda"), *meta))
+    assert (np.abs(got - want) <= bound).all()
+    one = torch.ones((T, d), dtype=torch.bfloat16, device="cuda")
+    bc = torch.zeros((T, 1, 16), dtype=torch.bfloat16, device="cuda")
+    got = f64(mcp.mixed_scan(one, one, -torch.ones((d, 16), device="cuda"), bc, bc,
+                             torch.zeros((1, d, 16), device="cuda"), *meta, D=torch.ones(d, device="cuda"), z=v.cuda()))
+    assert (np.abs(got - want) <= bound).all()
