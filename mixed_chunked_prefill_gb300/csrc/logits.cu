@@ -396,12 +396,12 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_
   const float temp = p.temperature ? p.temperature[row] : 0.f;
   const bool scale = temp > 0.f && temp != 1.f;
   const bool every = !p.inplace || scale;
-  // quotients as products: one rounding more, a tenth of the instructions;
-  // a temperature whose reciprocal overflows (subnormal) is taken 2^64 times, and
-  // its quotients again; such a repetition penalty divides
-  const float after = scale && temp < 1e-37f ? 0x1p64f : 1.f;
+  // quotients as products: one rounding more, a tenth of the instructions; a
+  // temperature whose reciprocal overflows or is subnormal (fewer bits) is taken
+  // 2^64 or 2^-64 times, and its quotients again; such a repetition penalty divides
+  const float after = !scale ? 1.f : temp < 1e-37f ? 0x1p64f : temp > 0x1p125f ? 0x1p-64f : 1.f;
   const float inv = scale ? 1.f / (temp * after) : 1.f, rinv = 1.f / rho;
-  const bool divide = rinv > 3.4e38f;
+  const bool divide = rinv > 3.4e38f || rinv < 0x1p-125f;
   __syncthreads();
   for (int32_t e = lo + threadIdx.x; e < hi; e += kLogitThreads) {
     if (e != lo + static_cast<int32_t>(threadIdx.x)) {

@@ -304,3 +304,28 @@ def test_silu_far_below_zero(mcp, T):
     got = f64(mcp.mixed_scan(one, one, -torch.ones((d, 16), device="cuda"), bc, bc,
                              torch.zeros((1, d, 16), device="cuda"), *meta, D=torch.ones(d, device="cuda"), z=v.cuda()))
     assert (np.abs(got - want) <= bound).all()
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("what", ["temperature", "repetition"])
+def test_logits_over_the_largest_divisors(mcp, what, inplace):
+    """Divisors whose reciprocal is subnormal in fp32: quotients that are normal numbers are
+    within 3 x 2^-24 (a reciprocal, a product, and half of it again)."""
+    rng = np.random.default_rng(5)
+    B, V = 64, 130
+    by = np.concatenate([[2.0 ** 125, 2.0 ** 126, 2.0 ** 127], rng.uniform(8e37, 3.4e38, B - 3)]).astype(np.float32)
+    rows = (10.0 ** rng.uniform(1.5, 38, (B, V))).astype(np.float32)
+    if what == "temperature":
+        rows *= rng.choice([-1, 1], (B, V))
+    src = torch.from_numpy(rows).cuda()
+    kw = dict(temperature=torch.from_numpy(by).cuda())
+    if what == "repetition":
+        seen = np.ones((B, 2, V), bool)
+        seen[:, 1] = False
+        sd, cd = device_state(seen, np.zeros((B, V), np.int64))
+        kw = dict(request_ids=i32(range(B)), seen=sd, counts=cd, repetition_penalty=torch.from_numpy(by).cuda())
+    got = f64(mcp.process_logits(src, None if inplace else torch.empty_like(src), **kw))
+    want = rows.astype(np.float64) / by.astype(np.float64)[:, None]
+    normal = np.abs(want) >= 2.0 ** -126
+    assert normal.mean() > 0.9
+    assert (np.abs(got - want) <= np.where(normal, 3 * 2.0 ** -24 * np.abs(want), 2.0 ** -148)).all()
