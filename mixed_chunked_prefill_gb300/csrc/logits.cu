@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kCountThreads) clear_counts_kernel(const Count
        i += static_cast<int64_t>(gridDim.x) * kCountThreads) {
     const int32_t r = static_cast<int32_t>(i / p.W), w = static_cast<int32_t>(i - static_cast<int64_t>(r) * p.W);
     const int32_t id = p.ids[r];
+    if (id >= p.R && w == 0 && p.err) atomicOr(p.err, MCP_DEVERR_REQUEST);
     if (id < 0 || id >= p.R) continue;
     int32_t* seen = p.seen + static_cast<int64_t>(id) * 2 * p.W + w;
     uint32_t had = static_cast<uint32_t>(seen[p.W]);

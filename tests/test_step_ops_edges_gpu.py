@@ -329,3 +329,19 @@ def test_logits_over_the_largest_divisors(mcp, what, inplace):
     normal = np.abs(want) >= 2.0 ** -126
     assert normal.mean() > 0.9
     assert (np.abs(got - want) <= np.where(normal, 3 * 2.0 ** -24 * np.abs(want), 2.0 ** -148)).all()
+
+
+@pytest.mark.parametrize("cu", [[0, 0, 0, 0], [0, 0, 3, 3]])
+@pytest.mark.parametrize("prompt", [True, False])
+def test_rows_that_cannot_be_cleared_are_reported(mcp, cu, prompt):
+    """A row outside the state is reported also where it has no token to add."""
+    V, R = 70, 2
+    seen, counts = np.ones((R, 2, V), bool), np.full((R, V), 3, np.int64)
+    sd, cd = device_state(seen, counts)
+    err = err_word()
+    ids = [R, 1, -1]
+    tokens = [5, 5, 69][:cu[-1]]
+    mcp.update_token_counts(i32(ids), i32(tokens), sd, cd, V, i32(cu), prompt, True, err)
+    assert int(err) == _capi.DEVERR_REQUEST
+    want = device_state(*ref.update_counts(seen, counts, ids, tokens, cu, V, prompt, True))
+    assert torch.equal(sd, want[0]) and torch.equal(cd, want[1])
