@@ -788,7 +788,7 @@ mcp_status mcp_mixed_scan_workspace(const mcp_scan_desc* desc, size_t* workspace
  * vocab_size (MCP_DEVERR_TOKEN_RANGE) is left out.  A request may stand in
  * several rows; the result does not depend on the order.  Clearing counts
  * relies on plane 1 marking every non-zero count (zero both to begin with).
- * num_tokens <= 2^30, vocab_size <= 2^28 (of the logits also).
+ * num_tokens and num_rows <= 2^30, vocab_size <= 2^28 (of the logits also).
  */
 #define MCP_COUNT_PROMPT 0x1
 #define MCP_COUNT_RESET 0x2

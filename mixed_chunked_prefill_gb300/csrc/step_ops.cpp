@@ -233,8 +233,9 @@ mcp_status mcp_update_token_counts(const int32_t* request_ids, int32_t num_rows,
   if (num_requests <= 0 || vocab_size <= 0)
     return fail(MCP_ERR_INVALID_ARG, "num_requests %d / vocab_size %d must be positive", num_requests,
                 vocab_size);
-  if (num_tokens > kMaxTokens || vocab_size > kMaxRow)
-    return fail(MCP_ERR_UNSUPPORTED, "num_tokens %d > 2^30 or vocab_size %d > 2^28", num_tokens, vocab_size);
+  if (num_tokens > kMaxTokens || num_rows > kMaxTokens || vocab_size > kMaxRow)
+    return fail(MCP_ERR_UNSUPPORTED, "num_tokens %d or num_rows %d > 2^30, or vocab_size %d > 2^28", num_tokens,
+                num_rows, vocab_size);
   if (flags & ~(MCP_COUNT_PROMPT | MCP_COUNT_RESET))
     return fail(MCP_ERR_INVALID_ARG, "flags 0x%x", flags);
   if (!cu_tokens && num_tokens != num_rows)

@@ -8,7 +8,7 @@ import ctypes
 import pytest
 
 from mixed_chunked_prefill_gb300 import _capi
-from test_step_ops_cpu import INVALID, OK, P16, UNSUPPORTED, lib, pool
+from test_step_ops_cpu import INVALID, OK, P16, UNSUPPORTED, counts, lib, pool
 
 assert lib is not None  # the fixture that builds and loads the library
 
@@ -22,3 +22,12 @@ def test_commit_built_step_refusals(lib, cap, over, ids, S, status):
     assert lib.mcp_commit_built_step(ctypes.byref(p), ids, P16, None, S, cap, None, None) == status
     assert lib.mcp_commit_built_step(None, P16, P16, None, 4, 64, None, None) == INVALID
     assert _capi.MAX_TOKENS == 1 << 30
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(rows=(1 << 30) + 1, n=4, cu=P16), UNSUPPORTED), (dict(rows=0x7fffffff, n=0, cu=P16, flags=2), UNSUPPORTED),
+    (dict(rows=1 << 30, n=5), INVALID),  # at the bound the other checks go on
+])
+def test_update_token_counts_of_many_rows(lib, over, status):
+    """The rows' 32-bit indices are rounded up to whole CTAs."""
+    assert counts(lib, **over) == status
