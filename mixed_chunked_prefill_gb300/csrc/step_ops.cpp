@@ -6,6 +6,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include "mcp.h"
 #include "mcp_internal.h"
@@ -34,6 +35,13 @@ constexpr int32_t kMaxRows = 1 << 24;     // request rows
 constexpr int32_t kMaxSegments = 1 << 20;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// int32 and fp32 arrays (NULL: one that is left out)
+mcp_status check_words(std::initializer_list<const void*> arrays) {
+  for (const void* p : arrays)
+    if (!aligned(p, 4)) return fail(MCP_ERR_INVALID_ARG, "an int32 or fp32 array is not 4-byte aligned");
+  return MCP_OK;
+}
 
 #define MCP_TRY(expr)                    \
   do {                                   \
@@ -64,7 +72,7 @@ mcp_status check_pool(const mcp_request_pool* p, int32_t num_seqs, const int32_t
       !aligned(p->free_count, 4))
     return fail(MCP_ERR_INVALID_ARG, "pool tensor misaligned (request_pages: 16 bytes)");
   if (num_seqs > 0 && (!ids || !q_lens)) return fail(MCP_ERR_INVALID_ARG, "NULL pointer argument");
-  return MCP_OK;
+  return check_words({ids, q_lens});
 }
 
 mcp_status check_max_tokens(int32_t max_tokens) {
@@ -132,6 +140,7 @@ mcp_status mcp_build_step_tables(const mcp_request_pool* pool, const int32_t* re
     return fail(MCP_ERR_INVALID_ARG, "NULL output pointer");
   if (!aligned(block_tables, 16) || !aligned(slot_mapping, 8))
     return fail(MCP_ERR_INVALID_ARG, "block_tables must be 16-byte, slot_mapping 8-byte aligned");
+  MCP_TRY(check_words({cu_seqlens_q, seqlens_k, positions, logits_indices, error_word}));
   return done(mcp::launch_build_step_tables(*pool, request_ids, q_lens, num_seqs, max_tokens,
                                             cu_seqlens_q, seqlens_k, block_tables, slot_mapping,
                                             positions, logits_indices, error_word, stream),
@@ -150,6 +159,7 @@ mcp_status mcp_commit_built_step(const mcp_request_pool* pool, const int32_t* re
                                  int32_t max_tokens, int32_t* error_word, void* stream) {
   MCP_TRY(check_pool(pool, num_seqs, request_ids, q_lens));
   MCP_TRY(check_max_tokens(max_tokens));
+  MCP_TRY(check_words({new_lens, error_word}));
   if (num_seqs == 0) return done(0, "");
   return done(mcp::launch_commit_step(*pool, request_ids, q_lens, new_lens, num_seqs, max_tokens,
                                       error_word, stream),
@@ -164,6 +174,7 @@ mcp_status mcp_mixed_conv(const mcp_conv_desc* d, const void* x, const void* wei
   MCP_TRY(check_stream_sizes(d->num_seqs, d->total_tokens, d->num_requests, d->channels, d->dtype));
   if (d->num_seqs > 0 && (!request_ids || !cu_seqlens_q || !seqlens_k))
     return fail(MCP_ERR_INVALID_ARG, "NULL metadata pointer");
+  MCP_TRY(check_words({request_ids, cu_seqlens_q, seqlens_k, error_word}));
   if (d->width < 2 || d->width > 4)
     return fail(MCP_ERR_UNSUPPORTED, "width %d (built: 2, 3, 4)", d->width);
   if (d->activation != 0 && d->activation != 1)
@@ -199,6 +210,7 @@ mcp_status mcp_mixed_scan(const mcp_scan_desc* d, const mcp_scan_tensors* t,
   if (!t) return fail(MCP_ERR_INVALID_ARG, "tensors is NULL");
   if (d->num_seqs > 0 && (!request_ids || !cu_seqlens_q || !seqlens_k))
     return fail(MCP_ERR_INVALID_ARG, "NULL metadata pointer");
+  MCP_TRY(check_words({request_ids, cu_seqlens_q, seqlens_k, error_word}));
   if (d->num_seqs == 0 || d->total_tokens == 0) return done(0, "");
   const int64_t gn = static_cast<int64_t>(d->num_groups) * d->state_size;
   MCP_TRY(check_rows(t->x, d->x_stride, d->channels, "x"));
@@ -243,6 +255,7 @@ mcp_status mcp_update_token_counts(const int32_t* request_ids, int32_t num_rows,
   if (num_rows == 0) return done(0, "");
   if (!request_ids || !seen || !counts || (num_tokens > 0 && !tokens))
     return fail(MCP_ERR_INVALID_ARG, "NULL tensor pointer");
+  MCP_TRY(check_words({request_ids, tokens, cu_tokens, seen, counts, error_word}));
   return done(mcp::launch_update_token_counts(request_ids, num_rows, tokens, num_tokens, cu_tokens,
                                               seen, counts, num_requests, vocab_size, flags,
                                               error_word, stream),
@@ -277,6 +290,9 @@ mcp_status mcp_process_logits(const mcp_logits_desc* d, const mcp_logits_tensors
     return fail(MCP_ERR_INVALID_ARG, "request_ids without seen and counts");
   if (!t->request_ids && (t->repetition_penalty || t->frequency_penalty || t->presence_penalty))
     return fail(MCP_ERR_INVALID_ARG, "penalties need request_ids, seen and counts");
+  MCP_TRY(check_words({t->request_ids, t->seen, t->temperature, t->repetition_penalty, t->frequency_penalty,
+                       t->presence_penalty, t->bias_offsets, t->bias_tokens, t->bias_values, t->mask,
+                       t->mask_rows, error_word}));
   if (!aligned(t->counts, 16)) return fail(MCP_ERR_INVALID_ARG, "counts must be 16-byte aligned");
   if (t->bias_offsets && d->num_biases > 0 && (!t->bias_tokens || !t->bias_values))
     return fail(MCP_ERR_INVALID_ARG, "bias_offsets without bias_tokens and bias_values");

@@ -8,7 +8,7 @@ import ctypes
 import pytest
 
 from mixed_chunked_prefill_gb300 import _capi
-from test_step_ops_cpu import INVALID, OK, P16, UNSUPPORTED, counts, lib, pool
+from test_step_ops_cpu import INVALID, OK, P16, UNSUPPORTED, conv, counts, lib, logits, pool, scan
 
 assert lib is not None  # the fixture that builds and loads the library
 
@@ -31,3 +31,28 @@ def test_commit_built_step_refusals(lib, cap, over, ids, S, status):
 def test_update_token_counts_of_many_rows(lib, over, status):
     """The rows' 32-bit indices are rounded up to whole CTAs."""
     assert counts(lib, **over) == status
+
+
+def test_misaligned_arrays_are_refused(lib):
+    """Addresses inside an int32 or fp32, for each array of each call (refused before a launch)."""
+    bad, p = P16 + 2, ctypes.byref(pool())
+    for k in range(9):  # ids, q_lens | cu, sk, bt, slots, positions, logits_indices, error word
+        a = [P16] * 9
+        a[k] = bad
+        assert lib.mcp_build_step_tables(p, *a[:2], 4, 64, *a[2:], None) == INVALID, k
+    for k in range(4):
+        a = [P16] * 4
+        a[k] = bad
+        assert lib.mcp_commit_step(p, *a[:3], 4, a[3], None) == INVALID, k
+        assert lib.mcp_commit_built_step(p, *a[:3], 4, 64, a[3], None) == INVALID, k
+    for k in range(3):
+        meta = [P16] * 3
+        meta[k] = bad
+        assert conv(lib, meta=meta, out=2 * P16) == INVALID
+        assert scan(lib, meta=meta, tensors=dict(out=2 * P16)) == INVALID
+    for name in ("ids", "tokens", "seen", "cnt", "cu"):
+        assert counts(lib, **{name: bad}) == INVALID, name
+    for name in ("request_ids", "seen", "temperature", "repetition_penalty", "frequency_penalty",
+                 "presence_penalty", "bias_offsets", "bias_tokens", "bias_values", "mask", "mask_rows"):
+        given = dict(bias_offsets=P16, bias_tokens=P16, bias_values=P16, mask=P16)
+        assert logits(lib, tensors={**given, name: bad}) == INVALID, name
