@@ -689,7 +689,7 @@ mcp_status mcp_commit_step(const mcp_request_pool* pool, const int32_t* request_
  * Token rows may be part of wider rows: *_stride is the distance of
  * consecutive tokens in elements, a multiple of 8; tensors are 16-byte
  * aligned.  Sums and the scan's state are fp32; outputs are rounded once.
- * num_seqs <= 2^20, total_tokens <= 2^30, num_requests <= 2^24.
+ * num_seqs <= 2^20, total_tokens and channels <= 2^30, num_requests <= 2^24.
  */
 typedef enum mcp_dtype { MCP_DTYPE_BF16 = 0, MCP_DTYPE_FP16 = 1, MCP_DTYPE_FP32 = 2 } mcp_dtype;
 

@@ -1068,6 +1068,7 @@ __global__ void __launch_bounds__(32 * long_warps(N), 1) scan_long_kernel(const 
   chunk();
   if (!kFirst) asm volatile("griddepcontrol.wait;" ::: "memory");  // the carry is over
   while (true) {
+    if (task < 0) return;  // past 2^31: overlapping segments (reported), see mixed_scan_fits
     const int32_t at = task / p.blocks;
     while (at >= base + __shfl_sync(0xffffffffu, incl, 31)) {
       base += __shfl_sync(0xffffffffu, incl, 31);
@@ -1202,15 +1203,23 @@ struct ScanCut {
   int32_t piece, slots;
   size_t bytes;  // of workspace: the counter, the sums, the end states
 };
+// Warps of the long kernel across the channels; the segments that can be its.
+int64_t long_blocks(const mcp_scan_desc& d) {
+  const int ns = d.state_size < 16 ? d.state_size : 16, cpw = 64 / (d.state_size / ns);
+  const int64_t per_group = d.channels / d.num_groups;
+  return d.num_groups * ((per_group + cpw - 1) / cpw);
+}
+int64_t max_long(int32_t tokens, int32_t seqs) {
+  const int32_t n = tokens / (kShortTokens + 1);
+  return n < seqs ? n : seqs;
+}
 ScanCut scan_cut(const mcp_scan_desc& d, int sms) {
   // 0.8 of a warp slot's share of the work, in tokens (0.7 to 1 measured the same
   // on average, 0.5 and 1.2 5% to 10% longer), but not below 4 tiles: a piece's
   // start costs a tile or two.  2 tiles where 4 leave half of the slots empty (300
   // tokens of 4096 channels: 32 us instead of 47, 720 53 and 59; four segments of
   // 512 tokens and 2048 channels, which fill more, 75 instead of 66).
-  const int ns = d.state_size < 16 ? d.state_size : 16, cpw = 64 / (d.state_size / ns);
-  const int64_t per_group = d.channels / d.num_groups;
-  const int64_t blocks = d.num_groups * ((per_group + cpw - 1) / cpw), slots = static_cast<int64_t>(sms) * long_warps(d.state_size);
+  const int64_t blocks = long_blocks(d), slots = static_cast<int64_t>(sms) * long_warps(d.state_size);
   const int64_t share = (d.total_tokens * blocks * kCutTenths + 10 * slots - 1) / (10 * slots);
   int64_t piece = (share + kTile - 1) / kTile * kTile;
   const bool few = d.total_tokens * blocks < slots / 2 * kUncut;
@@ -1233,8 +1242,7 @@ int scan_launch(ScanArgs a, cudaStream_t st) {
     l.short_max = kShortTokens;
     l.blocks = a.channels / a.per_group * ((a.per_group + C::CPW - 1) / C::CPW);
     // one CTA an SM stays, and each has a task before one has two
-    const int64_t longs = a.g.T / (kShortTokens + 1) < a.g.S ? a.g.T / (kShortTokens + 1) : a.g.S;
-    const int64_t tasks = (longs + a.slots) * l.blocks;
+    const int64_t tasks = (max_long(a.g.T, a.g.S) + a.slots) * l.blocks;
     const int64_t grid = tasks < sms ? tasks : sms;
     if (const int e = allow_smem<scan_long_kernel<T, N, true>>(C::kSmem)) return e;
     if (const int e = allow_smem<scan_long_kernel<T, N, false>>(C::kSmem)) return e;
@@ -1323,6 +1331,12 @@ int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight,
 }
 
 size_t mixed_scan_workspace(const mcp_scan_desc& d, int sms) { return scan_cut(d, sms).bytes; }
+
+bool mixed_scan_fits(const mcp_scan_desc& d) {
+  const int sms = step_num_sms();
+  const int64_t tasks = (max_long(d.total_tokens, d.num_seqs) + scan_cut(d, sms).slots) * long_blocks(d);
+  return tasks + static_cast<int64_t>(sms) * long_warps(d.state_size) < 0x7fffffff;
+}
 
 int launch_mixed_scan(const mcp_scan_desc& d, const mcp_scan_tensors& t,
                       const int32_t* request_ids, const int32_t* cu_seqlens_q,

@@ -33,6 +33,7 @@ constexpr int32_t kMaxTokens = 1 << 30;   // of a step, a stream, a list
 constexpr int32_t kMaxRow = 1 << 28;      // entries of a table row, tokens of a vocabulary
 constexpr int32_t kMaxRows = 1 << 24;     // request rows
 constexpr int32_t kMaxSegments = 1 << 20;
+constexpr int32_t kMaxChannels = 1 << 30;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -88,9 +89,10 @@ mcp_status check_stream_sizes(int32_t num_seqs, int32_t tokens, int32_t requests
   if (requests <= 0 || channels <= 0)
     return fail(MCP_ERR_INVALID_ARG, "num_requests %d / channels %d must be positive", requests,
                 channels);
-  if (num_seqs > kMaxSegments || tokens > kMaxTokens || requests > kMaxRows)
-    return fail(MCP_ERR_UNSUPPORTED, "num_seqs %d > 2^20, total_tokens %d > 2^30 or num_requests %d > 2^24",
-                num_seqs, tokens, requests);
+  if (num_seqs > kMaxSegments || tokens > kMaxTokens || requests > kMaxRows || channels > kMaxChannels)
+    return fail(MCP_ERR_UNSUPPORTED,
+                "num_seqs %d > 2^20, total_tokens %d > 2^30, num_requests %d > 2^24 or channels %d > 2^30",
+                num_seqs, tokens, requests, channels);
   if (channels % 8 != 0)
     return fail(MCP_ERR_INVALID_ARG, "channels %d is not a multiple of 8", channels);
   if (dtype != MCP_DTYPE_BF16 && dtype != MCP_DTYPE_FP16)
@@ -230,6 +232,9 @@ mcp_status mcp_mixed_scan(const mcp_scan_desc* d, const mcp_scan_tensors* t,
   }
   for (const void* in : {t->x, t->dt, t->B, t->C, t->z})
     if (t->out == in) return fail(MCP_ERR_INVALID_ARG, "out may not overlap an input");
+  if (!mcp::mixed_scan_fits(*d))
+    return fail(MCP_ERR_UNSUPPORTED, "num_seqs %d, total_tokens %d and channels %d exceed a launch", d->num_seqs,
+                d->total_tokens, d->channels);
   return done(mcp::launch_mixed_scan(*d, *t, request_ids, cu_seqlens_q, seqlens_k, workspace,
                                      error_word, stream),
               "mixed_scan launch");

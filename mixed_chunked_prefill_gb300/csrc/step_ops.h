@@ -27,6 +27,7 @@ bool mixed_conv_fits(const mcp_conv_desc& d);  // its grid is one that can be la
 int launch_mixed_conv(const mcp_conv_desc& d, const void* x, const void* weight, const void* bias,
                       void* state, const int32_t* request_ids, const int32_t* cu_seqlens_q,
                       const int32_t* seqlens_k, void* out, int32_t* error_word, void* stream);
+bool mixed_scan_fits(const mcp_scan_desc& d);  // its tasks have 32-bit numbers
 int launch_mixed_scan(const mcp_scan_desc& d, const mcp_scan_tensors& t,
                       const int32_t* request_ids, const int32_t* cu_seqlens_q,
                       const int32_t* seqlens_k, void* workspace, int32_t* error_word,

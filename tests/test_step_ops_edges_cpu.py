@@ -56,3 +56,19 @@ def test_misaligned_arrays_are_refused(lib):
                  "presence_penalty", "bias_offsets", "bias_tokens", "bias_values", "mask", "mask_rows"):
         given = dict(bias_offsets=P16, bias_tokens=P16, bias_values=P16, mask=P16)
         assert logits(lib, tensors={**given, name: bad}) == INVALID, name
+
+
+@pytest.mark.parametrize("call", [conv, scan])
+def test_recurrent_sizes_past_32_bits(lib, call):
+    """Channels whose index would wrap when rounded up to a launch, and more tasks of the long
+    segments than 32 bits number (2^20 segments of 5 tokens, 2^18 channels)."""
+    wide = dict(x_stride=(1 << 30) + 8, out_stride=(1 << 30) + 8)
+    many = dict(num_seqs=1 << 20, total_tokens=5 << 20, channels=1 << 18, x_stride=1 << 18, out_stride=1 << 18)
+    out = dict(out=2 * P16)
+    if call is scan:
+        wide.update(dt_stride=(1 << 30) + 8, z_stride=(1 << 30) + 8)
+        many.update(dt_stride=1 << 18, z_stride=1 << 18)
+        out = dict(tensors=out)
+    assert call(lib, channels=(1 << 30) + 8, **wide, **out) == UNSUPPORTED
+    if call is scan:
+        assert call(lib, **many, **out) == UNSUPPORTED
