@@ -81,7 +81,8 @@ class MixedStep:
     def from_tables(cls, tables, num_q_heads, num_kv_heads, head_dim, sm_scale, options=None,
                     stream=None, rows=None):
         """A step whose tables and slots were built on the device (``RequestTables.step``):
-        nothing but the work lists is copied to the device."""
+        nothing but the work lists is copied to the device.  Where they are padded
+        (``max_tokens``), ``append`` takes the step's tokens alone or padded ones as well."""
         self = cls.__new__(cls)
         pool = tables.pool
         self.cu_h, self.sk_h = tables.cu_h, tables.sk_h
@@ -115,8 +116,10 @@ class MixedStep:
         self.error_word = workspace_error_word(self.plan, self.workspace)
 
     def append(self, k_new, v_new, k_cache, v_cache):
-        paged_kv_append(k_new, v_new, self.slots_d, k_cache, v_cache, self.error_word,
-                        self.stream)
+        slots, n = self.slots_d, int(k_new.shape[0])
+        if int(self.cu_h[-1]) <= n < len(slots):  # a padded slot map (from_tables)
+            slots = slots[:n]
+        paged_kv_append(k_new, v_new, slots, k_cache, v_cache, self.error_word, self.stream)
 
     def attention(self, q, k_cache, v_cache, out, lse=None):
         mixed_attn_fwd(self.plan, q, k_cache, v_cache, self.bt_d, self.cu_d, self.sk_d, out, lse,

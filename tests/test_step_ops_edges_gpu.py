@@ -345,3 +345,58 @@ def test_rows_that_cannot_be_cleared_are_reported(mcp, cu, prompt):
     assert int(err) == _capi.DEVERR_REQUEST
     want = device_state(*ref.update_counts(seen, counts, ids, tokens, cu, V, prompt, True))
     assert torch.equal(sd, want[0]) and torch.equal(cd, want[1])
+
+
+@pytest.mark.parametrize("padded", [False, True])
+def test_attention_on_padded_tables(mcp, padded):
+    """A step whose slot map is longer than its tokens: keys and values of its tokens alone,
+    or padded like the slot map."""
+    import math
+
+    from mixed_chunked_prefill_gb300.step import MixedStep, RequestTables
+
+    rng = np.random.default_rng(17)
+    Hq, Hkv, D, P, cap = 4, 2, 64, 16, 64
+    outs = []
+    for room in (None, cap):
+        tables = RequestTables(12, P, 3, 4)
+        tb = tables.step([1, 0], [21, 9], room)
+        T = int(tb.cu_h[-1])
+        step = MixedStep.from_tables(tb, Hq, Hkv, D, 1 / math.sqrt(D))
+        kc = torch.zeros((12, P, Hkv, D), dtype=torch.bfloat16, device="cuda")
+        vc = torch.zeros_like(kc)
+        n = cap if padded and room else T
+        if not outs:
+            q, k, v = (values(rng, (cap, h, D), "bf16")[1] for h in (Hq, Hkv, Hkv))
+        out = torch.zeros((n, Hq, D), dtype=torch.bfloat16, device="cuda")
+        step.run(q[:n].contiguous(), k[:n].contiguous(), v[:n].contiguous(), kc, vc, out)
+        step.check()
+        outs.append((out[:T], kc, vc))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    with pytest.raises(ValueError):
+        step.append(k[:T - 1].contiguous(), v[:T - 1].contiguous(), kc, vc)
+    with pytest.raises(ValueError):
+        step.append(torch.cat([k, k]), torch.cat([v, v]), kc, vc)
+
+
+def test_tables_on_another_stream(mcp):
+    """Tables, commit and attention's append on a stream of the caller's, behind what it holds."""
+    p, d = ref.Pool(8, 16, 2, 4), Device(mcp, 8, 16, 2, 4)
+    s, busy = torch.cuda.Stream(), torch.randn((2048, 2048), device="cuda")
+    o = dict(cu=i32([77] * 2), sk=i32([77]), bt=i32([[77] * 4]), slots=torch.full((20,), 77, device="cuda"),
+             pos=i32([77] * 20), rows=i32([77]))
+    ids, late, q = i32([1]), i32([-1]), i32([20])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            torch.mm(busy, busy)
+        late.copy_(ids)
+    mcp.build_step_tables(d.pool, late, q, o["cu"], o["sk"], o["bt"], o["slots"], o["pos"], o["rows"], d.err,
+                          s.cuda_stream)
+    mcp.commit_step(d.pool, late, q, None, d.err, s)
+    s.synchronize()
+    want = p.build([1], [20], 20)
+    for got, w in zip(o.values(), want):
+        assert np.array_equal(got.cpu().numpy(), w)
+    p.commit([1], [20], [20], want[6])
+    d.equal(p)
