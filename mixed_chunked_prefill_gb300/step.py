@@ -16,6 +16,7 @@ from __future__ import annotations
 import numpy as np
 
 from . import (
+    _capi,
     PlanOptions,
     build_slot_mapping,
     build_step_tables,
@@ -35,6 +36,10 @@ from . import (
 
 def _i32(a):
     return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
+
+
+def _i64(a):
+    return np.asarray(a, dtype=np.int64)
 
 
 def _on_stream(stream):
@@ -143,7 +148,7 @@ class StepTables:
 
         self.pool, self.after = tables.pool, tables.commits
         dev = tables.device
-        ids, q = _i32(request_ids), _i32(q_lens)
+        ids, q = _i64(request_ids), _i64(q_lens)  # checked before they become 32 bits
         if ids.ndim != 1 or ids.shape != q.shape:
             raise ValueError("request_ids and q_lens must be [num_seqs]")
         live = ids >= 0
@@ -151,20 +156,21 @@ class StepTables:
             raise ValueError("request_ids must be distinct rows of the pool (or < 0)")
         if (q < 0).any():
             raise ValueError("q_lens must be >= 0")
-        q = np.where(live, q, 0).astype(np.int32)
+        q = np.where(live, q, 0)
         had = np.where(live, tables.lens_h[np.where(live, ids, 0)], 0)
         P = self.pool.page_size
-        self.ids_h, self.q_h, self.sk_h = ids, q, (had + q).astype(np.int32)
-        self.cu_h = np.concatenate([[0], np.cumsum(q)]).astype(np.int32)
-        if (self.sk_h > self.pool.max_pages_per_seq * P).any():
+        if (q > self.pool.max_pages_per_seq * P - had).any():
             raise ValueError("a request needs more than max_pages_per_seq pages")
-        self.new_pages = int((-(-self.sk_h // P) - -(-had // P)).sum())
+        self.new_pages = int((-(-(had + q) // P) - -(-had // P)).sum())
         if self.new_pages > tables.free_h:
             raise ValueError(f"{self.new_pages} new pages, {tables.free_h} are free")
-        S, T = len(ids), int(self.cu_h[-1])
+        S, T = len(ids), int(q.sum())
         cap = T if max_tokens is None else int(max_tokens)
-        if T > cap:
-            raise ValueError(f"{T} tokens > max_tokens {cap}")
+        if T > min(cap, _capi.MAX_TOKENS):
+            raise ValueError(f"{T} tokens > max_tokens {min(cap, _capi.MAX_TOKENS)}")
+        ids, q, self.sk_h = _i32(np.maximum(ids, -1 << 31)), _i32(q), _i32(had + q)
+        self.ids_h, self.q_h = ids, q
+        self.cu_h = _i32(np.concatenate([[0], np.cumsum(q)]))
         with _on_stream(stream):
             both = torch.from_numpy(np.concatenate([ids, q])).to(dev)
             self.request_ids, self.q_lens = both[:S], both[S:]
@@ -221,13 +227,13 @@ class RequestTables:
         if step.pool is not self.pool or step.after != self.commits:
             raise ValueError("the step was built before another commit, or from other tables")
         live = step.ids_h >= 0
-        after = step.sk_h if new_lens is None else _i32(new_lens)
+        after = step.sk_h if new_lens is None else _i64(new_lens)
         if after.shape != step.sk_h.shape or ((after < 0) | (after > step.sk_h))[live].any():
             raise ValueError("new_lens must be [num_seqs], at most the step's lengths")
         with _on_stream(stream):
             if step is not self.last:  # another step entered its pages since: the same again
                 step._build(self, stream)
-            to = None if new_lens is None else torch.from_numpy(after).to(self.device)
+            to = None if new_lens is None else torch.from_numpy(_i32(after)).to(self.device)
             commit_step(self.pool, step.request_ids, step.q_lens, to, self.error_word, stream,
                         max_tokens=step.slot_mapping.shape[0])
         self.commits += 1
@@ -239,7 +245,7 @@ class RequestTables:
 
     def release(self, request_ids, stream=None) -> None:
         """End requests: their pages are free and their rows may be used again."""
-        ids = _i32(request_ids)
+        ids = _i64(request_ids)
         none = np.zeros(len(ids), dtype=np.int32)
         self.commit(self.step(ids, none, stream=stream), none, stream)
 

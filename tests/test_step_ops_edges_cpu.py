@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 
+import numpy as np
 import pytest
 
 from mixed_chunked_prefill_gb300 import _capi
@@ -72,3 +73,20 @@ def test_recurrent_sizes_past_32_bits(lib, call):
     assert call(lib, channels=(1 << 30) + 8, **wide, **out) == UNSUPPORTED
     if call is scan:
         assert call(lib, **many, **out) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("ids,q", [([0], [2 ** 31 - 1]), ([0, 1], [2 ** 31 - 1] * 2), ([1], np.array([2 ** 32 + 1])),
+                                   (np.array([2 ** 32]), [1]), ([1], [2 ** 31])])
+def test_step_lengths_past_32_bits(ids, q):
+    """Lengths and rows are checked before they become 32 bits: nothing wraps into range."""
+    from types import SimpleNamespace
+
+    from mixed_chunked_prefill_gb300.step import RequestTables, StepTables
+
+    pool_ = SimpleNamespace(max_requests=4, max_pages_per_seq=1 << 20, page_size=64)
+    tables = SimpleNamespace(pool=pool_, commits=0, device="cpu", lens_h=np.array([5, 0, 0, 0]), free_h=1 << 26)
+    with pytest.raises(ValueError):
+        StepTables(tables, ids, q, None, None)
+    step = SimpleNamespace(pool=pool_, after=0, ids_h=np.array([0]), sk_h=np.array([7], dtype=np.int32))
+    with pytest.raises(ValueError):
+        RequestTables.commit(tables, step, np.array([2 ** 32 + 1]))
