@@ -42,8 +42,8 @@ def _i64(a):
     return np.asarray(a, dtype=np.int64)
 
 
-def _on_stream(stream):
-    """Allocations and copies inside belong to ``stream`` (None: the current one)."""
+def _on_stream(stream, device):
+    """Allocations and copies inside belong to ``stream`` of ``device`` (None: the current one)."""
     import contextlib
 
     import torch
@@ -51,7 +51,7 @@ def _on_stream(stream):
     if stream is None:
         return contextlib.nullcontext()
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
-                             else torch.cuda.ExternalStream(int(stream)))
+                             else torch.cuda.ExternalStream(int(stream), device))
 
 
 class MixedStep:
@@ -171,7 +171,7 @@ class StepTables:
         ids, q, self.sk_h = _i32(np.maximum(ids, -1 << 31)), _i32(q), _i32(had + q)
         self.ids_h, self.q_h = ids, q
         self.cu_h = _i32(np.concatenate([[0], np.cumsum(q)]))
-        with _on_stream(stream):
+        with _on_stream(stream, dev):
             both = torch.from_numpy(np.concatenate([ids, q])).to(dev)
             self.request_ids, self.q_lens = both[:S], both[S:]
             i32 = dict(dtype=torch.int32, device=dev)
@@ -230,7 +230,7 @@ class RequestTables:
         after = step.sk_h if new_lens is None else _i64(new_lens)
         if after.shape != step.sk_h.shape or ((after < 0) | (after > step.sk_h))[live].any():
             raise ValueError("new_lens must be [num_seqs], at most the step's lengths")
-        with _on_stream(stream):
+        with _on_stream(stream, self.device):
             if step is not self.last:  # another step entered its pages since: the same again
                 step._build(self, stream)
             to = None if new_lens is None else torch.from_numpy(_i32(after)).to(self.device)

@@ -90,3 +90,23 @@ def test_step_lengths_past_32_bits(ids, q):
     step = SimpleNamespace(pool=pool_, after=0, ids_h=np.array([0]), sk_h=np.array([7], dtype=np.int32))
     with pytest.raises(ValueError):
         RequestTables.commit(tables, step, np.array([2 ** 32 + 1]))
+
+
+def test_raw_streams_are_of_the_tables_device(monkeypatch):
+    """A stream given as an address is one of the tables' device, whatever the current one is."""
+    import contextlib
+
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+
+    from mixed_chunked_prefill_gb300 import step
+
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda ptr, device=None: made.append((ptr, device)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(step, "build_step_tables", lambda *a: None)
+    pool_ = SimpleNamespace(max_requests=4, max_pages_per_seq=4, page_size=16)
+    dev = torch.device("cpu")
+    tables = SimpleNamespace(pool=pool_, commits=0, device=dev, lens_h=np.zeros(4, np.int64), free_h=9, error_word=None)
+    built = step.StepTables(tables, [0, -1, 2], [5, 0, 20], 64, 77)
+    assert made == [(77, dev)] and built.cu_h.tolist() == [0, 5, 5, 25] and tables.last is built
