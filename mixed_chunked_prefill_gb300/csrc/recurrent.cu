@@ -547,6 +547,12 @@ __device__ __forceinline__ void softplus2(float& v0, float& v1) {
 // arithmetic (with one, 225 instructions a warp and segment kept the issue slots
 // 80% busy).  256 decodes of 8192 channels and 16 states: 49 us, 5.8 TB/s; one
 // channel a lane 61 us.
+//
+// A call with at most as many tokens as segments has no other launch, and a padded
+// step of it may hold a long segment.  The tokens behind a segment's first come in
+// asynchronous copies as well, up to four ahead, over the state that was read (900
+// tokens and 100 decodes of 8192 channels: 370 us, loaded one by one 914; with one
+// row of tokens more, through the long segments' launches, 138).
 template <typename T>
 __device__ __forceinline__ float scalar(const T* p) {
   if constexpr (std::is_same<T, __half>::value) return __half2float(*p);
@@ -574,6 +580,8 @@ struct ShortCfg {
   static constexpr int kX = 1024;                            // offsets in a slot: state first
   static constexpr int kB = kX + (3 * kXBytes + 15) / 16 * 16;
   static constexpr int kSlot = kB + 2 * N * 2;
+  static constexpr int kInputs = kSlot - kX;                 // bytes of a token beside the state
+  static constexpr int kTokens = 1024 / kInputs < 4 ? 1024 / kInputs : 4;  // that fit over a state
 };
 
 template <typename T, int N>
@@ -677,18 +685,39 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const ScanArg
       const int32_t old = __shfl_sync(0xffffffffu, m.old, i);
       id = __shfl_sync(0xffffffffu, m.id, i);
       float h[2][4], x[2], d[2], z[2];
+      uint2 b, q;
+      auto inputs = [&](const unsigned char* at) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const T* xs = reinterpret_cast<const T*>(at) + cl + e * C::kHalf;
+          x[e] = scalar<T>(xs);
+          d[e] = scalar<T>(xs + CPW);
+          z[e] = p.z ? scalar<T>(xs + 2 * CPW) : 0.f;
+        }
+        b = *reinterpret_cast<const uint2*>(at + C::kB - C::kX + 8 * sub);
+        q = *reinterpret_cast<const uint2*>(at + C::kB - C::kX + 2 * N + 8 * sub);
+      };
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (old) v = *reinterpret_cast<const float4*>(slot + 512 * e + 16 * lane);
         h[e][0] = v.x, h[e][1] = v.y, h[e][2] = v.z, h[e][3] = v.w;
-        const T* xs = reinterpret_cast<const T*>(slot + C::kX) + cl + e * C::kHalf;
-        x[e] = scalar<T>(xs);
-        d[e] = scalar<T>(xs + CPW);
-        z[e] = p.z ? scalar<T>(xs + 2 * CPW) : 0.f;
       }
-      uint2 b = *reinterpret_cast<const uint2*>(slot + C::kB + 8 * sub);
-      uint2 q = *reinterpret_cast<const uint2*>(slot + C::kB + 2 * N + 8 * sub);
+      inputs(slot + C::kX);
+      // the tokens behind the first, a few ahead, over the state that was read
+      auto token = [&](int32_t t) {
+        unsigned char* at = ring[i % kAhead] + (t - q0) % C::kTokens * C::kInputs + to - C::kX;
+        if (t < q1) {
+          if (what >= 3) copy_async<16>(at, src + t * ld);
+          else if (what >= 0) copy_async<C::kXPiece>(at, src + t * ld);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      if (q1 - q0 > 1) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 1; k <= C::kTokens; ++k) token(q0 + k);
+      }
       for (int32_t t = q0;;) {
         float bb[4], qq[4], y[2];
         unpack4<T>(b, bb);
@@ -722,14 +751,11 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const ScanArg
             static_cast<T*>(p.out)[t * p.ldo + (e ? cc[1] : cc[0])] = static_cast<T>(s);
         }
         if (++t >= q1) break;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          x[e] = scalar<T>(static_cast<const T*>(p.x) + t * p.ldx + cc[e]);
-          d[e] = scalar<T>(static_cast<const T*>(p.dt) + t * p.lddt + cc[e]);
-          z[e] = p.z ? scalar<T>(static_cast<const T*>(p.z) + t * p.ldz + cc[e]) : 0.f;
-        }
-        b = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.B) + t * p.ldb + gn + 4 * sub);
-        q = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.C) + t * p.ldc + gn + 4 * sub);
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kTokens - 1) : "memory");
+        __syncwarp();
+        inputs(slot + (t - q0) % C::kTokens * C::kInputs);
+        __syncwarp();
+        token(t + C::kTokens);
       }
       float* to_state = state + id * row;
       if (live[0]) *reinterpret_cast<float4*>(to_state) = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);

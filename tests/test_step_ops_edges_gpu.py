@@ -400,3 +400,18 @@ def test_tables_on_another_stream(mcp):
         assert np.array_equal(got.cpu().numpy(), w)
     p.commit([1], [20], [20], want[6])
     d.equal(p)
+
+
+# ------------------------------------------------------------------- many segments
+@pytest.mark.parametrize("lens,pad", [([50], 60), ([1] * 9 + [200, 7] + [1] * 9, 300), ([5, 4, 30], 39)])
+@pytest.mark.parametrize("N,d", [(16, 72), (64, 40)])
+def test_long_segments_among_more_slots_than_tokens(mcp, lens, pad, N, d):
+    """A padded step with at most as many tokens as segment slots may still hold a chunk."""
+    rng = np.random.default_rng(len(lens) + N)
+    ids, cu, sk, R, T = stream(rng, lens, [5] * len(lens), pad, 0)
+    assert T <= len(ids)
+    v = scan_inputs(rng, T, d, N, 1, "bf16", R, True, 1.0)
+    out, err = torch.full((T, d), 7.0, dtype=torch.bfloat16, device="cuda"), err_word()
+    _, (want, bound, end, ebound) = run_scan(mcp, v, ids, cu, sk, "Dzb", True, "bf16", out, err)
+    assert int(err) == 0 and (np.abs(f64(out) - want) <= bound).all()
+    assert (np.abs(f64(v["state"][1]) - end) <= ebound).all()
