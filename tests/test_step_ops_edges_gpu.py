@@ -403,6 +403,90 @@ def test_tables_on_another_stream(mcp):
 
 
 # ------------------------------------------------------------------- many segments
+def test_conv_of_many_segments(mcp):
+    """Three hundred segments, decodes with speculated tokens among chunks."""
+    rng = np.random.default_rng(51)
+    lens = rng.choice([1, 1, 1, 1, 2, 3, 4, 5, 17, 33, 0, 64], 300)
+    ids, cu, sk, R, T = stream(rng, lens, rng.choice([0, 9], 300), 4, 3)
+    for K, d, dtype in ((4, 136, "bf16"), (2, 520, "fp16")):
+        x, xd = values(rng, (T, d), dtype)
+        w, wd = values(rng, (d, K), dtype)
+        b, bd = values(rng, (d,), dtype)
+        st, sd = values(rng, (R, K - 1, d), dtype)
+        out = torch.full((T, d), 7.0, dtype=DT[dtype], device="cuda")
+        err = err_word()
+        mcp.mixed_conv(xd, wd, bd, sd, i32(ids), i32(cu), i32(sk), "silu", out, err)
+        want, bound, end = ref.conv(x, w, b, st, ids, cu, sk, True, dtype)
+        n = cu[-1]
+        assert int(err) == 0 and (f64(out)[n:] == 7).all()
+        assert (np.abs(f64(out)[:n] - want[:n]) <= bound[:n]).all()
+        assert np.array_equal(f64(sd), end)
+
+
+@pytest.mark.parametrize("N,G,d,dtype", [(16, 1, 72, "bf16"), (64, 2, 64, "fp16"), (8, 1, 264, "bf16"),
+                                         (32, 3, 96, "bf16")])
+def test_scan_of_many_segments(mcp, N, G, d, dtype):
+    """Decodes, padding inside the stream and long segments (many cut) in several blocks of 32."""
+    rng = np.random.default_rng(N)
+    lens = np.concatenate([rng.choice([1, 1, 2, 3, 4, 0], 90), rng.integers(5, 70, 40), [210, 131, 300, 65, 97]])
+    rng.shuffle(lens)
+    ids, cu, sk, R, T = stream(rng, lens, rng.choice([0, 9], len(lens)), 3, 2)
+    for s in (20, 77):
+        ids[s] = -1  # a padding segment that has tokens: left out
+    v = scan_inputs(rng, T, d, N, G, dtype, R, True, 1.0)
+    out = torch.full((T, d), 7.0, dtype=DT[dtype], device="cuda")
+    err = err_word()
+    _, (want, bound, end, ebound) = run_scan(mcp, v, ids, cu, sk, "Dzb", True, dtype, out, err)
+    ran = np.zeros(T, bool)
+    for s, r in enumerate(ids):
+        ran[cu[s]:cu[s + 1]] = r >= 0
+    assert int(err) == 0 and (f64(out)[~ran] == 7).all()
+    assert (np.abs(f64(out)[ran] - want[ran]) <= bound[ran]).all()
+    assert (np.abs(f64(v["state"][1]) - end) <= ebound).all()
+
+
+def test_scan_of_more_segments_than_one_load(mcp):
+    """A decode batch in which a warp's share is more than the 32 segments whose metadata it
+    loads at once: bit for bit what calls of a few segments each give, and some of them
+    against the definition."""
+    rng = np.random.default_rng(61)
+    S, d, N, R = 700, 8192, 16, 701
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+
+    def normal(*shape, dtype=torch.bfloat16):
+        return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+    x, dt, z, B, C = normal(S, d), normal(S, d), normal(S, d), normal(S, 1, N), normal(S, 1, N)
+    A, D, bias = -normal(d, N, dtype=torch.float32).exp(), normal(d, dtype=torch.float32), normal(d, dtype=torch.float32)
+    state = normal(R, d, N, dtype=torch.float32)
+    ids = torch.from_numpy(rng.permutation(R)[:S]).int().cuda()
+    ids[rng.permutation(S)[:40]] = -1
+    sk = torch.from_numpy(rng.choice([1, 9], S)).int().cuda()
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    states, outs = [], []
+    for step in (S, 60):
+        st, out, err = state.clone(), torch.full((S, d), 7.0, dtype=torch.bfloat16, device="cuda"), err_word()
+        for a in range(0, S, step):
+            s = slice(a, min(S, a + step))
+            mcp.mixed_scan(x[s], dt[s], A, B[s], C[s], st, ids[s], cu[:s.stop - a + 1].contiguous(), sk[s], D=D, z=z[s],
+                           dt_bias=bias, out=out[s], error_word=err)
+        assert int(err) == 0
+        states.append(st)
+        outs.append(out)
+    assert torch.equal(*states) and torch.equal(*outs)
+    for s in [0, 1, 31, 32, 33, 600, 607, 608, 609, 640, S - 1] + rng.integers(0, S, 8).tolist():
+        r = int(ids[s])
+        if r < 0:
+            assert (outs[0][s] == 7).all()
+            continue
+        want, bound, end, ebound = ref.scan(*(f64(t[s:s + 1]) for t in (x, dt)), f64(A), *(f64(t[s:s + 1]) for t in (B, C)),
+                                            f64(D), f64(z[s:s + 1]), f64(bias), True, f64(state[r:r + 1]), [0], [0, 1],
+                                            [int(sk[s])], "bf16")
+        assert (np.abs(f64(outs[0][s]) - want[0]) <= bound[0]).all()
+        assert (np.abs(f64(states[0][r]) - end[0]) <= ebound[0]).all()
+
+
 @pytest.mark.parametrize("lens,pad", [([50], 60), ([1] * 9 + [200, 7] + [1] * 9, 300), ([5, 4, 30], 39)])
 @pytest.mark.parametrize("N,d", [(16, 72), (64, 40)])
 def test_long_segments_among_more_slots_than_tokens(mcp, lens, pad, N, d):
