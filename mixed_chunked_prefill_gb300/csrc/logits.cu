@@ -272,6 +272,18 @@ struct alignas(n * sizeof(T)) Vec {
   T v[n];
 };
 
+// 1 / t for products: hi the part that fp32 holds, cut off, and lo > 0 what is left
+// of it, so that x / t = x hi + x lo is off by its one rounding (and 2^-46), and of an
+// infinite x both are infinite alike.  t from 2^-123 to 2^64.
+struct Reciprocal {
+  float hi, lo;
+  __device__ __forceinline__ explicit Reciprocal(float t) {
+    hi = __frcp_rz(t);
+    lo = fmaxf(hi * fmaf(-t, hi, 1.f), hi * 0x1p-60f);
+  }
+  __device__ __forceinline__ float times(float x) const { return fmaf(x, hi, x * lo); }
+};
+
 // The bias of token `tok`, which has one: entries [lo, hi) in rising order.
 template <typename Tokens, typename Values>
 __device__ __forceinline__ float find_bias(Tokens tokens, Values values, int32_t lo, int32_t hi, int32_t tok) {
@@ -397,12 +409,12 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_
   const float temp = p.temperature ? p.temperature[row] : 0.f;
   const bool scale = temp > 0.f && temp != 1.f;
   const bool every = !p.inplace || scale;
-  // quotients as products: one rounding more, a tenth of the instructions; a
-  // temperature whose reciprocal overflows or is subnormal (fewer bits) is taken
-  // 2^64 or 2^-64 times, and its quotients again; such a repetition penalty divides
-  const float after = !scale ? 1.f : temp < 1e-37f ? 0x1p64f : temp > 0x1p125f ? 0x1p-64f : 1.f;
-  const float inv = scale ? 1.f / (temp * after) : 1.f, rinv = 1.f / rho;
-  const bool divide = rinv > 3.4e38f || rinv < 0x1p-125f;
+  // quotients as products with the reciprocal in two parts (a tenth of the
+  // instructions of a division); a temperature near an end of fp32 is taken 2^64 or
+  // 2^-64 times, and its quotients again; such a repetition penalty divides
+  const float after = !scale ? 1.f : temp < 1e-37f ? 0x1p64f : temp > 0x1p64f ? 0x1p-64f : 1.f;
+  const Reciprocal inv(scale ? temp * after : 1.f), rinv(rho);
+  const bool divide = !(rho > 0x1p-64f && rho < 0x1p64f);
   __syncthreads();
   for (int32_t e = lo + threadIdx.x; e < hi; e += kLogitThreads) {
     if (e != lo + static_cast<int32_t>(threadIdx.x)) {
@@ -456,7 +468,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_
   };
   auto whole_tile = [&](int32_t base) { return base >= 0 && base + kLogitTile <= end; };
   // x / temperature, or the masked value
-  auto finish = [&](float x) { return x * inv * after; };
+  auto finish = [&](float x) { return inv.times(x) * after; };
   auto put = [&](int32_t v, const float* x, uint32_t touch) {
     Vec<TO, kVec> y;
 #pragma unroll
@@ -624,7 +636,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas<TI>) process_logits_
                                         : find_bias(p.bias_tokens, p.bias_values, lo, hi, v);
           had = plane[4 * kPlane + k[j]] >> sh[j] & 1;
         }
-        if (had) x = x <= 0.f ? x * rho : divide ? __fdiv_rn(x, rho) : x * rinv;
+        if (had) x = x <= 0.f ? x * rho : divide ? __fdiv_rn(x, rho) : rinv.times(x);
         if (n[j] > 0) x = x - __fmul_rn(freq, static_cast<float>(n[j])) - pres;
         out[v] = from_f<TO>(finish(x));
       }

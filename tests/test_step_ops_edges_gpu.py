@@ -331,6 +331,35 @@ def test_logits_over_the_largest_divisors(mcp, what, inplace):
     assert (np.abs(got - want) <= np.where(normal, 3 * 2.0 ** -24 * np.abs(want), 2.0 ** -148)).all()
 
 
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("what", ["temperature", "repetition"])
+def test_logits_are_divided(mcp, what, inplace):
+    """Quotients in fp32 are off by half a step (2^-24 of them, and 2^-44 of the way there);
+    infinities and NaN stay what a division makes of them, by powers of two as well."""
+    rng = np.random.default_rng(9)
+    B, V = 60, 4099
+    by = np.concatenate([[0.25, 0.5, 1.0, 2.0, 64.0, 0.7], 2.0 ** rng.uniform(-40, 40, 20), rng.uniform(0.2, 2, B - 26)])
+    by = by.astype(np.float32)
+    rows = (rng.normal(size=(B, V)) * 4).astype(np.float32)
+    if what == "repetition":
+        rows = np.abs(rows)
+    rows[:, :3] = np.inf, 0.0, np.nan
+    if what == "temperature":
+        rows[:, 3] = -np.inf
+    src = torch.from_numpy(rows).cuda()
+    kw = dict(temperature=torch.from_numpy(by).cuda())
+    if what == "repetition":
+        seen = np.zeros((B, 2, V), bool)
+        seen[:, 0] = True
+        sd, cd = device_state(seen, np.zeros((B, V), np.int64))
+        kw = dict(request_ids=i32(range(B)), seen=sd, counts=cd, repetition_penalty=torch.from_numpy(by).cuda())
+    got = f64(mcp.process_logits(src, None if inplace else torch.empty_like(src), **kw))
+    want = rows.astype(np.float64) / by.astype(np.float64)[:, None]
+    fine = np.isfinite(want)
+    assert np.array_equal(got[~fine], want[~fine], equal_nan=True)
+    assert (np.abs(got[fine] - want[fine]) <= 2.0 ** -24 * (1 + 2.0 ** -20) * np.abs(want[fine])).all()
+
+
 @pytest.mark.parametrize("cu", [[0, 0, 0, 0], [0, 0, 3, 3]])
 @pytest.mark.parametrize("prompt", [True, False])
 def test_rows_that_cannot_be_cleared_are_reported(mcp, cu, prompt):
