@@ -618,7 +618,8 @@ typedef struct mcp_request_pool {
  *       last one (mcp_paged_kv_append skips those)
  *   positions    int32 [max_tokens] or NULL: position of each new token, then 0
  *   logits_indices int32 [S] or NULL: the last token of every segment that has
- *       one, in segment order, then -1
+ *       one, in segment order, then -1 (mcp_gather_rows writes zero rows for
+ *       those and reports them)
  * request_ids[s] < 0 is a padding segment: no tokens, a row of -1 (a captured
  * step of fixed size).  The new pages are also entered into request_pages
  * behind the held ones; lengths and free list stay as they are until
@@ -761,7 +762,11 @@ mcp_status mcp_mixed_scan(const mcp_scan_desc* desc, const mcp_scan_tensors* ten
  * not).  The call needs none: without (workspace NULL) a segment is run in one
  * piece, which takes longer where few long segments leave most of the GPU idle.
  * 256-byte aligned; its contents need no preparation and mean nothing after the
- * call.  Calls that share one must be ordered.  The way a segment is cut does
+ * call.  Calls that share one must be ordered.  A call with total_tokens <=
+ * num_seqs is taken for a step of decodes and has no use for one: a long segment
+ * in it is run token after token (900 tokens of 8192 channels: 370 us instead of
+ * 138; rows of tokens behind the last segment make it a call of the other kind).
+ * The way a segment is cut does
  * not depend on other segments' values, but changes results within fp32
  * rounding.
  */
@@ -829,7 +834,8 @@ typedef struct mcp_logits_tensors {
 } mcp_logits_tensors;
 
 /*
- * For every row i with request row r and token v, in fp32, rounded once:
+ * For every row i with request row r and token v, in fp32 (each operation
+ * rounded), rounded to the type of out at the end:
  *   x = logits[i,v] + bias;   x = x > 0 ? x / repetition : x * repetition  if v
  *   is in the prompt or was sampled;   x -= frequency * counts[r,v] + presence
  *   if it was sampled;   x /= temperature if > 0;   x = -inf if the mask's bit

@@ -326,7 +326,7 @@ __device__ __forceinline__ void copy_wait() {
 // us longer for 512 rows).
 //
 // 512 rows of 128000 tokens, bf16 to fp32, us: 65 without anything seen (6.3
-// TB/s), 73 with 2000 seen tokens a row; half of the rows masked, 64 and 72.
+// TB/s), 74 with 2000 seen tokens a row; half of the rows masked, 64 and 71.
 // Beside the traffic it is the phases of a CTA, each of which begins with loads
 // that nothing hides but the SM's other CTAs.
 enum LogitRows { kWhole, kShifted, kSingle };
@@ -732,8 +732,9 @@ int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,
   a.num_bias = d.num_biases;
   a.num_masks = d.num_masks;
   // a CTA reads its row's parameters, bits and biases once for several tiles
-  // where there are enough for six CTAs on every SM (64 rows in place, 2000 seen
-  // tokens: 8.0 us; for three, four and eight 9.1)
+  // where there are enough for six CTAs on every SM (64 rows of bf16 in place, 2000
+  // seen tokens a row, no biases or masks: 8.3 us; for three and four 8.8, for eight
+  // 9.1; of fp32, of which four CTAs fit an SM, 10.0, 8.5 and 9.0)
   const int64_t row_tiles = (d.vocab_size + 3LL + kLogitTile - 1) / kLogitTile;  // shifted by up to 3
   const int64_t places = 6LL * step_num_sms();
   int64_t tiles = (row_tiles * d.num_rows + places - 1) / places;

@@ -6,8 +6,9 @@
 // varlen 接口": decodes and chunks are segments of different lengths; the
 // segment has history when seqlens_k counts more than its own tokens), so a
 // decode is a segment of one token and a continued chunk starts from its
-// request's state.  A segment's state is read and written by the one CTA (or
-// thread) that owns its channels: no state crosses CTAs.
+// request's state.  A segment's state is read and written by the one warp (or
+// thread) that owns its channels; only a long segment that the scan cuts hands its
+// states from piece to piece, through the workspace.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -164,7 +165,7 @@ __device__ __forceinline__ Segment read_segment(const Segments& g, int32_t s) {
   return x;
 }
 
-// One CTA of each launch looks the metadata over: segments outside the stream,
+// One CTA of a call (of the scan's last launch) looks the metadata over: segments outside the stream,
 // request rows outside the state, a request in two segments that have tokens
 // (its state would be written twice).  Rows are marked in windows of 32768.
 __device__ void check_segments(const Segments& g) {
@@ -196,15 +197,17 @@ __device__ void check_segments(const Segments& g) {
 // Each input is read once and each output written once.  Segments of at most 4
 // tokens (decodes) get a CTA per two of them and 512 channels: the kept inputs
 // and first tokens of both are requested at once, which is what their few
-// microseconds consist of (1000 decodes of 8192 channels: 27 us, 4.8 TB/s; one,
-// three or four segments a CTA 31, 32 and 33 us; 256 decodes: 8.8 us).  The
+// microseconds consist of (1000 decodes of 8192 channels: 28 us, 4.7 TB/s; one,
+// three or four segments a CTA 30, 32 and 34 us; 256 decodes: 8.8 us).  The
 // tokens of longer segments are dealt in runs of TT (8192 tokens of 8192
-// channels: 51 us, 5.3 TB/s; runs of 32 49, but 2048 tokens then take longer): a thread
-// carries the K - 1 last inputs of 4 channels in registers, so only the first
-// tokens of a run read inputs again (HBM-bound; 64 registers, so that 32 warps
-// an SM have 4 loads of 8 bytes in flight a thread).  The run that holds a segment's first token also takes its next K - 2
-// (even past its end: those still need the kept inputs) and writes the new kept
-// inputs, so nobody else reads or writes that state.
+// channels: 51 us, 5.2 TB/s; runs of 32 50, but 2048 tokens and 64 decodes 18.6
+// instead of 18.2): a thread carries the K - 1 last inputs of 4 channels in
+// registers, so only the first tokens of a run read inputs again (HBM-bound; 64
+// registers, so that 32 warps an SM have 4 loads of 8 bytes in flight a thread; with
+// four taps 64 bytes a thread are spilled for that).  The run that holds a
+// segment's first token also takes its next K - 2 (even past its end: those still
+// need the kept inputs) and writes the new kept inputs, so nobody else reads or
+// writes that state.
 struct ConvArgs {
   Segments g;
   const void* x;
@@ -475,8 +478,9 @@ int conv_width(const ConvArgs& a, int K, int64_t grid, cudaStream_t st) {
 // Per channel c and state n, along a segment's tokens:
 //   d = softplus(dt + dt_bias),  h = exp(d A[c, n]) h + d x B[n],
 //   y = sum_n C[n] h[c, n] + D[c] x,  out = y silu(z).
-// State and sums are fp32.  exp(d A) is ex2.approx of d (A log2 e): 2 ulp,
-// and the recurrence multiplies by it once a token.
+// State and sums are fp32.  exp(d A) is ex2.approx of d (A log2 e): the 2 ulp of
+// the instruction and three roundings of its argument, (4 + 3 |d A|) 2^-24 of it,
+// beside the error of d; the recurrence multiplies by it once a token.
 //
 // Least traffic: x, dt, z read and out written once (8 bytes per token and
 // channel in 16 bits) and the states once.  Segments of a few tokens (decodes)
@@ -545,7 +549,7 @@ __device__ __forceinline__ void softplus2(float& v0, float& v1) {
 // and inputs of the next segments in asynchronous copies to the warp's ring in
 // shared memory, and a second channel halves what a segment costs beside its
 // arithmetic (with one, 225 instructions a warp and segment kept the issue slots
-// 80% busy).  256 decodes of 8192 channels and 16 states: 49 us, 5.8 TB/s; one
+// 80% busy).  256 decodes of 8192 channels and 16 states: 48.6 us, 5.9 TB/s; one
 // channel a lane 61 us.
 //
 // A call with at most as many tokens as segments has no other launch, and a padded
@@ -775,12 +779,12 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const ScanArg
 // the layout is for: shared memory returns 128 bytes a clock, also for a
 // broadcast, and with fewer states times channels a lane the B and C loads
 // alone (32 to 40 clocks an SM for 32 channels of a token) outweigh the
-// arithmetic.  That is 107 instructions for 32 channels of a token and 16
+// arithmetic.  That is 110 instructions for 32 channels of a token and 16
 // states, 19 of them ex2 or reciprocals, some 40 packed pairs that take two
-// issue slots each: 178 clocks a sub-partition, whether 8, 12 or 16 warps an SM
-// run, with scalar products in place of the pairs or not (1.24 M such groups,
-// 12 x 340 tokens of 9728 channels: 183 us).  A lane of one channel needs 153
-// instructions and 221 clocks.  The next token's softplus stands beside the
+// issue slots each: 184 clocks a sub-partition (1.24 M such groups, 12 x 340 tokens
+// of 9728 channels: 192 us).  With 3 instructions less in the gate it was 178,
+// whether 8, 12 or 16 warps an SM ran, with scalar products in place of the pairs or
+// not; a lane of one channel needed 153 instructions and 221 clocks.  The next token's softplus stands beside the
 // recurrence, 32 independent chains of it.
 //
 // Tiles of 16 tokens of x, dt, z, B and C come in asynchronous copies to the
@@ -1289,8 +1293,8 @@ int scan_launch(ScanArgs a, cudaStream_t st) {
   a.blocks = (a.channels + per - 1) / per;
   // more warps than stay at once (32 an SM), as a warp's last segments end
   // unevenly; for little work one round of them, whose starts are not repeated
-  // (8192 channels, 28 and 64 warps an SM: 16 segments 6.6 and 8.0 us, 64 16.1 and
-  // 16.9, 128 28.4 and 27.7, 256 53 and 49)
+  // (8192 channels, 28 and 64 warps an SM: 16 segments 7.3 and 7.9 us, 64 17.1 and
+  // 16.9, 128 30.7 and 27.0, 256 54.0 and 48.6)
   const int64_t per_sm = static_cast<int64_t>(a.blocks) * a.g.S < 256LL * sms ? 28 : 64;
   const int64_t want = (per_sm * sms + a.blocks - 1) / a.blocks;
   a.split = static_cast<int32_t>(want < a.g.S ? want : a.g.S);
