@@ -420,6 +420,12 @@ def _row_arg(t, dtype, name, dev, shape):
     return t.data_ptr(), strides[0] if shape[0] > 1 else -(-row // 8) * 8
 
 
+def _sizes(*sizes):
+    """The C structures hold 32-bit sizes; a larger one would be cut off, not refused."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"a size of {max(sizes)} is past 32 bits")
+
+
 def _error(error_word, dev):
     """Address of an error word: None, an int32 CUDA tensor, or a device address."""
     if error_word is None:
@@ -507,6 +513,7 @@ def make_request_pool(request_pages, request_lens, free_pages, free_count,
     if request_pages.dim() != 2:
         raise ValueError("request_pages must be [max_requests, max_pages_per_seq]")
     R, width = request_pages.shape
+    _sizes(R, width, int(page_size), free_pages.numel())
     i32 = torch.int32
     pool = RequestPool(
         R, width, int(page_size), int(free_pages.numel()),
@@ -537,6 +544,7 @@ def build_step_tables(pool: RequestPool, request_ids, q_lens, cu_seqlens_q, seql
 
     dev, i32 = _pool_device(pool, request_ids), torch.int32
     S, cap = int(request_ids.shape[0]), int(slot_mapping.shape[0])
+    _sizes(S, cap)
     one = (S,)
     _launch("build_step_tables", dev, stream, load().mcp_build_step_tables, ctypes.byref(pool),
             _arg(request_ids, i32, "request_ids", dev, one), _arg(q_lens, i32, "q_lens", dev, one),
@@ -560,6 +568,7 @@ def commit_step(pool: RequestPool, request_ids, q_lens, new_lens=None, error_wor
     dev, i32 = _pool_device(pool, request_ids), torch.int32
     one = (int(request_ids.shape[0]),)
     cap = getattr(pool, "max_tokens", _capi.MAX_TOKENS) if max_tokens is None else int(max_tokens)
+    _sizes(one[0], cap)
     _launch("commit_step", dev, stream, load().mcp_commit_built_step, ctypes.byref(pool),
             _arg(request_ids, i32, "request_ids", dev, one), _arg(q_lens, i32, "q_lens", dev, one),
             _arg(new_lens, i32, "new_lens", dev, one), one[0], cap, _error(error_word, dev))
@@ -596,6 +605,7 @@ def mixed_conv(x, weight, bias, state, request_ids, cu_seqlens_q, seqlens_k, act
     rows = x.shape
     T, d = rows
     K, S, R = weight.shape[1], request_ids.shape[0], state.shape[0]
+    _sizes(T, d, K, S, R)
     if out is None:
         out = _empty(rows, dtype, x.device, stream, result=True)
     px, ldx = _row_arg(x, dtype, "x", dev, rows)
@@ -630,6 +640,7 @@ def mixed_scan(x, dt, A, B, C, state, request_ids, cu_seqlens_q, seqlens_k, D=No
     rows, bc = x.shape, B.shape
     T, d = rows
     G, N, S, R = bc[1], bc[2], request_ids.shape[0], state.shape[0]
+    _sizes(T, d, G, N, S, R)
     if out is None:
         out = _empty(rows, dtype, x.device, stream, result=True)
     px, ldx = _row_arg(x, dtype, "x", dev, rows)
@@ -682,6 +693,7 @@ def update_token_counts(request_ids, tokens, seen, counts, vocab_size, cu_tokens
     dev, i32 = _gpu(request_ids, "request_ids"), torch.int32
     n, rows, V = tokens.shape[0], request_ids.shape[0], int(vocab_size)
     R, ps, pc = _token_state(seen, counts, V, dev)
+    _sizes(n, rows, V, R)
     _launch("update_token_counts", dev, stream, load().mcp_update_token_counts,
             _arg(request_ids, i32, "request_ids", dev, (rows,)), rows,
             _arg(tokens, i32, "tokens", dev, (n,)), n,
@@ -729,6 +741,7 @@ def process_logits(logits, out=None, request_ids=None, seen=None, counts=None, t
             raise ValueError("bias must be (offsets [rows + 1], tokens [n], values [n])")
         biases = tok.shape[0]
     masks = 0 if mask is None else mask.shape[0]
+    _sizes(rows, V, R, biases, masks)
     desc = _capi.LogitsDesc(rows, V, R, _dtype_code(logits, "logits"), _dtype_code(out, "out"),
                             biases, masks, 0, ld[0], ld[1])
     tensors = _capi.LogitsTensors(

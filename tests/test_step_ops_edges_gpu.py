@@ -135,6 +135,26 @@ def test_step_committed_after_another_was_built(mcp, later):
     assert sorted(tables.free_pages.tolist()) == list(range(20))
 
 
+def test_sizes_past_32_bits_are_refused(mcp):
+    """A size that the C structures cannot hold is refused by the binding: 2^32 + 8 tokens
+    would be taken for 8."""
+    V, n = 40, (1 << 32) + 8
+    sd, cd = device_state(np.zeros((2, 2, V), bool), np.zeros((2, V), np.int64))
+    tokens = torch.empty(n, dtype=torch.int32, device="cuda")
+    tokens[:8] = 3
+    with pytest.raises(ValueError):
+        mcp.update_token_counts(i32([0, 1]), tokens, sd, cd, V, i32([0, 4, 8]))
+    assert not sd.any() and not cd.any()
+    d = Device(mcp, 10, 16, 3, 4)
+    one = i32([1])
+    with pytest.raises(ValueError):
+        mcp.commit_step(d.pool, one, one, None, d.err, max_tokens=n)
+    with pytest.raises(ValueError):
+        mcp.build_step_tables(d.pool, one, one, i32([0, 0]), one, i32([[0] * 4]), tokens.view(torch.int64)[:1].expand(n))
+    with pytest.raises(ValueError):
+        mcp.make_request_pool(d.pages, d.lens, tokens, d.count, 16)
+
+
 # ------------------------------------------------------------------ malformed streams
 def bad_streams():
     """Prefix sums that decrease, overlap or leave the stream, most with tokens enough for
