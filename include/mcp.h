@@ -159,7 +159,10 @@ typedef struct mcp_plan_options {
                                 /* after ~1 ms, so those items end through the   */
                                 /* bounded-wait abort path: no output rows, the  */
                                 /* error word reports MCP_ERR_TIMEOUT            */
-  int32_t reserved[4];          /* must be 0                                     */
+  int32_t tree;                 /* 1: the step may hold trees of drafted tokens  */
+                                /* (mcp_mixed_attn_fwd_tree): segments of two    */
+                                /* and more tokens take the tensor-core path     */
+  int32_t reserved[3];          /* must be 0                                     */
 } mcp_plan_options;
 
 /* Filled by mcp_mixed_attn_plan(); read by mcp_mixed_attn_fwd().  Plain data:
@@ -179,7 +182,8 @@ typedef struct mcp_plan {
   mcp_attn_desc desc;         /* the description the plan was built for          */
   int32_t combine_rows;       /* query rows (token, head) merged by the combine  */
   int32_t test_stall;         /* mcp_plan_options.test_stall                     */
-  int32_t reserved[6];
+  int32_t tree;               /* mcp_plan_options.tree                           */
+  int32_t reserved[5];
 } mcp_plan;
 
 /*
@@ -851,6 +855,168 @@ typedef struct mcp_logits_tensors {
 mcp_status mcp_process_logits(const mcp_logits_desc* desc, const mcp_logits_tensors* tensors,
                               int32_t* error_word, void* stream);
 
+/* ------------------------------------------------------------------------- */
+/* Trees of drafted tokens                                                    */
+/* ------------------------------------------------------------------------- */
+/*
+ * A request whose next tokens were drafted runs a segment of its last token
+ * (the root, place 0) and the drafts, any of which may follow any token before
+ * it: parents [T] int32 holds, for each token of the stream, the place of its
+ * parent inside its segment (< the token's own place; < 0: no parent, it
+ * follows the history).  The tokens' K/V are appended in the segment's order,
+ * as always; only what a token sees, and its position, follow the tree:
+ *   seen(i) = seen(parent) and i,   depth(i) = depth(parent) + 1 (no parent: 0).
+ *
+ * tree_mask [num_mask_rows, mask_words] int32 holds a row for each token of the
+ * trees: bit (j % 32) of word j / 32 of the row of token i = it sees token j of
+ * its segment.  mask_rows [S] is the row of each segment's first token, its
+ * other tokens following; < 0: the segment is causal (a chunk, a decode).
+ *
+ * mcp_build_tree_masks fills the rows and, unless NULL, positions [T]: history
+ * (seqlens_k minus the segment's tokens) plus depth, in causal segments plus
+ * the place.  Rows that no segment has, and positions behind the last segment,
+ * stay as they were.  A parent that is not before its token (the token is
+ * taken for one without) and a tree that exceeds 32 * mask_words tokens or
+ * num_mask_rows (its rows and positions are left out) set MCP_DEVERR_TREE; a
+ * segment past total_tokens or with seqlens_k < its tokens MCP_DEVERR_SEGMENT
+ * (the first is left out).
+ * All arrays are device int32.  num_seqs <= 2^20, total_tokens and
+ * num_mask_rows <= 2^30, mask_words <= 32: trees of up to 1024 tokens.
+ */
+mcp_status mcp_build_tree_masks(const int32_t* parents, const int32_t* cu_seqlens_q,
+                                const int32_t* seqlens_k, const int32_t* mask_rows,
+                                int32_t num_seqs, int32_t total_tokens, int32_t num_mask_rows,
+                                int32_t mask_words, int32_t* tree_mask, int32_t* positions,
+                                int32_t* error_word, void* stream);
+
+/*
+ * mcp_mixed_attn_fwd of a step in which segments with mask_rows[s] >= 0 are
+ * trees: token i of such a segment sees the whole history, itself, and every
+ * token j < i of its segment whose bit is set (bits of other tokens, and of
+ * words past mask_words, do not count, so a row may hold any mask of the tokens
+ * before it).  Causal segments are as in mcp_mixed_attn_fwd.  The plan is
+ * mcp_mixed_attn_plan's (or _plan_rows') with mcp_plan_options.tree = 1 and
+ * serves any trees of these lengths.
+ *
+ * What a token does not see has no part in its result, whatever it holds:
+ * infinities and NaN in K or V of hidden tokens of its own tree change nothing.
+ * tree_mask, mask_rows: device; a mask row >= num_mask_rows sets MCP_DEVERR_TREE
+ * in the workspace's error word and leaves its token the history and itself.
+ */
+mcp_status mcp_mixed_attn_fwd_tree(const mcp_plan* plan, const void* q, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_tables,
+                                   const int32_t* cu_seqlens_q, const int32_t* seqlens_k,
+                                   const int32_t* tree_mask, int32_t num_mask_rows,
+                                   int32_t mask_words, const int32_t* mask_rows, void* out,
+                                   float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+typedef struct mcp_verify_desc {
+  int32_t num_seqs;
+  int32_t total_rows;   /* rows of the probabilities                             */
+  int32_t vocab_size;
+  int32_t dtype;        /* of the probabilities: bf16, fp16 or fp32              */
+  int64_t target_stride, draft_stride; /* elements between rows, >= vocab_size   */
+} mcp_verify_desc;
+
+typedef struct mcp_verify_tensors {
+  const void* target;        /* [total_rows, vocab_size]                         */
+  const void* draft;         /* the same, or NULL                                */
+  const int32_t* tokens;     /* [total_rows]                                     */
+  const int32_t* parents;    /* [total_rows], or NULL: chains                    */
+  const int32_t* cu_rows;    /* [num_seqs + 1]                                   */
+  const float* uniform;      /* [total_rows] in [0, 1)                           */
+  const float* final_uniform; /* [num_seqs] in [0, 1)                            */
+  int32_t* accepted;         /* [num_seqs]                                       */
+  int32_t* path;             /* [total_rows]                                     */
+  int32_t* new_tokens;       /* [total_rows]                                     */
+} mcp_verify_tensors;
+
+/*
+ * Which drafted tokens stay, and the token behind them, such that what comes
+ * out is distributed as if each token had been sampled from the target alone.
+ * Segment s's rows are cu_rows[s] .. cu_rows[s+1]-1: row 0 its root, row i the
+ * node of drafted token tokens[i] under row parents[i] < i (NULL: i - 1; < 0:
+ * under none, never accepted).  target row i: the target model's probabilities
+ * of the token that follows node i; draft row i: those from which the nodes
+ * under i were drawn, independently of each other.  Without draft probabilities
+ * the drafts are taken for given (e.g. the draft model's likeliest tokens).  A
+ * one-hot target row is greedy sampling.  A segment of one row has no drafts:
+ * its token is sampled.
+ *
+ * From the root on, at node `cur` with p = target[cur], q = draft[cur], the
+ * nodes i under it are tried in order, x = tokens[i]:
+ *   with q:    accepted if uniform[i] N q(x) < p(x) - c q(x), with c = 0, N = 1
+ *              at first and, after each one refused, c = c + N and then
+ *              N = sum_v max(p(v) - c q(v), 0);
+ *   without:   accepted if uniform[i] N < p(x), with N = 1 at first and, after
+ *              each one refused, N = N - p(x) and then p(x) = 0.
+ * An accepted node is the next `cur`.  When none is left, the last token is
+ * drawn from what remains at cur, w(v) = max(p(v) - c q(v), 0) or p without the
+ * refused tokens: the first v with w(0) + .. + w(v) > final_uniform[s] * sum w
+ * (where nothing remains: of p; u >= 1: the last v with w > 0).
+ *
+ *   accepted[s]: rows accepted, the root among them (0: a segment without rows)
+ *   path[cu_rows[s] + k], k < accepted[s]: place of the k-th of them, then -1
+ *   new_tokens[cu_rows[s] + k]: the tokens of path 1, 2, .. and then the last
+ *       token, accepted[s] of them, then -1
+ * so that new_tokens and cu_rows go to mcp_update_token_counts, and path and
+ * accepted to mcp_kv_keep_path.  Rows behind the last segment stay as they were.
+ *
+ * Sums are held to 2^-40 of themselves and better; entries that are negative,
+ * infinite or NaN count as 0.  A row at which a walk ends without a positive
+ * entry sets MCP_DEVERR_PROBS and gives token -1.  A drafted token outside the
+ * vocabulary hangs under none (>= vocab_size sets MCP_DEVERR_TOKEN_RANGE, a
+ * negative one is padding), and so does a node whose parent is not before it
+ * (MCP_DEVERR_TREE).  A segment past total_rows, of more than 1024 rows or with
+ * decreasing cu_rows sets MCP_DEVERR_SEGMENT (accepted 0, nothing else written).  Rows need the alignment of their type only; they are read twice as
+ * fast where both matrices and their strides are multiples of 16 bytes.
+ * num_seqs <= 2^20, total_rows <= 2^30, vocab_size <= 2^28.
+ */
+mcp_status mcp_verify_drafts(const mcp_verify_desc* desc, const mcp_verify_tensors* tensors,
+                             int32_t* error_word, void* stream);
+
+typedef struct mcp_keep_desc {
+  int32_t num_seqs;
+  int32_t total_rows;        /* entries of path                                  */
+  int32_t num_layers;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;         /* 1, 8, 16, 32 or 64                               */
+  int32_t max_pages_per_seq;
+  int32_t num_pages;
+} mcp_keep_desc;
+
+/*
+ * The K/V of each segment's accepted tokens move to the front of the segment,
+ * behind its history, in every layer: for k < accepted[s] the rows of position
+ * history + path[cu_rows[s] + k] go to position history + k, so that the
+ * segment's first accepted[s] tokens are the request's next ones and the rest
+ * can be given back (mcp_commit_built_step with new_lens).  Bit-exact.  path
+ * must rise strictly (a tree's paths do); new_lens [S] (or NULL) receives
+ * history + accepted[s].
+ *
+ * A segment whose rows of path are not as many as its tokens (a chunk of which
+ * only the last token has a row; none) had no drafts: nothing moves and new_lens
+ * is seqlens_k.
+ *
+ * k_caches, v_caches: HOST arrays of num_layers device pointers to caches
+ * [num_pages, page_size, num_kv_heads, head_dim] bf16, 16-byte aligned, read
+ * before the call returns.  The rest are device arrays, as in the calls above;
+ * cu_rows NULL: the rows are the stream's tokens (cu_seqlens_q).  A path that
+ * does not rise or leaves its segment (MCP_DEVERR_TREE), accepted[s] outside
+ * its rows (MCP_DEVERR_TREE) and a segment with seqlens_k < its tokens, past
+ * total_rows or past its table row (MCP_DEVERR_SEGMENT) move nothing and give
+ * new_lens = seqlens_k; a page outside the pool (MCP_DEVERR_PAGE_RANGE) leaves
+ * out its token's row.  num_kv_heads * head_dim a multiple of 8; num_layers <=
+ * 1024; pages of different segments must differ where they are written.
+ */
+mcp_status mcp_kv_keep_path(const mcp_keep_desc* desc, void* const* k_caches, void* const* v_caches,
+                            const int32_t* block_tables, const int32_t* cu_seqlens_q,
+                            const int32_t* seqlens_k, const int32_t* cu_rows,
+                            const int32_t* accepted, const int32_t* path, int32_t* new_lens,
+                            int32_t* error_word, void* stream);
+
 /* Device-check bits written to an error word. */
 #define MCP_DEVERR_TIMEOUT 0x1      /* a bounded mbarrier wait gave up           */
 #define MCP_DEVERR_PAGE_RANGE 0x2   /* a block-table page id outside the pool    */
@@ -862,6 +1028,8 @@ mcp_status mcp_process_logits(const mcp_logits_desc* desc, const mcp_logits_tens
 #define MCP_DEVERR_REQUEST 0x80     /* a request row outside its state, or twice */
 #define MCP_DEVERR_TOKEN_RANGE 0x100 /* a token outside the vocabulary           */
 #define MCP_DEVERR_SEGMENT 0x200    /* a segment outside the token stream        */
+#define MCP_DEVERR_TREE 0x400       /* a malformed tree, or one outside its masks */
+#define MCP_DEVERR_PROBS 0x800      /* a row of probabilities without any        */
 
 #ifdef __cplusplus
 }

@@ -18,6 +18,7 @@ from ._capi import (  # noqa: F401
     DEVERR_ITEM_KIND,
     DEVERR_NO_PAGES,
     DEVERR_PAGE_RANGE,
+    DEVERR_PROBS,
     DEVERR_REQUEST,
     DEVERR_ROW_RANGE,
     DEVERR_SEGMENT,
@@ -25,6 +26,7 @@ from ._capi import (  # noqa: F401
     DEVERR_SLOT_RANGE,
     DEVERR_TIMEOUT,
     DEVERR_TOKEN_RANGE,
+    DEVERR_TREE,
     AttnDesc,
     MCPError,
     Plan,
@@ -38,7 +40,8 @@ __all__ = [
     "workspace_error_word", "merge_states", "make_desc", "mixed_attn_fwd_noalloc",
     "mixed_attn_plan_rows", "build_logits_indices", "gather_rows", "kv_copy_pages",
     "mixed_attn_varlen", "RequestPool", "make_request_pool", "build_step_tables", "commit_step",
-    "mixed_conv", "mixed_scan", "update_token_counts", "process_logits",
+    "mixed_conv", "mixed_scan", "update_token_counts", "process_logits", "build_tree_masks",
+    "mixed_attn_fwd_tree", "verify_drafts", "kv_keep_path",
 ]
 
 
@@ -757,3 +760,174 @@ def process_logits(logits, out=None, request_ids=None, seen=None, counts=None, t
     _launch("process_logits", dev, stream, load().mcp_process_logits, ctypes.byref(desc),
             ctypes.byref(tensors), _error(error_word, dev))
     return out
+
+
+# ---------------------------------------------------------------------------
+# trees of drafted tokens
+# ---------------------------------------------------------------------------
+
+def build_tree_masks(parents, cu_seqlens_q, seqlens_k, mask_rows, tree_mask, positions=None,
+                     error_word=None, stream=None) -> None:
+    """Which tokens of its tree each token of a step sees, and its position (see
+    include/mcp.h): parents [T] (the place of a token's parent in its segment, < 0: none),
+    cu_seqlens_q [S + 1], seqlens_k [S] and mask_rows [S] (the row of a tree's first token,
+    < 0: a causal segment) in; tree_mask [rows, words] and positions [T] (or None) out, all
+    int32 CUDA tensors."""
+    import torch
+
+    dev, i32 = _gpu(parents, "parents"), torch.int32
+    if parents.dim() != 1 or mask_rows.dim() != 1 or tree_mask.dim() != 2:
+        raise ValueError("parents must be [T], mask_rows [S], tree_mask [rows, words]")
+    T, S = parents.shape[0], mask_rows.shape[0]
+    rows, words = tree_mask.shape
+    _sizes(T, S, rows, words)
+    _launch("build_tree_masks", dev, stream, load().mcp_build_tree_masks,
+            _arg(parents, i32, "parents", dev), _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),
+            _arg(seqlens_k, i32, "seqlens_k", dev, (S,)), _arg(mask_rows, i32, "mask_rows", dev),
+            S, T, rows, words, _arg(tree_mask, i32, "tree_mask", dev),
+            _arg(positions, i32, "positions", dev, (T,)), _error(error_word, dev))
+
+
+def mixed_attn_fwd_tree(plan: Plan, q, k_cache, v_cache, block_tables, cu_seqlens_q, seqlens_k,
+                        tree_mask, mask_rows, out, lse=None, workspace=None, stream=None) -> None:
+    """``mixed_attn_fwd`` of a step in which segments with mask_rows[s] >= 0 are trees of
+    drafted tokens (see include/mcp.h): their tokens see the history, themselves and the tokens
+    before them whose bit is set in their row of tree_mask [rows, words] (int32).  The plan is
+    made with ``PlanOptions(tree=1)`` and serves any trees of its lengths."""
+    import torch
+
+    dev, i32, bf16 = _gpu(q, "q"), torch.int32, torch.bfloat16
+    d = plan.desc
+    if tree_mask.dim() != 2:
+        raise ValueError("tree_mask must be [rows, words]")
+    rows, words = tree_mask.shape
+    _sizes(rows, words)
+    if q.dim() != 3 or q.shape[0] < d.total_q:  # rows behind the step's tokens are padding
+        raise ValueError(f"q must be [tokens, H_q, D] with the plan's {d.total_q} tokens")
+    heads = (q.shape[0], d.num_q_heads, d.head_dim)
+    cache = (d.num_pages, d.page_size, d.num_kv_heads, d.head_dim)
+    S = d.num_seqs
+    _launch("mixed_attn_fwd_tree", dev, stream, load().mcp_mixed_attn_fwd_tree, ctypes.byref(plan),
+            _arg(q, bf16, "q", dev, heads), _arg(k_cache, bf16, "k_cache", dev, cache),
+            _arg(v_cache, bf16, "v_cache", dev, cache),
+            _arg(block_tables, i32, "block_tables", dev, (S, d.max_pages_per_seq)),
+            _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),
+            _arg(seqlens_k, i32, "seqlens_k", dev, (S,)), _arg(tree_mask, i32, "tree_mask", dev),
+            rows, words, _arg(mask_rows, i32, "mask_rows", dev, (S,)),
+            _arg(out, bf16, "out", dev, heads), _arg(lse, torch.float32, "lse", dev, heads[:2]),
+            _arg(workspace, torch.uint8, "workspace", dev),
+            0 if workspace is None else workspace.numel())
+
+
+def _prob_rows(t, dtype, name, dev, shape):
+    """(address, elements between rows) of [rows, vocab] probabilities."""
+    try:
+        good = t.dtype is dtype and t.get_device() == dev and t.shape == shape
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse(t, dtype, name, dev, shape)
+    strides = t.stride()
+    if shape[1] > 1 and strides[1] != 1:
+        raise ValueError(f"{name}: a row must be dense, got strides {strides}")
+    return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1]
+
+
+def verify_drafts(target_probs, tokens, cu_rows, uniform, final_uniform, parents=None,
+                  draft_probs=None, accepted=None, path=None, new_tokens=None, error_word=None,
+                  stream=None):
+    """Which drafted tokens stay, and the token behind them (see include/mcp.h): target_probs
+    [R, vocab] and draft_probs (the same, or None) of one type (bf16, fp16 or fp32; rows may be
+    part of wider ones), row i of a segment for what follows its node i; tokens [R], parents [R]
+    (None: chains), cu_rows [S + 1] int32; uniform [R] and final_uniform [S] fp32 in [0, 1).
+    Returns (accepted [S], path [R], new_tokens [R]), int32: the rows that stay, the root among
+    them, their places, and the tokens to go on with, behind them -1."""
+    import torch
+
+    dev, dtype = _gpu(target_probs, "target_probs"), target_probs.dtype
+    i32, f32 = torch.int32, torch.float32
+    if target_probs.dim() != 2 or cu_rows.dim() != 1 or cu_rows.shape[0] == 0:
+        raise ValueError("target_probs must be [rows, vocab], cu_rows [segments + 1]")
+    shape = target_probs.shape
+    R, V = shape
+    S = cu_rows.shape[0] - 1
+    _sizes(R, V, S)
+    pt, ldt = _prob_rows(target_probs, dtype, "target_probs", dev, shape)
+    pd, ldd = (None, 0) if draft_probs is None else _prob_rows(draft_probs, dtype, "draft_probs", dev,
+                                                               shape)
+    device = target_probs.device
+    if accepted is None:
+        accepted = _empty((S,), i32, device, stream, result=True)
+    if path is None:
+        path = _empty((R,), i32, device, stream, result=True)
+    if new_tokens is None:
+        new_tokens = _empty((R,), i32, device, stream, result=True)
+    desc = _capi.VerifyDesc(S, R, V, _dtype_code(target_probs, "target_probs"), ldt, ldd)
+    tensors = _capi.VerifyTensors(
+        pt, pd, _arg(tokens, i32, "tokens", dev, (R,)), _arg(parents, i32, "parents", dev, (R,)),
+        _arg(cu_rows, i32, "cu_rows", dev), _arg(uniform, f32, "uniform", dev, (R,)),
+        _arg(final_uniform, f32, "final_uniform", dev, (S,)),
+        _arg(accepted, i32, "accepted", dev, (S,)), _arg(path, i32, "path", dev, (R,)),
+        _arg(new_tokens, i32, "new_tokens", dev, (R,)))
+    _launch("verify_drafts", dev, stream, load().mcp_verify_drafts, ctypes.byref(desc),
+            ctypes.byref(tensors), _error(error_word, dev))
+    return accepted, path, new_tokens
+
+
+def _layers(caches, name, dev, shape):
+    """(shape of one cache, address of each layer's): one cache [pages, P, H_kv, D], all
+    layers' [layers, pages, P, H_kv, D], or a list of caches."""
+    import torch
+
+    bf16 = torch.bfloat16
+    if isinstance(caches, torch.Tensor):
+        if caches.dim() == 4:
+            caches = (caches,)
+        elif caches.dim() != 5:
+            raise ValueError(f"{name} must be caches [pages, P, H_kv, D] of one or all layers")
+        elif caches.is_contiguous() and caches.shape[0] and (shape is None or caches.shape[1:] == shape):
+            shape = caches.shape[1:]
+            base, step = _arg(caches, bf16, name, dev), shape.numel() * 2
+            return shape, [base + layer * step for layer in range(caches.shape[0])]
+    caches = tuple(caches)
+    if shape is None and caches:
+        _gpu(caches[0], name)
+        shape = caches[0].shape
+        if len(shape) != 4:
+            raise ValueError(f"{name} must be caches [pages, P, H_kv, D]")
+    return shape, [_arg(c, bf16, name, dev, shape) for c in caches]
+
+
+def kv_keep_path(k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k, accepted, path,
+                 cu_rows=None, new_lens=None, error_word=None, stream=None):
+    """The accepted tokens' K/V moved behind their history, in every layer (see include/mcp.h):
+    k_caches, v_caches: lists of bf16 caches [pages, P, H_kv, D], or one tensor [layers, pages, P,
+    H_kv, D]; block_tables [S, max_pages_per_seq], cu_seqlens_q [S + 1], seqlens_k [S]; accepted
+    [S], path [R] and cu_rows [S + 1] as ``verify_drafts`` takes and gives them (``cu_rows`` None:
+    its rows are the step's tokens), all int32 CUDA tensors.  Returns ``new_lens`` [S]: the tokens
+    that each request holds now (for ``commit_step``)."""
+    import torch
+
+    dev, i32 = _gpu(accepted, "accepted"), torch.int32
+    shape, ks = _layers(k_caches, "k_caches", dev, None)
+    _, vs = _layers(v_caches, "v_caches", dev, shape)
+    if not ks or len(ks) != len(vs):
+        raise ValueError("k_caches and v_caches must have the same layers, one at least")
+    if accepted.dim() != 1 or path.dim() != 1 or block_tables.dim() != 2:
+        raise ValueError("accepted must be [S], path [R], block_tables [S, max_pages_per_seq]")
+    S, R, L = accepted.shape[0], path.shape[0], len(ks)
+    pages, P, H, D = shape
+    width = block_tables.shape[1]
+    _sizes(S, R, L, pages, P, H, D, width)
+    one = (S,)
+    if new_lens is None:
+        new_lens = _empty(one, i32, accepted.device, stream, result=True)
+    desc = _capi.KeepDesc(S, R, L, H, D, P, width, pages)
+    addresses = ctypes.c_void_p * L
+    _launch("kv_keep_path", dev, stream, load().mcp_kv_keep_path, ctypes.byref(desc),
+            addresses(*ks), addresses(*vs), _arg(block_tables, i32, "block_tables", dev, (S, width)),
+            _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),
+            _arg(seqlens_k, i32, "seqlens_k", dev, one), _arg(cu_rows, i32, "cu_rows", dev, (S + 1,)),
+            _arg(accepted, i32, "accepted", dev, one), _arg(path, i32, "path", dev),
+            _arg(new_lens, i32, "new_lens", dev, one), _error(error_word, dev))
+    return new_lens

@@ -27,11 +27,14 @@ DEVERR_NO_PAGES = 0x40
 DEVERR_REQUEST = 0x80
 DEVERR_TOKEN_RANGE = 0x100
 DEVERR_SEGMENT = 0x200
+DEVERR_TREE = 0x400
+DEVERR_PROBS = 0x800
 BUILD_CHECKED = 0x1
 DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 COUNT_PROMPT = 0x1
 COUNT_RESET = 0x2
 MAX_TOKENS = 1 << 30  # of a build of step tables
+MAX_MASK_WORDS = 32  # of a tree's mask row
 
 
 class AttnDesc(ctypes.Structure):
@@ -54,7 +57,8 @@ class PlanOptions(ctypes.Structure):
         ("decode_split_tokens", c_int32),
         ("prefill_split_tokens", c_int32),
         ("test_stall", c_int32),
-        ("reserved", c_int32 * 4),
+        ("tree", c_int32),
+        ("reserved", c_int32 * 3),
     ]
 
 
@@ -78,7 +82,8 @@ class Plan(ctypes.Structure):
         ("desc", AttnDesc),
         ("combine_rows", c_int32),
         ("test_stall", c_int32),
-        ("reserved", c_int32 * 6),
+        ("tree", c_int32),
+        ("reserved", c_int32 * 5),
     ]
 
 
@@ -205,6 +210,29 @@ class LogitsTensors(ctypes.Structure):
         "mask", "mask_rows")]
 
 
+class VerifyDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", c_int32),
+        ("total_rows", c_int32),
+        ("vocab_size", c_int32),
+        ("dtype", c_int32),
+        ("target_stride", c_int64),
+        ("draft_stride", c_int64),
+    ]
+
+
+class VerifyTensors(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in (
+        "target", "draft", "tokens", "parents", "cu_rows", "uniform", "final_uniform", "accepted",
+        "path", "new_tokens")]
+
+
+class KeepDesc(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in (
+        "num_seqs", "total_rows", "num_layers", "num_kv_heads", "head_dim", "page_size",
+        "max_pages_per_seq", "num_pages")]
+
+
 # name -> (restype, argtypes); every symbol include/mcp.h declares
 SIGNATURES = {
     "mcp_status_string": (c_char_p, [c_int32]),
@@ -280,6 +308,17 @@ SIGNATURES = {
                                           c_void_p]),
     "mcp_process_logits": (c_int32, [POINTER(LogitsDesc), POINTER(LogitsTensors), c_void_p,
                                      c_void_p]),
+    "mcp_build_tree_masks": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                       c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "mcp_mixed_attn_fwd_tree": (c_int32, [POINTER(Plan), c_void_p, c_void_p, c_void_p, c_void_p,
+                                          c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                          c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                          c_void_p]),
+    "mcp_verify_drafts": (c_int32, [POINTER(VerifyDesc), POINTER(VerifyTensors), c_void_p,
+                                    c_void_p]),
+    "mcp_kv_keep_path": (c_int32, [POINTER(KeepDesc), c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p]),
 }
 
 _lib = None

@@ -28,7 +28,8 @@ LIB_PATH = os.path.join(LIB_DIR, "libmcp.so")
 CHECKED_LIB_PATH = os.path.join(LIB_DIR, "libmcp_checked.so")
 
 SOURCES = ["host.cpp", "sched.cpp", "append.cu", "attn_fwd.cu", "combine.cu",
-           "attn_fwd_noalloc.cu", "step_ops.cpp", "tables.cu", "recurrent.cu", "logits.cu"]
+           "attn_fwd_noalloc.cu", "step_ops.cpp", "tables.cu", "recurrent.cu", "logits.cu",
+           "tree.cu", "verify.cu"]
 HEADERS = ["mcp_internal.h", "ptx.cuh", "step_ops.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

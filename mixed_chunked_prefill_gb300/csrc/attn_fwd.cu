@@ -204,6 +204,11 @@ struct KParams {
                        // keys, landing [panel][8 keys][128 B]); 0: one box per panel
   int32_t test_stall;  // testing only: 1 = tensor-core items never issue their Q-tile load,
                        // so their softmax waits run out (1 ms bound) and the CTA aborts
+  // trees of drafted tokens (the kTree instantiations read these)
+  const uint32_t* tree_mask;  // [num_mask_rows, mask_words]
+  const int32_t* mask_rows;   // [S] first mask row of each segment, < 0: causal
+  int32_t mask_words;
+  int32_t num_mask_rows;
 };
 
 struct Seg {
@@ -239,9 +244,70 @@ __device__ __forceinline__ int oob_block(const KParams& p) {
 }
 
 // ------------------------------------------------------------------------
+// trees of drafted tokens
+// ------------------------------------------------------------------------
+// A tree segment's token i sees its history, itself, and the tokens before it
+// whose bit its mask row sets; what it does not see lies in the segment's last
+// Lq keys, so only the tiles that reach past the history read the mask (one to
+// three of them an item: the rest of the item runs as in a causal step).
+struct TreeRow {
+  const uint32_t* words;  // the token's mask row (nullptr: none, it sees itself alone)
+  int num_words, hist, tok;
+  bool tree;              // false: a causal segment
+
+  // Word `w` of the bits of the segment's tokens, bit 0 of word 0 the first;
+  // keys before the history's end are visible to all.
+  __device__ __forceinline__ uint32_t word(int w) const {
+    if (w < 0) return 0xffffffffu;
+    uint32_t v = words && w < num_words ? __ldg(words + w) : 0u;
+    if (w == tok >> 5) v |= 1u << (tok & 31);
+    return v;
+  }
+  // Visibility of keys key .. key + 31 (bit b: key + b), jmax the last one seen
+  __device__ __forceinline__ uint32_t visible(int key, int jmax) const {
+    uint32_t v = 0xffffffffu;
+    if (tree) {
+      const int t = key - hist;  // place of `key` among the segment's tokens
+      v = __funnelshift_r(word(t >> 5), word((t >> 5) + 1), t & 31);
+    }
+    const int n = jmax - key + 1;
+    return n >= 32 ? v : n <= 0 ? 0u : v & ((1u << n) - 1u);
+  }
+};
+
+// True when one of the two bf16 values of `v` is infinite or NaN
+__device__ __forceinline__ bool any_nonfinite(uint32_t v) {
+  return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t only_finite(uint32_t v) {
+  if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+  if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
+  return v;
+}
+
+// The infinities and NaN that were taken out of the product, added to columns
+// d0 .. d0 + 31 of a row's O for the keys j0 .. j1 that the row sees (a visible
+// key's weight is positive, so the value itself stands for its product).
+__device__ __noinline__ void add_nonfinite(const KParams& p, const WorkItem& it, const TreeRow& tr,
+                                           int j0, int j1, int d0, uint32_t* o) {
+  const int page_log2 = p.gather ? 0 : p.spp_log2 + p.box_log2;
+  for (int j = j0; j <= j1; ++j) {
+    if (!(tr.visible(j, j) & 1u)) continue;
+    const int page = p.bt[static_cast<size_t>(it.seg) * p.max_pages + (j >> page_log2)];
+    if (page < 0 || page >= p.num_pages) continue;
+    const size_t slot = (static_cast<size_t>(page) << page_log2) + (j & ((1 << page_log2) - 1));
+    const __nv_bfloat16* v = p.vc + (slot * p.hkv + it.kv_head) * p.dr + d0;
+    for (int i = 0; i < 32; ++i) {
+      const float x = __bfloat162float(v[i]);
+      if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------
 // tensor-core item
 // ------------------------------------------------------------------------
-template <int D>
+template <int D, bool kTree>
 __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, const Seg& sg,
                                              const KParams& p, uint32_t base, uint8_t* gb,
                                              uint32_t tmem, const CUtensorMap* tm_q,
@@ -262,6 +328,9 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
   // (with a single issuer the waits sat between every pair of MMA groups and
   // the tensor pipe idled for them).  Both feed the same in-order tensor pipe;
   // Q K^T(t) waits for P V(t - 2), the last reader of S buffer t & 1.
+  const int mask_row0 = kTree ? p.mask_rows[it.seg] : -1;
+  const bool tree = kTree && mask_row0 >= 0 && sg.lq > 1;
+  volatile int* nonfinite = c.abort + 1;  // a tree's V rows held an infinity or NaN
   constexpr uint32_t kIdQK = ptx::idesc_bf16(128, kKvTile, false);
   constexpr uint32_t kIdPV = ptx::idesc_bf16(128, D, true);
   if (warp == 0) {
@@ -307,6 +376,35 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
         ptx::fence_proxy_async_smem();
         __syncwarp();
       }
+      if constexpr (kTree) {
+        // P is 0 where a row does not see a token of its tree, but 0 * inf is
+        // not: infinities and NaN of the tree's V rows are taken out of the
+        // product and added in the epilogue to the rows that see them.  Runs
+        // while the softmax works on this tile; 64 tokens of 128 columns are 32
+        // loads a lane.
+        const int r0 = max(sg.hist - (kv0 + t * kKvTile), 0);
+        const int nr = min(nval, kKvTile) - r0;
+        if (tree && nr > 0) {
+          uint8_t* gV = gb + (sV(s) - base);
+          bool found = false;
+          for (int i = lane; i < nr * 8 * C::kHalves; i += 32) {
+            const int h = i / (nr * 8), rem = i - h * (nr * 8);
+            const int r = r0 + rem / 8, ch = rem & 7;
+            uint4* at = reinterpret_cast<uint4*>(gV + (r >> p.box_log2) * (C::kHalves * B * 128) +
+                                                 h * B * 128 + (r & (B - 1)) * 128 + ch * 16);
+            const uint4 v = *at;
+            if (any_nonfinite(v.x) || any_nonfinite(v.y) || any_nonfinite(v.z) || any_nonfinite(v.w)) {
+              *at = make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
+              found = true;
+            }
+          }
+          if (__any_sync(0xffffffffu, found)) {
+            if (lane == 0) *nonfinite = 1;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+      }
       ptx::tc_fence_after();
       if (lane == 0) {
         const uint64_t dv = dV0 + static_cast<uint64_t>((s * C::kKvBytes) >> 4);
@@ -325,6 +423,9 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
     __syncwarp();
     drain_wait(c, c.b(BDRAIN), 0);
     if (!p.test_stall) drain_wait(c, c.b(BQ), 0);  // the Q tile's copy (none was issued)
+    // hands *nonfinite to the epilogue (every wait above is bounded, and both
+    // sides come here whether or not they gave up)
+    if (kTree && tree) asm volatile("bar.sync 2, 160;" ::: "memory");
   } else if (warp >= 6 && p.gather) {
     // ------------------- K/V producers for 1-token pages: cp.async gathers
     // Every key is its own page, so a TMA box would carry one 128-byte row;
@@ -539,6 +640,14 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
     // right-aligned causal: token i sees keys 0 .. hist + i; the item covers keys < kv1
     int jmax = sg.hist + tok_c;
     jmax = jmax < kv1 - 1 ? jmax : kv1 - 1;
+    TreeRow tr{nullptr, p.mask_words, sg.hist, tok_c, tree};
+    if (kTree && tree) {
+      const int64_t mr = static_cast<int64_t>(mask_row0) + tok_c;
+      if (mr < p.num_mask_rows) tr.words = p.tree_mask + mr * p.mask_words;
+      else atomicOr(p.err, MCP_DEVERR_TREE);
+    }
+    // the last key of the tiles that this row sees whole
+    const int jfull = kTree && tree ? min(sg.hist - 1, jmax) : jmax;
     const float sl2 = p.scale_log2;
     float m_ref = neg_inf(), l = 0.f;
     bool ok = wait_on_warp(c, c.b(BQ), 0);
@@ -566,6 +675,14 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
     }
     for (int t = 0; ok && t < ntiles; ++t) {
       const int s = t & 1;
+      const int key0 = kv0 + t * kKvTile;
+      uint32_t vis[kTree ? kKvTile / 32 : 1];
+      if constexpr (kTree) {
+        if (key0 + kKvTile - 1 > jfull) {  // the mask is read while the scores are computed
+#pragma unroll
+          for (int j = 0; j < kKvTile / 32; ++j) vis[j] = tr.visible(key0 + 32 * j, jmax);
+        }
+      }
       if (!(ok = wait_on_warp(c, c.b(BS0 + s), (t >> 1) & 1))) break;
       ptx::tc_fence_after();
       // the scores, and the max of each 32 of them from the load itself
@@ -575,10 +692,9 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
       for (int j = 0; j < kKvTile / 32; ++j) ptx::tmem_ld32_max(tS + s * kKvTile + j * 32, r + j * 32, mj[j]);
 #pragma unroll
       for (int j = 0; j < kKvTile / 32; ++j) ptx::tmem_wait_ld_dep_max(r + j * 32, mj[j]);
-      const int key0 = kv0 + t * kKvTile;
       // max of the raw scores (sm_scale > 0 keeps the order)
       float mx;
-      if (key0 + kKvTile - 1 <= jmax) {  // every key of the tile is visible to this row
+      if (key0 + kKvTile - 1 <= jfull) {  // every key of the tile is visible to this row
         mx = kKvTile == 128 ? fmaxf(fmaxf(mj[0], mj[1]), fmaxf(mj[kKvTile / 32 - 2], mj[kKvTile / 32 - 1]))
                             : fmaxf(mj[0], mj[kKvTile / 32 - 1]);
       } else {  // diagonal / last tile: mask keys past this row's last visible key
@@ -587,7 +703,8 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
         for (int j = 0; j < 8; ++j) mxp[j] = neg_inf();
 #pragma unroll
         for (int i = 0; i < kKvTile; ++i) {
-          const float x = (key0 + i <= jmax) ? __uint_as_float(r[i]) : neg_inf();
+          const bool seen = kTree ? (vis[i / 32 * kTree] >> (i & 31)) & 1u : key0 + i <= jmax;
+          const float x = seen ? __uint_as_float(r[i]) : neg_inf();
           r[i] = __float_as_uint(x);
           mxp[i & 7] = fmaxf(mxp[i & 7], x);
         }
@@ -651,6 +768,13 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
     // every MMA of the item (each issuing warp commits once after its last MMA)
     if (ok && ntiles > 0) ok = wait_on_warp(c, c.b(BDRAIN), 0);
     ptx::tc_fence_after();
+    bool bad_v = false;
+    if constexpr (kTree) {
+      if (tree) {
+        asm volatile("bar.sync 2, 160;" ::: "memory");
+        bad_v = *nonfinite != 0;
+      }
+    }
     const bool store = ok && valid && !*c.abort;
     const bool direct = it.part_row < 0;
     const float inv_l = l > 0.f ? 1.f / l : 0.f;
@@ -660,6 +784,16 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
       uint32_t o[32];
       ptx::tmem_ld32(tO + j * 32, o);
       ptx::tmem_wait_ld();
+      if constexpr (kTree) {
+        if (bad_v && store && j * 32 < p.dr) {
+          uint32_t od[32];  // a copy: o stays in registers where nothing is to be added
+#pragma unroll
+          for (int i = 0; i < 32; ++i) od[i] = o[i];
+          add_nonfinite(p, it, tr, max(kv0, sg.hist), jmax, j * 32, od);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = od[i];
+        }
+      }
       if (store && j * 32 < p.dr) {  // columns past the tensors' head_dim are not stored
         if (direct) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + orow * p.dr + j * 32);
@@ -1254,7 +1388,7 @@ __device__ __forceinline__ void decode_item(const Ctx& c, const WorkItem& it, co
   merge_rows<D>(p, it, sg, mo, mm, ml, hw, HG, ps, head, R, lane);
 }
 
-template <int D>
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     mixed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
@@ -1288,6 +1422,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       ptx::mbar_init(c.b(i), count);
     }
     *c.abort = 0;
+    if (kTree) c.abort[1] = 0;  // no infinity or NaN found
     ptx::fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -1314,7 +1449,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   sg.hist = sg.lk - sg.lq;
 
   if (prefill) {
-    prefill_item<D>(c, it, sg, p, base, gb, *tmem_slot, &tm_q, &tm_k, &tm_v, warp, lane);
+    prefill_item<D, kTree>(c, it, sg, p, base, gb, *tmem_slot, &tm_q, &tm_k, &tm_v, warp, lane);
   } else if constexpr (D <= 128) {
     decode_item<D>(c, it, sg, p, base, gb, &tm_kd, &tm_vd, warp, lane);
   } else {
@@ -1379,7 +1514,7 @@ int decode_stages(int HG) {
   return ns;
 }
 
-template <int D>
+template <int D, bool kTree>
 int launch_fwd_d(const FwdArgs& a, cudaStream_t st) {
   using C = Cfg<D>;
   const int G = a.num_q_heads / a.num_kv_heads;
@@ -1481,10 +1616,14 @@ int launch_fwd_d(const FwdArgs& a, cudaStream_t st) {
   kp.scale_log2 = a.sm_scale * kLog2e;
   kp.test_stall = a.test_stall;
   kp.k_box5 = k_box5 ? 1 : 0;
-  cudaError_t e = cudaFuncSetAttribute(mixed_attn_fwd_kernel<D>,
+  kp.tree_mask = reinterpret_cast<const uint32_t*>(a.tree_mask);
+  kp.mask_rows = a.mask_rows;
+  kp.mask_words = a.mask_words;
+  kp.num_mask_rows = a.num_mask_rows;
+  cudaError_t e = cudaFuncSetAttribute(mixed_attn_fwd_kernel<D, kTree>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return static_cast<int>(e);
-  mixed_attn_fwd_kernel<D><<<a.num_items, kFwdThreads, C::kSmemBytes, st>>>(tq, tk, tv, tkd, tvd, kp);
+  mixed_attn_fwd_kernel<D, kTree><<<a.num_items, kFwdThreads, C::kSmemBytes, st>>>(tq, tk, tv, tkd, tvd, kp);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -1496,9 +1635,11 @@ int launch_mixed_attn(const FwdArgs& a, void* stream) {
   g_detail[0] = 0;
   if (a.num_items <= 0) return 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (a.head_dim == 128 || a.head_dim == 96) return launch_fwd_d<128>(a, st);
-  if (a.head_dim == 64) return launch_fwd_d<64>(a, st);
-  if (a.head_dim == 256) return launch_fwd_d<256>(a, st);
+  const bool tree = a.mask_rows != nullptr;
+  if (a.head_dim == 128 || a.head_dim == 96)
+    return tree ? launch_fwd_d<128, true>(a, st) : launch_fwd_d<128, false>(a, st);
+  if (a.head_dim == 64) return tree ? launch_fwd_d<64, true>(a, st) : launch_fwd_d<64, false>(a, st);
+  if (a.head_dim == 256) return tree ? launch_fwd_d<256, true>(a, st) : launch_fwd_d<256, false>(a, st);
   snprintf(g_detail, sizeof(g_detail), "head_dim %d not built", a.head_dim);
   return -1;
 }

@@ -136,19 +136,22 @@ struct Unit {
 // consecutive tokens of one segment grouped (at most 16 query rows on the
 // decode path; a lone token of G > 16 heads takes a tensor-core tile).
 std::vector<Unit> plan_units(const mcp_attn_desc& d, const int32_t* cu, const int32_t* rows,
-                             int32_t num_rows) {
+                             int32_t num_rows, bool tree) {
   const int G = d.num_q_heads / d.num_kv_heads;
   const int TQ = mcp::kTileRows / G;
   // the decode path is built up to head_dim 128 and for pages of 8 or more
   // tokens; at head_dim 256 or 1-token pages every segment takes tensor-core
   // tiles (a decode token fills G of a tile's 128 rows)
   const bool dec_ok = d.head_dim <= 128 && d.page_size >= 8;
+  // a step with trees: a segment of several tokens may be one, and trees are
+  // built for tensor-core tiles only
+  auto decodes = [&](int s) { return dec_ok && !(tree && cu[s + 1] - cu[s] > 1); };
   std::vector<Unit> u;
   if (!rows) {
     for (int s = 0; s < d.num_seqs; ++s) {
       const int64_t lq = cu[s + 1] - cu[s];
       if (lq == 0) continue;
-      if (dec_ok && lq * G <= mcp::kDecodeMaxRows) {
+      if (decodes(s) && lq * G <= mcp::kDecodeMaxRows) {
         u.push_back({s, 0, lq, true});
       } else {
         for (int64_t qb = 0; qb < lq; qb += TQ) u.push_back({s, qb, std::min<int64_t>(TQ, lq - qb), false});
@@ -161,7 +164,7 @@ std::vector<Unit> plan_units(const mcp_attn_desc& d, const int32_t* cu, const in
   for (int32_t i = 0; i < num_rows;) {
     const int32_t t = rows[i];
     while (cu[s + 1] <= t) ++s;
-    const bool dec = dec_ok && G <= mcp::kDecodeMaxRows;
+    const bool dec = decodes(s) && G <= mcp::kDecodeMaxRows;
     const int64_t cap = dec ? dec_max : TQ;
     int32_t j = i + 1;
     while (j < num_rows && rows[j] == rows[j - 1] + 1 && rows[j] < cu[s + 1] && j - i < cap) ++j;
@@ -181,7 +184,7 @@ void build(const mcp_attn_desc& d, const int32_t* cu, const int32_t* sk, int num
   const int HG = mcp::decode_head_group(H);
   const int dopt = o ? o->decode_split_tokens : 0;
   const int popt = o ? o->prefill_split_tokens : 0;
-  const std::vector<Unit> units = plan_units(d, cu, rows, num_rows);
+  const std::vector<Unit> units = plan_units(d, cu, rows, num_rows, o && o->tree);
   // keys visible to the unit's last token (right-aligned causal)
   auto vis_of = [&](const Unit& x) {
     return static_cast<int64_t>(sk[x.s]) - (cu[x.s + 1] - cu[x.s]) + x.qb + x.qc;
@@ -557,12 +560,14 @@ mcp_status plan_common(const mcp_attn_desc* desc, const int32_t* cu, const int32
   if (st != MCP_OK) return st;
   if (!plan) return fail(MCP_ERR_INVALID_ARG, "plan is NULL");
   if (opts) {
-    for (int i = 0; i < 4; ++i)
-      if (opts->reserved[i] != 0) return fail(MCP_ERR_INVALID_ARG, "opts->reserved must be 0");
+    for (int32_t r : opts->reserved)
+      if (r != 0) return fail(MCP_ERR_INVALID_ARG, "opts->reserved must be 0");
     if (opts->num_sms < 0 || opts->decode_split_tokens < 0 || opts->prefill_split_tokens < 0)
       return fail(MCP_ERR_INVALID_ARG, "negative plan option");
     if (opts->test_stall != 0 && opts->test_stall != 1)
       return fail(MCP_ERR_INVALID_ARG, "opts->test_stall must be 0 or 1");
+    if (opts->tree != 0 && opts->tree != 1)
+      return fail(MCP_ERR_INVALID_ARG, "opts->tree must be 0 or 1");
   }
   st = validate_meta(desc->num_seqs, desc->total_q, desc->page_size, desc->max_pages_per_seq, cu, sk);
   if (st != MCP_OK) return st;
@@ -616,6 +621,7 @@ mcp_status plan_common(const mcp_attn_desc* desc, const int32_t* cu, const int32
   pl.workspace_bytes = pl.off_error + 256;
   pl.desc = *desc;
   pl.test_stall = opts ? opts->test_stall : 0;
+  pl.tree = opts ? opts->tree : 0;
   *plan = pl;
   return MCP_OK;
 }
@@ -843,10 +849,17 @@ mcp_status mcp_mixed_attn_plan_host(const mcp_attn_desc* desc, const int32_t* h_
   }
 }
 
-mcp_status mcp_mixed_attn_fwd(const mcp_plan* plan, const void* q, const void* k_cache,
-                              const void* v_cache, const int32_t* block_tables,
-                              const int32_t* cu_seqlens_q, const int32_t* seqlens_k, void* out,
-                              float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// The fused forward of a planned step over the paged caches; mask_rows != NULL:
+// with trees of drafted tokens.
+mcp_status run_fwd(const mcp_plan* plan, const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, const int32_t* cu_seqlens_q,
+                   const int32_t* seqlens_k, const int32_t* tree_mask, int32_t num_mask_rows,
+                   int32_t mask_words, const int32_t* mask_rows, void* out, float* lse,
+                   void* workspace, size_t workspace_bytes, void* stream) {
   mcp_status st = mcp::check_fwd_args(plan, q, k_cache, v_cache, block_tables, cu_seqlens_q,
                                       seqlens_k, out, lse);
   if (st != MCP_OK) return st;
@@ -884,11 +897,48 @@ mcp_status mcp_mixed_attn_fwd(const mcp_plan* plan, const void* q, const void* k
   a.num_pages = d.num_pages;
   a.sm_scale = d.sm_scale;
   a.test_stall = plan->test_stall;
+  a.tree_mask = tree_mask;
+  a.mask_rows = mask_rows;
+  a.mask_words = mask_words;
+  a.num_mask_rows = num_mask_rows;
   int e = mcp::launch_mixed_attn(a, stream);
   if (e != 0) return cuda_fail(e, "mixed_attn_fwd launch");
   e = mcp::launch_combine(a, stream);
   if (e != 0) return cuda_fail(e, "combine launch");
   return okay();
+}
+
+}  // namespace
+
+extern "C" {
+
+mcp_status mcp_mixed_attn_fwd(const mcp_plan* plan, const void* q, const void* k_cache,
+                              const void* v_cache, const int32_t* block_tables,
+                              const int32_t* cu_seqlens_q, const int32_t* seqlens_k, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_fwd(plan, q, k_cache, v_cache, block_tables, cu_seqlens_q, seqlens_k, nullptr, 0, 0,
+                 nullptr, out, lse, workspace, workspace_bytes, stream);
+}
+
+mcp_status mcp_mixed_attn_fwd_tree(const mcp_plan* plan, const void* q, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_tables,
+                                   const int32_t* cu_seqlens_q, const int32_t* seqlens_k,
+                                   const int32_t* tree_mask, int32_t num_mask_rows,
+                                   int32_t mask_words, const int32_t* mask_rows, void* out,
+                                   float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  if (!plan || plan->magic != kPlanMagic) return fail(MCP_ERR_INVALID_ARG, "plan not initialised");
+  if (!plan->tree)
+    return fail(MCP_ERR_INVALID_ARG, "the step was planned without mcp_plan_options.tree");
+  if (num_mask_rows < 0 || mask_words <= 0)
+    return fail(MCP_ERR_INVALID_ARG, "num_mask_rows %d / mask_words %d", num_mask_rows, mask_words);
+  if (plan->num_items == 0) return okay();
+  if (!mask_rows || (num_mask_rows > 0 && !tree_mask))
+    return fail(MCP_ERR_INVALID_ARG, "NULL pointer argument (tree_mask, mask_rows)");
+  if (!aligned(tree_mask, 4) || !aligned(mask_rows, 4))
+    return fail(MCP_ERR_INVALID_ARG, "tree_mask / mask_rows not 4-byte aligned");
+  return run_fwd(plan, q, k_cache, v_cache, block_tables, cu_seqlens_q, seqlens_k, tree_mask,
+                 num_mask_rows, mask_words, mask_rows, out, lse, workspace, workspace_bytes, stream);
 }
 
 mcp_status mcp_mixed_attn_fwd_varlen(const mcp_plan* plan, const void* q, const void* k,

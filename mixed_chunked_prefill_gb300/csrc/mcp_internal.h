@@ -91,6 +91,11 @@ struct FwdArgs {
   const int32_t* cu_seqlens_k = nullptr;
   int64_t total_k = 0;
   int32_t test_stall = 0;  // mcp_plan_options.test_stall of the plan
+  // trees of drafted tokens (mask_rows != nullptr): see mcp_mixed_attn_fwd_tree
+  const int32_t* tree_mask = nullptr;
+  const int32_t* mask_rows = nullptr;
+  int32_t mask_words = 0;
+  int32_t num_mask_rows = 0;
 };
 
 // Launchers (return a cudaError_t value; 0 = success).  Defined in *.cu.

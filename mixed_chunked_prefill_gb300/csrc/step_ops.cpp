@@ -1,5 +1,5 @@
 // C entries of the operators around a step's attention: argument checks and
-// launches (tables.cu, recurrent.cu, logits.cu).
+// launches (tables.cu, recurrent.cu, logits.cu, tree.cu, verify.cu).
 #include "step_ops.h"
 
 #include <cuda_runtime.h>
@@ -306,6 +306,92 @@ mcp_status mcp_process_logits(const mcp_logits_desc* d, const mcp_logits_tensors
                 d->num_rows);
   if (!t->mask && t->mask_rows) return fail(MCP_ERR_INVALID_ARG, "mask_rows without mask");
   return done(mcp::launch_process_logits(*d, *t, error_word, stream), "process_logits launch");
+}
+
+mcp_status mcp_build_tree_masks(const int32_t* parents, const int32_t* cu_seqlens_q,
+                                const int32_t* seqlens_k, const int32_t* mask_rows,
+                                int32_t num_seqs, int32_t total_tokens, int32_t num_mask_rows,
+                                int32_t mask_words, int32_t* tree_mask, int32_t* positions,
+                                int32_t* error_word, void* stream) {
+  if (num_seqs < 0 || total_tokens < 0 || num_mask_rows < 0 || mask_words <= 0)
+    return fail(MCP_ERR_INVALID_ARG, "num_seqs %d / total_tokens %d / num_mask_rows %d / mask_words %d",
+                num_seqs, total_tokens, num_mask_rows, mask_words);
+  if (num_seqs > kMaxSegments || total_tokens > kMaxTokens || num_mask_rows > kMaxTokens ||
+      mask_words > mcp::kMaxMaskWords)
+    return fail(MCP_ERR_UNSUPPORTED,
+                "num_seqs %d > 2^20, total_tokens %d or num_mask_rows %d > 2^30, or mask_words %d > %d",
+                num_seqs, total_tokens, num_mask_rows, mask_words, mcp::kMaxMaskWords);
+  MCP_TRY(check_words({parents, cu_seqlens_q, seqlens_k, mask_rows, tree_mask, positions, error_word}));
+  if (num_seqs == 0 || total_tokens == 0) return done(0, "");
+  if (!parents || !cu_seqlens_q || !seqlens_k || !mask_rows || (num_mask_rows > 0 && !tree_mask))
+    return fail(MCP_ERR_INVALID_ARG, "NULL pointer argument");
+  return done(mcp::launch_build_tree_masks(parents, cu_seqlens_q, seqlens_k, mask_rows, num_seqs,
+                                           total_tokens, num_mask_rows, mask_words, tree_mask,
+                                           positions, error_word, stream),
+              "build_tree_masks launch");
+}
+
+mcp_status mcp_verify_drafts(const mcp_verify_desc* d, const mcp_verify_tensors* t,
+                             int32_t* error_word, void* stream) {
+  if (!d || !t) return fail(MCP_ERR_INVALID_ARG, "desc or tensors is NULL");
+  if (d->num_seqs < 0 || d->total_rows < 0 || d->vocab_size <= 0)
+    return fail(MCP_ERR_INVALID_ARG, "num_seqs %d / total_rows %d / vocab_size %d", d->num_seqs,
+                d->total_rows, d->vocab_size);
+  if (d->num_seqs > kMaxSegments || d->total_rows > kMaxTokens || d->vocab_size > kMaxRow)
+    return fail(MCP_ERR_UNSUPPORTED, "num_seqs %d > 2^20, total_rows %d > 2^30 or vocab_size %d > 2^28",
+                d->num_seqs, d->total_rows, d->vocab_size);
+  if (d->dtype != MCP_DTYPE_BF16 && d->dtype != MCP_DTYPE_FP16 && d->dtype != MCP_DTYPE_FP32)
+    return fail(MCP_ERR_UNSUPPORTED, "dtype %d", d->dtype);
+  if (d->target_stride < d->vocab_size || (t->draft && d->draft_stride < d->vocab_size))
+    return fail(MCP_ERR_INVALID_ARG, "row stride below vocab_size %d", d->vocab_size);
+  if (d->num_seqs == 0) return done(0, "");
+  if (!t->cu_rows || !t->final_uniform || !t->accepted ||
+      (d->total_rows > 0 && (!t->target || !t->tokens || !t->uniform || !t->path || !t->new_tokens)))
+    return fail(MCP_ERR_INVALID_ARG, "NULL tensor pointer");
+  const uintptr_t size = d->dtype == MCP_DTYPE_FP32 ? 4 : 2;
+  if (!aligned(t->target, size) || !aligned(t->draft, size))
+    return fail(MCP_ERR_INVALID_ARG, "target or draft misaligned");
+  MCP_TRY(check_words({t->tokens, t->parents, t->cu_rows, t->uniform, t->final_uniform, t->accepted,
+                       t->path, t->new_tokens, error_word}));
+  return done(mcp::launch_verify_drafts(*d, *t, error_word, stream), "verify_drafts launch");
+}
+
+mcp_status mcp_kv_keep_path(const mcp_keep_desc* d, void* const* k_caches, void* const* v_caches,
+                            const int32_t* block_tables, const int32_t* cu_seqlens_q,
+                            const int32_t* seqlens_k, const int32_t* cu_rows,
+                            const int32_t* accepted, const int32_t* path, int32_t* new_lens,
+                            int32_t* error_word, void* stream) {
+  if (!d) return fail(MCP_ERR_INVALID_ARG, "desc is NULL");
+  if (d->num_seqs < 0 || d->total_rows < 0 || d->num_layers < 0)
+    return fail(MCP_ERR_INVALID_ARG, "num_seqs %d / total_rows %d / num_layers %d < 0", d->num_seqs,
+                d->total_rows, d->num_layers);
+  if (d->num_seqs > kMaxSegments || d->total_rows > kMaxTokens || d->num_layers > mcp::kMaxKeepLayers)
+    return fail(MCP_ERR_UNSUPPORTED, "num_seqs %d > 2^20, total_rows %d > 2^30 or num_layers %d > %d",
+                d->num_seqs, d->total_rows, d->num_layers, mcp::kMaxKeepLayers);
+  if (d->num_kv_heads <= 0 || d->head_dim <= 0 || d->max_pages_per_seq <= 0 || d->num_pages <= 0)
+    return fail(MCP_ERR_INVALID_ARG, "sizes must be positive (heads %d, dim %d, table row %d, pages %d)",
+                d->num_kv_heads, d->head_dim, d->max_pages_per_seq, d->num_pages);
+  if (d->page_size != 1 && d->page_size != 8 && d->page_size != 16 && d->page_size != 32 &&
+      d->page_size != 64)
+    return fail(MCP_ERR_UNSUPPORTED, "page_size %d (built: 1, 8, 16, 32, 64)", d->page_size);
+  const int64_t row = static_cast<int64_t>(d->num_kv_heads) * d->head_dim;
+  if (row % 8 != 0)
+    return fail(MCP_ERR_INVALID_ARG, "num_kv_heads * head_dim = %lld is not a multiple of 8",
+                static_cast<long long>(row));
+  if (row > 1 << 20 || d->max_pages_per_seq > kMaxRow)
+    return fail(MCP_ERR_UNSUPPORTED, "num_kv_heads * head_dim %lld > 2^20 or max_pages_per_seq %d > 2^28",
+                static_cast<long long>(row), d->max_pages_per_seq);
+  MCP_TRY(check_words({block_tables, cu_seqlens_q, seqlens_k, cu_rows, accepted, path, new_lens, error_word}));
+  if (d->num_seqs == 0) return done(0, "");
+  if (!block_tables || !cu_seqlens_q || !seqlens_k || !accepted || (d->total_rows > 0 && !path) ||
+      (d->num_layers > 0 && (!k_caches || !v_caches)))
+    return fail(MCP_ERR_INVALID_ARG, "NULL pointer argument");
+  for (int32_t l = 0; l < d->num_layers; ++l)
+    if (!k_caches[l] || !v_caches[l] || !aligned(k_caches[l], 16) || !aligned(v_caches[l], 16))
+      return fail(MCP_ERR_INVALID_ARG, "cache of layer %d is NULL or not 16-byte aligned", l);
+  return done(mcp::launch_kv_keep_path(*d, k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k,
+                                       cu_rows, accepted, path, new_lens, error_word, stream),
+              "kv_keep_path launch");
 }
 
 }  // extern "C"

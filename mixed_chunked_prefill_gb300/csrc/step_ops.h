@@ -41,6 +41,21 @@ int launch_update_token_counts(const int32_t* request_ids, int32_t num_rows,
                                int32_t* error_word, void* stream);
 int launch_process_logits(const mcp_logits_desc& d, const mcp_logits_tensors& t,
                           int32_t* error_word, void* stream);
+// tree.cu
+constexpr int32_t kMaxMaskWords = 32;   // a tree's rows fit one CTA's shared memory
+constexpr int32_t kMaxKeepLayers = 1024;
+int launch_build_tree_masks(const int32_t* parents, const int32_t* cu_seqlens_q,
+                            const int32_t* seqlens_k, const int32_t* mask_rows, int32_t num_seqs,
+                            int32_t total_tokens, int32_t num_mask_rows, int32_t mask_words,
+                            int32_t* tree_mask, int32_t* positions, int32_t* error_word,
+                            void* stream);
+int launch_kv_keep_path(const mcp_keep_desc& d, void* const* k_caches, void* const* v_caches,
+                        const int32_t* block_tables, const int32_t* cu_seqlens_q,
+                        const int32_t* seqlens_k, const int32_t* cu_rows, const int32_t* accepted,
+                        const int32_t* path, int32_t* new_lens, int32_t* error_word, void* stream);
+// verify.cu
+int launch_verify_drafts(const mcp_verify_desc& d, const mcp_verify_tensors& t, int32_t* error_word,
+                         void* stream);
 
 // SMs of the current device (read once per device and thread).
 int step_num_sms();

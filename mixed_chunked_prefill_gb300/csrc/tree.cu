@@ -1,0 +1,261 @@
+// Trees of drafted tokens: which tokens of its tree each token sees, and the
+// move of an accepted path's K/V to the front of its segment.
+//
+// A tree's token i has a parent before it (or none); it sees
+//   seen(i) = seen(parent) and i,   at position history + |seen(i)| - 1.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mcp.h"
+#include "step_ops.h"
+
+namespace mcp {
+namespace {
+
+// ------------------------------------------------------------------- masks
+constexpr int kMaskThreads = 256;
+
+struct MaskArgs {
+  const int32_t* parents;
+  const int32_t* cu;
+  const int32_t* sk;
+  const int32_t* mask_rows;
+  uint32_t* mask;
+  int32_t* positions;
+  int32_t* err;
+  int32_t T, rows, W;
+};
+
+// A CTA a segment.  The rows are filled by doubling: row[i] holds the tokens
+// from i up to, but without, up[i]; each round takes over row[up[i]] and
+// up[up[i]], so a tree of depth d takes log2(d) rounds where a walk up takes d
+// steps.  A row that another thread has already extended in the same round only
+// holds more of the same ancestors; up, which must not run ahead of the rows, is
+// written to a second array.  Depth is the number of bits.
+__global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs p) {
+  extern __shared__ uint32_t smem[];
+  const int s = blockIdx.x, tid = threadIdx.x, W = p.W;
+  const int t0 = p.cu[s], t1 = p.cu[s + 1];
+  const int n = t1 - t0, hist = p.sk[s] - n, m0 = p.mask_rows[s];
+  if (n <= 0) {
+    if (n < 0 && tid == 0 && p.err) atomicOr(p.err, MCP_DEVERR_SEGMENT);
+    return;
+  }
+  int bad = hist < 0 ? MCP_DEVERR_SEGMENT : 0;
+  const bool outside = t0 < 0 || t1 > p.T;
+  if (outside) bad |= MCP_DEVERR_SEGMENT;
+  const bool tree = m0 >= 0;
+  const bool large = tree && (n > 32 * W || m0 > p.rows - n);
+  if (large) bad |= MCP_DEVERR_TREE;
+  if (bad && tid == 0 && p.err) atomicOr(p.err, bad);
+  if (outside || large) return;
+  if (!tree) {
+    if (p.positions)
+      for (int i = tid; i < n; i += kMaskThreads) p.positions[t0 + i] = hist + i;
+    return;
+  }
+  uint32_t* row = smem;                                     // [n][W]
+  int32_t* up = reinterpret_cast<int32_t*>(smem + 32 * W * W);  // two of [32 W]
+  int32_t* next = up + 32 * W;
+  for (int i = tid; i < n * W; i += kMaskThreads) row[i] = 0;
+  __syncthreads();
+  bool some = false;
+  for (int i = tid; i < n; i += kMaskThreads) {
+    int32_t a = p.parents[t0 + i];
+    if (a >= i) {
+      if (p.err) atomicOr(p.err, MCP_DEVERR_TREE);
+      a = -1;
+    }
+    up[i] = a < 0 ? -1 : a;
+    some |= a >= 0;
+    row[i * W + (i >> 5)] = 1u << (i & 31);
+  }
+  while (__syncthreads_or(some)) {
+    some = false;
+    for (int x = tid; x < n * W; x += kMaskThreads) {
+      const int i = x / W;
+      const int a = up[i];
+      if (a >= 0) row[x] |= row[a * W + x - i * W];
+    }
+    for (int i = tid; i < n; i += kMaskThreads) {
+      const int a = up[i];
+      const int b = a >= 0 ? up[a] : -1;
+      next[i] = b;
+      some |= b >= 0;
+    }
+    int32_t* const t = up;
+    up = next;
+    next = t;
+  }
+  uint32_t* out = p.mask + static_cast<int64_t>(m0) * W;
+  for (int x = tid; x < n * W; x += kMaskThreads) out[x] = row[x];
+  if (p.positions)
+    for (int i = tid; i < n; i += kMaskThreads) {
+      int bits = 0;
+      for (int w = 0; w <= i >> 5; ++w) bits += __popc(row[i * W + w]);
+      p.positions[t0 + i] = hist + bits - 1;
+    }
+}
+
+// -------------------------------------------------------------------- keep
+constexpr int kKeepThreads = 256;
+constexpr int kKeepLayers = 64;  // whose addresses fit a launch's arguments
+constexpr int kKeepSlots = 256;  // moves whose slots a CTA has at hand
+constexpr int kKeepBatch = 8;    // rows in flight a thread
+
+struct KeepArgs {
+  uint4* caches[2 * kKeepLayers];  // K and V of each layer
+  const int32_t* bt;
+  const int32_t* cu;
+  const int32_t* sk;
+  const int32_t* cu_rows;
+  const int32_t* accepted;
+  const int32_t* path;
+  int32_t* new_lens;
+  int32_t* err;
+  int32_t total_rows, page_log2, max_pages, num_pages, vec;
+  int32_t columns;   // 16-byte columns of all layers' K and V rows: 2 * layers * vec
+  int32_t per_cta;   // columns of a CTA, a multiple of its threads
+  int32_t chunks;    // CTAs of a segment
+};
+
+__device__ __forceinline__ int64_t slot_of(const KeepArgs& p, const int32_t* bt, int pos, int& bad) {
+  const int32_t page = bt[pos >> p.page_log2];
+  if (page < 0 || page >= p.num_pages) {
+    bad |= MCP_DEVERR_PAGE_RANGE;
+    return -1;
+  }
+  return (static_cast<int64_t>(page) << p.page_log2) + (pos & ((1 << p.page_log2) - 1));
+}
+
+// A CTA moves some 16-byte columns of the rows of all layers for one segment.
+// One thread takes a column through all moves in their order, up to kKeepBatch of
+// them loaded before the first is stored: a path rises strictly, so move k reads
+// place path[k] >= k, which only moves after it write.
+__global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const __grid_constant__ KeepArgs p) {
+  __shared__ int64_t from[kKeepSlots], to[kKeepSlots];
+  const int s = blockIdx.x / p.chunks, chunk = blockIdx.x - s * p.chunks, tid = threadIdx.x;
+  const int lq = p.cu[s + 1] - p.cu[s], sk = p.sk[s], hist = sk - lq;
+  const int r0 = p.cu_rows[s], n = p.cu_rows[s + 1] - r0, m = p.accepted[s];
+  int bad = 0;
+  bool move = n == lq && lq > 0;
+  if (lq < 0 || n < 0 || hist < 0 || r0 < 0 || r0 > p.total_rows - n ||
+      sk > static_cast<int64_t>(p.max_pages) << p.page_log2) {
+    bad = MCP_DEVERR_SEGMENT;
+    move = false;
+  } else if (move && (m < 0 || m > n)) {
+    bad = MCP_DEVERR_TREE;
+    move = false;
+  }
+  if (move) {  // the whole path before the first move
+    bool sound = true;
+    for (int k = tid; k < m; k += kKeepThreads) {
+      const int a = p.path[r0 + k], before = k ? p.path[r0 + k - 1] : -1;
+      sound &= a > before && a < n && a >= 0;
+    }
+    if (!__syncthreads_and(sound)) {
+      bad = MCP_DEVERR_TREE;
+      move = false;
+    }
+  }
+  if (chunk == 0 && tid == 0) {
+    if (p.new_lens) p.new_lens[s] = move ? hist + m : sk;
+    if (bad && p.err) atomicOr(p.err, bad);
+  }
+  if (!move) return;
+  const int32_t* bt = p.bt + static_cast<int64_t>(s) * p.max_pages;
+  const int c0 = chunk * p.per_cta, c1 = min(c0 + p.per_cta, p.columns);
+  for (int k0 = 0; k0 < m; k0 += kKeepSlots) {
+    const int left = min(kKeepSlots, m - k0);
+    if (tid < left) {
+      const int a = p.path[r0 + k0 + tid], k = k0 + tid;
+      int64_t src = -1, dst = -1;
+      if (a != k) {
+        int page_bad = 0;
+        src = slot_of(p, bt, hist + a, page_bad);
+        dst = slot_of(p, bt, hist + k, page_bad);
+        if (page_bad) {
+          src = -1;
+          if (chunk == 0 && p.err) atomicOr(p.err, page_bad);
+        }
+      }
+      from[tid] = src;
+      to[tid] = dst;
+    }
+    __syncthreads();
+    for (int c = c0 + tid; c < c1; c += kKeepThreads) {
+      const int which = c / p.vec;
+      uint4* cache = p.caches[which] + (c - which * p.vec);
+      for (int b = 0; b < left; b += kKeepBatch) {
+        uint4 v[kKeepBatch];
+#pragma unroll
+        for (int j = 0; j < kKeepBatch; ++j)
+          if (b + j < left && from[b + j] >= 0) v[j] = cache[from[b + j] * p.vec];
+#pragma unroll
+        for (int j = 0; j < kKeepBatch; ++j)
+          if (b + j < left && from[b + j] >= 0) cache[to[b + j] * p.vec] = v[j];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+int launch_build_tree_masks(const int32_t* parents, const int32_t* cu_seqlens_q,
+                            const int32_t* seqlens_k, const int32_t* mask_rows, int32_t num_seqs,
+                            int32_t total_tokens, int32_t num_mask_rows, int32_t mask_words,
+                            int32_t* tree_mask, int32_t* positions, int32_t* error_word,
+                            void* stream) {
+  const int smem = 4 * (32 * mask_words * mask_words + 2 * 32 * mask_words);  // at most 136 KB
+  if (smem > 48 * 1024) {
+    const int e = allow_smem<tree_masks_kernel>(4 * (32 * 32 * 32 + 2 * 32 * 32));
+    if (e != 0) return e;
+  }
+  const MaskArgs a = {parents, cu_seqlens_q, seqlens_k, mask_rows,
+                      reinterpret_cast<uint32_t*>(tree_mask), positions, error_word,
+                      total_tokens, num_mask_rows, mask_words};
+  tree_masks_kernel<<<num_seqs, kMaskThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+  return static_cast<int>(cudaGetLastError());
+}
+
+int launch_kv_keep_path(const mcp_keep_desc& d, void* const* k_caches, void* const* v_caches,
+                        const int32_t* block_tables, const int32_t* cu_seqlens_q,
+                        const int32_t* seqlens_k, const int32_t* cu_rows, const int32_t* accepted,
+                        const int32_t* path, int32_t* new_lens, int32_t* error_word, void* stream) {
+  KeepArgs a;
+  a.bt = block_tables;
+  a.cu = cu_seqlens_q;
+  a.sk = seqlens_k;
+  a.cu_rows = cu_rows ? cu_rows : cu_seqlens_q;
+  a.accepted = accepted;
+  a.path = path;
+  a.new_lens = new_lens;
+  a.err = error_word;
+  a.total_rows = d.total_rows;
+  a.page_log2 = __builtin_ctz(static_cast<unsigned>(d.page_size));
+  a.max_pages = d.max_pages_per_seq;
+  a.num_pages = d.num_pages;
+  a.vec = static_cast<int32_t>(static_cast<int64_t>(d.num_kv_heads) * d.head_dim / 8);
+  for (int l0 = 0; l0 == 0 || l0 < d.num_layers; l0 += kKeepLayers) {
+    const int layers = d.num_layers - l0 < kKeepLayers ? d.num_layers - l0 : kKeepLayers;
+    for (int l = 0; l < layers; ++l) {
+      a.caches[2 * l] = static_cast<uint4*>(k_caches[l0 + l]);
+      a.caches[2 * l + 1] = static_cast<uint4*>(v_caches[l0 + l]);
+    }
+    a.columns = 2 * layers * a.vec;
+    // a column a thread, more of them where that would be over 8 CTAs an SM
+    const int64_t all = static_cast<int64_t>(d.num_seqs) * ((a.columns + kKeepThreads - 1) / kKeepThreads);
+    const int64_t rounds = (all + 8LL * step_num_sms() - 1) / (8LL * step_num_sms());
+    const int64_t per = kKeepThreads * (rounds < 1 ? 1 : rounds);
+    a.per_cta = static_cast<int32_t>(per < a.columns ? per : (a.columns > 0 ? a.columns : 1));
+    a.chunks = a.columns > 0 ? (a.columns + a.per_cta - 1) / a.per_cta : 1;
+    const int64_t grid = static_cast<int64_t>(d.num_seqs) * a.chunks;
+    keep_path_kernel<<<static_cast<unsigned>(grid), kKeepThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return static_cast<int>(e);
+  }
+  return 0;
+}
+
+}  // namespace mcp

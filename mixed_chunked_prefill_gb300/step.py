@@ -20,11 +20,14 @@ from . import (
     PlanOptions,
     build_slot_mapping,
     build_step_tables,
+    build_tree_masks,
     check_device_errors,
     commit_step,
+    kv_keep_path,
     make_desc,
     make_request_pool,
     mixed_attn_fwd,
+    mixed_attn_fwd_tree,
     mixed_attn_plan,
     mixed_attn_plan_rows,
     paged_kv_append,
@@ -54,14 +57,48 @@ def _on_stream(stream, device):
                              else torch.cuda.ExternalStream(int(stream), device))
 
 
+class StepTrees:
+    """Trees of drafted tokens of one step: their visibility masks, and the positions of all
+    of the step's tokens (``mcp_build_tree_masks``).  ``trees``: which segments are trees
+    (the others are causal: chunks, decodes); ``parents`` [T]: for each token of the step the
+    place of its parent in its segment, < 0: none (not looked at in causal segments)."""
+
+    def __init__(self, cu_seqlens_q, cu_d, seqlens_k_d, trees, parents, error_word=None,
+                 stream=None):
+        import torch
+
+        cu, dev = _i64(cu_seqlens_q), cu_d.device
+        q = np.diff(cu)
+        is_tree = np.asarray(trees, dtype=bool)
+        if is_tree.shape != q.shape:
+            raise ValueError("trees must be one truth value a segment")
+        sizes = np.where(is_tree, q, 0)
+        rows = np.concatenate([[0], np.cumsum(sizes)])
+        words = max(1, -(-int(sizes.max(initial=0)) // 32))
+        if words > _capi.MAX_MASK_WORDS:
+            raise ValueError(f"a tree of {int(sizes.max())} tokens > {32 * _capi.MAX_MASK_WORDS}")
+        with _on_stream(stream, dev):
+            if not isinstance(parents, torch.Tensor):
+                parents = torch.from_numpy(_i32(parents))
+            self.parents = parents.to(dev)
+            self.mask_rows = torch.from_numpy(_i32(np.where(is_tree, rows[:-1], -1))).to(dev)
+            self.tree_mask = torch.empty((int(rows[-1]), words), dtype=torch.int32, device=dev)
+            self.positions = torch.empty(self.parents.shape[0], dtype=torch.int32, device=dev)
+            if self.parents.shape[0] < int(cu[-1]):
+                raise ValueError("parents must have an entry for each token of the step")
+            build_tree_masks(self.parents, cu_d, seqlens_k_d, self.mask_rows, self.tree_mask,
+                             self.positions, error_word, stream)
+
+
 class MixedStep:
     """Device-side state of one step: metadata, slot mapping, plan, workspace."""
 
     def __init__(self, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, sm_scale,
                  cu_seqlens_q, seqlens_k, block_tables, device="cuda", options=None,
-                 stream=None, rows=None):
+                 stream=None, rows=None, trees=None, parents=None):
         """``rows``: None for every query row, else the token indices (e.g.
-        logits_indices) whose attention rows this step computes."""
+        logits_indices) whose attention rows this step computes.  ``trees``, ``parents``:
+        None, or the step's trees of drafted tokens (see ``StepTrees``, kept as ``trees``)."""
         import torch
 
         self.cu_h = _i32(cu_seqlens_q)
@@ -80,11 +117,11 @@ class MixedStep:
         self.sk_d = torch.from_numpy(self.sk_h).to(device)
         self.bt_d = torch.from_numpy(self.bt_h).to(device)
         self.slots_d = torch.from_numpy(self.slots_h).to(device)
-        self._plan(rows)
+        self._plan(rows, trees, parents)
 
     @classmethod
     def from_tables(cls, tables, num_q_heads, num_kv_heads, head_dim, sm_scale, options=None,
-                    stream=None, rows=None):
+                    stream=None, rows=None, trees=None, parents=None):
         """A step whose tables and slots were built on the device (``RequestTables.step``):
         nothing but the work lists is copied to the device.  Where they are padded
         (``max_tokens``), ``append`` takes the step's tokens alone or padded ones as well."""
@@ -98,13 +135,19 @@ class MixedStep:
         self.tables = tables
         self.cu_d, self.sk_d = tables.cu_seqlens_q, tables.seqlens_k
         self.bt_d, self.slots_d = tables.block_tables, tables.slot_mapping
-        self._plan(rows)
+        self._plan(rows, trees, parents)
         return self
 
-    def _plan(self, rows):
+    def _plan(self, rows, trees=None, parents=None):
         import torch
 
         options, device, stream = self.options, self.device, self.stream
+        self.trees = None
+        if (trees is None) != (parents is None):
+            raise ValueError("trees and parents go together")
+        if trees is not None:
+            options = PlanOptions.from_buffer_copy(options) if options is not None else PlanOptions()
+            options.tree = 1
         if rows is None:
             def planner(ws=None, st=None):
                 return mixed_attn_plan(self.desc, self.cu_h, self.sk_h, options, ws, st)
@@ -119,6 +162,9 @@ class MixedStep:
                                      device=device)
         self.plan = planner(self.workspace, stream)
         self.error_word = workspace_error_word(self.plan, self.workspace)
+        if trees is not None:
+            self.trees = StepTrees(self.cu_h, self.cu_d, self.sk_d, trees, parents,
+                                   self.error_word, stream)
 
     def append(self, k_new, v_new, k_cache, v_cache):
         slots, n = self.slots_d, int(k_new.shape[0])
@@ -127,12 +173,23 @@ class MixedStep:
         paged_kv_append(k_new, v_new, slots, k_cache, v_cache, self.error_word, self.stream)
 
     def attention(self, q, k_cache, v_cache, out, lse=None):
+        if self.trees is not None:
+            mixed_attn_fwd_tree(self.plan, q, k_cache, v_cache, self.bt_d, self.cu_d, self.sk_d,
+                                self.trees.tree_mask, self.trees.mask_rows, out, lse,
+                                self.workspace, self.stream)
+            return
         mixed_attn_fwd(self.plan, q, k_cache, v_cache, self.bt_d, self.cu_d, self.sk_d, out, lse,
                        self.workspace, self.stream)
 
     def run(self, q, k_new, v_new, k_cache, v_cache, out, lse=None):
         self.append(k_new, v_new, k_cache, v_cache)
         self.attention(q, k_cache, v_cache, out, lse)
+
+    def keep(self, k_caches, v_caches, accepted, path, cu_rows=None):
+        """Move the accepted paths (``verify_drafts``) behind their histories in all layers'
+        caches; returns the tokens that each request holds then (``RequestTables.commit``)."""
+        return kv_keep_path(k_caches, v_caches, self.bt_d, self.cu_d, self.sk_d, accepted, path,
+                            cu_rows, None, self.error_word, self.stream)
 
     def check(self):
         """Synchronise and raise if a device-side check or bounded wait failed."""
