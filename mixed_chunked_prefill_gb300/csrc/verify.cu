@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "mcp.h"
@@ -34,10 +35,14 @@
 namespace mcp {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kMaxNodes = 1024;
+constexpr int kGoneBits = 65536;  // of the bitmap of refused tokens
+constexpr int kSlots = 8;         // 16-byte pieces that a thread has in flight
+constexpr int kSlotsGiven = 6;    // without q, where the bitmap takes the room of two
+constexpr int kPerSM = 4;        // CTAs
 
 // ------------------------------------------------------- sums of two fp32
 struct Two {
@@ -48,19 +53,30 @@ __device__ __forceinline__ Two two_sum(float a, float b) {
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ Two normal(float h, float l) {  // |h| >= |l|
-  const float s = __fadd_rn(h, l);
-  return {s, __fsub_rn(l, __fsub_rn(s, h))};
+__device__ __forceinline__ Two normal(Two a) {  // |h| >= |l|
+  const float s = __fadd_rn(a.h, a.l);
+  return {s, __fsub_rn(a.l, __fsub_rn(s, a.h))};
 }
+// the sum, whose l may have grown past half a step of h
 __device__ __forceinline__ Two add(Two a, Two b) {
   const Two s = two_sum(a.h, b.h);
-  return normal(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+  return {s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l))};
 }
-__device__ __forceinline__ bool above(Two a, Two b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
+__device__ __forceinline__ bool above(Two a, Two b) {  // of normal ones
+  return a.h > b.h || (a.h == b.h && a.l > b.l);
+}
 __device__ __forceinline__ double wide(Two a) { return static_cast<double>(a.h) + a.l; }
 __device__ __forceinline__ Two two_of(double x) {
   const float h = static_cast<float>(x);
   return {h, static_cast<float>(x - h)};
+}
+// acc += w for w >= 0 and acc.h >= 0: with the larger first, the error of the sum
+// takes two operations instead of four
+__device__ __forceinline__ void accumulate(Two& acc, float w) {
+  const float a = fmaxf(acc.h, w), b = fminf(acc.h, w);
+  const float s = __fadd_rn(a, b);
+  acc.l = __fadd_rn(acc.l, __fsub_rn(b, __fsub_rn(s, a)));
+  acc.h = s;
 }
 
 // ------------------------------------------------------------ probabilities
@@ -114,118 +130,214 @@ struct VerifyArgs {
   int32_t S, R, V;
 };
 
-// The weights of one row: p, p - c q, or p without some tokens.
-template <typename T, bool kDraft>
+// What a weight is made of: p, p - q after one refusal, p - c q after several.
+enum Mode : int { kOnlyP = 0, kLessQ = 1, kLessCQ = 2 };
+
+// The weights of one row
+template <typename T>
 struct Row {
   const T* p;
-  const T* q;          // kDraft
-  float ch, cl;        // c as two fp32
-  const int32_t* gone;  // tokens whose weight is 0 (!kDraft)
+  const T* q;
+  int mode;
+  float ch, cl;         // c as two fp32
+  const int32_t* gone;  // tokens whose weight is 0
   int num_gone;
+  const uint32_t* bitmap;  // bit (place % kGoneBits): the token there may be one of them
+  int off;                 // place of token 0: values of its 16-byte piece before it
+  bool folded;             // the places are more than the bits: the list decides
 
-  __device__ __forceinline__ Two weight(float p_raw, float q_raw) const {
-    const float pv = clean(p_raw);
-    if constexpr (!kDraft) {
-      return {pv, 0.f};
-    } else {
-      const float qv = clean(q_raw);
-      // p - (ch + cl) q: the product and the difference each with its error
-      const float t = __fmul_rn(ch, qv), e = __fmaf_rn(ch, qv, -t);
-      const Two d = two_sum(pv, -t);
-      const Two w = normal(d.h, __fsub_rn(__fsub_rn(d.l, e), __fmul_rn(cl, qv)));
-      return w.h > 0.f ? w : Two{0.f, 0.f};
-    }
-  }
-  __device__ __forceinline__ bool is_gone(int v) const {
+  __device__ __forceinline__ bool is_gone(int64_t place) const {
+    const uint32_t f = static_cast<uint32_t>(place) % kGoneBits;
+    if (!(bitmap[f >> 5] >> (f & 31) & 1u)) return false;
+    if (!folded) return true;
     for (int i = 0; i < num_gone; ++i)
-      if (gone[i] == v) return true;
+      if (gone[i] + off == place) return true;
     return false;
-  }
-  // weight of token v, read alone
-  __device__ __forceinline__ Two at(int v) const {
-    if (!kDraft && num_gone && is_gone(v)) return {0.f, 0.f};
-    return weight(as_float(p[v]), kDraft ? as_float(q[v]) : 0.f);
   }
 };
 
-__device__ __forceinline__ void accumulate(Two& acc, Two w) {
-  const Two s = two_sum(acc.h, w.h);
-  acc.h = s.h;
-  acc.l = __fadd_rn(acc.l, __fadd_rn(s.l, w.l));
+// max(p - (ch + cl) q, 0) of values as they stand there, the product and the
+// difference each with its error.  Not inlined: the kernel waits for instructions
+// more than for anything else where they are run once a row.
+__device__ __noinline__ Two weight_of(float p_raw, float q_raw, float ch, float cl) {
+  const float pv = clean(p_raw), qv = clean(q_raw);
+  const float t = __fmul_rn(ch, qv), e = __fmaf_rn(ch, qv, -t);
+  const Two d = two_sum(pv, -t);
+  const Two w = normal({d.h, __fsub_rn(__fsub_rn(d.l, e), __fmul_rn(cl, qv))});
+  return w.h > 0.f ? w : Two{0.f, 0.f};
+}
+// Weight of token v, read alone
+template <typename T>
+__device__ __forceinline__ Two weight_at(const Row<T>& r, int v) {
+  if (r.num_gone && r.is_gone(static_cast<int64_t>(v) + r.off)) return {0.f, 0.f};
+  if (r.mode == kOnlyP) return {clean(as_float(r.p[v])), 0.f};
+  return weight_of(as_float(r.p[v]), as_float(r.q[v]), r.ch, r.cl);
+}
+
+// Weights of tokens v .. v + 3 (0 from `end` on), their loads in flight together
+template <typename T>
+__device__ __forceinline__ void weights_at(const Row<T>& r, int64_t v, int64_t end, Two* x) {
+  float pv[4], qv[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool in = v + j < end;
+    pv[j] = in ? as_float(r.p[v + j]) : 0.f;
+    qv[j] = in && r.mode != kOnlyP ? as_float(r.q[v + j]) : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[j] = r.mode == kOnlyP ? Two{clean(pv[j]), 0.f} : weight_of(pv[j], qv[j], r.ch, r.cl);
+    if (r.num_gone && r.is_gone(v + j + r.off)) x[j] = {0.f, 0.f};
+  }
+}
+
+__device__ __forceinline__ void copy_async(uint4* to, const uint4* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+               "l"(from)
+               : "memory");
+}
+// The largest bits of `worst` and a piece, and whether they are of a value that is
+// negative, infinite or NaN (those have the largest): one operation for two values
+template <typename T>
+__device__ __forceinline__ uint32_t worst_of(uint32_t worst, uint4 w) {
+  if constexpr (std::is_same_v<T, float>)
+    return __vimax3_u32(__vimax3_u32(worst, w.x, w.y), w.z, w.w);
+  else
+    return __vimax3_u16x2(__vimax3_u16x2(worst, w.x, w.y), w.z, w.w);
+}
+template <typename T>
+__device__ __forceinline__ bool no_probability(uint32_t worst) {
+  if constexpr (std::is_same_v<T, float>) return worst >= 0x7f800000u;
+  constexpr uint32_t kInf = std::is_same_v<T, __half> ? 0x7c00u : 0x7f80u;
+  return (worst >> 16) >= kInf || (worst & 0xffffu) >= kInf;
 }
 
 // Sum of the weights of tokens [a, b) over the lanes of a warp, each holding its
-// part.  `off`: element of its 16 bytes at which row p (and q) begins, or < 0
-// when p and q begin at different ones and are read value by value.
-template <typename T, bool kDraft>
-__device__ __forceinline__ Two lane_sum(const Row<T, kDraft>& r, int64_t a, int64_t b, int off, int lane) {
-  constexpr int N = Vec<T>::N, kAhead = 4;
+// part.  `off`: element of its 16 bytes at which row p (and q) begins, or < 0 when
+// p and q begin at different ones and are read value by value.
+//
+// p and q are taken as they stand, and their bits' maximum tells whether one of
+// them was negative, infinite or NaN (1 operation a value where setting those to 0
+// takes 2): then the part is summed again value by value.  max(p, q) - q instead of
+// max(p - q, 0) leaves no error to be cleared.
+template <typename T, int kMode, int kRing>
+__device__ __forceinline__ Two lane_sum(const Row<T>& r, int64_t a, int64_t b, int off, int lane,
+                                        uint4* ring) {
+  constexpr int N = Vec<T>::N;
   Two acc = {0.f, 0.f};
-  bool some_gone = false;
-  if constexpr (!kDraft) {  // a few parts of the row hold refused tokens
-    bool mine = false;
-    for (int i = lane; i < r.num_gone; i += 32) mine |= r.gone[i] >= a && r.gone[i] < b;
-    some_gone = __any_sync(0xffffffffu, mine);
-  }
-  if (off >= 0 && !some_gone) {
-    // whole 16-byte pieces, counted from the one that holds the row's first value
+  uint32_t worst = 0;  // of 16-bit types: of both halves
+  auto take = [&](float pv, float qv) {
+    if constexpr (kMode == kOnlyP) {
+      accumulate(acc, pv);
+    } else {
+      float t = qv, lo = 0.f;
+      if constexpr (kMode == kLessCQ) {
+        t = __fmul_rn(r.ch, qv);
+        lo = __fmaf_rn(r.cl, qv, __fmaf_rn(r.ch, qv, -t));
+      }
+      const float m = fmaxf(pv, t), w = __fsub_rn(m, t);
+      float e = __fsub_rn(__fsub_rn(m, w), t);
+      if constexpr (kMode == kLessCQ) e = w > 0.f ? __fsub_rn(e, lo) : 0.f;
+      accumulate(acc, w);
+      acc.l = __fadd_rn(acc.l, e);
+    }
+  };
+  int64_t head = b, tail = b;  // [a, head) and [tail, b) are read value by value
+  if (off >= 0) {
+    // whole 16-byte pieces, counted from the one that holds the row's first value.
+    // A thread copies its own to shared memory, kDepth of them ahead of the one it
+    // adds up: in registers, four pieces of p and q ahead left the SM waiting for
+    // memory between rounds.
+    constexpr int kDepth = kMode == kOnlyP ? kRing : kRing / 2;
     const int64_t first = (a + off + N - 1) / N, last = (b + off) / N;  // inside [a, b)
-    const uint4* pv = reinterpret_cast<const uint4*>(r.p - off);
-    const uint4* qv = kDraft ? reinterpret_cast<const uint4*>(r.q - off) : nullptr;
-    for (int64_t k = first + lane; k < last; k += 32 * kAhead) {
-      uint4 wp[kAhead], wq[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const bool in = k + 32 * j < last;
-        wp[j] = in ? __ldg(pv + k + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
-        if (kDraft) wq[j] = in ? __ldg(qv + k + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+    head = min(first * N - off, b);
+    tail = max(last * N - off, head);
+    const int count = static_cast<int>(max(last - first, static_cast<int64_t>(0)));
+    const uint4* pv = reinterpret_cast<const uint4*>(r.p - off) + first + lane;
+    const uint4* qv = kMode == kOnlyP ? nullptr : reinterpret_cast<const uint4*>(r.q - off) + first + lane;
+    uint4* const slot = ring + threadIdx.x;
+    int ahead = lane;  // the piece to be fetched next
+    auto fetch = [&](int at) {
+      if (ahead < count) {
+        copy_async(slot + at * kThreads, pv);
+        if (kMode != kOnlyP) copy_async(slot + (kDepth + at) * kThreads, qv);
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ahead += 32;
+      pv += 32;
+      if (kMode != kOnlyP) qv += 32;
+    };
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
+    for (int j = 0; j < kDepth - 1; ++j) fetch(j);
+    for (int k = lane; k < count;) {
+#pragma unroll
+      for (int at = 0; at < kDepth; ++at) {  // the slots in turn
+        if (k >= count) break;
+        fetch((at + kDepth - 1) % kDepth);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+        const uint4 wp = slot[at * kThreads];
+        uint4 wq = make_uint4(0u, 0u, 0u, 0u);
+        if (kMode != kOnlyP) wq = slot[(kDepth + at) * kThreads];
+        worst = worst_of<T>(worst, wp);
+        if (kMode != kOnlyP) worst = worst_of<T>(worst, wq);
         float x[N], y[N];
-        unpack<T>(wp[j], x);
-        if (kDraft) unpack<T>(wq[j], y);
+        unpack<T>(wp, x);
+        if (kMode != kOnlyP) unpack<T>(wq, y);
+        if (kMode == kOnlyP && r.num_gone) {
+          const int64_t place = (first + k) * N;  // of the piece's first value, N bits of one word
+          const uint32_t f = static_cast<uint32_t>(place) % kGoneBits;
+          if (r.bitmap[f >> 5] >> (f & 31) & ((1u << N) - 1u)) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) accumulate(acc, r.weight(x[i], kDraft ? y[i] : 0.f));
+            for (int i = 0; i < N; ++i)
+              if (r.is_gone(place + i)) x[i] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) take(x[i], kMode == kOnlyP ? 0.f : y[i]);
+        k += 32;
       }
-    }
-    // the values before and behind the whole pieces
-    const int64_t head = first * N - off < b ? first * N - off : b;
-    const int64_t tail = last * N - off > head ? last * N - off : head;
-    for (int64_t v = a + lane; v < head; v += 32) accumulate(acc, r.at(static_cast<int>(v)));
-    for (int64_t v = tail + lane; v < b; v += 32) accumulate(acc, r.at(static_cast<int>(v)));
-  } else {
-    for (int64_t v = a + lane; v < b; v += 32 * kAhead) {
-      float x[kAhead], y[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const bool in = v + 32 * j < b;
-        x[j] = in ? as_float(r.p[v + 32 * j]) : 0.f;
-        y[j] = kDraft && in ? as_float(r.q[v + 32 * j]) : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (kDraft || !some_gone || !r.is_gone(static_cast<int>(v + 32 * j)))
-          accumulate(acc, r.weight(x[j], y[j]));
     }
   }
-  return normal(acc.h, acc.l);
+  bool odd = no_probability<T>(worst);
+#pragma unroll 1
+  for (int64_t v = a + lane; v < b; v += 32) {
+    if (v >= head && v < tail) {  // on to the first of this lane's that is behind the pieces
+      v += (tail - v + 31) / 32 * 32;
+      if (v >= b) break;
+    }
+    if (kMode == kOnlyP && r.num_gone && r.is_gone(v + r.off)) continue;
+    const float x = as_float(r.p[v]), y = kMode == kOnlyP ? 0.f : as_float(r.q[v]);
+    odd |= __float_as_uint(x) >= 0x7f800000u || __float_as_uint(y) >= 0x7f800000u;
+    take(x, y);
+  }
+  if (__any_sync(0xffffffffu, odd)) {  // by all lanes, which share the part anew
+    acc = {0.f, 0.f};
+#pragma unroll 1
+    for (int64_t v = a + lane; v < b; v += 32) {
+      const Two w = weight_at(r, static_cast<int>(v));
+      accumulate(acc, w.h);
+      acc.l = __fadd_rn(acc.l, w.l);
+    }
+  }
+  return acc;
 }
 
-__device__ __forceinline__ Two warp_sum(Two a) {
+// Sum over groups of kLanes lanes, the same bits in all of them
+template <int kLanes>
+__device__ __forceinline__ Two lanes_sum(Two a) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Two b = {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
-    // the same order of operands on both sides: one result in all lanes
-    a = (threadIdx.x & o) ? add(b, a) : add(a, b);
-  }
+  for (int o = kLanes / 2; o > 0; o >>= 1)  // two_sum and + do not depend on the operands' order
+    a = add(a, {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)});
   return a;
 }
-__device__ __forceinline__ Two warp_scan(Two a, int lane) {  // inclusive
+// Inclusive prefix sums over groups of kLanes lanes
+template <int kLanes>
+__device__ __forceinline__ Two lanes_scan(Two a, int lane) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const Two b = {__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
-    if (lane >= o) a = add(b, a);
+  for (int o = 1; o < kLanes; o <<= 1) {
+    const Two b = {__shfl_up_sync(0xffffffffu, a.h, o, kLanes), __shfl_up_sync(0xffffffffu, a.l, o, kLanes)};
+    if ((lane & (kLanes - 1)) >= o) a = add(b, a);
   }
   return a;
 }
@@ -240,8 +352,11 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 // store two fp32 at the place of `local` in the shared memory of CTA `rank`
 __device__ __forceinline__ void store_remote(const Two* local, uint32_t rank, Two x) {
@@ -252,89 +367,97 @@ __device__ __forceinline__ void store_remote(const Two* local, uint32_t rank, Tw
       : "memory");
 }
 
+template <bool kDraft>
 struct Shared {
-  Two sums[2][kMaxCluster * kWarps];  // of the row's parts, two calls' worth
-  float pt[kMaxNodes], qt[kMaxNodes], u[kMaxNodes];
+  static constexpr int kRing = kDraft ? kSlots : kSlotsGiven;
+  uint4 ring[kRing * kThreads];
+  uint32_t bitmap[kDraft ? 4 : kGoneBits / 32];
+  Two sums[2][kMaxCluster];  // of the CTAs' parts of the row, two passes' worth
+  Two part[kWarps];          // of this CTA's warps'
+  float pt[kMaxNodes], u[kMaxNodes];
+  union {
+    float qt[kMaxNodes];      // with q
+    int32_t gone[kMaxNodes];  // without
+  };
   int32_t tok[kMaxNodes];
   int16_t par[kMaxNodes];
-  int32_t gone[kMaxNodes];
+  bool first_ok[kMaxNodes];  // accepted if it is the first that is tried under its parent
   int32_t num_gone;
-  // the walk's state
-  int32_t cur, next, kept;
-  int32_t need;    // another node waits for N
-  int32_t refused;  // a node under cur was refused since N
-  double c, N;
-  // the place where the prefix sum passes
+  // the pass that is asked for: row, c, and whether the walk is over
+  int32_t cur, kept, over;
+  Two c;
+  // the part in which the prefix sum passes (-1: none of this CTA's), the sum before
+  // it, and what its threads found
+  int32_t in, last, hit;
+  Two start, aim;
   Two scan[kWarps];
-  int32_t last, hit;
 };
 
-// The walk from where it stands until it ends or needs a sum; one warp.  `out`
-// and `path` are written where `lead` (one CTA of the cluster).
+// Where a walk stands; the same in all lanes of the warp that walks
+struct Walk {
+  int cur = 0, next = 1, kept = 1;
+  double c = 0.0, N = 1.0;
+  bool refused = false;  // a node under cur was refused (with q: since N)
+};
+
+// On until the walk ends (true) or needs N of what is left (false).  `out` and
+// `path` are written where `lead` (one CTA of the cluster).
 template <bool kDraft>
-__device__ __forceinline__ void walk(Shared& sh, const VerifyArgs& p, int r0, int n, bool lead, int lane) {
-  int cur = sh.cur, i = sh.next, kept = sh.kept;
-  double c = sh.c, N = sh.N;
-  bool refused = sh.refused;
-  int need = 0;
-  while (true) {
-    int found = -1;
-    for (int b = i; b < n && found < 0; b += 32) {
-      const unsigned m = __ballot_sync(0xffffffffu, b + lane < n && sh.par[b + lane] == cur);
-      if (m) found = b + __ffs(m) - 1;
-    }
-    if (found < 0) break;
-    i = found;
-    const double pv = sh.pt[i], u = sh.u[i];
-    const int tok = sh.tok[i];
-    bool ok, again = false;
-    if constexpr (kDraft) {
-      if (refused) {  // N of the new residual first
-        need = 1;
-        break;
+__device__ __forceinline__ bool walk(Walk& w, const Shared<kDraft>& sh, const VerifyArgs& p, int r0, int n, bool lead,
+                                     int lane) {
+#pragma unroll 1
+  for (int base = w.next & ~31; base < n; base += 32) {
+    const int par = base + lane < n ? sh.par[base + lane] : -1;
+    const unsigned first_ok = __ballot_sync(0xffffffffu, base + lane < n && sh.first_ok[base + lane]);
+#pragma unroll 1
+    while (true) {
+      const int from = w.next - base;
+      const unsigned m = __ballot_sync(0xffffffffu, par == w.cur) & (from < 32 ? ~0u << from : 0u);
+      if (!m) break;
+      const int i = base + __ffs(m) - 1;
+      const int tok = sh.tok[i];
+      bool ok, again = false;
+      if (kDraft && w.refused) return false;  // N of the new residual first
+      if (kDraft ? w.c == 0.0 : !w.refused) {
+        ok = first_ok >> (i & 31) & 1u;
+      } else if constexpr (kDraft) {
+        const double qv = sh.qt[i];
+        ok = __dmul_rn(__dmul_rn(sh.u[i], w.N), qv) < __dsub_rn(sh.pt[i], __dmul_rn(w.c, qv));
+      } else {
+        // a token that was already refused under this node has no weight left
+        for (int b = w.cur + 1; b < i; b += 32)
+          again |= b + lane < i && sh.par[b + lane] == w.cur && sh.tok[b + lane] == tok;
+        again = __any_sync(0xffffffffu, again);
+        ok = !again && __dmul_rn(sh.u[i], w.N) < sh.pt[i];
       }
-      const double qv = sh.qt[i];
-      ok = __dmul_rn(__dmul_rn(u, N), qv) < __dsub_rn(pv, __dmul_rn(c, qv));
-    } else {
-      // a token that was already refused under this node has no weight left
-      if (refused)
-        for (int b = cur + 1; b < i; b += 32)
-          again |= b + lane < i && sh.par[b + lane] == cur && sh.tok[b + lane] == tok;
-      again = __any_sync(0xffffffffu, again);
-      ok = !again && __dmul_rn(u, N) < pv;
-    }
-    if (ok) {
-      if (lead && lane == 0) {
-        p.path[r0 + kept] = i;
-        p.out[r0 + kept - 1] = tok;
+      w.next = i + 1;
+      w.refused = !ok;
+      if (ok) {
+        if (lead && lane == 0) {
+          p.path[r0 + w.kept] = i;
+          p.out[r0 + w.kept - 1] = tok;
+        }
+        ++w.kept;
+        w.cur = i;
+        w.c = 0.0;
+        w.N = 1.0;
+      } else if (kDraft) {
+        w.c += w.N;
+      } else if (!again) {
+        const double pv = sh.pt[i];
+        w.N = w.N > pv ? w.N - pv : 0.0;
       }
-      ++kept;
-      cur = i;
-      c = 0.0;
-      N = 1.0;
-      refused = false;
-    } else {
-      if (kDraft) c += N;
-      else if (!again) N = N > pv ? N - pv : 0.0;
-      refused = true;
     }
-    ++i;
+    w.next = max(w.next, base + 32);
   }
-  __syncwarp();
-  if (lane == 0) {
-    sh.cur = cur;
-    sh.next = i;
-    sh.kept = kept;
-    sh.c = c;
-    sh.N = N;
-    sh.refused = refused;
-    sh.need = need;
-  }
+  return true;
 }
 
 template <typename T, bool kDraft>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs p) {
-  __shared__ Shared sh;
+__global__ void __launch_bounds__(kThreads, kPerSM) verify_kernel(const VerifyArgs p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using Sh = Shared<kDraft>;
+  Sh& sh = *reinterpret_cast<Sh*>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int s = blockIdx.x / C;
@@ -347,13 +470,17 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs p)
     }
     return;
   }
+  const float u_last = p.u_last[s];
+  if (C > 1) cluster_arrive();  // this CTA runs; waited for before the first remote write
   const T* const P = static_cast<const T*>(p.target);
   const T* const Q = static_cast<const T*>(p.draft);
   // every node's token under its parent's rows
   int bad = 0;
+#pragma unroll 1
   for (int i = tid; i < n; i += kThreads) {
     const int t = p.tokens[r0 + i];
     int a = i == 0 ? -1 : p.parents ? p.parents[r0 + i] : i - 1;
+    const float u = p.u[r0 + i];
     if (a >= i && i > 0) {
       bad |= MCP_DEVERR_TREE;
       a = -1;
@@ -368,82 +495,120 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs p)
     sh.par[i] = static_cast<int16_t>(a < 0 ? -1 : a);
     sh.tok[i] = t;
     sh.pt[i] = pv;
-    sh.qt[i] = qv;
-    sh.u[i] = p.u[r0 + i];
+    if (kDraft) sh.qt[i] = qv;
+    sh.u[i] = u;
+    // u q < p: the product's error decides where it rounds to p
+    const float uq = kDraft ? __fmul_rn(u, qv) : u;
+    sh.first_ok[i] = uq < pv || (kDraft && uq == pv && __fmaf_rn(u, qv, -uq) < 0.f);
   }
   if (lead && bad && p.err) atomicOr(p.err, bad);
   if (tid == 0) {
-    sh.cur = 0;
-    sh.next = 1;
-    sh.kept = 1;
-    sh.c = 0.0;
-    sh.N = 1.0;
-    sh.refused = 0;
     sh.num_gone = 0;
     if (lead) p.path[r0] = 0;
   }
-  // every CTA of the cluster runs before another writes to its shared memory
-  if (C == 1) __syncthreads();
-  else cluster_sync();
+  __syncthreads();
 
-  // the part of a row that this warp sums: pieces of 32 bytes and more
-  const int parts = C * kWarps;
-  const int64_t per = ((static_cast<int64_t>(p.V) + parts - 1) / parts + 15) / 16 * 16;
-  const int part = rank * kWarps + warp;
-  const int64_t a = per * part < p.V ? per * part : p.V, b = a + per < p.V ? a + per : p.V;
-  int calls = 0;
-  Row<T, kDraft> row;
-  int off = 0;
-  // sum of the weights of row `cur`, in all CTAs; the parts' sums are in sh.sums[calls & 1]
-  auto pass = [&](int cur, double c) -> Two {
-    row.p = P + (r0 + cur) * p.ldp;
-    row.q = kDraft ? Q + (r0 + cur) * p.ldq : nullptr;
-    const Two cc = two_of(c);
-    row.ch = cc.h;
-    row.cl = cc.l;
-    const int op = static_cast<int>((reinterpret_cast<uintptr_t>(row.p) & 15) / sizeof(T));
-    const int oq = static_cast<int>((reinterpret_cast<uintptr_t>(row.q) & 15) / sizeof(T));
-    off = !kDraft || op == oq ? op : -1;
-    const Two mine = warp_sum(lane_sum<T, kDraft>(row, a, b, off, lane));
-    Two* sums = sh.sums[++calls & 1];
-    if (C == 1) {
-      if (lane == 0) sums[part] = mine;
-      __syncthreads();
-    } else {
-      if (lane < C) store_remote(sums + part, lane, mine);
-      cluster_sync();
-    }
-    Two t = {0.f, 0.f};
-    for (int k = lane; k < parts; k += 32) t = add(t, sums[k]);
-    return warp_sum(t);
+  // A row is cut into parts of whole 16-byte pieces, counted from the piece that holds
+  // its first value (`off` values before that one): a warp's part ends inside a piece
+  // only where the row does
+  const int64_t per = ((static_cast<int64_t>(p.V) + 16 + C * kWarps - 1) / (C * kWarps) + 15) / 16 * 16;
+  auto begin_of = [&](int64_t part, int off) {
+    return min(max(per * part - max(off, 0), static_cast<int64_t>(0)), static_cast<int64_t>(p.V));
   };
-
+  Row<T> row;
   row.gone = sh.gone;
   row.num_gone = 0;
+  row.bitmap = sh.bitmap;
+  row.folded = static_cast<int64_t>(p.V) + 16 > kGoneBits;
+  Walk w;
+  bool over = false;
+  Two total;
+  int passes = 0, off = 0;
+  // Warp 0 walks and says which row is to be summed; all warps sum; until the walk is
+  // over and something remains where it ended.
   while (true) {
-    if (warp == 0) walk<kDraft>(sh, p, r0, n, lead, lane);
-    __syncthreads();
-    if (!kDraft || !sh.need) break;
-    const Two t = pass(sh.cur, sh.c);
-    __syncthreads();  // everybody has read the walk's state
-    if (tid == 0) {
-      sh.N = wide(t);
-      sh.refused = 0;
+    if (warp == 0) {
+      if (!over) over = walk<kDraft>(w, sh, p, r0, n, lead, lane);
+      if (lane == 0) {
+        sh.cur = w.cur;
+        sh.kept = w.kept;
+        sh.c = two_of(w.c);
+        sh.over = over;
+      }
     }
     __syncthreads();
-  }
-  const int cur = sh.cur, kept = sh.kept;
-  if constexpr (!kDraft) {  // the refused tokens: all that hang under the last node
-    for (int i = tid; i < n; i += kThreads)
-      if (sh.par[i] == cur) sh.gone[atomicAdd(&sh.num_gone, 1)] = sh.tok[i];
+    const int cur = sh.cur;
+    const Two c = sh.c;
+    over = sh.over;
+    row.p = P + (r0 + cur) * p.ldp;
+    row.q = kDraft ? Q + (r0 + cur) * p.ldq : nullptr;
+    row.mode = !kDraft || c.h == 0.f ? kOnlyP : c.h == 1.f && c.l == 0.f ? kLessQ : kLessCQ;
+    row.ch = c.h;
+    row.cl = c.l;
+    const int op = static_cast<int>((reinterpret_cast<uintptr_t>(row.p) & 15) / sizeof(T));
+    if constexpr (!kDraft) {
+      if (passes == 0) {  // the refused tokens: all that hang under the last node
+        for (int i = tid; i < kGoneBits / 128; i += kThreads)
+          reinterpret_cast<uint4*>(sh.bitmap)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads)
+          if (sh.par[i] == cur) {
+            sh.gone[atomicAdd(&sh.num_gone, 1)] = sh.tok[i];
+            const uint32_t f = static_cast<uint32_t>(sh.tok[i] + op) % kGoneBits;
+            atomicOr(&sh.bitmap[f >> 5], 1u << (f & 31));
+          }
+        __syncthreads();
+        row.num_gone = sh.num_gone;
+      } else {
+        row.num_gone = 0;  // nothing remained: the target's row itself
+      }
+    }
+    off = op;
+    if (kDraft && row.mode != kOnlyP && op != static_cast<int>((reinterpret_cast<uintptr_t>(row.q) & 15) / sizeof(T)))
+      off = -1;
+    row.off = op;
+    const int64_t a = begin_of(rank * kWarps + warp, off), b = begin_of(rank * kWarps + warp + 1, off);
+    Two mine;
+    if constexpr (kDraft) {
+      mine = row.mode == kOnlyP ? lane_sum<T, kOnlyP, Sh::kRing>(row, a, b, off, lane, sh.ring)
+             : row.mode == kLessQ ? lane_sum<T, kLessQ, Sh::kRing>(row, a, b, off, lane, sh.ring)
+                                  : lane_sum<T, kLessCQ, Sh::kRing>(row, a, b, off, lane, sh.ring);
+    } else {
+      mine = lane_sum<T, kOnlyP, Sh::kRing>(row, a, b, off, lane, sh.ring);
+    }
+    mine = lanes_sum<32>(mine);
+    if (lane == 0) sh.part[warp] = normal(mine);
     __syncthreads();
-    row.num_gone = sh.num_gone;
+    // the CTA's sum to every CTA of the cluster, all of which run by now (the first
+    // wait); two passes' sums are kept, so that no CTA writes what another still reads
+    Two* sums = sh.sums[passes & 1];
+    if (C > 1 && passes == 0) cluster_wait();
+    if (warp == 0) {
+      const Two all = normal(lanes_sum<kWarps>(sh.part[lane & (kWarps - 1)]));
+      if (C == 1) {
+        if (lane == 0) sums[0] = all;
+      } else if (lane < C) {
+        store_remote(sums + rank, lane, all);
+      }
+    }
+    if (C == 1) {
+      __syncthreads();
+    } else {
+      cluster_arrive();
+      cluster_wait();
+    }
+    ++passes;
+    const int k = lane & (kMaxCluster - 1);
+    total = normal(lanes_sum<kMaxCluster>(k < C ? sums[k] : Two{0.f, 0.f}));
+    if (!over) {
+      w.N = wide(total);
+      w.refused = false;
+    } else {
+      if (total.h > 0.f || (row.mode == kOnlyP && row.num_gone == 0)) break;
+      w.c = 0.0;  // nothing remains: the target's row itself
+    }
   }
-  Two total = pass(cur, sh.c);
-  if (!(total.h > 0.f)) {  // nothing remains: the target's row itself
-    row.num_gone = 0;
-    total = pass(cur, 0.0);
-  }
+  const int kept = sh.kept;
   if (lead) {  // places behind the path
     for (int i = kept + tid; i < n; i += kThreads) {
       p.path[r0 + i] = -1;
@@ -459,55 +624,69 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs p)
     }
     return;
   }
-  // the part in which the prefix sum passes u * total (every warp for itself): the
-  // first whose end is above it, else the last that holds anything
-  const Two aim = two_of(static_cast<double>(p.u_last[s]) * wide(total));
-  const Two* sums = sh.sums[calls & 1];
-  int in = -1, last = 0;
-  Two before = {0.f, 0.f}, at_last = {0.f, 0.f};
-  for (int k0 = 0; k0 < parts && in < 0; k0 += 32) {
-    const int k = k0 + lane;
-    const Two x = k < parts ? sums[k] : Two{0.f, 0.f};
-    const Two incl = add(before, warp_scan(x, lane));
-    const unsigned m = __ballot_sync(0xffffffffu, x.h > 0.f && above(incl, aim));
-    const unsigned some = __ballot_sync(0xffffffffu, x.h > 0.f);
-    const int at = m ? __ffs(m) - 1 : some ? 31 - __clz(some) : -1;
-    if (at >= 0) {  // the sum before part `at`
-      const Two up = {__shfl_sync(0xffffffffu, incl.h, at ? at - 1 : 0),
-                      __shfl_sync(0xffffffffu, incl.l, at ? at - 1 : 0)};
-      at_last = at ? up : before;
-      last = k0 + at;
+  if (warp == 0) {
+    // the part in which the prefix sum passes u * total: the first whose end is above
+    // it, else the last that holds anything
+    const float aim_h = __fmul_rn(u_last, total.h);
+    const Two aim = normal({aim_h, __fmaf_rn(u_last, total.l, __fmaf_rn(u_last, total.h, -aim_h))});
+    Two start = {0.f, 0.f};
+    int in = -1;
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {  // among the CTAs, then among this one's warps
+      const Two* of = level ? sh.part : sh.sums[(passes - 1) & 1];
+      const Two x = lane < (level ? kWarps : C) ? of[lane] : Two{0.f, 0.f};
+      const Two incl = normal(add(start, lanes_scan<16>(x, lane)));
+      const unsigned m = __ballot_sync(0xffffffffu, x.h > 0.f && above(incl, aim));
+      const unsigned some = __ballot_sync(0xffffffffu, x.h > 0.f);
+      in = m ? __ffs(m) - 1 : some ? 31 - __clz(some) : 0;
+      const Two up = {__shfl_sync(0xffffffffu, incl.h, in ? in - 1 : 0),
+                      __shfl_sync(0xffffffffu, incl.l, in ? in - 1 : 0)};
+      if (in) start = up;
+      if (level == 0 && in != rank) {
+        in = -1;
+        break;
+      }
     }
-    if (m) in = last;
-    before = {__shfl_sync(0xffffffffu, incl.h, 31), __shfl_sync(0xffffffffu, incl.l, 31)};
+    if (lane == 0) {
+      sh.in = in;
+      sh.start = start;
+      sh.aim = aim;
+      sh.last = -1;
+      sh.hit = 0x7fffffff;
+    }
   }
-  if (in < 0) in = last;
-  if (in / kWarps != rank) return;
+  __syncthreads();
+  if (sh.in < 0) return;
   // this CTA's threads take a piece of the part each, in order
-  const int64_t a1 = per * in, b1 = a1 + per < p.V ? a1 + per : p.V;
+  const Two aim = sh.aim;
+  const int64_t a1 = begin_of(rank * kWarps + sh.in, off), b1 = begin_of(rank * kWarps + sh.in + 1, off);
   const int64_t each = (per + kThreads - 1) / kThreads;
-  const int64_t v0 = a1 + each * tid < b1 ? a1 + each * tid : b1, v1 = v0 + each < b1 ? v0 + each : b1;
-  if (tid == 0) {
-    sh.last = -1;
-    sh.hit = 0x7fffffff;
-  }
+  const int64_t v0 = min(a1 + each * tid, b1), v1 = min(v0 + each, b1);
   Two mine = {0.f, 0.f};
   int32_t positive = -1;
-  for (int64_t v = v0; v < v1; ++v) {
-    const Two w = row.at(static_cast<int>(v));
-    if (w.h > 0.f) positive = static_cast<int32_t>(v);
-    accumulate(mine, w);
+#pragma unroll 1
+  for (int64_t v = v0; v < v1; v += 4) {
+    Two x[4];
+    weights_at(row, v, v1, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (x[j].h > 0.f) positive = static_cast<int32_t>(v) + j;
+      accumulate(mine, x[j].h);
+      mine.l = __fadd_rn(mine.l, x[j].l);
+    }
   }
-  mine = normal(mine.h, mine.l);
-  const Two inside = warp_scan(mine, lane);
+  const Two inside = lanes_scan<32>(mine, lane);
   const Two ahead = {__shfl_up_sync(0xffffffffu, inside.h, 1), __shfl_up_sync(0xffffffffu, inside.l, 1)};
   if (lane == 31) sh.scan[warp] = inside;
   __syncthreads();
-  Two base = at_last;
-  for (int w = 0; w < warp; ++w) base = add(base, sh.scan[w]);
-  const bool passes = positive >= 0 && above(add(base, inside), aim);
-  if (passes) atomicMin(&sh.hit, tid);
-  if (positive >= 0) atomicMax(&sh.last, positive);
+  const Two warps = lanes_scan<kWarps>(sh.scan[lane & (kWarps - 1)], lane);
+  const Two up = {__shfl_sync(0xffffffffu, warps.h, warp ? warp - 1 : 0),
+                  __shfl_sync(0xffffffffu, warps.l, warp ? warp - 1 : 0)};
+  const Two base = warp ? add(sh.start, up) : sh.start;
+  if (positive >= 0) {
+    if (above(normal(add(base, inside)), aim)) atomicMin(&sh.hit, tid);
+    atomicMax(&sh.last, positive);
+  }
   __syncthreads();
   if (sh.hit == 0x7fffffff) {  // u = 1, or the sums' last bits
     if (tid == 0) *answer = sh.last;
@@ -515,42 +694,68 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs p)
   }
   if (sh.hit != tid) return;
   Two run = lane ? add(base, ahead) : base;
-  int32_t found = positive;
-  for (int64_t v = v0; v < v1; ++v) {
-    const Two w = row.at(static_cast<int>(v));
-    run = add(run, w);
-    if (w.h > 0.f && above(run, aim)) {
-      found = static_cast<int32_t>(v);
-      break;
+  int32_t found = -1;
+#pragma unroll 1
+  for (int64_t v = v0; v < v1 && found < 0; v += 4) {
+    Two x[4];
+    weights_at(row, v, v1, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      run = add(run, x[j]);
+      if (found < 0 && x[j].h > 0.f && above(normal(run), aim)) found = static_cast<int32_t>(v) + j;
     }
   }
-  *answer = found;
+  *answer = found >= 0 ? found : positive;
 }
 
-// CTAs that share a segment: as many as the GPU has room for at once (two a SM),
-// but none with less than 4096 values of a row.
+// CTAs that share a segment: as many as the GPU has room for at once, but none with
+// less than 4096 values of a row.
 int cluster_of(const mcp_verify_desc& d) {
   int c = kMaxCluster;
-  while (c > 1 && (static_cast<int64_t>(d.num_seqs) * c > 2LL * step_num_sms() || d.vocab_size / c < 4096))
+  while (c > 1 && (static_cast<int64_t>(d.num_seqs) * c > kPerSM * static_cast<int64_t>(step_num_sms()) || d.vocab_size / c < 4096))
     c /= 2;
   return c;
 }
 
-template <typename T>
+// Clusters of more than 8 CTAs have to be asked for, once per kernel and device.
+template <auto kernel>
+int allow_large_clusters() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return 0;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return static_cast<int>(e);
+}
+
+template <typename T, bool kDraft>
 int launch_typed(const mcp_verify_desc& d, const VerifyArgs& a, void* stream) {
-  cudaLaunchAttribute at = {};
+  int e = allow_smem<verify_kernel<T, kDraft>>(sizeof(Shared<kDraft>));
+  if (e != 0) return e;
   const int c = cluster_of(d);
+  if (c > 8) {
+    e = allow_large_clusters<verify_kernel<T, kDraft>>();
+    if (e != 0) return e;
+  }
+  cudaLaunchAttribute at = {};
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = static_cast<unsigned>(c);
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(d.num_seqs * c));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared<kDraft>);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return static_cast<int>(a.draft ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true>, a)
-                                  : cudaLaunchKernelEx(&cfg, verify_kernel<T, false>, a));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, verify_kernel<T, kDraft>, a));
+}
+
+template <typename T>
+int launch_either(const mcp_verify_desc& d, const VerifyArgs& a, void* stream) {
+  return a.draft ? launch_typed<T, true>(d, a, stream) : launch_typed<T, false>(d, a, stream);
 }
 
 }  // namespace
@@ -574,9 +779,9 @@ int launch_verify_drafts(const mcp_verify_desc& d, const mcp_verify_tensors& t, 
   a.S = d.num_seqs;
   a.R = d.total_rows;
   a.V = d.vocab_size;
-  if (d.dtype == MCP_DTYPE_BF16) return launch_typed<__nv_bfloat16>(d, a, stream);
-  if (d.dtype == MCP_DTYPE_FP16) return launch_typed<__half>(d, a, stream);
-  return launch_typed<float>(d, a, stream);
+  if (d.dtype == MCP_DTYPE_BF16) return launch_either<__nv_bfloat16>(d, a, stream);
+  if (d.dtype == MCP_DTYPE_FP16) return launch_either<__half>(d, a, stream);
+  return launch_either<float>(d, a, stream);
 }
 
 }  // namespace mcp
