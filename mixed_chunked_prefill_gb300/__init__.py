@@ -875,27 +875,31 @@ def verify_drafts(target_probs, tokens, cu_rows, uniform, final_uniform, parents
 
 
 def _layers(caches, name, dev, shape):
-    """(shape of one cache, address of each layer's): one cache [pages, P, H_kv, D], all
-    layers' [layers, pages, P, H_kv, D], or a list of caches."""
+    """(shape of one cache, layers, array of their addresses) of one cache [pages, P, H_kv, D],
+    all layers' [layers, pages, P, H_kv, D], or a list of caches."""
     import torch
 
     bf16 = torch.bfloat16
     if isinstance(caches, torch.Tensor):
-        if caches.dim() == 4:
+        if caches.dim() == 5:
+            full = caches.shape
+            one = full[1:]
+            if full[0] and (shape is None or one == shape) and caches.is_contiguous():
+                step = caches.stride(0) * 2
+                base = _arg(caches, bf16, name, dev)
+                return one, full[0], np.arange(base, base + step * full[0], step or 1, dtype=np.uint64)
+        elif caches.dim() == 4:
             caches = (caches,)
-        elif caches.dim() != 5:
+        else:
             raise ValueError(f"{name} must be caches [pages, P, H_kv, D] of one or all layers")
-        elif caches.is_contiguous() and caches.shape[0] and (shape is None or caches.shape[1:] == shape):
-            shape = caches.shape[1:]
-            base, step = _arg(caches, bf16, name, dev), shape.numel() * 2
-            return shape, [base + layer * step for layer in range(caches.shape[0])]
     caches = tuple(caches)
     if shape is None and caches:
         _gpu(caches[0], name)
         shape = caches[0].shape
         if len(shape) != 4:
             raise ValueError(f"{name} must be caches [pages, P, H_kv, D]")
-    return shape, [_arg(c, bf16, name, dev, shape) for c in caches]
+    return shape, len(caches), np.array([_arg(c, bf16, name, dev, shape) for c in caches],
+                                        dtype=np.uint64)
 
 
 def kv_keep_path(k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k, accepted, path,
@@ -909,13 +913,13 @@ def kv_keep_path(k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k, acce
     import torch
 
     dev, i32 = _gpu(accepted, "accepted"), torch.int32
-    shape, ks = _layers(k_caches, "k_caches", dev, None)
-    _, vs = _layers(v_caches, "v_caches", dev, shape)
-    if not ks or len(ks) != len(vs):
+    shape, L, ks = _layers(k_caches, "k_caches", dev, None)
+    _, more, vs = _layers(v_caches, "v_caches", dev, shape)
+    if not L or L != more:
         raise ValueError("k_caches and v_caches must have the same layers, one at least")
     if accepted.dim() != 1 or path.dim() != 1 or block_tables.dim() != 2:
         raise ValueError("accepted must be [S], path [R], block_tables [S, max_pages_per_seq]")
-    S, R, L = accepted.shape[0], path.shape[0], len(ks)
+    S, R = accepted.shape[0], path.shape[0]
     pages, P, H, D = shape
     width = block_tables.shape[1]
     _sizes(S, R, L, pages, P, H, D, width)
@@ -923,9 +927,8 @@ def kv_keep_path(k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k, acce
     if new_lens is None:
         new_lens = _empty(one, i32, accepted.device, stream, result=True)
     desc = _capi.KeepDesc(S, R, L, H, D, P, width, pages)
-    addresses = ctypes.c_void_p * L
     _launch("kv_keep_path", dev, stream, load().mcp_kv_keep_path, ctypes.byref(desc),
-            addresses(*ks), addresses(*vs), _arg(block_tables, i32, "block_tables", dev, (S, width)),
+            ks.ctypes.data, vs.ctypes.data, _arg(block_tables, i32, "block_tables", dev, (S, width)),
             _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),
             _arg(seqlens_k, i32, "seqlens_k", dev, one), _arg(cu_rows, i32, "cu_rows", dev, (S + 1,)),
             _arg(accepted, i32, "accepted", dev, one), _arg(path, i32, "path", dev),

@@ -215,21 +215,32 @@ struct Seg {
   int q_start, lq, lk, hist;
 };
 
+__device__ __forceinline__ Seg segment_of(const KParams& p, int seg) {
+  Seg sg;
+  sg.q_start = p.cu_q[seg];
+  sg.lq = p.cu_q[seg + 1] - sg.q_start;
+  sg.lk = p.cu_k ? p.cu_k[seg + 1] - p.cu_k[seg] : p.seqlens_k[seg];
+  sg.hist = sg.lk - sg.lq;
+  return sg;
+}
+
 // The kernels move KV in boxes of B = 16 tokens (page size 16, 32, 64) or
 // B = 8 tokens (page size 8).  Box `u` of segment `seg` lives in cache page
 // bt[seg][u / (P/B)] at token (u % (P/B)) * B.  box_of packs both as
 // (page << spp_log2) | (u % (P/B)); a block-table entry outside the pool gives
 // page num_pages (an out-of-range TMA coordinate: the copy fills zeros) and an
 // error bit.
-__device__ __forceinline__ int box_of(const KParams& p, int seg, int u) {
-  // non-paged K/V: the box is rows cu_k[seg] + B u ... of one tensor (the
-  // tensor maps then have a single "page" spanning every row)
-  if (p.cu_k) return p.cu_k[seg] + (u << p.box_log2);
-  const int v = p.bt[static_cast<size_t>(seg) * p.max_pages + (u >> p.spp_log2)];
+__device__ __forceinline__ int box_in_page(const KParams& p, int v, int u) {
   const int sub = u & ((1 << p.spp_log2) - 1);
   if (v >= 0 && v < p.num_pages) return (v << p.spp_log2) | sub;
   atomicOr(p.err, MCP_DEVERR_PAGE_RANGE);
   return p.num_pages << p.spp_log2;
+}
+__device__ __forceinline__ int box_of(const KParams& p, int seg, int u) {
+  // non-paged K/V: the box is rows cu_k[seg] + B u ... of one tensor (the
+  // tensor maps then have a single "page" spanning every row)
+  if (p.cu_k) return p.cu_k[seg] + (u << p.box_log2);
+  return box_in_page(p, p.bt[static_cast<size_t>(seg) * p.max_pages + (u >> p.spp_log2)], u);
 }
 // cache page and first token of a packed box
 __device__ __forceinline__ int blk_page(const KParams& p, int b) {
@@ -275,14 +286,42 @@ struct TreeRow {
   }
 };
 
-// True when one of the two bf16 values of `v` is infinite or NaN
-__device__ __forceinline__ bool any_nonfinite(uint32_t v) {
-  return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
-}
+// Of the two bf16 values of `v` those that are finite, 0 for the others
 __device__ __forceinline__ uint32_t only_finite(uint32_t v) {
   if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
   if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
   return v;
+}
+
+// Set the infinities and NaN in rows r0 .. r1 - 1 of a V tile to 0; true (in every
+// lane) when there were any.  A lane takes 16 bytes of every fourth row and keeps the
+// largest magnitude: what is not finite has the largest bits.
+template <int D>
+__device__ __forceinline__ bool take_nonfinite(uint8_t* tile, int r0, int r1, int box_log2, int lane) {
+  constexpr int kHalves = Cfg<D>::kHalves;
+  constexpr uint32_t kMagnitude = 0x7fff7fffu;
+  const int B = 1 << box_log2;
+  uint8_t* const mine = tile + (lane & 7) * 16;
+  auto row = [&](int r, int h) {
+    return reinterpret_cast<uint4*>(mine + (r >> box_log2) * (kHalves * B * 128) + h * B * 128 + (r & (B - 1)) * 128);
+  };
+  uint32_t worst = 0;
+#pragma unroll 4
+  for (int r = r0 + (lane >> 3); r < r1; r += 4)
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const uint4 v = *row(r, h);
+      worst = __vimax3_u16x2(worst, v.x & kMagnitude, v.y & kMagnitude);
+      worst = __vimax3_u16x2(worst, v.z & kMagnitude, v.w & kMagnitude);
+    }
+  if (!__any_sync(0xffffffffu, (worst >> 16) >= 0x7f80u || (worst & 0xffffu) >= 0x7f80u)) return false;
+#pragma unroll 1
+  for (int r = r0 + (lane >> 3); r < r1; r += 4)
+    for (int h = 0; h < kHalves; ++h) {
+      const uint4 v = *row(r, h);
+      *row(r, h) = make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
+    }
+  return true;
 }
 
 // The infinities and NaN that were taken out of the product, added to columns
@@ -312,7 +351,7 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
                                              const KParams& p, uint32_t base, uint8_t* gb,
                                              uint32_t tmem, const CUtensorMap* tm_q,
                                              const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                             int warp, int lane) {
+                                             int warp, int lane, int first_page) {
   using C = Cfg<D>;
   constexpr int kKvTile = C::kKvTile;  // keys per tile (shadows the 128 of the planner)
   const int G = p.G;
@@ -351,13 +390,33 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
     // 16-token box and one box (D/64 KB) apart with 8-token boxes
     const int B = 1 << p.box_log2;
     const uint64_t dV0 = ptx::sdesc_sw128(sV(0), B * 128, B == 16 ? 1024 : C::kHalves * 1024);
+    // first tile that reaches past the history
+    const int t_tree = tree ? max(sg.hist - kv0, 0) / kKvTile : ntiles;
     bool ok = true;
     for (int t = 0; ok && t < ntiles; ++t) {
       // P(t) barriers alternate with the tile parity, like the S buffers: the
       // barrier is reused by tile t + 2 only after Q K^T(t + 2), which waits
       // for this P V(t), so no waiter falls two phases behind
-      if (!(ok = wait_on(c, c.b(BP0 + (t & 1)), (t >> 1) & 1))) break;
       const int s = t % C::kVStages;
+      if constexpr (kTree) {
+        // P is 0 where a row does not see a token of its tree, but 0 * inf is
+        // not: infinities and NaN of the tree's V rows are taken out of the
+        // product and added in the epilogue to the rows that see them.  Done
+        // while the softmax works on this tile (after it, the 32 loads a lane for
+        // 64 tokens of 128 columns stood in front of the item's last product:
+        // 1.6 us an item).
+        if (t >= t_tree) {
+          if (!(ok = wait_on(c, c.b(BV0 + s), (t / C::kVStages) & 1))) break;
+          const int key0 = kv0 + t * kKvTile;
+          if (take_nonfinite<D>(gb + (sV(s) - base), max(sg.hist - key0, 0), min(kv1 - key0, kKvTile),
+                                p.box_log2, lane)) {
+            if (lane == 0) *nonfinite = 1;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+      }
+      if (!(ok = wait_on(c, c.b(BP0 + (t & 1)), (t >> 1) & 1))) break;
       if (!(ok = wait_on(c, c.b(BV0 + s), (t / C::kVStages) & 1))) break;
       const int nval = kv1 - (kv0 + t * kKvTile);
       if (nval < kKvTile && (nval & (B - 1))) {
@@ -375,35 +434,6 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-      }
-      if constexpr (kTree) {
-        // P is 0 where a row does not see a token of its tree, but 0 * inf is
-        // not: infinities and NaN of the tree's V rows are taken out of the
-        // product and added in the epilogue to the rows that see them.  Runs
-        // while the softmax works on this tile; 64 tokens of 128 columns are 32
-        // loads a lane.
-        const int r0 = max(sg.hist - (kv0 + t * kKvTile), 0);
-        const int nr = min(nval, kKvTile) - r0;
-        if (tree && nr > 0) {
-          uint8_t* gV = gb + (sV(s) - base);
-          bool found = false;
-          for (int i = lane; i < nr * 8 * C::kHalves; i += 32) {
-            const int h = i / (nr * 8), rem = i - h * (nr * 8);
-            const int r = r0 + rem / 8, ch = rem & 7;
-            uint4* at = reinterpret_cast<uint4*>(gV + (r >> p.box_log2) * (C::kHalves * B * 128) +
-                                                 h * B * 128 + (r & (B - 1)) * 128 + ch * 16);
-            const uint4 v = *at;
-            if (any_nonfinite(v.x) || any_nonfinite(v.y) || any_nonfinite(v.z) || any_nonfinite(v.w)) {
-              *at = make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
-              found = true;
-            }
-          }
-          if (__any_sync(0xffffffffu, found)) {
-            if (lane == 0) *nonfinite = 1;
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
       }
       ptx::tc_fence_after();
       if (lane == 0) {
@@ -533,7 +563,13 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
         const bool mine = lane < nu && u0 + lane < nbox;
         return mine ? box_of(p, it.seg, (key0 >> kLog) + u0 + lane) : oob_block(p);
       };
-      int pg_next = ntiles > 0 ? fetch(0) : oob_block(p);
+      int pg_next;
+      if constexpr (kTree) {  // the block-table entry is here already
+        const bool mine = lane < nu && u0 + lane < (kv1 - kv0 + B - 1) >> kLog;
+        pg_next = mine ? box_in_page(p, first_page, (kv0 >> kLog) + u0 + lane) : oob_block(p);
+      } else {
+        pg_next = ntiles > 0 ? fetch(0) : oob_block(p);
+      }
       int t = 0;
       for (; t < ntiles; ++t) {
         const int s = t % NS;
@@ -677,12 +713,6 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
       const int s = t & 1;
       const int key0 = kv0 + t * kKvTile;
       uint32_t vis[kTree ? kKvTile / 32 : 1];
-      if constexpr (kTree) {
-        if (key0 + kKvTile - 1 > jfull) {  // the mask is read while the scores are computed
-#pragma unroll
-          for (int j = 0; j < kKvTile / 32; ++j) vis[j] = tr.visible(key0 + 32 * j, jmax);
-        }
-      }
       if (!(ok = wait_on_warp(c, c.b(BS0 + s), (t >> 1) & 1))) break;
       ptx::tc_fence_after();
       // the scores, and the max of each 32 of them from the load itself
@@ -698,6 +728,10 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
         mx = kKvTile == 128 ? fmaxf(fmaxf(mj[0], mj[1]), fmaxf(mj[kKvTile / 32 - 2], mj[kKvTile / 32 - 1]))
                             : fmaxf(mj[0], mj[kKvTile / 32 - 1]);
       } else {  // diagonal / last tile: mask keys past this row's last visible key
+        if constexpr (kTree) {
+#pragma unroll
+          for (int j = 0; j < kKvTile / 32; ++j) vis[j] = tr.visible(key0 + 32 * j, jmax);
+        }
         float mxp[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) mxp[j] = neg_inf();
@@ -779,21 +813,76 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
     const bool direct = it.part_row < 0;
     const float inv_l = l > 0.f ? 1.f / l : 0.f;
     const size_t orow = static_cast<size_t>(sg.q_start + tok) * p.hq + it.kv_head * G + g;
+    if constexpr (kTree) {
+      // A row a thread is 32 rows an instruction where it goes to memory as it is; its
+      // 16-byte pieces are turned in shared memory instead (piece c of row r at c ^ r % 8;
+      // every product is done with the tiles there), so that a warp writes whole rows.
+      const unsigned rows = __ballot_sync(0xffffffffu, valid);
+      auto write = [&](auto bytes, uint8_t* to, long long at_row) {
+        constexpr int kBytes = decltype(bytes)::value;  // of a value: 2 bf16, 4 fp32 partials
+        constexpr int kPieces = D * kBytes / 16;        // of a row
+        uint8_t* const mine = gb + qw * 32 * D * kBytes;
+        uint8_t* const own = mine + lane * D * kBytes;
+#pragma unroll 1
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t o[32];
+          ptx::tmem_ld32(tO + j * 32, o);
+          ptx::tmem_wait_ld();
+          if (bad_v && valid && j * 32 < p.dr) {
+            uint32_t od[32];  // a copy: o stays in registers where nothing is to be added
+#pragma unroll
+            for (int i = 0; i < 32; ++i) od[i] = o[i];
+            add_nonfinite(p, it, tr, max(kv0, sg.hist), jmax, j * 32, od);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = od[i];
+          }
+#pragma unroll
+          for (int v = 0; v < 2 * kBytes; ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (kBytes == 2)
+                w[i] = ptx::pack_bf16x2(__uint_as_float(o[8 * v + 2 * i]) * inv_l,
+                                        __uint_as_float(o[8 * v + 2 * i + 1]) * inv_l);
+              else
+                w[i] = __float_as_uint(__uint_as_float(o[4 * v + i]) * inv_l);
+            }
+            *reinterpret_cast<uint4*>(own + (((j * 2 * kBytes + v) ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+        const int live = p.dr * kBytes / 16;  // 96 of 128 columns
+        to += at_row * p.dr * kBytes;         // of this lane's row
+        constexpr int kStep = kPieces >= 32 ? 1 : 32 / kPieces;  // rows a round
+        const int ch0 = lane % (kPieces < 32 ? kPieces : 32);
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += kStep) {
+          const int r = r0 + lane / (kPieces < 32 ? kPieces : 32);
+          uint8_t* const dst = reinterpret_cast<uint8_t*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
+          if (rows >> r & 1u) {
+#pragma unroll
+            for (int ch = ch0; ch < kPieces; ch += 32)
+              if (ch < live)
+                *reinterpret_cast<uint4*>(dst + ch * 16) =
+                    *reinterpret_cast<const uint4*>(mine + r * D * kBytes + ((ch ^ (r & 7)) << 4));
+          }
+        }
+      };
+      if (ok && rows && !__any_sync(0xffffffffu, *c.abort != 0)) {
+        if (direct)
+          write(std::integral_constant<int, 2>{}, reinterpret_cast<uint8_t*>(p.out), static_cast<long long>(orow));
+        else
+          write(std::integral_constant<int, 4>{}, reinterpret_cast<uint8_t*>(p.part_o),
+                static_cast<long long>(it.part_row) + row);
+      }
+    } else {
 #pragma unroll 1
     for (int j = 0; j < D / 32; ++j) {
       uint32_t o[32];
       ptx::tmem_ld32(tO + j * 32, o);
       ptx::tmem_wait_ld();
-      if constexpr (kTree) {
-        if (bad_v && store && j * 32 < p.dr) {
-          uint32_t od[32];  // a copy: o stays in registers where nothing is to be added
-#pragma unroll
-          for (int i = 0; i < 32; ++i) od[i] = o[i];
-          add_nonfinite(p, it, tr, max(kv0, sg.hist), jmax, j * 32, od);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = od[i];
-        }
-      }
       if (store && j * 32 < p.dr) {  // columns past the tensors' head_dim are not stored
         if (direct) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + orow * p.dr + j * 32);
@@ -814,6 +903,7 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
                                  __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
         }
       }
+    }
     }
     if (store) {
       const float lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : neg_inf();
@@ -1388,6 +1478,28 @@ __device__ __forceinline__ void decode_item(const Ctx& c, const WorkItem& it, co
   merge_rows<D>(p, it, sg, mo, mm, ml, hw, HG, ps, head, R, lane);
 }
 
+// Arrivals that complete a phase of barrier i
+__device__ __forceinline__ uint32_t barrier_count(int i, int gather, bool prefill, int num_heads) {
+  uint32_t count = 1;
+  if (i >= BK0 && i < BV0 + 3) count = gather ? 64 : 2;   // producer warps (threads) per tile
+  if (i == BP0 || i == BP0 + 1 || i == BQT) count = 128;  // every softmax thread
+  if (i == BDRAIN) count = 2;                             // the Q K^T and the P V issuer
+  if (i >= BEMPTY0) count = prefill ? 1 : num_heads;      // one warp per head reads a stage
+  // a decode stage: the K-half and the V-half producer warps arrive
+  if (!prefill && i >= BFULL0 && i < BFULL0 + kMaxDecStages) count = 2;
+  return count;
+}
+
+// Boxes of a tile that a producer warp loads, and the first of them
+template <int D>
+__device__ __forceinline__ int boxes_per_warp(const KParams& p) {
+  return (Cfg<D>::kKvTile / 2) >> p.box_log2;
+}
+template <int D>
+__device__ __forceinline__ int first_boxes(const KParams& p, int warp) {
+  return (warp & 1) * boxes_per_warp<D>(p);
+}
+
 template <int D, bool kTree>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     mixed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -1401,55 +1513,79 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gb = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const WorkItem it = p.items[blockIdx.x];
   Ctx c;
   c.bar = base + C::kOffBar;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + C::kOffBar + kNumBars * 8);
   c.abort = reinterpret_cast<volatile int*>(gb + C::kOffBar + kNumBars * 8 + 16);
   c.err = p.err;
   c.limit_ns = p.test_stall ? kTestWaitLimitNs : kWaitLimitNs;
-  const bool prefill = it.kind == kPrefillItem;
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) {
-      uint32_t count = 1;
-      if (i >= BK0 && i < BV0 + 3) count = p.gather ? 64 : 2;  // producer warps (threads) per tile
-      if (i == BP0 || i == BP0 + 1 || i == BQT) count = 128;  // every softmax thread
-      if (i == BDRAIN) count = 2;                       // the Q K^T and the P V issuer
-      if (i >= BEMPTY0) count = prefill ? 1 : it.num_heads;  // one warp per head reads a stage
-      // a decode stage: the K-half and the V-half producer warps arrive
-      if (!prefill && i >= BFULL0 && i < BFULL0 + kMaxDecStages) count = 2;
-      ptx::mbar_init(c.b(i), count);
-    }
-    *c.abort = 0;
-    if (kTree) c.abort[1] = 0;  // no infinity or NaN found
-    ptx::fence_mbar_init();
-  }
-  if (warp == 0 && lane == 0) {
-    if (prefill) {
+  WorkItem it;
+  Seg sg;
+  int first_page = -1;
+  if constexpr (kTree) {
+    // The items of a step with trees are short, so their set-up counts: what does not
+    // depend on the item is made while the item, its segment's numbers and the
+    // producers' first block-table entries are on their way.
+    asm volatile("griddepcontrol.launch_dependents;");  // the combine's launch
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < BFULL0; ++i) ptx::mbar_init(c.b(i), barrier_count(i, p.gather, true, 0));
+      c.abort[0] = 0;
+      c.abort[1] = 0;  // no infinity or NaN found
+      ptx::fence_mbar_init();
       ptx::prefetch_tmap(&tm_q);
-    } else {
-      ptx::prefetch_tmap(&tm_kd);
-      ptx::prefetch_tmap(&tm_vd);
+    }
+    if (warp == 1) {
+      ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+      ptx::tmem_relinquish();
+    }
+    if (warp >= 6 && lane == 0) ptx::prefetch_tmap(warp < 8 ? &tm_k : &tm_v);
+    it = p.items[blockIdx.x];
+    sg = segment_of(p, it.seg);
+    if (it.kind == kPrefillItem) {
+      if (warp >= 6 && !p.gather) {
+        const int u = first_boxes<D>(p, warp) + lane;
+        if (lane < boxes_per_warp<D>(p) && u < (it.kv_end - it.kv_begin + (1 << p.box_log2) - 1) >> p.box_log2)
+          first_page = p.bt[static_cast<size_t>(it.seg) * p.max_pages +
+                            (((it.kv_begin >> p.box_log2) + u) >> p.spp_log2)];
+      }
+    } else if (warp >= 2 && warp < 2 + 2 * kMaxDecStages / 32) {
+      const int i = BFULL0 + (warp - 2) * 32 + lane;
+      ptx::mbar_init(c.b(i), barrier_count(i, p.gather, false, it.num_heads));
+      ptx::fence_mbar_init();
+    }
+  } else {
+    it = p.items[blockIdx.x];
+    const bool prefill = it.kind == kPrefillItem;
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < kNumBars; ++i)
+        ptx::mbar_init(c.b(i), barrier_count(i, p.gather, prefill, it.num_heads));
+      *c.abort = 0;
+      ptx::fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+      if (prefill) {
+        ptx::prefetch_tmap(&tm_q);
+      } else {
+        ptx::prefetch_tmap(&tm_kd);
+        ptx::prefetch_tmap(&tm_vd);
+      }
+    }
+    if (prefill && warp >= 6 && lane == 0) ptx::prefetch_tmap(warp < 8 ? &tm_k : &tm_v);
+    if (prefill && warp == 1) {
+      ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+      ptx::tmem_relinquish();
     }
   }
-  if (prefill && warp >= 6 && lane == 0) ptx::prefetch_tmap(warp < 8 ? &tm_k : &tm_v);
-  if (prefill && warp == 1) {
-    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
-    ptx::tmem_relinquish();
-  }
+  const bool prefill = it.kind == kPrefillItem;
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
 
-  Seg sg;
-  sg.q_start = p.cu_q[it.seg];
-  sg.lq = p.cu_q[it.seg + 1] - sg.q_start;
-  sg.lk = p.cu_k ? p.cu_k[it.seg + 1] - p.cu_k[it.seg] : p.seqlens_k[it.seg];
-  sg.hist = sg.lk - sg.lq;
+  if constexpr (!kTree) sg = segment_of(p, it.seg);
 
   if (prefill) {
-    prefill_item<D, kTree>(c, it, sg, p, base, gb, *tmem_slot, &tm_q, &tm_k, &tm_v, warp, lane);
+    prefill_item<D, kTree>(c, it, sg, p, base, gb, *tmem_slot, &tm_q, &tm_k, &tm_v, warp, lane,
+                           first_page);
   } else if constexpr (D <= 128) {
     decode_item<D>(c, it, sg, p, base, gb, &tm_kd, &tm_vd, warp, lane);
   } else {
@@ -1459,7 +1595,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (prefill && warp == 1) {
+  if ((kTree || prefill) && warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(*tmem_slot, 512);
   }

@@ -12,6 +12,7 @@
 
 #include "mcp_internal.h"
 #include "ptx.cuh"
+#include "step_ops.h"
 
 namespace mcp {
 namespace {
@@ -31,6 +32,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Parts written by a launch that this one began beside are read through L2 alone.
+template <bool kBeside, typename T>
+__device__ __forceinline__ T load_part(const T* p) {
+  return kBeside ? __ldcg(p) : __ldg(p);
+}
+
 // One warp per merged row.  The rows of all entries are numbered
 // consecutively (entry e owns rows [row_base, row_base + rows)), so the grid
 // covers exactly the rows that have parts, whatever the mix of short decode
@@ -39,7 +46,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 // to its own row's entry (a block's 8 rows span at most 8 entries).  Lane k
 // holds the LSE of part k (32 parts per pass); lane l accumulates columns
 // [l * D/32, (l + 1) * D/32) of O.
-template <int D>
+//
+// kBeside: launched beside the forward (programmatic serialization); the entries
+// come from the plan and are looked up before the forward's parts are waited for.
+template <int D, bool kBeside>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineEntry* __restrict__ ents,
                                                       int num_ents, int total_rows,
                                                       const int32_t* __restrict__ cu_q,
@@ -59,6 +69,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineEntry* __rest
   const int row = r - e.row_base;
   const int n = e.num_splits;
   const int64_t pr0 = static_cast<int64_t>(e.part_row) + row;  // part k: row pr0 + k * e.rows
+  if constexpr (kBeside) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   float acc[V];
 #pragma unroll
@@ -72,7 +83,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineEntry* __rest
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < n)
-        ov[j] = __ldg(reinterpret_cast<const float4*>(
+        ov[j] = load_part<kBeside>(reinterpret_cast<const float4*>(
             part_o + (pr0 + static_cast<int64_t>(j) * e.rows) * D + lane * V));
     M = warp_max(lk);
     const float w = (lk == neg_inf()) ? 0.f : ptx::ex2((lk - M) * kLog2e);
@@ -101,18 +112,18 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineEntry* __rest
       const float wj = __shfl_sync(0xffffffffu, w, j);
       const float* src = part_o + (pr0 + static_cast<int64_t>(k0 + j) * e.rows) * D + lane * V;
       if constexpr (V == 4) {
-        const float4 o = __ldg(reinterpret_cast<const float4*>(src));
+        const float4 o = load_part<kBeside>(reinterpret_cast<const float4*>(src));
         acc[0] += wj * o.x;
         acc[1] += wj * o.y;
         acc[2] += wj * o.z;
         acc[3] += wj * o.w;
       } else if constexpr (V == 2) {
-        const float2 o = __ldg(reinterpret_cast<const float2*>(src));
+        const float2 o = load_part<kBeside>(reinterpret_cast<const float2*>(src));
         acc[0] += wj * o.x;
         acc[1] += wj * o.y;
       } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] += wj * __ldg(src + v);
+        for (int v = 0; v < V; ++v) acc[v] += wj * load_part<kBeside>(src + v);
       }
     }
   }
@@ -172,24 +183,18 @@ int launch_combine(const FwdArgs& a, void* stream) {
   const int G = a.num_q_heads / a.num_kv_heads;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int blocks = (a.combine_rows + kCombineRowsPerBlock - 1) / kCombineRowsPerBlock;
-  if (a.head_dim == 128) {
-    combine_kernel<128><<<blocks, 256, 0, st>>>(
-        a.combine, a.num_combine, a.combine_rows, a.cu_seqlens_q, a.part_o, a.part_lse,
-        static_cast<__nv_bfloat16*>(a.out), a.lse, a.num_q_heads, G);
-  } else if (a.head_dim == 256) {
-    combine_kernel<256><<<blocks, 256, 0, st>>>(
-        a.combine, a.num_combine, a.combine_rows, a.cu_seqlens_q, a.part_o, a.part_lse,
-        static_cast<__nv_bfloat16*>(a.out), a.lse, a.num_q_heads, G);
-  } else if (a.head_dim == 96) {
-    combine_kernel<96><<<blocks, 256, 0, st>>>(
-        a.combine, a.num_combine, a.combine_rows, a.cu_seqlens_q, a.part_o, a.part_lse,
-        static_cast<__nv_bfloat16*>(a.out), a.lse, a.num_q_heads, G);
-  } else {
-    combine_kernel<64><<<blocks, 256, 0, st>>>(
-        a.combine, a.num_combine, a.combine_rows, a.cu_seqlens_q, a.part_o, a.part_lse,
-        static_cast<__nv_bfloat16*>(a.out), a.lse, a.num_q_heads, G);
-  }
-  return static_cast<int>(cudaGetLastError());
+  auto launch = [&](auto kernel, bool beside) {
+    return launch_beside(kernel, beside, blocks, 256, 0, st, a.combine, static_cast<int>(a.num_combine),
+                         static_cast<int>(a.combine_rows), a.cu_seqlens_q,
+                         static_cast<const float*>(a.part_o), static_cast<const float*>(a.part_lse),
+                         static_cast<__nv_bfloat16*>(a.out), a.lse, static_cast<int>(a.num_q_heads), G);
+  };
+  // behind a forward with trees, whose launch lets the next one begin
+  const bool beside = a.mask_rows != nullptr;
+  if (a.head_dim == 128) return beside ? launch(combine_kernel<128, true>, true) : launch(combine_kernel<128, false>, false);
+  if (a.head_dim == 256) return beside ? launch(combine_kernel<256, true>, true) : launch(combine_kernel<256, false>, false);
+  if (a.head_dim == 96) return beside ? launch(combine_kernel<96, true>, true) : launch(combine_kernel<96, false>, false);
+  return beside ? launch(combine_kernel<64, true>, true) : launch(combine_kernel<64, false>, false);
 }
 
 int launch_merge_states(const float* o_parts, const float* lse_parts, int32_t n, int32_t rows,

@@ -238,7 +238,13 @@ void build(const mcp_attn_desc& d, const int32_t* cu, const int32_t* sk, int num
   // overlap on different SMs, which this model does not capture (measured:
   // it chose a split 2.5% slower on the long-context step).
   if (popt <= 0) {
-    const double tile_ns = 750.0 * DK / 128.0, item_ns = 5000.0;
+    // Steps with trees are short and few rows: their estimates include the cold
+    // caches that a tree's few tiles do not hide (measured 8 us an item and 0.9 us
+    // a tile), splits go down to 512 keys, and the combine that a split brings
+    // counts (a tree of 32 tokens over 8192 keys, splits of 512 / 1024 / 2048 keys:
+    // 22 / 22 / 27 us; 32 trees over 1024 keys unsplit 36 us, in 512s 61).
+    const bool tree = o && o->tree;
+    const double tile_ns = (tree ? 900.0 : 750.0) * DK / 128.0, item_ns = tree ? 8000.0 : 5000.0;
     double pre_ns = 0.0, dec_ns = 0.0;
     for (const Unit& x : units) {
       if (x.decode) dec_ns += vis_of(x) * 4.0 * DK * H / 45.0;
@@ -261,6 +267,7 @@ void build(const mcp_attn_desc& d, const int32_t* cu, const int32_t* sk, int num
       };
       std::vector<double> cost, load;
       auto makespan = [&](int64_t cand_ps) {
+        int64_t parts = 1;  // of the unit split most
         cost.clear();
         for (const Unit& x : units) {
           int64_t n, sz;
@@ -272,6 +279,7 @@ void build(const mcp_attn_desc& d, const int32_t* cu, const int32_t* sk, int num
                                             DK * HG / 45.0);
           } else {
             even_split(vis_of(x), cand_ps, mcp::kKvTile, &n, &sz);
+            parts = std::max(parts, n);
             for (int64_t k = 0; k < n; ++k) {
               const double tiles = static_cast<double>(
                   cdiv(std::min<int64_t>(sz, vis_of(x) - k * sz), mcp::kKvTile));
@@ -286,13 +294,14 @@ void build(const mcp_attn_desc& d, const int32_t* cu, const int32_t* sk, int num
           load.back() += c;
           std::push_heap(load.begin(), load.end(), std::greater<double>());
         }
-        return *std::max_element(load.begin(), load.end());
+        const double combine = !tree || parts == 1 ? 0.0 : 4000.0 + 250.0 * std::max<int64_t>(0, parts - 8);
+        return *std::max_element(load.begin(), load.end()) + combine;
       };
       const double t0 = makespan(ps);
       const int64_t ps_sig = signature(ps);
       int64_t best = ps, last_sig = -1;
       double best_t = t0;
-      for (int64_t cand = 65536; cand >= 2048; cand /= 2) {
+      for (int64_t cand = 65536; cand >= (tree ? 512 : 2048); cand = cand > 2048 || !tree ? cand / 2 : cand - 512) {
         // candidates finer than the rule's split stop past sixteen items per SM
         // (counts grow as cand shrinks); coarser ones are always evaluated
         if (cand < ps && count(ds, cand) > 16LL * std::max(1, num_sms)) break;
