@@ -985,6 +985,8 @@ typedef struct mcp_keep_desc {
   int32_t page_size;         /* 1, 8, 16, 32 or 64                               */
   int32_t max_pages_per_seq;
   int32_t num_pages;
+  int64_t layer_stride;      /* 0: each layer's caches are listed; else elements  */
+                             /* between the layers' caches, a multiple of 8       */
 } mcp_keep_desc;
 
 /*
@@ -1002,7 +1004,8 @@ typedef struct mcp_keep_desc {
  *
  * k_caches, v_caches: HOST arrays of num_layers device pointers to caches
  * [num_pages, page_size, num_kv_heads, head_dim] bf16, 16-byte aligned, read
- * before the call returns.  The rest are device arrays, as in the calls above;
+ * before the call returns; with layer_stride, of one pointer to the first
+ * layer's.  The rest are device arrays, as in the calls above;
  * cu_rows NULL: the rows are the stream's tokens (cu_seqlens_q).  A path that
  * does not rise or leaves its segment (MCP_DEVERR_TREE), accepted[s] outside
  * its rows (MCP_DEVERR_TREE) and a segment with seqlens_k < its tokens, past

@@ -875,20 +875,19 @@ def verify_drafts(target_probs, tokens, cu_rows, uniform, final_uniform, parents
 
 
 def _layers(caches, name, dev, shape):
-    """(shape of one cache, layers, array of their addresses) of one cache [pages, P, H_kv, D],
-    all layers' [layers, pages, P, H_kv, D], or a list of caches."""
+    """(shape of one cache, layers, elements between them, array of addresses) of one cache
+    [pages, P, H_kv, D], all layers' [layers, pages, P, H_kv, D] (one address), or a list of
+    caches (elements 0)."""
     import torch
 
     bf16 = torch.bfloat16
     if isinstance(caches, torch.Tensor):
-        if caches.dim() == 5:
-            full = caches.shape
-            one = full[1:]
-            if full[0] and (shape is None or one == shape) and caches.is_contiguous():
-                step = caches.stride(0) * 2
-                base = _arg(caches, bf16, name, dev)
-                return one, full[0], np.arange(base, base + step * full[0], step or 1, dtype=np.uint64)
-        elif caches.dim() == 4:
+        full = caches.shape
+        if len(full) == 5:
+            one, stride = full[1:], caches.stride(0)
+            if full[0] and stride and (shape is None or one == shape):
+                return one, full[0], stride, ctypes.c_void_p(_arg(caches, bf16, name, dev))
+        elif len(full) == 4:
             caches = (caches,)
         else:
             raise ValueError(f"{name} must be caches [pages, P, H_kv, D] of one or all layers")
@@ -898,8 +897,8 @@ def _layers(caches, name, dev, shape):
         shape = caches[0].shape
         if len(shape) != 4:
             raise ValueError(f"{name} must be caches [pages, P, H_kv, D]")
-    return shape, len(caches), np.array([_arg(c, bf16, name, dev, shape) for c in caches],
-                                        dtype=np.uint64)
+    return shape, len(caches), 0, (ctypes.c_void_p * len(caches))(
+        *(_arg(c, bf16, name, dev, shape) for c in caches))
 
 
 def kv_keep_path(k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k, accepted, path,
@@ -913,10 +912,11 @@ def kv_keep_path(k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k, acce
     import torch
 
     dev, i32 = _gpu(accepted, "accepted"), torch.int32
-    shape, L, ks = _layers(k_caches, "k_caches", dev, None)
-    _, more, vs = _layers(v_caches, "v_caches", dev, shape)
-    if not L or L != more:
-        raise ValueError("k_caches and v_caches must have the same layers, one at least")
+    shape, L, stride, ks = _layers(k_caches, "k_caches", dev, None)
+    _, more, other, vs = _layers(v_caches, "v_caches", dev, shape)
+    if not L or L != more or stride != other:
+        raise ValueError("k_caches and v_caches must have the same layers, one at least, both listed "
+                         "or both one tensor")
     if accepted.dim() != 1 or path.dim() != 1 or block_tables.dim() != 2:
         raise ValueError("accepted must be [S], path [R], block_tables [S, max_pages_per_seq]")
     S, R = accepted.shape[0], path.shape[0]
@@ -926,9 +926,9 @@ def kv_keep_path(k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k, acce
     one = (S,)
     if new_lens is None:
         new_lens = _empty(one, i32, accepted.device, stream, result=True)
-    desc = _capi.KeepDesc(S, R, L, H, D, P, width, pages)
+    desc = _capi.KeepDesc(S, R, L, H, D, P, width, pages, stride)
     _launch("kv_keep_path", dev, stream, load().mcp_kv_keep_path, ctypes.byref(desc),
-            ks.ctypes.data, vs.ctypes.data, _arg(block_tables, i32, "block_tables", dev, (S, width)),
+            ctypes.byref(ks), ctypes.byref(vs), _arg(block_tables, i32, "block_tables", dev, (S, width)),
             _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (S + 1,)),
             _arg(seqlens_k, i32, "seqlens_k", dev, one), _arg(cu_rows, i32, "cu_rows", dev, (S + 1,)),
             _arg(accepted, i32, "accepted", dev, one), _arg(path, i32, "path", dev),

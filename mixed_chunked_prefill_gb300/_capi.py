@@ -230,7 +230,7 @@ class VerifyTensors(ctypes.Structure):
 class KeepDesc(ctypes.Structure):
     _fields_ = [(n, c_int32) for n in (
         "num_seqs", "total_rows", "num_layers", "num_kv_heads", "head_dim", "page_size",
-        "max_pages_per_seq", "num_pages")]
+        "max_pages_per_seq", "num_pages")] + [("layer_stride", c_int64)]
 
 
 # name -> (restype, argtypes); every symbol include/mcp.h declares

@@ -386,7 +386,10 @@ mcp_status mcp_kv_keep_path(const mcp_keep_desc* d, void* const* k_caches, void*
   if (!block_tables || !cu_seqlens_q || !seqlens_k || !accepted || (d->total_rows > 0 && !path) ||
       (d->num_layers > 0 && (!k_caches || !v_caches)))
     return fail(MCP_ERR_INVALID_ARG, "NULL pointer argument");
-  for (int32_t l = 0; l < d->num_layers; ++l)
+  if (d->layer_stride < 0 || d->layer_stride % 8 != 0)
+    return fail(MCP_ERR_INVALID_ARG, "layer_stride %lld is not a multiple of 8",
+                static_cast<long long>(d->layer_stride));
+  for (int32_t l = 0; l < (d->layer_stride && d->num_layers ? 1 : d->num_layers); ++l)
     if (!k_caches[l] || !v_caches[l] || !aligned(k_caches[l], 16) || !aligned(v_caches[l], 16))
       return fail(MCP_ERR_INVALID_ARG, "cache of layer %d is NULL or not 16-byte aligned", l);
   return done(mcp::launch_kv_keep_path(*d, k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k,

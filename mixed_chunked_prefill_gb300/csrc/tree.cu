@@ -13,8 +13,6 @@ namespace mcp {
 namespace {
 
 // ------------------------------------------------------------------- masks
-constexpr int kMaskThreads = 256;
-
 struct MaskArgs {
   const int32_t* parents;
   const int32_t* cu;
@@ -24,6 +22,7 @@ struct MaskArgs {
   int32_t* positions;
   int32_t* err;
   int32_t T, rows, W;
+  int32_t lanes_log2;  // threads of a token: W rounded up to a power of two
 };
 
 // A CTA a segment.  The rows are filled by doubling: row[i] holds the tokens
@@ -32,7 +31,11 @@ struct MaskArgs {
 // steps.  A row that another thread has already extended in the same round only
 // holds more of the same ancestors; up, which must not run ahead of the rows, is
 // written to a second array.  Depth is the number of bits.
-__global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs p) {
+//
+// Bound by its launch and the chain of loads in front of the rounds (1024 trees of 48
+// to 128 tokens 6.5 us, 4 of 16 2.9); with 256 threads 8 trees of 1024 tokens took 54.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) tree_masks_kernel(const MaskArgs p) {
   extern __shared__ uint32_t smem[];
   const int s = blockIdx.x, tid = threadIdx.x, W = p.W;
   const int t0 = p.cu[s], t1 = p.cu[s + 1];
@@ -51,16 +54,17 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs
   if (outside || large) return;
   if (!tree) {
     if (p.positions)
-      for (int i = tid; i < n; i += kMaskThreads) p.positions[t0 + i] = hist + i;
+      for (int i = tid; i < n; i += kThreads) p.positions[t0 + i] = hist + i;
     return;
   }
-  uint32_t* row = smem;                                     // [n][W]
+  uint32_t* row = smem;                                         // [n][W]
   int32_t* up = reinterpret_cast<int32_t*>(smem + 32 * W * W);  // two of [32 W]
   int32_t* next = up + 32 * W;
-  for (int i = tid; i < n * W; i += kMaskThreads) row[i] = 0;
-  __syncthreads();
+  // a thread takes word `w` of tokens i0, i0 + step, ..; words behind a token's own
+  // stay 0
+  const int w = tid & ((1 << p.lanes_log2) - 1), i0 = tid >> p.lanes_log2, step = kThreads >> p.lanes_log2;
   bool some = false;
-  for (int i = tid; i < n; i += kMaskThreads) {
+  for (int i = tid; i < n; i += kThreads) {
     int32_t a = p.parents[t0 + i];
     if (a >= i) {
       if (p.err) atomicOr(p.err, MCP_DEVERR_TREE);
@@ -68,16 +72,17 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs
     }
     up[i] = a < 0 ? -1 : a;
     some |= a >= 0;
-    row[i * W + (i >> 5)] = 1u << (i & 31);
   }
+  if (w < W)
+    for (int i = i0; i < n; i += step) row[i * W + w] = w == i >> 5 ? 1u << (i & 31) : 0u;
   while (__syncthreads_or(some)) {
     some = false;
-    for (int x = tid; x < n * W; x += kMaskThreads) {
-      const int i = x / W;
+#pragma unroll 4
+    for (int i = i0; i < n; i += step) {
       const int a = up[i];
-      if (a >= 0) row[x] |= row[a * W + x - i * W];
+      if (a >= 0 && w <= a >> 5) row[i * W + w] |= row[a * W + w];
     }
-    for (int i = tid; i < n; i += kMaskThreads) {
+    for (int i = tid; i < n; i += kThreads) {
       const int a = up[i];
       const int b = a >= 0 ? up[a] : -1;
       next[i] = b;
@@ -88,12 +93,13 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs
     next = t;
   }
   uint32_t* out = p.mask + static_cast<int64_t>(m0) * W;
-  for (int x = tid; x < n * W; x += kMaskThreads) out[x] = row[x];
+  for (int x = tid; x < n * W; x += kThreads) out[x] = row[x];
   if (p.positions)
-    for (int i = tid; i < n; i += kMaskThreads) {
-      int bits = 0;
-      for (int w = 0; w <= i >> 5; ++w) bits += __popc(row[i * W + w]);
-      p.positions[t0 + i] = hist + bits - 1;
+    for (int base = 0; base < n; base += step) {  // the words of a token lie in its threads' lanes
+      const int i = base + i0;
+      int bits = w < W && i < n ? __popc(row[i * W + w]) : 0;
+      for (int o = 1 << p.lanes_log2 >> 1; o > 0; o >>= 1) bits += __shfl_xor_sync(0xffffffffu, bits, o);
+      if (w == 0 && i < n) p.positions[t0 + i] = hist + bits - 1;
     }
 }
 
@@ -103,8 +109,17 @@ constexpr int kKeepLayers = 64;  // whose addresses fit a launch's arguments
 constexpr int kKeepSlots = 256;  // moves whose slots a CTA has at hand
 constexpr int kKeepBatch = 8;    // rows in flight a thread
 
+// K and V of each layer: listed, or all layers' at one distance
+struct ListedCaches {
+  uint4* at[2 * kKeepLayers];
+  __device__ __forceinline__ uint4* operator[](int i) const { return at[i]; }
+};
+struct EvenCaches {
+  uint4* at[2];
+  int64_t stride;  // in 16 bytes
+  __device__ __forceinline__ uint4* operator[](int i) const { return at[i & 1] + (i >> 1) * stride; }
+};
 struct KeepArgs {
-  uint4* caches[2 * kKeepLayers];  // K and V of each layer
   const int32_t* bt;
   const int32_t* cu;
   const int32_t* sk;
@@ -119,6 +134,7 @@ struct KeepArgs {
   int32_t chunks;    // CTAs of a segment
 };
 
+// Slot of position `pos`, -1 (and an error bit) where its page is none of the pool's
 __device__ __forceinline__ int64_t slot_of(const KeepArgs& p, const int32_t* bt, int pos, int& bad) {
   const int32_t page = bt[pos >> p.page_log2];
   if (page < 0 || page >= p.num_pages) {
@@ -132,7 +148,9 @@ __device__ __forceinline__ int64_t slot_of(const KeepArgs& p, const int32_t* bt,
 // One thread takes a column through all moves in their order, up to kKeepBatch of
 // them loaded before the first is stored: a path rises strictly, so move k reads
 // place path[k] >= k, which only moves after it write.
-__global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const __grid_constant__ KeepArgs p) {
+template <typename Caches>
+__global__ void __launch_bounds__(kKeepThreads)
+    keep_path_kernel(const __grid_constant__ KeepArgs p, const __grid_constant__ Caches caches) {
   __shared__ int64_t from[kKeepSlots], to[kKeepSlots];
   const int s = blockIdx.x / p.chunks, chunk = blockIdx.x - s * p.chunks, tid = threadIdx.x;
   const int lq = p.cu[s + 1] - p.cu[s], sk = p.sk[s], hist = sk - lq;
@@ -185,7 +203,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const __grid_co
     __syncthreads();
     for (int c = c0 + tid; c < c1; c += kKeepThreads) {
       const int which = c / p.vec;
-      uint4* cache = p.caches[which] + (c - which * p.vec);
+      uint4* cache = caches[which] + (c - which * p.vec);
       for (int b = 0; b < left; b += kKeepBatch) {
         uint4 v[kKeepBatch];
 #pragma unroll
@@ -208,14 +226,17 @@ int launch_build_tree_masks(const int32_t* parents, const int32_t* cu_seqlens_q,
                             int32_t* tree_mask, int32_t* positions, int32_t* error_word,
                             void* stream) {
   const int smem = 4 * (32 * mask_words * mask_words + 2 * 32 * mask_words);  // at most 136 KB
-  if (smem > 48 * 1024) {
-    const int e = allow_smem<tree_masks_kernel>(4 * (32 * 32 * 32 + 2 * 32 * 32));
+  MaskArgs a = {parents, cu_seqlens_q, seqlens_k, mask_rows, reinterpret_cast<uint32_t*>(tree_mask),
+                positions, error_word, total_tokens, num_mask_rows, mask_words, 0};
+  while (1 << a.lanes_log2 < mask_words) ++a.lanes_log2;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (mask_words <= 4) {  // up to 128 tokens: two words a thread
+    tree_masks_kernel<256><<<num_seqs, 256, smem, st>>>(a);
+  } else {
+    const int e = allow_smem<tree_masks_kernel<1024>>(4 * (32 * 32 * 32 + 2 * 32 * 32));
     if (e != 0) return e;
+    tree_masks_kernel<1024><<<num_seqs, 1024, smem, st>>>(a);
   }
-  const MaskArgs a = {parents, cu_seqlens_q, seqlens_k, mask_rows,
-                      reinterpret_cast<uint32_t*>(tree_mask), positions, error_word,
-                      total_tokens, num_mask_rows, mask_words};
-  tree_masks_kernel<<<num_seqs, kMaskThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -237,12 +258,7 @@ int launch_kv_keep_path(const mcp_keep_desc& d, void* const* k_caches, void* con
   a.max_pages = d.max_pages_per_seq;
   a.num_pages = d.num_pages;
   a.vec = static_cast<int32_t>(static_cast<int64_t>(d.num_kv_heads) * d.head_dim / 8);
-  for (int l0 = 0; l0 == 0 || l0 < d.num_layers; l0 += kKeepLayers) {
-    const int layers = d.num_layers - l0 < kKeepLayers ? d.num_layers - l0 : kKeepLayers;
-    for (int l = 0; l < layers; ++l) {
-      a.caches[2 * l] = static_cast<uint4*>(k_caches[l0 + l]);
-      a.caches[2 * l + 1] = static_cast<uint4*>(v_caches[l0 + l]);
-    }
+  auto launch = [&](const auto& caches, int layers) {
     a.columns = 2 * layers * a.vec;
     // a column a thread, more of them where that would be over 8 CTAs an SM
     const int64_t all = static_cast<int64_t>(d.num_seqs) * ((a.columns + kKeepThreads - 1) / kKeepThreads);
@@ -251,9 +267,23 @@ int launch_kv_keep_path(const mcp_keep_desc& d, void* const* k_caches, void* con
     a.per_cta = static_cast<int32_t>(per < a.columns ? per : (a.columns > 0 ? a.columns : 1));
     a.chunks = a.columns > 0 ? (a.columns + a.per_cta - 1) / a.per_cta : 1;
     const int64_t grid = static_cast<int64_t>(d.num_seqs) * a.chunks;
-    keep_path_kernel<<<static_cast<unsigned>(grid), kKeepThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return static_cast<int>(e);
+    keep_path_kernel<<<static_cast<unsigned>(grid), kKeepThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, caches);
+    return static_cast<int>(cudaGetLastError());
+  };
+  if (d.layer_stride != 0) {
+    const EvenCaches caches = {{static_cast<uint4*>(k_caches[0]), static_cast<uint4*>(v_caches[0])},
+                               d.layer_stride / 8};
+    return launch(caches, d.num_layers);
+  }
+  for (int l0 = 0; l0 == 0 || l0 < d.num_layers; l0 += kKeepLayers) {
+    const int layers = d.num_layers - l0 < kKeepLayers ? d.num_layers - l0 : kKeepLayers;
+    ListedCaches caches = {};
+    for (int l = 0; l < layers; ++l) {
+      caches.at[2 * l] = static_cast<uint4*>(k_caches[l0 + l]);
+      caches.at[2 * l + 1] = static_cast<uint4*>(v_caches[l0 + l]);
+    }
+    const int e = launch(caches, layers);
+    if (e != 0) return e;
   }
   return 0;
 }

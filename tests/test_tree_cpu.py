@@ -78,7 +78,7 @@ def test_verify_drafts_without_structures(lib):
 def keep(lib, ks=(P16, P16), vs=(P16, P16), **over):
     a = dict(bt=P16, cu=P16, sk=P16, cu_rows=None, accepted=P16, path=P16, new_lens=None, err=None)
     f = dict(num_seqs=2, total_rows=8, num_layers=2, num_kv_heads=2, head_dim=64, page_size=16,
-             max_pages_per_seq=4, num_pages=8)
+             max_pages_per_seq=4, num_pages=8, layer_stride=0)
     for name, value in over.items():
         (a if name in a else f)[name] = value
     d = _capi.KeepDesc(*(f[n] for n, _ in _capi.KeepDesc._fields_))
@@ -98,7 +98,8 @@ def keep(lib, ks=(P16, P16), vs=(P16, P16), **over):
     *[(dict([(n, None)]), INVALID) for n in ("bt", "cu", "sk", "accepted", "path", "ks", "vs")],
     *[(dict([(n, P16 + 2)]), INVALID) for n in
       ("bt", "cu", "sk", "cu_rows", "accepted", "path", "new_lens", "err")],
-    (dict(ks=(P16, None)), INVALID), (dict(vs=(P16 + 8, P16)), INVALID), (dict(num_seqs=0), OK),
+    (dict(layer_stride=-8), INVALID), (dict(layer_stride=12), INVALID),
+    (dict(layer_stride=64, ks=(None,)), INVALID), (dict(ks=(P16, None)), INVALID), (dict(vs=(P16 + 8, P16)), INVALID), (dict(num_seqs=0), OK),
 ])
 def test_kv_keep_path_refusals(lib, over, status):
     assert keep(lib, **over) == status
