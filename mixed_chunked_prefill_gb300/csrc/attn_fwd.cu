@@ -879,31 +879,31 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
       }
     } else {
 #pragma unroll 1
-    for (int j = 0; j < D / 32; ++j) {
-      uint32_t o[32];
-      ptx::tmem_ld32(tO + j * 32, o);
-      ptx::tmem_wait_ld();
-      if (store && j * 32 < p.dr) {  // columns past the tensors' head_dim are not stored
-        if (direct) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * p.dr + j * 32);
+      for (int j = 0; j < D / 32; ++j) {
+        uint32_t o[32];
+        ptx::tmem_ld32(tO + j * 32, o);
+        ptx::tmem_wait_ld();
+        if (store && j * 32 < p.dr) {  // columns past the tensors' head_dim are not stored
+          if (direct) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * p.dr + j * 32);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            dst[v] = make_uint4(
-                ptx::pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv_l, __uint_as_float(o[8 * v + 1]) * inv_l),
-                ptx::pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv_l, __uint_as_float(o[8 * v + 3]) * inv_l),
-                ptx::pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv_l, __uint_as_float(o[8 * v + 5]) * inv_l),
-                ptx::pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv_l, __uint_as_float(o[8 * v + 7]) * inv_l));
+            for (int v = 0; v < 4; ++v) {
+              dst[v] = make_uint4(
+                  ptx::pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv_l, __uint_as_float(o[8 * v + 1]) * inv_l),
+                  ptx::pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv_l, __uint_as_float(o[8 * v + 3]) * inv_l),
+                  ptx::pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv_l, __uint_as_float(o[8 * v + 5]) * inv_l),
+                  ptx::pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv_l, __uint_as_float(o[8 * v + 7]) * inv_l));
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(
+                p.part_o + static_cast<size_t>(it.part_row + row) * p.dr + j * 32);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
+                                   __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
           }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(
-              p.part_o + static_cast<size_t>(it.part_row + row) * p.dr + j * 32);
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
-                                 __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
         }
       }
-    }
     }
     if (store) {
       const float lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : neg_inf();

@@ -351,6 +351,51 @@ def test_attention_refusals(mcp):
         mcp.mixed_attn_fwd_tree(**{**good, "plan": plain})
 
 
+def test_waits_that_run_out_end_a_step_with_trees(mcp):
+    """The abort path (no Q tile arrives, waits give up after 1 ms): no row is written, the error
+    is reported, and the next plan in the same workspace runs."""
+    st = Step([(40, 200, "tree"), (1, 30, None), (20, 0, "star")], 8, 2, 128, 16, seed=12)
+    plan, ws = st.plan(mcp, test_stall=1)
+    mask, mask_rows = st.masks()
+    out = torch.full_like(st.qs, float("nan"))
+    lse = torch.full((st.T, 8), float("nan"), device="cuda")
+    args = (st.qs, st.k, st.v, i32(st.bt), i32(st.cu), i32(st.lens), mask, mask_rows, out, lse)
+    mcp.mixed_attn_fwd_tree(plan, *args, ws)
+    with pytest.raises(_capi.MCPError) as e:
+        mcp.check_device_errors(mcp.workspace_error_word(plan, ws))
+    assert e.value.status == _capi.MCP_ERR_TIMEOUT
+    trees = torch.as_tensor([True] * 40 + [False] + [True] * 20).cuda()
+    assert torch.isnan(out[trees]).all() and not torch.isnan(out[~trees]).any()
+    desc, options = plan.desc, mcp.PlanOptions(tree=1)
+    big = torch.empty(max(ws.numel(), mcp.mixed_attn_plan(desc, st.cu, st.lens, options).workspace_bytes),
+                      dtype=torch.uint8, device="cuda")
+    plan = mcp.mixed_attn_plan(desc, st.cu, st.lens, options, big)
+    mcp.mixed_attn_fwd_tree(plan, *args, big)
+    mcp.check_device_errors(mcp.workspace_error_word(plan, big))
+    st.compare(out, lse)
+
+
+def test_attention_past_32_bits(mcp):
+    """Pages whose elements lie past 2^31 of the caches."""
+    P, H, D, pages = 16, 8, 128, (1 << 31) // (16 * 8 * 128) + 64
+    st = Step([(20, 300, "tree"), (1, 100, None), (34, 90, "star")], 8, H, D, P, seed=13)
+    big_k = torch.empty((pages, P, H, D), dtype=torch.bfloat16, device="cuda")
+    big_v = torch.empty_like(big_k)
+    used = torch.as_tensor(np.unique(st.bt[st.bt >= 0])).cuda()
+    top = pages - 1 - torch.arange(st.pages, device="cuda")
+    big_k[top[used]], big_v[top[used]] = st.k[used], st.v[used]
+    big_v[top[used[0]]] = st.v[used[0]]
+    st.bt = np.where(st.bt >= 0, pages - 1 - st.bt, -1)
+    st.k, st.v, st.pages = big_k, big_v, pages
+    st.check(mcp, *st.run(mcp))
+    page, off = st.slots(0, np.array([300 + 5]))
+    st.v[page, off, 0, 0] = float("inf")  # read again by the rows that see it
+    out, _ = st.run(mcp)
+    sees = torch.as_tensor(st.bits[0][:, 5]).cuda()
+    assert torch.isinf(out[:20][sees][:, 0, 0].float()).all()
+    assert torch.isfinite(out[:20][~sees].float()).all()
+
+
 # ----------------------------------------------------------------------- verification
 class Drafts:
     """Trees of drafted tokens with the probabilities that they are tried against."""
@@ -560,6 +605,36 @@ def test_verified_tokens_are_distributed_like_the_target(mcp, draft):
     assert (np.abs(first - p) < 5 * np.sqrt(p * (1 - p) / S)).all()  # five standard deviations
 
 
+def test_verify_rows_past_32_bits(mcp):
+    """The last rows of matrices of more than 2^31 elements."""
+    V, n = 100000, 6
+    R = (1 << 31) // V + 20
+    d = Drafts([n], V, "bf16", "tree", True, seed=16)
+    target, draft = (torch.empty((R, V), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    target[R - n:], draft[R - n:] = d.target, d.draft
+    tokens, parents = (torch.full((R,), -1, dtype=torch.int32, device="cuda") for _ in range(2))
+    tokens[R - n:], parents[R - n:] = i32(d.tokens), i32(d.parents)
+    u = torch.zeros(R, device="cuda")
+    u[R - n:] = torch.tensor(d.u)
+    accepted, path, new = mcp.verify_drafts(target, tokens, i32([R - n, R]), u, torch.tensor(d.u_last).cuda(),
+                                            parents=parents, draft_probs=draft)
+    want = d.want()
+    assert accepted.tolist() == want[0].tolist()
+    assert path[R - n:].tolist() == want[1].tolist() and new[R - n:].tolist() == want[2].tolist()
+
+
+def test_verify_at_once_on_two_streams(mcp):
+    a, b = (Drafts([7] * 50, 40000, "fp32", "tree", True, seed=s) for s in (17, 18))
+    want = [a.run(mcp), b.run(mcp)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [d.run(mcp, stream=st) for d, st in zip((a, b), streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
 def test_verify_refusals(mcp):
     d = Drafts([3, 4], 50)
     d.run(mcp)
@@ -666,6 +741,20 @@ def test_keep_leaves_out_pages_outside_the_pool(mcp):
     c, d = st.slots(0, np.array([10 + 38]))
     before[a, b] = before[c, d]  # the one move whose pages are there
     assert torch.equal(st.k.view(torch.int16), before.view(torch.int16))
+
+
+def test_keep_past_32_bits(mcp):
+    P, H, D, pages = 16, 8, 128, (1 << 31) // (16 * 8 * 128) + 8
+    k = torch.zeros((pages, P, H, D), dtype=torch.bfloat16, device="cuda")
+    k[pages - 1, 3], k[2, 1] = 5, 7
+    v = k.clone()
+    bt = i32([[1, pages - 2], [2, pages - 1]])
+    new = mcp.kv_keep_path(k, v, bt, i32([0, 20, 40]), i32([20, 20]), i32([1, 3]),
+                           i32([0] + [-1] * 19 + [0, 17, 19] + [-1] * 17))
+    assert new.tolist() == [1, 3]
+    for c in (k, v):
+        assert (c[2, 2] == 5).all() and (c[2, 1] == 0).all() and (c[pages - 1, 3] == 5).all()
+        assert float(c.float().sum()) == 2 * 5 * H * D
 
 
 def test_keep_refusals(mcp):
