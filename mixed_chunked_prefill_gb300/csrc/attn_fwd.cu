@@ -39,6 +39,9 @@
 //
 // A split KV range writes (O, LSE) partials that combine.cu merges.
 //
+// The kTree instantiations (mcp_mixed_attn_fwd_tree) also run segments that are
+// trees of drafted tokens: see "trees of drafted tokens" below.
+//
 // Every mbarrier wait is bounded in time.  On time-out the CTA records
 // MCP_DEVERR_TIMEOUT in the error word, every role leaves its loop, in-flight
 // TMA copies and MMAs are drained (again with a bound), TMEM is freed and the
@@ -261,6 +264,14 @@ __device__ __forceinline__ int oob_block(const KParams& p) {
 // whose bit its mask row sets; what it does not see lies in the segment's last
 // Lq keys, so only the tiles that reach past the history read the mask (one to
 // three of them an item: the rest of the item runs as in a causal step).
+//
+// A tree takes tensor-core tiles whatever its size.  Up to 128 query rows a kv head
+// (32 tokens at G = 4) it is bound by HBM: 57 trees over 16384 keys, 4 to 32 tokens
+// each, 6.7 to 6.8 TB/s (a copy makes 6.8).  From two tiles on, which share K/V through
+// L2, by the 0.9 us that a tile of 128 x 128 takes (64 tokens each 1.2 PFLOP/s, 4.8
+// TB/s), and at a few hundred keys by the 6 us around an item's tiles (152 trees over
+// 1024 keys 4.2 TB/s): loads of the item, its segment and its first pages in a row, the
+// first tile from memory, the epilogue.
 struct TreeRow {
   const uint32_t* words;  // the token's mask row (nullptr: none, it sees itself alone)
   int num_words, hist, tok;
