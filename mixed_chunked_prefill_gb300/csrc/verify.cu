@@ -21,6 +21,12 @@
 // about 2 V d a token, 1% with the 2^-24 of fp32 at V = 128000.  Values and sums are
 // therefore pairs of fp32, about 2^-46 (fp64 would take the pass from its loads to
 // the fp64 unit: 2 a clock and SM).
+//
+// Measured: 64 chains of 4 to 8 rows of 128000 fp32 values (65 MB of p and q where the
+// walks end) 19.2 us, the pass itself at 5.5 TB/s behind 5 us of loads that depend on
+// each other; 32 trees of up to 32 rows, some with eight passes, 25.4; 256 given trees of
+// 50257 bf16 values 20.0 (26 MB, bound by the latencies and the sums' operations); one
+// chain 7.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,7 +48,7 @@ constexpr int kMaxNodes = 1024;
 constexpr int kGoneBits = 65536;  // of the bitmap of refused tokens
 constexpr int kSlots = 8;         // 16-byte pieces that a thread has in flight
 constexpr int kSlotsGiven = 6;    // without q, where the bitmap takes the room of two
-constexpr int kPerSM = 4;        // CTAs
+constexpr int kPerSM = 4;         // CTAs
 
 // ------------------------------------------------------- sums of two fp32
 struct Two {
@@ -355,6 +361,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -471,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM) verify_kernel(const VerifyAr
     return;
   }
   const float u_last = p.u_last[s];
-  if (C > 1) cluster_arrive();  // this CTA runs; waited for before the first remote write
+  if (C > 1) cluster_arrive_relaxed();  // this CTA runs; waited for before the first remote write
   const T* const P = static_cast<const T*>(p.target);
   const T* const Q = static_cast<const T*>(p.draft);
   // every node's token under its parent's rows
@@ -594,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, kPerSM) verify_kernel(const VerifyAr
     if (C == 1) {
       __syncthreads();
     } else {
-      cluster_arrive();
+      if (warp == 0) cluster_arrive();
+      else cluster_arrive_relaxed();
       cluster_wait();
     }
     ++passes;
@@ -709,7 +719,8 @@ __global__ void __launch_bounds__(kThreads, kPerSM) verify_kernel(const VerifyAr
 }
 
 // CTAs that share a segment: as many as the GPU has room for at once, but none with
-// less than 4096 values of a row.
+// less than 4096 values of a row.  With 4, 8 and 16 of them 64 chains took 27, 21 and 32
+// us, one chain 13.6, 10.3 and 8.5; with 1, 2 and 4 256 given trees 35, 27 and 32.
 int cluster_of(const mcp_verify_desc& d) {
   int c = kMaxCluster;
   while (c > 1 && (static_cast<int64_t>(d.num_seqs) * c > kPerSM * static_cast<int64_t>(step_num_sms()) || d.vocab_size / c < 4096))
