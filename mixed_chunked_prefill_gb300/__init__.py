@@ -886,7 +886,9 @@ def _layers(caches, name, dev, shape):
         if len(full) == 5:
             one, stride = full[1:], caches.stride(0)
             if full[0] and stride and (shape is None or one == shape):
-                return one, full[0], stride, ctypes.c_void_p(_arg(caches, bf16, name, dev))
+                # K and V may alternate in one pool: each layer's cache is dense, not all of them
+                first = caches if caches.is_contiguous() else caches[0]
+                return one, full[0], stride, ctypes.c_void_p(_arg(first, bf16, name, dev))
         elif len(full) == 4:
             caches = (caches,)
         else:

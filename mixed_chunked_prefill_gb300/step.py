@@ -80,12 +80,12 @@ class StepTrees:
         with _on_stream(stream, dev):
             if not isinstance(parents, torch.Tensor):
                 parents = torch.from_numpy(_i32(parents))
-            self.parents = parents.to(dev)
+            self.parents = parents.to(device=dev, dtype=torch.int32)
             self.mask_rows = torch.from_numpy(_i32(np.where(is_tree, rows[:-1], -1))).to(dev)
-            self.tree_mask = torch.empty((int(rows[-1]), words), dtype=torch.int32, device=dev)
-            self.positions = torch.empty(self.parents.shape[0], dtype=torch.int32, device=dev)
-            if self.parents.shape[0] < int(cu[-1]):
-                raise ValueError("parents must have an entry for each token of the step")
+            self.tree_mask = torch.zeros((int(rows[-1]), words), dtype=torch.int32, device=dev)
+            if self.parents.dim() != 1 or self.parents.shape[0] < int(cu[-1]):
+                raise ValueError("parents must be [T], an entry for each token of the step")
+            self.positions = torch.zeros(self.parents.shape[0], dtype=torch.int32, device=dev)
             build_tree_masks(self.parents, cu_d, seqlens_k_d, self.mask_rows, self.tree_mask,
                              self.positions, error_word, stream)
 

@@ -328,6 +328,33 @@ def test_chains_are_causal(mcp):
     assert torch.equal(out, causal) and torch.equal(lse, cl)
 
 
+def test_attention_of_padded_rows(mcp):
+    """Queries behind the step's tokens are padding: their rows are not written."""
+    st = Step([(9, 40, "tree"), (1, 10, None)], 8, 2, 128, 16, seed=14)
+    plan, ws = st.plan(mcp)
+    mask, mask_rows = st.masks()
+    q = torch.cat([st.qs, torch.full((6, 8, 128), float("nan"), dtype=torch.bfloat16, device="cuda")])
+    out, lse = torch.full_like(q, 7.0), torch.full((st.T + 6, 8), 7.0, device="cuda")
+    mcp.mixed_attn_fwd_tree(plan, q, st.k, st.v, i32(st.bt), i32(st.cu), i32(st.lens), mask, mask_rows, out, lse, ws)
+    mcp.check_device_errors(mcp.workspace_error_word(plan, ws))
+    st.compare(out[:st.T], lse[:st.T])
+    assert (out[st.T:] == 7).all() and (lse[st.T:] == 7).all()
+
+
+@pytest.mark.parametrize("hq,hkv", [(128, 1), (100, 1), (64, 1), (66, 2)])
+def test_attention_of_large_groups(mcp, hq, hkv):
+    """One to three tokens a tile."""
+    st = Step([(7, 150, "tree"), (3, 300, "star"), (1, 40, None)], hq, hkv, 64, 16, seed=hq)
+    st.check(mcp, *st.run(mcp))
+
+
+def test_attention_of_a_mask_of_many_words(mcp):
+    """More tokens than build_tree_masks takes: any mask of 1100 tokens."""
+    st = Step([(1100, 200, "chain")], 2, 1, 64, 16, seed=15)
+    st.bits = [st.rng.random((1100, 1100)) < 0.3]
+    st.check(mcp, *st.run(mcp))
+
+
 def test_attention_refusals(mcp):
     st = Step([(4, 10, "tree")], 4, 2, 64, 16)
     plan, ws = st.plan(mcp)
@@ -555,6 +582,17 @@ def test_verify_entries_that_are_no_probabilities(mcp):
     d.check(mcp, bits=mcp.DEVERR_PROBS)
 
 
+def test_verify_nothing(mcp):
+    """No segments, no rows, segments without rows."""
+    f = torch.zeros(0, device="cuda")
+    none = torch.zeros((0, 50), device="cuda")
+    got = mcp.verify_drafts(none, i32([]), i32([0]), f, f)
+    assert [x.shape[0] for x in got] == [0, 0, 0]
+    err = err_word()
+    got = mcp.verify_drafts(none, i32([]), i32([0, 0, 0]), f, torch.zeros(2, device="cuda"), error_word=err)
+    assert got[0].tolist() == [0, 0] and bits_of(err) == 0
+
+
 def test_verify_malformed_drafts(mcp):
     d = Drafts([5, 5], 100, "fp32", "tree", True, seed=12)
     d.u[:] = 0.0
@@ -689,6 +727,24 @@ def test_keep(mcp, P, layers, H, D):
     mcp.kv_keep_path(list(lists[0]), lists[1], *args)
     for got, w in zip(lists, want):
         assert all((a.view(torch.int16).cpu().numpy() == b).all() for a, b in zip(got, w))
+
+
+def test_keep_in_a_pool_of_both(mcp):
+    """K and V of each layer side by side in one tensor."""
+    st = Step([(9, 20, None), (4, 7, None)], 2, 2, 64, 16, seed=8)
+    pool = torch.randn((3, 2, st.pages, 16, 2, 64), device="cuda").to(torch.bfloat16)
+    want = pool.view(torch.int16).cpu().numpy()
+    accepted, path = [3, 2], [0, 4, 7] + [-1] * 6 + [0, 3, -1, -1]
+    for layer in range(3):
+        for half in range(2):
+            for s in range(2):
+                ref.keep(want[layer, half], st.bt[s], st.hist[s],
+                         path[st.cu[s]:st.cu[s] + accepted[s]], 16)
+    mcp.kv_keep_path(pool[:, 0], pool[:, 1], i32(st.bt), i32(st.cu), i32(st.lens), i32(accepted), i32(path))
+    assert (pool.view(torch.int16).cpu().numpy() == want).all()
+    with pytest.raises(ValueError):  # a layer's cache that is not dense
+        mcp.kv_keep_path(pool[:, 0, :, ::2], pool[:, 1, :, ::2], i32(st.bt), i32(st.cu), i32(st.lens),
+                         i32(accepted), i32(path))
 
 
 def test_keep_of_steps_with_chunks(mcp):
@@ -855,12 +911,13 @@ def test_captured_and_replayed(mcp):
     """Masks, attention, verification and keep in one graph, replayed with other trees, drafts and
     contents; a second graph over the same workspace in turn."""
     def fresh(seed):
-        st = Step([(20, 100, "tree"), (1, 40, None), (33, 260, "tree")], 8, 2, 128, 16, seed=seed)
+        st = Step([(20, 100, "tree"), (1, 40, None), (33, 2100, "tree")], 8, 2, 128, 16, seed=seed)
         return st, Drafts(st.q, 9000, "fp32", "tree", True, seed=seed)
 
     st, d = fresh(1)
     d.parents = st.parents
     plan, ws = st.plan(mcp)
+    assert plan.num_combine > 0
     mask = torch.zeros((53, 2), dtype=torch.int32, device="cuda")
     mask_rows = i32([0, -1, 20])
     buf = dict(parents=i32(st.parents), bt=i32(st.bt), tokens=i32(d.tokens), u=torch.tensor(d.u).cuda(),
