@@ -241,8 +241,9 @@ void build(const mcp_attn_desc& d, const int32_t* cu, const int32_t* sk, int num
     // Steps with trees are short and few rows: their estimates include the cold
     // caches that a tree's few tiles do not hide (measured 8 us an item and 0.9 us
     // a tile), splits go down to 512 keys, and the combine that a split brings
-    // counts (a tree of 32 tokens over 8192 keys, splits of 512 / 1024 / 2048 keys:
-    // 22 / 22 / 27 us; 32 trees over 1024 keys unsplit 36 us, in 512s 61).
+    // counts (a tree of 32 tokens over 8192 keys, splits of 512 / 768 / 1024 / 2048
+    // keys: 19.1 / 17.4 / 18.2 / 22.7 us; 16 trees over 1000 to 4000 keys unsplit 44.6
+    // us, in 512s 78).
     const bool tree = o && o->tree;
     const double tile_ns = (tree ? 900.0 : 750.0) * DK / 128.0, item_ns = tree ? 8000.0 : 5000.0;
     double pre_ns = 0.0, dec_ns = 0.0;
@@ -294,14 +295,14 @@ void build(const mcp_attn_desc& d, const int32_t* cu, const int32_t* sk, int num
           load.back() += c;
           std::push_heap(load.begin(), load.end(), std::greater<double>());
         }
-        const double combine = !tree || parts == 1 ? 0.0 : 4000.0 + 250.0 * std::max<int64_t>(0, parts - 8);
+        const double combine = !tree || parts == 1 ? 0.0 : 4000.0 + 400.0 * std::max<int64_t>(0, parts - 8);
         return *std::max_element(load.begin(), load.end()) + combine;
       };
       const double t0 = makespan(ps);
       const int64_t ps_sig = signature(ps);
       int64_t best = ps, last_sig = -1;
       double best_t = t0;
-      for (int64_t cand = 65536; cand >= (tree ? 512 : 2048); cand = cand > 2048 || !tree ? cand / 2 : cand - 512) {
+      for (int64_t cand = 65536; cand >= (tree ? 512 : 2048); cand = cand > 2048 || !tree ? cand / 2 : cand - 256) {
         // candidates finer than the rule's split stop past sixteen items per SM
         // (counts grow as cand shrinks); coarser ones are always evaluated
         if (cand < ps && count(ds, cand) > 16LL * std::max(1, num_sms)) break;

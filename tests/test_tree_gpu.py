@@ -244,6 +244,17 @@ def test_attention_with_split_keys(mcp, split, D, P):
     st.check(mcp, *st.run(mcp, prefill_split_tokens=split))
 
 
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("hist", [1200, 5200])
+def test_attention_with_many_parts(mcp, D, hist):
+    """10 and 41 parts of a row; few rows and more than the GPU merges at once."""
+    st = Step([(5, hist, "tree")], 8, 2, D, 16, seed=D + hist)
+    st.check(mcp, *st.run(mcp, prefill_split_tokens=128))
+    if hist == 1200:
+        st = Step([(30, hist, "tree")] * 4, 64, 2, D, 16, seed=D)
+        st.check(mcp, *st.run(mcp, prefill_split_tokens=640))
+
+
 def test_attention_of_any_mask_of_tokens_before(mcp):
     """Masks that no tree has: bits of tokens behind a token, and of words that are not there, do
     not count; rows with more words than their tree needs."""
