@@ -969,8 +969,9 @@ typedef struct mcp_verify_tensors {
  * vocabulary hangs under none (>= vocab_size sets MCP_DEVERR_TOKEN_RANGE, a
  * negative one is padding), and so does a node whose parent is not before it
  * (MCP_DEVERR_TREE).  A segment past total_rows, of more than 1024 rows or with
- * decreasing cu_rows sets MCP_DEVERR_SEGMENT (accepted 0, nothing else written).  Rows need the alignment of their type only; they are read twice as
- * fast where both matrices and their strides are multiples of 16 bytes.
+ * decreasing cu_rows sets MCP_DEVERR_SEGMENT (accepted 0, nothing else written).
+ * Rows need the alignment of their type only; they are read 16 bytes at a time
+ * where a token's rows in both matrices begin at the same place of their 16 bytes.
  * num_seqs <= 2^20, total_rows <= 2^30, vocab_size <= 2^28.
  */
 mcp_status mcp_verify_drafts(const mcp_verify_desc* desc, const mcp_verify_tensors* tensors,

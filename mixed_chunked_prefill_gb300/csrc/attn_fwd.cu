@@ -403,32 +403,7 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
     const uint64_t dV0 = ptx::sdesc_sw128(sV(0), B * 128, B == 16 ? 1024 : C::kHalves * 1024);
     // first tile that reaches past the history
     const int t_tree = tree ? max(sg.hist - kv0, 0) / kKvTile : ntiles;
-    bool ok = true;
-    for (int t = 0; ok && t < ntiles; ++t) {
-      // P(t) barriers alternate with the tile parity, like the S buffers: the
-      // barrier is reused by tile t + 2 only after Q K^T(t + 2), which waits
-      // for this P V(t), so no waiter falls two phases behind
-      const int s = t % C::kVStages;
-      if constexpr (kTree) {
-        // P is 0 where a row does not see a token of its tree, but 0 * inf is
-        // not: infinities and NaN of the tree's V rows are taken out of the
-        // product and added in the epilogue to the rows that see them.  Done
-        // while the softmax works on this tile (after it, the 32 loads a lane for
-        // 64 tokens of 128 columns stood in front of the item's last product:
-        // 1.6 us an item).
-        if (t >= t_tree) {
-          if (!(ok = wait_on(c, c.b(BV0 + s), (t / C::kVStages) & 1))) break;
-          const int key0 = kv0 + t * kKvTile;
-          if (take_nonfinite<D>(gb + (sV(s) - base), max(sg.hist - key0, 0), min(kv1 - key0, kKvTile),
-                                p.box_log2, lane)) {
-            if (lane == 0) *nonfinite = 1;
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-      }
-      if (!(ok = wait_on(c, c.b(BP0 + (t & 1)), (t >> 1) & 1))) break;
-      if (!(ok = wait_on(c, c.b(BV0 + s), (t / C::kVStages) & 1))) break;
+    auto clear_rows = [&](int t, int s) {
       const int nval = kv1 - (kv0 + t * kKvTile);
       if (nval < kKvTile && (nval & (B - 1))) {
         // Rows past the item's last key inside its last box may be unused
@@ -446,6 +421,37 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
         ptx::fence_proxy_async_smem();
         __syncwarp();
       }
+    };
+    bool ok = true;
+    for (int t = 0; ok && t < ntiles; ++t) {
+      // P(t) barriers alternate with the tile parity, like the S buffers: the
+      // barrier is reused by tile t + 2 only after Q K^T(t + 2), which waits
+      // for this P V(t), so no waiter falls two phases behind
+      const int s = t % C::kVStages;
+      if constexpr (kTree) {
+        // P is 0 where a row does not see a token of its tree, but 0 * inf is
+        // not: infinities and NaN of the tree's V rows are taken out of the
+        // product and added in the epilogue to the rows that see them.  That, and
+        // the rows behind the last key, while the softmax works on this tile: after
+        // it, the 32 loads a lane for 64 tokens of 128 columns stood in front of the
+        // item's last product (1.6 us an item; the clearing 0.4: 48 trees and 2
+        // chunks 331 us, with it here 327).
+        if (t >= t_tree || t == ntiles - 1) {
+          if (!(ok = wait_on(c, c.b(BV0 + s), (t / C::kVStages) & 1))) break;
+          clear_rows(t, s);
+          const int key0 = kv0 + t * kKvTile;
+          if (t >= t_tree &&
+              take_nonfinite<D>(gb + (sV(s) - base), max(sg.hist - key0, 0), min(kv1 - key0, kKvTile),
+                                p.box_log2, lane)) {
+            if (lane == 0) *nonfinite = 1;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+      }
+      if (!(ok = wait_on(c, c.b(BP0 + (t & 1)), (t >> 1) & 1))) break;
+      if (!(ok = wait_on(c, c.b(BV0 + s), (t / C::kVStages) & 1))) break;
+      if constexpr (!kTree) clear_rows(t, s);
       ptx::tc_fence_after();
       if (lane == 0) {
         const uint64_t dv = dV0 + static_cast<uint64_t>((s * C::kKvBytes) >> 4);

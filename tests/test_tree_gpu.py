@@ -841,6 +841,58 @@ def test_keep_refusals(mcp):
             mcp.kv_keep_path(**{**good, name: bad})
 
 
+# ---------------------------------------------------------- a step of host metadata
+@pytest.mark.parametrize("some_rows", [False, True])
+def test_a_step_of_host_metadata(mcp, some_rows):
+    """MixedStep built from lists on the host: its masks and positions, the append of the step's
+    K/V, and the attention of all rows or of some."""
+    from mixed_chunked_prefill_gb300.step import MixedStep
+
+    st = Step(SEGMENTS, 8, 2, 128, 16, seed=31)
+    own = [st.slots(s, np.arange(h, n)) for s, (h, n) in enumerate(zip(st.hist, st.lens))]
+    at = tuple(torch.cat(x) for x in zip(*own))
+    k_new, v_new = st.k[at].clone(), st.v[at].clone()
+    st.k[at] = st.v[at] = float("nan")
+    rows = np.flatnonzero(st.rng.random(st.T) < 0.3) if some_rows else None
+    options = mcp.PlanOptions(split_kv=256)
+    step = MixedStep(st.hq, st.hkv, st.D, st.P, st.pages, st.scale, st.cu, st.lens, st.bt, options=options,
+                     rows=rows, trees=st.tree, parents=st.parents)
+    assert options.tree == 0  # the caller's stay as they were
+    bits, depths = zip(*(ref.tree_rows(st.parents[a:b]) for a, b in zip(st.cu, st.cu[1:])))
+    assert step.trees.positions.tolist() == [h + int(x) for h, d in zip(st.hist, depths) for x in d]
+    mask, mask_rows = st.masks()
+    assert torch.equal(step.trees.tree_mask, mask) and torch.equal(step.trees.mask_rows, mask_rows)
+    out = torch.full_like(st.qs, float("nan"))
+    lse = torch.full((st.T, st.hq), float("nan"), device="cuda")
+    step.run(st.qs, k_new, v_new, st.k, st.v, out, lse)
+    step.check()
+    st.compare(out, lse, rows)
+    if some_rows:
+        others = np.setdiff1d(np.arange(st.T), rows)
+        assert torch.isnan(out[others]).all() and torch.isnan(lse[others]).all()
+
+
+def test_a_step_of_host_metadata_refusals(mcp):
+    from mixed_chunked_prefill_gb300.step import MixedStep
+
+    def step(q, hist, **more):
+        lens = [a + b for a, b in zip(q, hist)]
+        width = -(-max(lens) // 16)
+        bt = np.arange(len(q) * width).reshape(len(q), width)
+        return MixedStep(4, 2, 64, 16, bt.size, 0.125, cumulated(q), lens, bt, **more)
+
+    step([3, 1], [5, 9], trees=[True, False], parents=[-1, 0, 0, -1])
+    step([1024], [0], trees=[True], parents=np.arange(1024) - 1).check()
+    for bad in (dict(trees=[True, False]), dict(parents=[-1, 0, 0, -1]),
+                dict(trees=[True], parents=[-1, 0, 0, -1]), dict(trees=[True, False], parents=[-1, 0, 0]),
+                dict(trees=[True, False], parents=[[-1, 0, 0, -1]])):
+        with pytest.raises(ValueError):
+            step([3, 1], [5, 9], **bad)
+    with pytest.raises(ValueError):  # a tree of more tokens than a mask has bits
+        step([1025], [0], trees=[True], parents=np.arange(1025) - 1)
+    step([1025], [0], trees=[False], parents=np.arange(1025) - 1).check()  # a chunk has no limit
+
+
 # ------------------------------------------------------------------ all of them together
 def test_serving_with_drafted_trees(mcp):
     """Requests served with trees beside chunks and decodes: tables, masks, append, attention,
