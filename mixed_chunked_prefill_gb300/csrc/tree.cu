@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) tree_masks_kernel(const MaskArgs p) 
     if (n < 0 && tid == 0 && p.err) atomicOr(p.err, MCP_DEVERR_SEGMENT);
     return;
   }
-  int bad = hist < 0 ? MCP_DEVERR_SEGMENT : 0;
+  int bad = p.sk[s] < n ? MCP_DEVERR_SEGMENT : 0;
   const bool outside = t0 < 0 || t1 > p.T;
   if (outside) bad |= MCP_DEVERR_SEGMENT;
   const bool tree = m0 >= 0;
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kKeepThreads)
   const int r0 = p.cu_rows[s], n = p.cu_rows[s + 1] - r0, m = p.accepted[s];
   int bad = 0;
   bool move = n == lq && lq > 0;
-  if (lq < 0 || n < 0 || hist < 0 || r0 < 0 || r0 > p.total_rows - n ||
+  if (lq < 0 || n < 0 || sk < lq || r0 < 0 || r0 > p.total_rows - n ||
       sk > static_cast<int64_t>(p.max_pages) << p.page_log2) {
     bad = MCP_DEVERR_SEGMENT;
     move = false;

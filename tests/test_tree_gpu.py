@@ -121,6 +121,15 @@ def test_masks_of_malformed_trees(mcp):
     assert bits_of(err) == mcp.DEVERR_SEGMENT
 
 
+def test_masks_of_lengths_at_the_end_of_32_bits(mcp):
+    for low in (-(1 << 31), -1, 3):
+        for rows in ([0], [-1]):
+            err, mask = err_word(), torch.zeros((4, 1), dtype=torch.int32, device="cuda")
+            mcp.build_tree_masks(i32([-1, 0, 0, 1]), i32([0, 4]), i32([low]), i32(rows), mask, None, err)
+            assert bits_of(err) == mcp.DEVERR_SEGMENT
+            assert mask[:, 0].tolist() == ([1, 3, 5, 11] if rows == [0] else [0] * 4)
+
+
 # ------------------------------------------------------------------------ attention
 class Step:
     """A step of segments (tokens, history, shape or None for causal) with random contents."""
@@ -794,6 +803,18 @@ def test_keep_of_malformed_paths(mcp, accepted, path, change, bits):
                            error_word=err)
     assert bits_of(err) == getattr(mcp, "DEVERR_" + bits)
     assert new.tolist() == list(sk) and torch.equal(st.k.view(torch.int16), before.view(torch.int16))
+
+
+def test_keep_of_lengths_at_the_end_of_32_bits(mcp):
+    st = Step([(5, 30, "chain"), (1, 3, None)], 2, 2, 64, 16)
+    k, v = st.k.clone(), st.v.clone()
+    for low in (-(1 << 31), -(1 << 31) + 4, -1, 4):
+        err = err_word()
+        new = mcp.kv_keep_path(st.k, st.v, i32(st.bt), i32(st.cu), i32([low, 4]), i32([2, 1]),
+                               i32([0, 2, -1, -1, -1, 0]), error_word=err)
+        assert bits_of(err) == mcp.DEVERR_SEGMENT and new.tolist() == [low, 4]
+    assert (k.view(torch.int16) == st.k.view(torch.int16)).all()
+    assert (v.view(torch.int16) == st.v.view(torch.int16)).all()
 
 
 def test_keep_leaves_out_pages_outside_the_pool(mcp):
