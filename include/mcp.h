@@ -875,12 +875,13 @@ mcp_status mcp_process_logits(const mcp_logits_desc* desc, const mcp_logits_tens
  * mcp_build_tree_masks fills the rows and, unless NULL, positions [T]: history
  * (seqlens_k minus the segment's tokens) plus depth, in causal segments plus
  * the place.  Rows that no segment has, and positions behind the last segment,
- * stay as they were.  A parent that is not before its token (the token is
- * taken for one without) and a tree that exceeds 32 * mask_words tokens or
+ * stay as they were; segments may not share rows.  A parent that is not before
+ * its token (the token is taken for one without) and a tree that exceeds 32 * mask_words tokens or
  * num_mask_rows (its rows and positions are left out) set MCP_DEVERR_TREE; a
  * segment past total_tokens or with seqlens_k < its tokens MCP_DEVERR_SEGMENT
  * (the first is left out).
- * All arrays are device int32.  num_seqs <= 2^20, total_tokens and
+ * All arrays are device int32; the two results overlap neither each other nor an
+ * input.  num_seqs <= 2^20, total_tokens and
  * num_mask_rows <= 2^30, mask_words <= 32: trees of up to 1024 tokens.
  */
 mcp_status mcp_build_tree_masks(const int32_t* parents, const int32_t* cu_seqlens_q,
@@ -972,6 +973,7 @@ typedef struct mcp_verify_tensors {
  * decreasing cu_rows sets MCP_DEVERR_SEGMENT (accepted 0, nothing else written).
  * Rows need the alignment of their type only; they are read 16 bytes at a time
  * where a token's rows in both matrices begin at the same place of their 16 bytes.
+ * The results overlap neither each other nor an input.
  * num_seqs <= 2^20, total_rows <= 2^30, vocab_size <= 2^28.
  */
 mcp_status mcp_verify_drafts(const mcp_verify_desc* desc, const mcp_verify_tensors* tensors,
@@ -1013,7 +1015,8 @@ typedef struct mcp_keep_desc {
  * total_rows or past its table row (MCP_DEVERR_SEGMENT) move nothing and give
  * new_lens = seqlens_k; a page outside the pool (MCP_DEVERR_PAGE_RANGE) leaves
  * out its token's row.  num_kv_heads * head_dim a multiple of 8; num_layers <=
- * 1024; pages of different segments must differ where they are written.
+ * 1024; pages of different segments must differ where they are written, and
+ * new_lens overlaps no input.
  */
 mcp_status mcp_kv_keep_path(const mcp_keep_desc* desc, void* const* k_caches, void* const* v_caches,
                             const int32_t* block_tables, const int32_t* cu_seqlens_q,

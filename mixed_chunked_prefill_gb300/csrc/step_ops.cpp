@@ -44,6 +44,30 @@ mcp_status check_words(std::initializer_list<const void*> arrays) {
   return MCP_OK;
 }
 
+// An array that a call reads or writes (NULL: none)
+struct Span {
+  const void* at;
+  unsigned __int128 bytes;  // rows times a stride
+};
+Span words(const void* at, int64_t n) { return {at, static_cast<unsigned __int128>(n) * 4}; }
+
+// The first CTA of a segment writes results while the others still read, and where CTAs
+// exchange sums they have to take the same steps: a result may not be an input, nor two
+// results one.
+mcp_status check_apart(std::initializer_list<Span> results, std::initializer_list<Span> inputs) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x && y && a.bytes && b.bytes && (x < y ? y - x < a.bytes : x - y < b.bytes);
+  };
+  for (const Span* r = results.begin(); r != results.end(); ++r) {
+    for (const Span& i : inputs)
+      if (meet(*r, i)) return fail(MCP_ERR_INVALID_ARG, "a result may not overlap an input");
+    for (const Span* q = results.begin(); q != r; ++q)
+      if (meet(*r, *q)) return fail(MCP_ERR_INVALID_ARG, "results may not overlap each other");
+  }
+  return MCP_OK;
+}
+
 #define MCP_TRY(expr)                    \
   do {                                   \
     const mcp_status st_ = (expr);       \
@@ -325,6 +349,10 @@ mcp_status mcp_build_tree_masks(const int32_t* parents, const int32_t* cu_seqlen
   if (num_seqs == 0 || total_tokens == 0) return done(0, "");
   if (!parents || !cu_seqlens_q || !seqlens_k || !mask_rows || (num_mask_rows > 0 && !tree_mask))
     return fail(MCP_ERR_INVALID_ARG, "NULL pointer argument");
+  MCP_TRY(check_apart({words(tree_mask, static_cast<int64_t>(num_mask_rows) * mask_words),
+                       words(positions, total_tokens)},
+                      {words(parents, total_tokens), words(cu_seqlens_q, num_seqs + 1),
+                       words(seqlens_k, num_seqs), words(mask_rows, num_seqs), words(error_word, 1)}));
   return done(mcp::launch_build_tree_masks(parents, cu_seqlens_q, seqlens_k, mask_rows, num_seqs,
                                            total_tokens, num_mask_rows, mask_words, tree_mask,
                                            positions, error_word, stream),
@@ -353,6 +381,16 @@ mcp_status mcp_verify_drafts(const mcp_verify_desc* d, const mcp_verify_tensors*
     return fail(MCP_ERR_INVALID_ARG, "target or draft misaligned");
   MCP_TRY(check_words({t->tokens, t->parents, t->cu_rows, t->uniform, t->final_uniform, t->accepted,
                        t->path, t->new_tokens, error_word}));
+  auto rows = [&](const void* at, int64_t stride) {
+    return Span{at, d->total_rows == 0 ? 0 : (static_cast<unsigned __int128>(d->total_rows - 1) * stride +
+                                              d->vocab_size) * size};
+  };
+  MCP_TRY(check_apart({words(t->accepted, d->num_seqs), words(t->path, d->total_rows),
+                       words(t->new_tokens, d->total_rows)},
+                      {rows(t->target, d->target_stride), rows(t->draft, d->draft_stride),
+                       words(t->tokens, d->total_rows), words(t->parents, d->total_rows),
+                       words(t->cu_rows, d->num_seqs + 1), words(t->uniform, d->total_rows),
+                       words(t->final_uniform, d->num_seqs), words(error_word, 1)}));
   return done(mcp::launch_verify_drafts(*d, *t, error_word, stream), "verify_drafts launch");
 }
 
@@ -392,6 +430,11 @@ mcp_status mcp_kv_keep_path(const mcp_keep_desc* d, void* const* k_caches, void*
   for (int32_t l = 0; l < (d->layer_stride && d->num_layers ? 1 : d->num_layers); ++l)
     if (!k_caches[l] || !v_caches[l] || !aligned(k_caches[l], 16) || !aligned(v_caches[l], 16))
       return fail(MCP_ERR_INVALID_ARG, "cache of layer %d is NULL or not 16-byte aligned", l);
+  MCP_TRY(check_apart({words(new_lens, d->num_seqs)},
+                      {words(block_tables, static_cast<int64_t>(d->num_seqs) * d->max_pages_per_seq),
+                       words(cu_seqlens_q, d->num_seqs + 1), words(seqlens_k, d->num_seqs),
+                       words(cu_rows, d->num_seqs + 1), words(accepted, d->num_seqs),
+                       words(path, d->total_rows), words(error_word, 1)}));
   return done(mcp::launch_kv_keep_path(*d, k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k,
                                        cu_rows, accepted, path, new_lens, error_word, stream),
               "kv_keep_path launch");

@@ -105,6 +105,46 @@ def test_kv_keep_path_refusals(lib, over, status):
     assert keep(lib, **over) == status
 
 
+def test_results_may_not_overlap(lib):
+    """A result at an input's address, over its last word, or at another result's."""
+    def at(i):
+        return P16 + (i << 16)
+
+    def refused(status):
+        return status == INVALID and b"overlap" in lib.mcp_last_error()
+
+    names = ("parents", "cu", "sk", "mask_rows", "mask", "positions", "err")
+    good = {n: at(i) for i, n in enumerate(names)}
+    ends = dict(parents=36, cu=8, sk=4, mask_rows=4, err=0, mask=76, positions=36)  # the last word
+    for result in ("mask", "positions"):
+        for other in names:
+            for off in (0, ends[other]):
+                a = {**good, result: good[other] + off}
+                if other != result:
+                    assert refused(lib.mcp_build_tree_masks(
+                        a["parents"], a["cu"], a["sk"], a["mask_rows"], 2, 10, 10, 2, a["mask"],
+                        a["positions"], a["err"], None)), (result, other, off)
+
+    names = [n for n, _ in _capi.VerifyTensors._fields_]
+    good = {n: at(i) for i, n in enumerate(names)}
+    ends = dict(target=4 * 1399 - 400, draft=4 * 1399 - 400, cu_rows=8, final_uniform=4, accepted=4)
+    for result in ("accepted", "path", "new_tokens"):
+        for other in names:
+            if other != result:
+                for off in (0, ends.get(other, 28)):
+                    a = {**good, result: good[other] + off}
+                    assert refused(verify(lib, a, target_stride=180, draft_stride=180)), (result, other, off)
+    for big in (1 << 40, (1 << 63) - 1):  # rows past all addresses
+        assert refused(verify(lib, {**good, "path": good["draft"] + 4}, draft_stride=big))
+
+    names = ("bt", "cu", "sk", "cu_rows", "accepted", "path", "err")
+    good = {n: at(i) for i, n in enumerate(names)}
+    ends = dict(bt=28, cu=8, sk=4, cu_rows=8, accepted=4, path=28, err=0)
+    for other in names:
+        for off in (0, ends[other]):
+            assert refused(keep(lib, **good, new_lens=good[other] + off)), (other, off)
+
+
 def test_tree_forward_refusals(lib):
     d = mcp.make_desc(2, 9, 8, 2, 64, 16, 4, 8, 0.125)
     cu, sk = [0, 1, 9], [20, 30]
