@@ -32,7 +32,9 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Parts written by a launch that this one began beside are read through L2 alone.
+// Parts (O and LSE) of a launch that this one began beside change while this kernel runs:
+// they are read through L2, by loads that stay behind griddepcontrol.wait (a plain load
+// of what is promised to be constant need not).
 template <bool kBeside, typename T>
 __device__ __forceinline__ T load_part(const T* p) {
   return kBeside ? __ldcg(p) : __ldg(p);
@@ -74,8 +76,8 @@ template <int D, bool kBeside, bool kBatched>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineEntry* __restrict__ ents,
                                                       int num_ents, int total_rows,
                                                       const int32_t* __restrict__ cu_q,
-                                                      const float* __restrict__ part_o,
-                                                      const float* __restrict__ part_lse,
+                                                      const float* part_o,  // by load_part
+                                                      const float* part_lse,
                                                       __nv_bfloat16* __restrict__ out,
                                                       float* __restrict__ lse, int hq, int G) {
   constexpr int V = D / 32;
@@ -91,6 +93,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineEntry* __rest
   const int n = e.num_splits;
   const int64_t pr0 = static_cast<int64_t>(e.part_row) + row;  // part k: row pr0 + k * e.rows
   if constexpr (kBeside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  auto lse_of = [&](int k) { return load_part<kBeside>(part_lse + pr0 + static_cast<int64_t>(k) * e.rows); };
 
   float acc[V];
 #pragma unroll
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineEntry* __rest
     constexpr int kBatch = 32 / V;
     const float* src = part_o + pr0 * D + lane * V;
     const int64_t step = static_cast<int64_t>(e.rows) * D;
-    const float lk = lane < n ? part_lse[pr0 + static_cast<int64_t>(lane) * e.rows] : neg_inf();
+    const float lk = lane < n ? lse_of(lane) : neg_inf();
     float w = 0.f;
     for (int k0 = 0; k0 < n; k0 += kBatch) {
       float o[kBatch][V];
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineEntry* __rest
     // few parts (every split chunk tile, most decodes): the LSEs and every
     // part's slice of O are loaded at once, one memory latency for the row
     float4 ov[8];
-    const float lk = lane < n ? part_lse[pr0 + static_cast<int64_t>(lane) * e.rows] : neg_inf();
+    const float lk = lane < n ? lse_of(lane) : neg_inf();
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < n)
@@ -145,11 +148,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineEntry* __rest
       }
     }
   } else {
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, part_lse[pr0 + static_cast<int64_t>(k) * e.rows]);
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, lse_of(k));
   M = warp_max(M);
   for (int k0 = 0; k0 < n; k0 += 32) {
     const int k = k0 + lane;
-    const float lk = k < n ? part_lse[pr0 + static_cast<int64_t>(k) * e.rows] : neg_inf();
+    const float lk = k < n ? lse_of(k) : neg_inf();
     const float w = (lk == neg_inf()) ? 0.f : ptx::ex2((lk - M) * kLog2e);
     L += w;
     const int cnt = n - k0 < 32 ? n - k0 : 32;

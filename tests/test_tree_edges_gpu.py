@@ -1,0 +1,52 @@
+"""Trees of drafted tokens on the GPU: calls that only some contents, lengths or orders of work bring
+about."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import draft_ref as ref  # noqa: F401
+from test_tree_gpu import Drafts, Step, bits_of, cumulated, err_word, i32, mcp  # noqa: F401
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------ attention
+@pytest.mark.parametrize("segments,hq,hkv,D,split", [
+    ([(6, 700, "tree")], 8, 2, 128, 128),                  # parts of a row at once
+    ([(6, 1500, "tree"), (1, 90, None)], 8, 2, 128, 128),  # in batches
+    ([(30, 1200, "tree")] * 4, 64, 2, 128, 640),           # more rows than the GPU merges at once
+    ([(5, 5200, "tree")], 4, 2, 128, 128),                 # more parts than lanes
+    ([(6, 900, "tree")], 4, 2, 64, 128), ([(6, 900, "forest")], 4, 2, 96, 128),
+    ([(6, 900, "chain")], 4, 2, 256, 128)])
+def test_replays_merge_the_parts_of_their_own_contents(mcp, segments, hq, hkv, D, split):  # noqa: F811
+    """A graph replayed without a pause: the merge, launched beside the forward, never takes parts
+    or LSEs that the replay before it left in the workspace."""
+    steps = [Step(segments, hq, hkv, D, 16, seed=s) for s in (41, 42, 43)]
+    steps[1].qs *= 4  # other LSEs, too
+    want = []
+    for st in steps:
+        out, lse = st.run(mcp, prefill_split_tokens=split)
+        st.check(mcp, out, lse)
+        want.append((out, lse))
+    st = steps[0]
+    plan, ws = st.plan(mcp, prefill_split_tokens=split)
+    assert plan.num_combine > 0
+    sets = [(s.qs, s.k, s.v, i32(s.bt), s.masks()[0]) for s in steps]
+    buf = [x.clone() for x in sets[0]]
+    mask_rows, cu, sk = st.masks()[1], i32(st.cu), i32(st.lens)
+    out, lse = torch.empty_like(st.qs), torch.empty((st.T, hq), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mcp.mixed_attn_fwd_tree(plan, buf[0], buf[1], buf[2], buf[3], cu, sk, buf[4], mask_rows, out, lse, ws)
+    got = []
+    for turn in range(9):
+        for b, x in zip(buf, sets[turn % 3]):
+            b.copy_(x)
+        graph.replay()
+        got.append((out.clone(), lse.clone()))
+    torch.cuda.synchronize()
+    for turn, pair in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(pair, want[turn % 3])), turn
