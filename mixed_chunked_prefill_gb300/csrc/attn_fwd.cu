@@ -853,6 +853,8 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = od[i];
           }
+          // the lanes' loops above are of different lengths, the next load is the warp's
+          if (bad_v) __syncwarp();
 #pragma unroll
           for (int v = 0; v < 2 * kBytes; ++v) {
             uint32_t w[4];

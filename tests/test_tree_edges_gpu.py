@@ -50,3 +50,34 @@ def test_replays_merge_the_parts_of_their_own_contents(mcp, segments, hq, hkv, D
     torch.cuda.synchronize()
     for turn, pair in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(pair, want[turn % 3])), turn
+
+
+@pytest.mark.parametrize("D,P,split", [(64, 8, 0), (96, 16, 0), (128, 16, 0), (256, 32, 0), (128, 1, 0),
+                                       (128, 16, 128), (256, 16, 128)])
+def test_rows_that_see_different_numbers_of_infinities(mcp, D, P, split):  # noqa: F811
+    """Infinities and NaN all over a tree's V: each row takes those of the tokens that it sees, one
+    row a handful and its neighbour a hundred, and what it does not see stays out."""
+    st = Step([(120, 130, "tree"), (33, 300, "chain"), (40, 0, "forest")], 6, 2, D, P, seed=D + P + split)
+    odd = [float("inf"), -float("inf"), float("nan")]
+    for s in range(3):
+        for i in np.flatnonzero(st.rng.random(st.q[s]) < 0.4):
+            page, off = st.slots(s, np.array([st.hist[s] + i]))
+            for c in st.rng.integers(0, D, 3):
+                st.v[page, off, int(st.rng.integers(0, 2)), int(c)] = odd[int(st.rng.integers(0, 3))]
+    out, lse = st.run(mcp, **(dict(prefill_split_tokens=split) if split else {}))
+    mcp.check_device_errors(st.error)
+    out = out.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        for s in range(3):
+            page, off = st.slots(s, np.arange(st.lens[s]))
+            k, v = (c[page, off].double().cpu().numpy() for c in (st.k, st.v))
+            a, b = st.cu[s], st.cu[s + 1]
+            want, wl, mass = ref.tree_attention(st.qs[a:b].double().cpu().numpy(), k, v, st.hist[s], st.bits[s],
+                                                st.scale)
+            good = np.isfinite(want)
+            assert good.any() and not good.all()
+            # infinities keep their sign, both signs and NaN give NaN
+            assert np.array_equal(np.where(good, 0, out[a:b]), np.where(good, 0, want), equal_nan=True), s
+            bound = 2.0 ** -8 * (np.abs(want) + mass) * 1.01 + 1e-3 * mass + 1e-6  # as in Step.compare
+            assert (np.abs(out[a:b] - want)[good] <= bound[good]).all(), s
+            assert (np.abs(lse[a:b].double().cpu().numpy() - wl) <= 1e-3).all(), s
