@@ -437,7 +437,7 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
         // item's last product (1.6 us an item; the clearing 0.4: 48 trees and 2
         // chunks 331 us, with it here 327).
         if (t >= t_tree || t == ntiles - 1) {
-          if (!(ok = wait_on(c, c.b(BV0 + s), (t / C::kVStages) & 1))) break;
+          if (!(ok = wait_on_warp(c, c.b(BV0 + s), (t / C::kVStages) & 1))) break;
           clear_rows(t, s);
           const int key0 = kv0 + t * kKvTile;
           if (t >= t_tree &&
@@ -449,8 +449,10 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
           }
         }
       }
-      if (!(ok = wait_on(c, c.b(BP0 + (t & 1)), (t >> 1) & 1))) break;
-      if (!(ok = wait_on(c, c.b(BV0 + s), (t / C::kVStages) & 1))) break;
+      ok = wait_on(c, c.b(BP0 + (t & 1)), (t >> 1) & 1) && wait_on(c, c.b(BV0 + s), (t / C::kVStages) & 1);
+      // a tree's tiles hold votes and the item's end a barrier of two roles: no lane gives up alone
+      if constexpr (kTree) ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       if constexpr (!kTree) clear_rows(t, s);
       ptx::tc_fence_after();
       if (lane == 0) {
