@@ -266,11 +266,11 @@ __device__ __forceinline__ int oob_block(const KParams& p) {
 // three of them an item: the rest of the item runs as in a causal step).
 //
 // A tree takes tensor-core tiles whatever its size.  Up to 128 query rows a kv head
-// (32 tokens at G = 4) it is bound by HBM: 57 trees over 16384 keys, 4 to 32 tokens
-// each, 6.7 to 6.8 TB/s (a copy makes 6.8).  From two tiles on, which share K/V through
-// L2, by the 0.9 us that a tile of 128 x 128 takes (64 tokens each 1.2 PFLOP/s, 4.8
-// TB/s), and at a few hundred keys by the 6 us around an item's tiles (152 trees over
-// 1024 keys 4.2 TB/s): loads of the item, its segment and its first pages in a row, the
+// (32 tokens at G = 4) it is bound by HBM: 57 trees over 16384 keys, 4 to 32 tokens each, 32/8
+// heads of 128, 558 us, 6.8 TB/s (a copy makes 6.8).  From two tiles on, which share K/V
+// through L2, by the 0.9 us that a tile of 128 x 128 takes (64 tokens each 851 us, 1.15
+// PFLOP/s, 4.5 TB/s), and at a few hundred keys by the 6 us around an item's tiles (152 trees
+// of 8 tokens over 1024 keys 148 us, 4.3 TB/s): loads of the item, its segment and its first pages in a row, the
 // first tile from memory, the epilogue.
 struct TreeRow {
   const uint32_t* words;  // the token's mask row (nullptr: none, it sees itself alone)
@@ -774,7 +774,10 @@ __device__ __forceinline__ void prefill_item(const Ctx& c, const WorkItem& it, c
       const float neg_m = m_ref == neg_inf() ? 0.f : -m_ref;
       // P = 2^(s * scale_log2 - m).  bf16 pairs of P overwrite the consumed
       // scores in place: r[i/2] after r[i], r[i+1]; the row sum runs in eight
-      // independent chains, two per packed add.
+      // independent chains, two per packed add.  The weights go to P V in bf16, half a step
+      // (2^-8 at most, of each weight alone), since both operands of one MMA have V's type; their
+      // sum takes them as they are.  Against 64 bits the output's error is 0.0023 of it, where
+      // its own rounding to bf16 makes 0.0017 (both root mean square).
       float sp[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) sp[j] = 0.f;
