@@ -39,11 +39,12 @@ __global__ void __launch_bounds__(kThreads) tree_masks_kernel(const MaskArgs p) 
   extern __shared__ uint32_t smem[];
   const int s = blockIdx.x, tid = threadIdx.x, W = p.W;
   const int t0 = p.cu[s], t1 = p.cu[s + 1];
-  const int n = t1 - t0, hist = p.sk[s] - n, m0 = p.mask_rows[s];
-  if (n <= 0) {
-    if (n < 0 && tid == 0 && p.err) atomicOr(p.err, MCP_DEVERR_SEGMENT);
+  if (t1 <= t0) {  // compared as they are: the difference of wild bounds leaves 32 bits
+    if (t1 < t0 && tid == 0 && p.err) atomicOr(p.err, MCP_DEVERR_SEGMENT);
     return;
   }
+  const int n = static_cast<int>(min(static_cast<int64_t>(t1) - t0, static_cast<int64_t>(0x7fffffff)));
+  const int hist = p.sk[s] - n, m0 = p.mask_rows[s];
   int bad = p.sk[s] < n ? MCP_DEVERR_SEGMENT : 0;
   const bool outside = t0 < 0 || t1 > p.T;
   if (outside) bad |= MCP_DEVERR_SEGMENT;

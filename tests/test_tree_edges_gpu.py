@@ -81,3 +81,21 @@ def test_rows_that_see_different_numbers_of_infinities(mcp, D, P, split):  # noq
             bound = 2.0 ** -8 * (np.abs(want) + mass) * 1.01 + 1e-3 * mass + 1e-6  # as in Step.compare
             assert (np.abs(out[a:b] - want)[good] <= bound[good]).all(), s
             assert (np.abs(lse[a:b].double().cpu().numpy() - wl) <= 1e-3).all(), s
+
+
+# ------------------------------------------------------------------ segments that are none
+LOW, HIGH = -(1 << 31), (1 << 31) - 1
+# bounds whose difference leaves 32 bits, and others that are far outside
+WILD = [(2, LOW), (HIGH, LOW), (HIGH - 1, LOW + 5), (0, LOW), (LOW, HIGH), (LOW, 0), (HIGH, 3), (-1, 3)]
+
+
+@pytest.mark.parametrize("a,b", WILD)
+@pytest.mark.parametrize("row", [0, -1])
+def test_masks_of_bounds_far_outside(mcp, a, b, row):  # noqa: F811
+    """The segment is reported and left out, whatever its bounds; the one beside it is not touched."""
+    err = err_word()
+    mask = torch.full((8, 1), 7, dtype=torch.int32, device="cuda")
+    pos = i32([-5] * 4)
+    mcp.build_tree_masks(i32([-1, 0, 0, 1]), i32([a, b]), i32([100]), i32([row]), mask, pos, err)
+    assert bits_of(err) & mcp.DEVERR_SEGMENT
+    assert (mask == 7).all() and (pos == -5).all()
