@@ -471,14 +471,16 @@ __global__ void __launch_bounds__(kThreads, kPerSM) verify_kernel(const VerifyAr
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int s = blockIdx.x / C;
   const bool lead = rank == 0;
-  const int r0 = p.cu[s], r1 = p.cu[s + 1], n = r1 - r0;
-  if (n <= 0 || r0 < 0 || r1 > p.R || n > kMaxNodes) {  // the same in all CTAs of the cluster
+  const int r0 = p.cu[s], r1 = p.cu[s + 1];
+  // compared as they are: the difference of wild bounds leaves 32 bits
+  if (r1 <= r0 || r0 < 0 || r1 > p.R || r1 - r0 > kMaxNodes) {  // the same in all CTAs of the cluster
     if (lead && tid == 0) {
       p.accepted[s] = 0;
-      if (n != 0 && p.err) atomicOr(p.err, MCP_DEVERR_SEGMENT);
+      if (r1 != r0 && p.err) atomicOr(p.err, MCP_DEVERR_SEGMENT);
     }
     return;
   }
+  const int n = r1 - r0;
   const float u_last = p.u_last[s];
   if (C > 1) cluster_arrive_relaxed();  // this CTA runs; waited for before the first remote write
   const T* const P = static_cast<const T*>(p.target);

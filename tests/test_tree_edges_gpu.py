@@ -99,3 +99,13 @@ def test_masks_of_bounds_far_outside(mcp, a, b, row):  # noqa: F811
     mcp.build_tree_masks(i32([-1, 0, 0, 1]), i32([a, b]), i32([100]), i32([row]), mask, pos, err)
     assert bits_of(err) & mcp.DEVERR_SEGMENT
     assert (mask == 7).all() and (pos == -5).all()
+
+
+@pytest.mark.parametrize("a,b", WILD)
+@pytest.mark.parametrize("draft", [True, False])
+def test_verification_of_bounds_far_outside(mcp, a, b, draft):  # noqa: F811
+    d = Drafts([4], 5000, "fp32", "tree", draft, seed=3)
+    err, path, new = err_word(), i32([9] * 4), i32([9] * 4)
+    accepted, _, _ = d.run(mcp, err, cu_rows=i32([a, b]), path=path, new_tokens=new)
+    assert bits_of(err) == mcp.DEVERR_SEGMENT and accepted.tolist() == [0]
+    assert (path == 9).all() and (new == 9).all()
