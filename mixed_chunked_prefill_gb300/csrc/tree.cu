@@ -158,11 +158,12 @@ __global__ void __launch_bounds__(kKeepThreads)
     keep_path_kernel(const __grid_constant__ KeepArgs p, const __grid_constant__ Caches caches) {
   __shared__ int64_t from[kKeepSlots], to[kKeepSlots];
   const int s = blockIdx.x / p.chunks, chunk = blockIdx.x - s * p.chunks, tid = threadIdx.x;
-  const int lq = p.cu[s + 1] - p.cu[s], sk = p.sk[s], hist = sk - lq;
-  const int r0 = p.cu_rows[s], n = p.cu_rows[s + 1] - r0, m = p.accepted[s];
+  const int sk = p.sk[s], r0 = p.cu_rows[s], r1 = p.cu_rows[s + 1], m = p.accepted[s];
+  const int64_t tokens = static_cast<int64_t>(p.cu[s + 1]) - p.cu[s];
+  const int lq = static_cast<int>(tokens), hist = sk - lq, n = r1 - r0;  // used of sound segments only
   int bad = 0;
   bool move = n == lq && lq > 0;
-  if (lq < 0 || n < 0 || sk < lq || r0 < 0 || r0 > p.total_rows - n ||
+  if (tokens < 0 || sk < tokens || r1 < r0 || r0 < 0 || r1 > p.total_rows ||
       sk > static_cast<int64_t>(p.max_pages) << p.page_log2) {
     bad = MCP_DEVERR_SEGMENT;
     move = false;

@@ -109,3 +109,22 @@ def test_verification_of_bounds_far_outside(mcp, a, b, draft):  # noqa: F811
     accepted, _, _ = d.run(mcp, err, cu_rows=i32([a, b]), path=path, new_tokens=new)
     assert bits_of(err) == mcp.DEVERR_SEGMENT and accepted.tolist() == [0]
     assert (path == 9).all() and (new == 9).all()
+
+
+@pytest.mark.parametrize("a,b", WILD)
+@pytest.mark.parametrize("rows", [None, [0, 1], [0, 4]])
+def test_kept_paths_of_bounds_far_outside(mcp, a, b, rows):  # noqa: F811
+    """Lengths that are none: of a segment's tokens, of its rows, or of both."""
+    st = Step([(4, 30, "tree")], 2, 2, 64, 16, seed=6)
+    k, v = st.k.clone(), st.v.clone()
+    for cu, cu_rows in ([(a, b), rows], [rows or (0, 4), (a, b)]):
+        # (-1, 3) is four tokens whose place in the stream is not looked at: a path of four rows, or
+        # no drafts beside one row
+        sound = (cu == (-1, 3) and cu_rows is not None)
+        err = err_word()
+        new = mcp.kv_keep_path(st.k, st.v, i32(st.bt), i32(cu), i32([34]), i32([1]), i32([0, 1, 2, 3]),
+                               cu_rows=None if cu_rows is None else i32(cu_rows), error_word=err)
+        assert bits_of(err) == (0 if sound else mcp.DEVERR_SEGMENT), (cu, cu_rows)
+        assert new.tolist() == [31 if sound and cu_rows == [0, 4] else 34], (cu, cu_rows)
+    assert torch.equal(st.k.view(torch.int16), k.view(torch.int16))
+    assert torch.equal(st.v.view(torch.int16), v.view(torch.int16))
