@@ -277,7 +277,7 @@ int launch_kv_keep_path(const mcp_keep_desc& d, void* const* k_caches, void* con
     keep_path_kernel<<<static_cast<unsigned>(grid), kKeepThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, caches);
     return static_cast<int>(cudaGetLastError());
   };
-  if (d.layer_stride != 0) {
+  if (d.layer_stride != 0 && d.num_layers > 0) {  // without layers there is no address to read
     const EvenCaches caches = {{static_cast<uint4*>(k_caches[0]), static_cast<uint4*>(v_caches[0])},
                                d.layer_stride / 8};
     return launch(caches, d.num_layers);

@@ -128,3 +128,20 @@ def test_kept_paths_of_bounds_far_outside(mcp, a, b, rows):  # noqa: F811
         assert new.tolist() == [31 if sound and cu_rows == [0, 4] else 34], (cu, cu_rows)
     assert torch.equal(st.k.view(torch.int16), k.view(torch.int16))
     assert torch.equal(st.v.view(torch.int16), v.view(torch.int16))
+
+
+def test_kept_paths_of_no_layers(mcp):  # noqa: F811
+    """The lengths alone, whatever distance is given for layers that are not there."""
+    import ctypes
+
+    from mixed_chunked_prefill_gb300 import _capi
+
+    st = Step([(5, 30, "chain"), (1, 3, None)], 2, 2, 64, 16)
+    bt, cu, sk, acc, path = i32(st.bt), i32(st.cu), i32(st.lens), i32([2, 1]), i32([0, 2, -1, -1, -1, 0])
+    for stride in (0, 64):
+        new, err = i32([-7, -7]), err_word()
+        d = _capi.KeepDesc(2, 6, 0, 2, 64, 16, st.bt.shape[1], st.pages, stride)
+        assert mcp.load().mcp_kv_keep_path(
+            ctypes.byref(d), None, None, bt.data_ptr(), cu.data_ptr(), sk.data_ptr(), None, acc.data_ptr(),
+            path.data_ptr(), new.data_ptr(), err.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+        assert new.tolist() == [32, 4] and bits_of(err) == 0
