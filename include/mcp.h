@@ -1015,8 +1015,9 @@ typedef struct mcp_keep_desc {
  * total_rows or past its table row (MCP_DEVERR_SEGMENT) move nothing and give
  * new_lens = seqlens_k; a page outside the pool (MCP_DEVERR_PAGE_RANGE) leaves
  * out its token's row.  num_kv_heads * head_dim a multiple of 8; num_layers <=
- * 1024; pages of different segments must differ where they are written, and
- * new_lens overlaps no input.
+ * 1024; pages of different segments must differ where they are written,
+ * new_lens overlaps no input, and no two of the caches share memory (rows move in
+ * place: a cache that several layers share is listed once).
  */
 mcp_status mcp_kv_keep_path(const mcp_keep_desc* desc, void* const* k_caches, void* const* v_caches,
                             const int32_t* block_tables, const int32_t* cu_seqlens_q,

@@ -909,8 +909,9 @@ def kv_keep_path(k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k, acce
     k_caches, v_caches: lists of bf16 caches [pages, P, H_kv, D], or one tensor [layers, pages, P,
     H_kv, D]; block_tables [S, max_pages_per_seq], cu_seqlens_q [S + 1], seqlens_k [S]; accepted
     [S], path [R] and cu_rows [S + 1] as ``verify_drafts`` takes and gives them (``cu_rows`` None:
-    its rows are the step's tokens), all int32 CUDA tensors.  Returns ``new_lens`` [S]: the tokens
-    that each request holds now (for ``commit_step``)."""
+    its rows are the step's tokens), all int32 CUDA tensors.  No two caches share memory: one that
+    several layers share is given once.  Returns ``new_lens`` [S]: the tokens that each request
+    holds now (for ``commit_step``)."""
     import torch
 
     dev, i32 = _gpu(accepted, "accepted"), torch.int32

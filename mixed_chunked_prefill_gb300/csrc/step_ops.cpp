@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <initializer_list>
@@ -66,6 +67,34 @@ mcp_status check_apart(std::initializer_list<Span> results, std::initializer_lis
       if (meet(*r, *q)) return fail(MCP_ERR_INVALID_ARG, "results may not overlap each other");
   }
   return MCP_OK;
+}
+
+// Whether two of the caches of a call to mcp_kv_keep_path share memory: rows move in place, so a
+// cache that stands for two layers, or for K and V, would move its rows twice.
+bool caches_overlap(const mcp_keep_desc& d, void* const* k, void* const* v) {
+  using Wide = __int128;
+  const Wide bytes = static_cast<Wide>(d.num_pages) * d.page_size * d.num_kv_heads * d.head_dim * 2;
+  const int32_t L = d.num_layers;
+  if (L == 0) return false;
+  if (d.layer_stride != 0) {
+    const Wide step = static_cast<Wide>(d.layer_stride) * 2;
+    if (L > 1 && step < bytes) return true;
+    const Wide apart = static_cast<Wide>(reinterpret_cast<uintptr_t>(v[0])) - reinterpret_cast<uintptr_t>(k[0]);
+    // V of layer l lies apart + (l - m) step behind K of layer m: the nearest of these
+    const Wide near = L > 1 ? -apart / step : 0;
+    for (Wide j = near - 1; j <= near + 1; ++j)
+      if (j > -L && j < L && apart + j * step < bytes && apart + j * step > -bytes) return true;
+    return false;
+  }
+  uintptr_t at[2 * mcp::kMaxKeepLayers];
+  for (int32_t l = 0; l < L; ++l) {
+    at[2 * l] = reinterpret_cast<uintptr_t>(k[l]);
+    at[2 * l + 1] = reinterpret_cast<uintptr_t>(v[l]);
+  }
+  std::sort(at, at + 2 * L);
+  for (int32_t i = 1; i < 2 * L; ++i)
+    if (at[i] - at[i - 1] < bytes) return true;
+  return false;
 }
 
 #define MCP_TRY(expr)                    \
@@ -435,6 +464,8 @@ mcp_status mcp_kv_keep_path(const mcp_keep_desc* d, void* const* k_caches, void*
                        words(cu_seqlens_q, d->num_seqs + 1), words(seqlens_k, d->num_seqs),
                        words(cu_rows, d->num_seqs + 1), words(accepted, d->num_seqs),
                        words(path, d->total_rows), words(error_word, 1)}));
+  if (caches_overlap(*d, k_caches, v_caches))
+    return fail(MCP_ERR_INVALID_ARG, "caches overlap: each layer's K and V must be memory of their own");
   return done(mcp::launch_kv_keep_path(*d, k_caches, v_caches, block_tables, cu_seqlens_q, seqlens_k,
                                        cu_rows, accepted, path, new_lens, error_word, stream),
               "kv_keep_path launch");

@@ -32,3 +32,52 @@ def test_kept_paths_of_no_layers_read_no_caches(lib, caches, stride):  # noqa: F
     got = alone("import mixed_chunked_prefill_gb300 as m; from test_tree_cpu import keep; "
                 f"print('status', keep(m.load(), ks={caches}, vs={caches}, num_layers=0, layer_stride={stride}))")
     assert got.returncode == 0 and f"status {_capi.MCP_ERR_CUDA}" in got.stdout, (got.returncode, got.stderr)
+
+
+def overlapping(ks, vs, size, layers, stride):
+    """Whether any two of a call's caches share a byte, one pair after another."""
+    if stride:
+        ks, vs = ([x[0] + 2 * stride * l for l in range(layers)] for x in (ks, vs))
+    all_of = list(ks) + list(vs)
+    return any(abs(a - b) < size for i, a in enumerate(all_of) for b in all_of[:i])
+
+
+SIZE = 8 * 16 * 2 * 64 * 2  # bytes of a cache of `keep`
+
+
+@pytest.mark.parametrize("ks,vs,more", [
+    ((0, 0), (2, 3), {}), ((0, 1), (2, 0), {}), ((0, 1), (2, 2), {}), ((0,), (0,), dict(num_layers=1)),
+    ((0, 1), (1.5, 3), {}), ((3, 0), (1, 2.99), {}), ((5, 1), (3, 5 - 1 / 1024), {}),
+    ((0,), (0,), dict(layer_stride=SIZE)), ((0,), (0.5,), dict(layer_stride=SIZE)),
+    ((0,), (1,), dict(layer_stride=SIZE // 2)),        # K's second layer is V's first
+    ((2,), (0,), dict(layer_stride=SIZE // 2, num_layers=3)),
+    ((0,), (8,), dict(layer_stride=SIZE // 2 - 8)),    # layers that run into each other
+    ((0,), (1 - 1 / 1024,), dict(layer_stride=64, num_layers=1)),
+    ((0,), (40.5,), dict(layer_stride=SIZE, num_layers=30)),
+])
+def test_kept_paths_refuse_caches_that_share_memory(lib, ks, vs, more):  # noqa: F811
+    """The same cache listed twice, for two layers or for K and V, would have its rows moved twice."""
+    ks, vs = ([P16 + int(x * SIZE) // 16 * 16 for x in xs] for xs in (ks, vs))
+    assert overlapping(ks, vs, SIZE, more.get("num_layers", 2), more.get("layer_stride", 0))
+    assert keep(lib, ks=ks, vs=vs, **more) == INVALID and b"caches overlap" in lib.mcp_last_error()
+
+
+def test_kept_paths_take_caches_that_only_touch(lib):  # noqa: F811
+    """Pools that hold K and V of a layer, or of all layers, side by side, in any order: they come as
+    far as their launch."""
+    rng = np.random.default_rng(1)
+    calls = []
+    for _ in range(300):
+        layers, listed = int(rng.integers(1, 6)), rng.random() < 0.5
+        if listed:
+            at = P16 + SIZE * rng.choice(40, 2 * layers, replace=rng.random() < 0.3) + 16 * rng.integers(0, 3)
+            calls.append((at[:layers].tolist(), at[layers:].tolist(), layers, 0))
+        else:
+            k, v = (P16 + SIZE * rng.integers(0, 12, 2) // 2).tolist()
+            calls.append(([k], [v], layers, int(SIZE // 4 * rng.integers(1, 9))))
+    got = alone("import mixed_chunked_prefill_gb300 as m; from test_tree_cpu import keep; lib = m.load()\n"
+                f"for k, v, n, s in {calls}:\n"
+                "    print(keep(lib, ks=k, vs=v, num_layers=n, layer_stride=s))")
+    want = [INVALID if overlapping(k, v, SIZE, n, s) else _capi.MCP_ERR_CUDA for k, v, n, s in calls]
+    assert got.returncode == 0 and [int(x) for x in got.stdout.split()] == want, got.stderr
+    assert 50 < want.count(INVALID) < 250

@@ -145,3 +145,20 @@ def test_kept_paths_of_no_layers(mcp):  # noqa: F811
             ctypes.byref(d), None, None, bt.data_ptr(), cu.data_ptr(), sk.data_ptr(), None, acc.data_ptr(),
             path.data_ptr(), new.data_ptr(), err.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
         assert new.tolist() == [32, 4] and bits_of(err) == 0
+
+
+def test_kept_paths_of_a_cache_given_twice_are_refused(mcp):  # noqa: F811
+    """Its rows would be moved twice: 2 -> 1 and 4 -> 2, and then 2, which holds 4 now, -> 1."""
+    st = Step([(5, 30, "chain")], 2, 2, 64, 16)
+    args = (i32(st.bt), i32(st.cu), i32(st.lens), i32([3]), i32([0, 2, 4, -1, -1]))
+    before = st.k.clone()
+    layers = torch.stack([st.k, st.v])
+    # an expanded tensor is its one layer listed twice
+    for k, v in (([st.k, st.k], [st.v, layers[1]]), (st.k, st.k), (layers, layers),
+                 (st.k.expand(2, *st.k.shape), st.v.expand(2, *st.k.shape))):
+        with pytest.raises(mcp.MCPError, match="caches overlap"):
+            mcp.kv_keep_path(k, v, *args)
+    assert torch.equal(st.k.view(torch.int16), before.view(torch.int16))
+    mcp.kv_keep_path([st.k, layers[0]], [st.v, layers[1]], *args)
+    moved = st.slots(0, np.array([31, 32])), st.slots(0, np.array([32, 34]))
+    assert torch.equal(st.k[moved[0]].view(torch.int16), before[moved[1]].view(torch.int16))
