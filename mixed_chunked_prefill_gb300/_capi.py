@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -52,6 +53,9 @@ class AttnDesc(ctypes.Structure):
 
 
 class PlanOptions(ctypes.Structure):
+    """``mcp_plan_options``.  A name that is none of its fields would only become an attribute of
+    the Python object, which the planner never sees: it warns."""
+
     _fields_ = [
         ("num_sms", c_int32),
         ("decode_split_tokens", c_int32),
@@ -60,6 +64,13 @@ class PlanOptions(ctypes.Structure):
         ("tree", c_int32),
         ("reserved", c_int32 * 3),
     ]
+
+    def __setattr__(self, name, value):
+        names = [n for n, _ in self._fields_]
+        if name not in names:
+            warnings.warn(f"PlanOptions has no option {name!r}, which changes nothing (it has "
+                          f"{', '.join(names)})", stacklevel=2)
+        super().__setattr__(name, value)
 
 
 class Plan(ctypes.Structure):

@@ -81,3 +81,17 @@ def test_kept_paths_take_caches_that_only_touch(lib):  # noqa: F811
     want = [INVALID if overlapping(k, v, SIZE, n, s) else _capi.MCP_ERR_CUDA for k, v, n, s in calls]
     assert got.returncode == 0 and [int(x) for x in got.stdout.split()] == want, got.stderr
     assert 50 < want.count(INVALID) < 250
+
+
+@pytest.mark.filterwarnings("error")
+def test_options_that_are_none_warn():
+    """A misspelt option would leave the plan at its defaults without a word."""
+    for make in (lambda: mcp.PlanOptions(prefil_split_tokens=128),
+                 lambda: setattr(mcp.PlanOptions(), "trees", 1)):
+        with pytest.raises(UserWarning, match="has no option '(prefil_split_tokens|trees)'"):
+            make()
+    options = mcp.PlanOptions(152, prefill_split_tokens=128, tree=1)
+    options.decode_split_tokens = 64
+    assert [getattr(options, n) for n in ("num_sms", "decode_split_tokens", "prefill_split_tokens", "tree")] == [
+        152, 64, 128, 1]
+    assert mcp.PlanOptions.from_buffer_copy(options).prefill_split_tokens == 128

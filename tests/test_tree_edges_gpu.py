@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from oracle import draft_ref as ref  # noqa: F401
-from test_tree_gpu import Drafts, Step, bits_of, cumulated, err_word, i32, mcp  # noqa: F401
+from test_tree_gpu import SEGMENTS, Drafts, Step, bits_of, cumulated, err_word, i32, mcp  # noqa: F401
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -162,3 +162,27 @@ def test_kept_paths_of_a_cache_given_twice_are_refused(mcp):  # noqa: F811
     mcp.kv_keep_path([st.k, layers[0]], [st.v, layers[1]], *args)
     moved = st.slots(0, np.array([31, 32])), st.slots(0, np.array([32, 34]))
     assert torch.equal(st.k[moved[0]].view(torch.int16), before[moved[1]].view(torch.int16))
+
+
+# ------------------------------------------------------------------------ steps' options
+@pytest.mark.parametrize("some_rows", [False, True])
+def test_a_step_with_trees_keeps_its_callers_options(mcp, some_rows):  # noqa: F811
+    """MixedStep sets the trees in a copy of the options that it is given: the splits asked for are the
+    plan's, and their parts are merged to the same results."""
+    from mixed_chunked_prefill_gb300.step import MixedStep
+
+    st = Step(SEGMENTS, 8, 2, 128, 16, seed=33)
+    rows = np.flatnonzero(st.rng.random(st.T) < 0.4) if some_rows else None
+    options, items = mcp.PlanOptions(prefill_split_tokens=128), []
+    for given in (options, None):
+        step = MixedStep(st.hq, st.hkv, st.D, st.P, st.pages, st.scale, st.cu, st.lens, st.bt, options=given,
+                         rows=rows, trees=st.tree, parents=st.parents)
+        assert step.plan.tree == 1
+        items.append((step.plan.num_items, step.plan.num_combine))
+        out = torch.full_like(st.qs, float("nan"))
+        lse = torch.full((st.T, st.hq), float("nan"), device="cuda")
+        step.attention(st.qs, st.k, st.v, out, lse)
+        step.check()
+        st.compare(out, lse, rows)
+    assert items[0][1] > 0 and items[0] != items[1]
+    assert options.tree == 0 and options.prefill_split_tokens == 128
