@@ -227,6 +227,9 @@ __device__ __forceinline__ bool no_probability(uint32_t worst) {
 // them was negative, infinite or NaN (1 operation a value where setting those to 0
 // takes 2): then the part is summed again value by value.  max(p, q) - q instead of
 // max(p - q, 0) leaves no error to be cleared.
+//
+// c q is t + lo, |lo| up to 1.5 units of t's last place: where p is that close to t (p - t is
+// exact there) lo says whether p - c q is positive, and may be all of it.
 template <typename T, int kMode, int kRing>
 __device__ __forceinline__ Two lane_sum(const Row<T>& r, int64_t a, int64_t b, int off, int lane,
                                         uint4* ring) {
@@ -237,14 +240,18 @@ __device__ __forceinline__ Two lane_sum(const Row<T>& r, int64_t a, int64_t b, i
     if constexpr (kMode == kOnlyP) {
       accumulate(acc, pv);
     } else {
-      float t = qv, lo = 0.f;
-      if constexpr (kMode == kLessCQ) {
-        t = __fmul_rn(r.ch, qv);
-        lo = __fmaf_rn(r.cl, qv, __fmaf_rn(r.ch, qv, -t));
+      float w, e;
+      if constexpr (kMode == kLessQ) {
+        const float m = fmaxf(pv, qv);
+        w = __fsub_rn(m, qv);
+        e = __fsub_rn(__fsub_rn(m, w), qv);
+      } else {
+        const float t = __fmul_rn(r.ch, qv), lo = __fmaf_rn(r.cl, qv, __fmaf_rn(r.ch, qv, -t));
+        const float d = __fsub_rn(pv, t);
+        w = fmaxf(d, 0.f);
+        e = __fsub_rn(__fsub_rn(__fsub_rn(pv, d), t), lo);  // w + e = p - c q where p > t
+        e = fmaxf(__fadd_rn(e, __fsub_rn(d, w)), -w);       // where it is below, e alone; none below 0
       }
-      const float m = fmaxf(pv, t), w = __fsub_rn(m, t);
-      float e = __fsub_rn(__fsub_rn(m, w), t);
-      if constexpr (kMode == kLessCQ) e = w > 0.f ? __fsub_rn(e, lo) : 0.f;
       accumulate(acc, w);
       acc.l = __fadd_rn(acc.l, e);
     }

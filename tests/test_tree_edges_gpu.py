@@ -186,3 +186,50 @@ def test_a_step_with_trees_keeps_its_callers_options(mcp, some_rows):  # noqa: F
         st.compare(out, lse, rows)
     assert items[0][1] > 0 and items[0] != items[1]
     assert options.tree == 0 and options.prefill_split_tokens == 128
+
+
+# ----------------------------------------------------------------------- verification
+def refused_twice(V, seed, delta, others):
+    """Rows p and q of a root with two nodes of token 0, which p does not have, so that both are
+    refused and c = 1 + N, N = sum max(p - q, 0).  q of the other tokens are multiples of 2^-24 that
+    add up to 1 and p = q (1 + delta) rounded to fp32, which makes N = delta up to the roundings: p - c q
+    is what p was rounded by, but for `others` tokens of larger p."""
+    rng = np.random.default_rng(seed)
+    k = np.floor(rng.dirichlet(np.ones(V - 1)) * (2 ** 24 - V)).astype(np.int64) + 1
+    k[0] += 2 ** 24 - k.sum()
+    q = np.concatenate([[0.5], k / 2.0 ** 24]).astype(np.float32)
+    p = (q.astype(np.float64) * (1 + delta)).astype(np.float32)
+    p[0] = 0
+    d = Drafts([3], V, "fp32", "star", True, seed=seed)
+    for at in others:  # more of one token, and as much less of another: N as before
+        p[at] += np.float32(2.0 ** -20)
+        p[at + 1] -= np.float32(2.0 ** -20)
+    d.target[:], d.draft[:] = torch.tensor(p), torch.tensor(q)
+    d.tokens[:] = 0
+    d.u[:] = 0.5
+    return d, p.astype(np.float64), q.astype(np.float64)
+
+
+@pytest.mark.parametrize("V", [300, 5000, 40000])
+@pytest.mark.parametrize("others", [[], [20, 80, 200]])
+def test_what_remains_is_what_the_rows_were_rounded_by(mcp, V, others):  # noqa: F811
+    """After two refusals p - c q lies below the rounding of c q nearly everywhere.  What remains is
+    those differences, not nothing (the token would be drawn from p then), and the token is drawn
+    from them."""
+    for seed in range(6):
+        d, p, q = refused_twice(V, seed, 0.37 + 0.01 * seed, others)
+        c = 1 + np.maximum(p - q, 0).sum()
+        w = np.maximum(p - c * q, 0)
+        assert 0 < w.sum() < 2.0 ** -15 and (others or (np.abs(p - c * q)[1:] <= 2.0 ** -22 * p[1:]).all())
+        # c is a sum of V differences as a pair of fp32, off by 2^-44 (2^-49 of the sum for each value
+        # of a lane, 160 at most); so is each c q, by 2^-47 of it: prefix sums of w are off by less
+        # than 2^-43 of sum p + c sum q < 4
+        off = 2.0 ** -41
+        s = np.concatenate([[0], np.cumsum(w)])
+        for last in (0.01, 0.3, 0.5, 0.77, 0.99):
+            d.u_last[:] = last
+            accepted, path, new = d.run(mcp, err_word())
+            v, aim = int(new[0]), float(d.u_last[0]) * s[-1]
+            assert accepted.tolist() == [1] and path.tolist() == [0, -1, -1]
+            assert s[v] <= aim + off and aim - off <= s[v + 1], (seed, last, v)
+            assert w[v] > 0 or abs(p[v] - c * q[v]) < off
