@@ -964,8 +964,12 @@ typedef struct mcp_verify_tensors {
  * so that new_tokens and cu_rows go to mcp_update_token_counts, and path and
  * accepted to mcp_kv_keep_path.  Rows behind the last segment stay as they were.
  *
- * Sums are held to 2^-40 of themselves and better; entries that are negative,
- * infinite or NaN count as 0.  A row at which a walk ends without a positive
+ * Values and sums are pairs of fp32: each p - c q is off by at most 2^-47 of
+ * p + c q, a sum of positive values by about 2^-45 of itself over 128000 of them,
+ * 2^-41 over 2^22 and 2^-36 over 2^24 (the low words of 256 lanes are added up in
+ * fp32; fewer values a lane, and so less, where several blocks share a segment).
+ * What remains after refusals can be a small part of p and of c q, and is known
+ * to that many bits less.  Entries that are negative, infinite or NaN count as 0.  A row at which a walk ends without a positive
  * entry sets MCP_DEVERR_PROBS and gives token -1.  A drafted token outside the
  * vocabulary hangs under none (>= vocab_size sets MCP_DEVERR_TOKEN_RANGE, a
  * negative one is padding), and so does a node whose parent is not before it

@@ -233,3 +233,48 @@ def test_what_remains_is_what_the_rows_were_rounded_by(mcp, V, others):  # noqa:
             assert accepted.tolist() == [1] and path.tolist() == [0, -1, -1]
             assert s[v] <= aim + off and aim - off <= s[v + 1], (seed, last, v)
             assert w[v] > 0 or abs(p[v] - c * q[v]) < off
+
+
+@pytest.mark.parametrize("copies", [1, 64])
+@pytest.mark.parametrize("children", [0, 1, 2, 4, 6])
+def test_borders_of_what_remains_when_the_draft_is_close(mcp, copies, children):  # noqa: F811
+    """Rows of 128000 values whose draft is off by half a percent, every child refused: what remains is
+    a thousandth of p.  Random numbers right above and below borders between two tokens find the
+    token that 64-bit sums give."""
+    V, rng = 128000, np.random.default_rng(children)
+    z = rng.standard_normal(V) * 2.5
+    p, q = (np.exp(x) / np.exp(x).sum() for x in (z, z + rng.standard_normal(V) * 0.005))
+    p[0] = 0  # the children's token
+    p, q = p.astype(np.float32), q.astype(np.float32)
+    c, P, Q = 0.0, p.astype(np.float64), q.astype(np.float64)
+    mass = 1.0
+    for _ in range(children):
+        c += mass
+        mass = np.maximum(P - c * Q, 0).sum()
+    w = np.maximum(P - c * Q, 0)
+    s = np.concatenate([[0], np.cumsum(w)])
+    assert children == 0 or 2.0 ** -13 < s[-1] < 2.0 ** -7
+    # A lane adds up n values, n = 500 where a CTA has the row, and sums of w are off by at most
+    # n^2 2^-48 of themselves (its low word is at most n 2^-24 of the high one, and rounded n times by
+    # 2^-24 of that); a weight by 2^-47 of p + c q.  All of p: sums off by 2^-30; a part of 2^-7 with
+    # the weights' part: 2^-37 + 2^-45, and c is a sum of up to six such.  Rounds of 16 and of 8 CTAs
+    # have n = 32 and 63 and so 2^-36 of all, 2^-43 + 2^-45 of a part: with c, 2^-36 and 2^-39.
+    off = 2.0 ** -36 if children == 0 else 2.0 ** -39
+    rows = children + 1
+    d = Drafts([rows] * copies, 4, "fp32", "star", True)
+    d.V = V
+    d.target, d.draft = (torch.tensor(x).cuda().expand(rows * copies, V).contiguous() for x in (p, q))
+    d.tokens[:], d.u[:] = 0, 0.5
+    told = 0
+    for _ in range(-(-256 // copies)):
+        at = rng.choice(np.flatnonzero(w > 0), copies, p=w[w > 0] / s[-1])  # a border is the one before it
+        u = (s[at] / s[-1]).astype(np.float32)
+        up = rng.random(copies) < 0.5
+        d.u_last = np.where(up, np.nextafter(u, np.float32(1)), np.nextafter(u, np.float32(0))).astype(np.float32)
+        accepted, path, new = d.run(mcp, err_word())
+        assert (accepted == 1).all()
+        aim = d.u_last.astype(np.float64) * s[-1]
+        v = new.cpu().numpy()[::rows]
+        assert (w[v] > 0).all() and (s[v] <= aim + off).all() and (aim - off <= s[v + 1]).all()
+        told += ((s[v] <= aim - off) & (aim + off <= s[v + 1])).sum()
+    assert told > 100  # most numbers lie further from the borders than the sums may be off
