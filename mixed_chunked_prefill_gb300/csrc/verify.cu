@@ -25,10 +25,10 @@
 // What remains after refusals is a part of p and c q and keeps the fewer bits the smaller it is.
 //
 // Measured: 64 chains of 4 to 8 rows of 128000 fp32 values (65 MB of p and q where the
-// walks end) 19.2 us, the pass itself at 5.5 TB/s behind 5 us of loads that depend on
-// each other; 32 trees of up to 32 rows, some with eight passes, 25.4; 256 given trees of
-// 50257 bf16 values 20.0 (26 MB, bound by the latencies and the sums' operations); one
-// chain 7.4.
+// walks end) 19.3 us, the pass itself at 5.5 TB/s behind 5 us of loads that depend on
+// each other; 32 trees of up to 32 rows, the mean of three sets of them, some with eight
+// passes, 31.4; 256 given trees of 50257 bf16 values 20.5 (26 MB,
+// bound by the latencies and the sums' operations); one chain 7.6.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -730,8 +730,9 @@ __global__ void __launch_bounds__(kThreads, kPerSM) verify_kernel(const VerifyAr
 }
 
 // CTAs that share a segment: as many as the GPU has room for at once, but none with
-// less than 4096 values of a row.  With 4, 8 and 16 of them 64 chains took 27, 21 and 32
-// us, one chain 13.6, 10.3 and 8.5; with 1, 2 and 4 256 given trees 35, 27 and 32.
+// less than 4096 values of a row.  With 4, 8 and 16 of them 64 chains take 22.9, 18.9 and
+// 25.8 us, one chain 14.2, 9.5 and 7.5, 32 trees 50, 36.6 and 31.6; with 1, 2 and 4 256 given
+// trees 22.8, 20.6 and 24.6.
 int cluster_of(const mcp_verify_desc& d) {
   int c = kMaxCluster;
   while (c > 1 && (static_cast<int64_t>(d.num_seqs) * c > kPerSM * static_cast<int64_t>(step_num_sms()) || d.vocab_size / c < 4096))
