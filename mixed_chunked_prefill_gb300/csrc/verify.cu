@@ -250,9 +250,10 @@ __device__ __forceinline__ Two lane_sum(const Row<T>& r, int64_t a, int64_t b, i
       } else {
         const float t = __fmul_rn(r.ch, qv), lo = __fmaf_rn(r.cl, qv, __fmaf_rn(r.ch, qv, -t));
         const float d = __fsub_rn(pv, t);
-        w = fmaxf(d, 0.f);
-        e = __fsub_rn(__fsub_rn(__fsub_rn(pv, d), t), lo);  // w + e = p - c q where p > t
-        e = fmaxf(__fadd_rn(e, __fsub_rn(d, w)), -w);       // where it is below, e alone; none below 0
+        e = __fsub_rn(__fsub_rn(__fsub_rn(pv, d), t), lo);  // d + e = p - c q
+        const float all = __fadd_rn(d, e);
+        w = fmaxf(all, 0.f);
+        e = all > 0.f ? __fsub_rn(e, __fsub_rn(all, d)) : 0.f;
       }
       accumulate(acc, w);
       acc.l = __fadd_rn(acc.l, e);

@@ -278,3 +278,46 @@ def test_borders_of_what_remains_when_the_draft_is_close(mcp, copies, children):
         assert (w[v] > 0).all() and (s[v] <= aim + off).all() and (aim - off <= s[v + 1]).all()
         told += ((s[v] <= aim - off) & (aim + off <= s[v + 1])).sum()
     assert told > 100  # most numbers lie further from the borders than the sums may be off
+
+
+@pytest.mark.parametrize("V", [3000, 30000])
+def test_nothing_remains_within_a_rounding(mcp, V):  # noqa: F811
+    """After two refusals p is below c q everywhere, by less than one and a half units of its last
+    place, and above c q's rounded value in some places: nothing remains, and the token is p's."""
+    some = 0
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        first = float(np.float32(1.25 + 0.1 * seed))
+        c = first + 0.45 * 2.0 ** -23  # the second fp32 of c as large as it gets
+
+        def below(x):  # the largest fp32 that is not above x
+            y = x.astype(np.float32)
+            return np.where(y > x, np.nextafter(y, np.float32(0)), y).astype(np.float32)
+
+        # q of the tokens but 0 add up to 1 + h, so that N = sum (p - q) = c h + c - 1 - h - (what p was
+        # rounded by, r), and 1 + N = c + (c - 1) h - r, above c by a tenth of r where h = 1.1 r / (c - 1)
+        k = np.floor(rng.dirichlet(np.ones(V - 1) * 4) * (2 ** 24 - V)).astype(np.int64) + 1
+        k[0] += 2 ** 24 - k.sum()
+        q = k / 2.0 ** 24
+        r = (c * q - below(c * q)).sum()
+        q *= 1 + 1.1 * r / (c - 1)
+        q = np.concatenate([[0.5], q]).astype(np.float32)
+        p = below(c * q.astype(np.float64))
+        p[0] = 0
+        P, Q = p.astype(np.float64), q.astype(np.float64)
+        now = 1 + np.maximum(P - Q, 0).sum()
+        if ((P - now * Q) / Q).max() > -2.0 ** -32:
+            continue  # q's own rounding moved its sum too far
+        some += int((p > np.float32(now) * q).sum())
+        d = Drafts([3], V, "fp32", "star", True, seed=seed)
+        d.target[:], d.draft[:] = torch.tensor(p), torch.tensor(q)
+        d.tokens[:], d.u[:] = 0, 0.5
+        s = np.concatenate([[0], np.cumsum(P)])
+        for last in (0.03, 0.4, 0.8, 0.999):
+            d.u_last[:] = last
+            err = err_word()
+            accepted, _, new = d.run(mcp, err)
+            v, aim = int(new[0]), float(d.u_last[0]) * s[-1]
+            assert bits_of(err) == 0 and accepted.tolist() == [1]
+            assert p[v] > 0 and s[v] <= aim + 2.0 ** -36 and aim - 2.0 ** -36 <= s[v + 1], (seed, last, v)
+    assert some > 100
