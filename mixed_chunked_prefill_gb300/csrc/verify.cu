@@ -164,15 +164,21 @@ struct Row {
   }
 };
 
-// max(p - (ch + cl) q, 0) of values as they stand there, the product and the
-// difference each with its error.  Not inlined: the kernel waits for instructions
-// more than for anything else where they are run once a row.
+// max(p - (ch + cl) q, 0) of probabilities p and q as a sum of two fp32.  c q is t + lo, |lo|
+// up to 1.5 units of t's last place: where p is that close to t (p - t is exact there) lo
+// says whether p - c q is positive, and may be all of it.
+__device__ __forceinline__ Two less_cq(float pv, float qv, float ch, float cl) {
+  const float t = __fmul_rn(ch, qv), lo = __fmaf_rn(cl, qv, __fmaf_rn(ch, qv, -t));
+  const float d = __fsub_rn(pv, t);
+  const float e = __fsub_rn(__fsub_rn(__fsub_rn(pv, d), t), lo);  // d + e = p - c q
+  const float all = __fadd_rn(d, e);
+  return {fmaxf(all, 0.f), all > 0.f ? __fsub_rn(e, __fsub_rn(all, d)) : 0.f};
+}
+// The same of values as they stand there, so that a part whose sum is positive holds a
+// positive value.  Not inlined: the kernel waits for instructions more than for anything
+// else where they are run once a row.
 __device__ __noinline__ Two weight_of(float p_raw, float q_raw, float ch, float cl) {
-  const float pv = clean(p_raw), qv = clean(q_raw);
-  const float t = __fmul_rn(ch, qv), e = __fmaf_rn(ch, qv, -t);
-  const Two d = two_sum(pv, -t);
-  const Two w = normal({d.h, __fsub_rn(__fsub_rn(d.l, e), __fmul_rn(cl, qv))});
-  return w.h > 0.f ? w : Two{0.f, 0.f};
+  return less_cq(clean(p_raw), clean(q_raw), ch, cl);
 }
 // Weight of token v, read alone
 template <typename T>
@@ -229,9 +235,6 @@ __device__ __forceinline__ bool no_probability(uint32_t worst) {
 // them was negative, infinite or NaN (1 operation a value where setting those to 0
 // takes 2): then the part is summed again value by value.  max(p, q) - q instead of
 // max(p - q, 0) leaves no error to be cleared.
-//
-// c q is t + lo, |lo| up to 1.5 units of t's last place: where p is that close to t (p - t is
-// exact there) lo says whether p - c q is positive, and may be all of it.
 template <typename T, int kMode, int kRing>
 __device__ __forceinline__ Two lane_sum(const Row<T>& r, int64_t a, int64_t b, int off, int lane,
                                         uint4* ring) {
@@ -248,12 +251,9 @@ __device__ __forceinline__ Two lane_sum(const Row<T>& r, int64_t a, int64_t b, i
         w = __fsub_rn(m, qv);
         e = __fsub_rn(__fsub_rn(m, w), qv);
       } else {
-        const float t = __fmul_rn(r.ch, qv), lo = __fmaf_rn(r.cl, qv, __fmaf_rn(r.ch, qv, -t));
-        const float d = __fsub_rn(pv, t);
-        e = __fsub_rn(__fsub_rn(__fsub_rn(pv, d), t), lo);  // d + e = p - c q
-        const float all = __fadd_rn(d, e);
-        w = fmaxf(all, 0.f);
-        e = all > 0.f ? __fsub_rn(e, __fsub_rn(all, d)) : 0.f;
+        const Two x = less_cq(pv, qv, r.ch, r.cl);
+        w = x.h;
+        e = x.l;
       }
       accumulate(acc, w);
       acc.l = __fadd_rn(acc.l, e);
