@@ -25,10 +25,10 @@
 // What remains after refusals is a part of p and c q and keeps the fewer bits the smaller it is.
 //
 // Measured: 64 chains of 4 to 8 rows of 128000 fp32 values (65 MB of p and q where the
-// walks end) 19.3 us, the pass itself at 5.5 TB/s behind 5 us of loads that depend on
+// walks end) 18.8 us, the pass itself at 5.5 TB/s behind 5 us of loads that depend on
 // each other; 32 trees of up to 32 rows, the mean of three sets of them, some with eight
-// passes, 31.4; 256 given trees of 50257 bf16 values 20.5 (26 MB,
-// bound by the latencies and the sums' operations); one chain 7.6.
+// passes, 31.6; 256 given trees of 50257 bf16 values 20.5 (26 MB,
+// bound by the latencies and the sums' operations); one chain 7.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
