@@ -159,9 +159,9 @@ __device__ __forceinline__ Segment read_segment(const Segments& g, int32_t s) {
   x.q0 = g.cu[s];
   x.q1 = g.cu[s + 1];
   x.id = g.ids[s];
-  const int32_t n = x.q1 - x.q0;
-  x.old = g.sk[s] > n;
-  if (x.q0 < 0 || n < 0 || x.q1 > g.T || x.id >= g.R) x.id = -1;
+  x.old = g.sk[s] > x.q1 - x.q0;
+  // compared as they are: the difference of wild bounds leaves 32 bits
+  if (x.q0 < 0 || x.q1 < x.q0 || x.q1 > g.T || x.id >= g.R) x.id = -1;
   return x;
 }
 
